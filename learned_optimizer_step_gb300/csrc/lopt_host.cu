@@ -20,6 +20,7 @@
 #include <vector>
 
 #include "lopt.h"
+#include "lopt_train.h"
 #include "lopt_internal.cuh"
 
 namespace lopt {
@@ -502,6 +503,7 @@ const char* lopt_strerror(int code) {
     case LOPT_E_TIMEOUT: return "device-side wait timed out";
     case LOPT_E_ALIAS: return "tensor buffers overlap";
     case LOPT_E_TOO_LARGE: return "tensor needs more scratch than the static no-allocation buffer";
+    case LOPT_E_INDEX: return "index out of range";
     default: return "unknown error";
   }
 }
