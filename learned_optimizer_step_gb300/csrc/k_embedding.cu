@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(256) k_embed_fwd(const EmbedFwd a) {
   if (i >= a.n || j >= a.cols) return;
   const int64_t id = load_index(a.index, i, a.itype);
   const bool real = id >= 0 && id < a.rows;
-  if (id >= a.rows && a.status && j == 0) atomicOr(a.status, 1);
+  if (id >= a.rows && a.status && j == 0) atomicOr(a.status, kStatusIndex);
   Pack<TO, VEC> o;
   if (real) {
     const Pack<TI, VEC> p = *reinterpret_cast<const Pack<TI, VEC>*>(static_cast<const TI*>(a.table) + id * a.ts + j);
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const EmbedSort a) 
       }
     }
   }
-  if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, 1);
+  if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, kStatusIndex);
   for (int o = 16; o > 0; o >>= 1) below += __shfl_xor_sync(0xffffffffu, below, o);
   if (lane == 0 && below) atomicAdd(&below_sum, below);   // integers: any order gives the same
   __syncthreads();

@@ -44,6 +44,10 @@ __device__ __forceinline__ int64_t load_index(const void* p, int64_t i, int type
   return type == LOPT_I32 ? (int64_t) static_cast<const int32_t*>(p)[i] : static_cast<const int64_t*>(p)[i];
 }
 
+// Bits of the caller's status word.
+constexpr int32_t kStatusIndex = 1;    // an index at or above its limit
+constexpr int32_t kStatusGaveUp = 2;   // a bounded wait ran out: results are not valid
+
 // ---- reductions ----------------------------------------------------------------
 // Butterflies: every lane ends with the same bits, since a + b == b + a.
 __device__ __forceinline__ float warp_sum(float v) {
