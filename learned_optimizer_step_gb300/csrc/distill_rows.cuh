@@ -222,12 +222,13 @@ template <typename T> struct Slice {
   int cols, mis, beg, cnt;
   int first, last;     // the slice's slots that are not whole, or -1
   bool same;           // the gradient's row starts alike
-  __device__ __forceinline__ Slice(const Distill& a, int64_t row, int rank, int C) {
+  // One of 2^log_c slices.
+  __device__ __forceinline__ Slice(const Distill& a, int64_t row, int rank, int log_c) {
     z = static_cast<const T*>(a.logits) + row * a.ls;
     g = a.grad ? static_cast<T*>(a.grad) + row * a.gs : nullptr;
     cols = (int)a.cols;
     mis = (int)(((uintptr_t)z / sizeof(T)) % N);
-    const int total = (mis + cols + N - 1) / N, per = (total + C - 1) / C;
+    const int total = (mis + cols + N - 1) / N, per = (total + (1 << log_c) - 1) >> log_c;
     beg = min(rank * per, total);
     cnt = min(per, total - beg);
     same = (int)(((uintptr_t)g / sizeof(T)) % N) == mis;
@@ -237,25 +238,41 @@ template <typename T> struct Slice {
   __device__ __forceinline__ const uint4* z16() const { return reinterpret_cast<const uint4*>(z - mis) + beg; }
   __device__ __forceinline__ bool whole(int q) const { return q != first && q != last; }
   // A slot that is not whole, -inf outside the row.
-  __device__ __forceinline__ void read_edge(int q, uint32_t v[4]) const {
+  __device__ __forceinline__ uint4 read_edge(int q) const { return read_elements(z, (beg + q) * N - mis, cols); }
+  static __device__ __noinline__ uint4 read_elements(const T* z, int j, int cols) {
+    uint32_t v[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = Slots<T>::kNegInf;
-    T* e = reinterpret_cast<T*>(v);
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      const int j = (beg + q) * N + k - mis;
-      if (j >= 0 && j < cols) e[k] = z[j];
+      if (j + k < 0 || j + k >= cols) continue;
+      if constexpr (sizeof(T) == 4) {
+        v[k] = reinterpret_cast<const uint32_t*>(z)[j + k];
+      } else {
+        const uint32_t e = reinterpret_cast<const uint16_t*>(z)[j + k];
+        v[k / 2] = k & 1 ? (v[k / 2] & 0xffffu) | e << 16 : (v[k / 2] & 0xffff0000u) | e;
+      }
     }
+    return make_uint4(v[0], v[1], v[2], v[3]);
   }
   __device__ __forceinline__ void write(int q, const uint32_t v[4]) const {
     if (same && whole(q)) {
       reinterpret_cast<uint4*>(g - mis)[beg + q] = make_uint4(v[0], v[1], v[2], v[3]);
     } else {
-      const T* e = reinterpret_cast<const T*>(v);
+      write_elements(g, (beg + q) * N - mis, cols, make_uint4(v[0], v[1], v[2], v[3]));
+    }
+  }
+  // Columns j .. j + N - 1, those that the row has.
+  static __device__ __noinline__ void write_elements(T* g, int j, int cols, uint4 x) {
+    const uint32_t v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const int j = (beg + q) * N + k - mis;
-        if (j >= 0 && j < cols) g[j] = e[k];
+    for (int k = 0; k < N; ++k) {
+      const uint32_t w = v[k * (int)sizeof(T) / 4];
+      if (j + k < 0 || j + k >= cols) continue;
+      if constexpr (sizeof(T) == 4) {
+        reinterpret_cast<uint32_t*>(g)[j + k] = w;
+      } else {
+        reinterpret_cast<uint16_t*>(g)[j + k] = (uint16_t)(k & 1 ? w >> 16 : w);
       }
     }
   }
@@ -336,7 +353,7 @@ __global__ void __launch_bounds__(256) k_distill_warp(const Distill a) {
   float* p = reinterpret_cast<float*>(id + a.top);
   float* zi = p + a.top;
   float* tl = zi + a.top;
-  const Slice<T> r(a, row, 0, 1);
+  const Slice<T> r(a, row, 0, 0);
   const float w = a.row_weight ? a.row_weight[row] : 1.f;
   uint32_t v[NV][4];
   float tmax, ps;
@@ -345,15 +362,9 @@ __global__ void __launch_bounds__(256) k_distill_warp(const Distill a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int q = i * 32 + lane;
-      if (q < r.cnt && r.whole(q)) {
-        const uint4 x = r.z16()[q];
-        v[i][0] = x.x; v[i][1] = x.y; v[i][2] = x.z; v[i][3] = x.w;
-      } else if (q < r.cnt) {
-        r.read_edge(q, v[i]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[i][k] = S::kNegInf;
-      }
+      uint4 x = make_uint4(S::kNegInf, S::kNegInf, S::kNegInf, S::kNegInf);
+      if (q < r.cnt) x = r.whole(q) ? r.z16()[q] : r.read_edge(q);
+      v[i][0] = x.x; v[i][1] = x.y; v[i][2] = x.z; v[i][3] = x.w;
     }
     for (int k = lane; k < a.top; k += 32) {
       load_top(a, row, k, true, id[k], tl[k]);
@@ -417,176 +428,454 @@ __device__ __forceinline__ void send_pair(const float2* at, const uint64_t* bar,
                :: "r"(ra), "r"(__float_as_uint(m)), "r"(__float_as_uint(s)), "r"(rb) : "memory");
 }
 
-// Persistent: cluster i takes rows i, i + clusters, ...  Each block's slice
-// of the next row lands in shared memory by a bulk copy, issued as soon as
-// the last read of the current row is done, so that loads run while the
-// block still stores and another block of the SM computes.  A thread reads
-// its slots twice: for its part of (m, s), and for the dense gradient.
+// A row's list as one warp keeps it in shared memory.  Per slot: the class
+// (none if it does not count), its weight 2^((t - max) log2e / T), its logit
+// z, and, for the first slot of a class of this block's slice, the class's
+// place in a hash table (at most half full) that sums the weights of repeats.
+struct List {
+  int32_t *id, *place, *key;
+  float *e, *z, *sum;
+  int top, log_size;
+  // Of the whole list: 1 / sum of e, sum of p log p; whether any slot counts.
+  float inv, p_log_p;
+  bool any;
+};
+__host__ __device__ inline int table_log_size(int top) {
+  int n = 5;
+  while (1 << n < 2 * top) ++n;
+  return n;
+}
+__host__ __device__ inline int list_words(int top) { return 4 * top + 2 * (1 << table_log_size(top)); }
+
+// Slots are taken 128 at a time, four of a lane's side by side: the list is
+// a chain of short steps, and its warp has latency to lose, not work.
+#define LOPT_LIST_SLOTS(k0, top)                 \
+  for (int k0 = 0; k0 < (top); k0 += 128)
+
+// The first 128 slots as loaded, a row ahead of their use.
+struct ListAhead {
+  int64_t id[4];
+  uint32_t t[4];
+};
+template <typename T>
+__device__ __forceinline__ void load_list(const Distill& a, int64_t row, int k0, ListAhead& x) {
+  const int lane = threadIdx.x % 32;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int k = k0 + u * 32 + lane;
+    x.id[u] = -1;
+    x.t[u] = 0;
+    if (k >= a.top) continue;
+    if (a.itype == LOPT_I32) x.id[u] = static_cast<const int32_t*>(a.top_index)[row * a.is + k];
+    else x.id[u] = static_cast<const int64_t*>(a.top_index)[row * a.is + k];
+    if (a.ttype == LOPT_F32) x.t[u] = static_cast<const uint32_t*>(a.top_logits)[row * a.ts + k];
+    else x.t[u] = static_cast<const uint16_t*>(a.top_logits)[row * a.ts + k];
+  }
+}
+template <typename T>
+__device__ __forceinline__ float top_logit(const Distill& a, uint32_t raw) {
+  if (a.ttype == LOPT_F32) return __uint_as_float(raw);
+  if constexpr (sizeof(T) == 4) {
+    return __uint_as_float(raw);
+  } else {
+    const uint16_t h = (uint16_t)raw;
+    return to_f(*reinterpret_cast<const T*>(&h));
+  }
+}
+
+template <typename T, bool GRAD>
+__device__ __forceinline__ void make_list(const Distill& a, const Slice<T>& r, int64_t row, bool report, ListAhead x, List& l) {
+  const int lane = threadIdx.x % 32, size = 1 << l.log_size;
+  if (GRAD) {
+    for (int h = lane; h < size; h += 32) {
+      l.key[h] = -1;
+      l.sum[h] = 0.f;
+    }
+  }
+  float tmax = -INFINITY;
+  bool any = false, bad = false;
+  LOPT_LIST_SLOTS(k0, l.top) {
+    if (k0 > 0) load_list<T>(a, row, k0, x);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int k = k0 + u * 32 + lane;
+      const float t = top_logit<T>(a, x.t[u]);
+      bad |= x.id[u] >= a.cols;
+      const bool counts = x.id[u] >= 0 && x.id[u] < a.cols && t != -INFINITY;
+      if (k < l.top) {
+        l.id[k] = counts ? (int32_t)x.id[u] : -1;
+        l.e[k] = t;
+      }
+      if (counts) tmax = fmaxf(tmax, t);
+      any |= counts;
+    }
+  }
+  if (bad && report && a.status) atomicOr(a.status, kStatusIndex);
+  l.any = __any_sync(0xffffffffu, any);
+  if (l.any) {   // the same for all lanes
+    tmax = warp_max(tmax);
+    float es = 0.f, ed = 0.f;
+    LOPT_LIST_SLOTS(k0, l.top) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int k = k0 + u * 32 + lane;
+        if (k >= l.top) continue;
+        const float d = l.e[k] - tmax, e = l.id[k] < 0 ? 0.f : ex2(d * a.log2e_t);
+        es += e;
+        if (e != 0.f) ed = fmaf(e, d, ed);   // 0 log 0 = 0
+        l.e[k] = e;
+      }
+    }
+    es = warp_sum(es);
+    ed = warp_sum(ed);
+    l.inv = 1.f / es;
+    l.p_log_p = ed * l.inv * a.inv_t - logf(es);   // sum p (d / T - log es), sum p = 1
+    __syncwarp();
+    if (GRAD) {
+      for (int k0 = 0; k0 < l.top; k0 += 32) {
+        const int k = k0 + lane;
+        int32_t i = k < l.top ? l.id[k] : -1;
+        if (!r.holds(i)) i = -1;   // another block's
+        int place = -1;
+        const unsigned alike = __match_any_sync(0xffffffffu, i);
+        if (i >= 0 && lane == __ffs(alike) - 1) {   // its first slot here: sums in slot order
+          float e = 0.f;
+          for (unsigned rest = alike; rest; rest &= rest - 1) e += l.e[k0 + __ffs(rest) - 1];
+          unsigned h = (unsigned)i * 2654435761u >> (32 - l.log_size);
+          int32_t old;
+          while ((old = atomicCAS(l.key + h, -1, i)) != -1 && old != i) h = (h + 1) & (size - 1);
+          l.sum[h] += e;
+          if (old == -1) place = (int)h;
+        }
+        if (k < l.top) l.place[k] = place;
+        __syncwarp();
+      }
+    }
+  }
+}
+
+// The logits of the slots of this slice, from where it landed: those in whole
+// 16-byte slots, or those in the others.
+template <typename T, bool WHOLE>
+__device__ __forceinline__ void read_listed(const Slice<T>& r, const uint4* buf, const List& l) {
+  const T* z = reinterpret_cast<const T*>(buf) + (r.mis - r.beg * Slice<T>::N);   // column j at z[j]
+  LOPT_LIST_SLOTS(k0, l.top) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int k = k0 + u * 32 + (int)(threadIdx.x % 32);
+      if (k >= l.top) continue;
+      const int j = l.id[k];
+      if (r.holds(j) && r.whole((j + r.mis) / Slice<T>::N - r.beg) == WHOLE) l.z[k] = to_f(z[j]);
+    }
+  }
+}
+
+// The slice's part of sum p z, as (ref, sum of p (z - ref)) and sum of p: exact
+// about any row maximum.
+template <typename T>
+__device__ __forceinline__ void sum_listed(const Slice<T>& r, const List& l, float& ref, float& pz, float& ps) {
+  const int lane = threadIdx.x % 32;
+  ref = -INFINITY;
+  LOPT_LIST_SLOTS(k0, l.top) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int k = k0 + u * 32 + lane;
+      if (k < l.top && r.holds(l.id[k]) && l.e[k] != 0.f) ref = fmaxf(ref, l.z[k]);
+    }
+  }
+  ref = warp_max(ref);
+  if (ref == -INFINITY) ref = 0.f;
+  pz = ps = 0.f;
+  LOPT_LIST_SLOTS(k0, l.top) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int k = k0 + u * 32 + lane;
+      if (k >= l.top || !r.holds(l.id[k])) continue;
+      const float p = l.e[k] * l.inv;
+      if (p == 0.f) continue;   // 0 log 0 = 0
+      pz = fmaf(p, l.z[k] - ref, pz);
+      ps += p;
+    }
+  }
+  pz = warp_sum(pz);
+  ps = warp_sum(ps);
+}
+
+// The row's (m, s) from all its warps' pairs, by one warp, in a fixed order.
+template <int N>
+__device__ __forceinline__ void join_pairs(const float2* got, int n, float c, float& m, float& s) {
+  const int lane = threadIdx.x % 32;
+  m = -INFINITY;
+  s = 0.f;
+#pragma unroll
+  for (int k = 0; k < N; k += 32) {
+    if (k >= n) break;
+    float mk = -INFINITY, sk = 0.f;
+    if (k + lane < n) {
+      const float2 x = got[k + lane];
+      mk = x.x;
+      sk = x.y;
+    }
+    join_warp(mk, sk, c);
+    const float top = fmaxf(m, mk);
+    s = (m == -INFINITY ? s : s * ex2((m - top) * c)) + (mk == -INFINITY ? sk : sk * ex2((mk - top) * c));
+    m = top;
+  }
+}
+
+// Persistent: cluster i takes rows i, i + clusters, ...  TH threads compute
+// and one more warp works ahead of them: it has each block's slice of the next
+// row copied into shared memory as soon as the last read of the current one
+// is done, so that loads run while the block still stores and the SM's other
+// blocks compute; it prepares the next row's list, whose loads went out a row
+// before; it reads the listed classes' logits where they landed; and it
+// writes their gradient again once the dense part is stored.  A
+// computing thread reads its slots twice: for its part of (m, s), and for the
+// dense gradient.
 //
-// Hand-offs, per row: the block barrier after the sums publishes the lists
-// and (one block per row) the warps' pairs; the barrier after the dense part
-// frees the landing buffer and publishes p.  Between blocks only the pairs
-// move, by stores that count on the receiver's barrier; two sets of pairs
-// alternate, and a block cannot be two rows ahead of another, since it needs
-// the other's pairs for the row between.  Every block of a cluster sees the
-// same rows and weights and so makes the same number of exchanges.
+// Hand-offs of a row of weight other than 0 (the others use none), all by
+// mbarriers whose phase is the row's number among those:
+//   full    the copy's bytes are there
+//   summed  the computing warps have their (m, s), and are done with the
+//           buffer if no gradient is wanted
+//   listed  the row's list is ready
+//   empty   the computing warps' dense stores are out: the buffer is free and
+//           the listed classes may be written
+// Blocks of a cluster send their warps' pairs to each other, and their parts
+// of the loss to the first one, by stores that count on the receiver's `xch`
+// and `parts`.  The ahead warp of a block fetches row e + 1 only after it
+// waited for summed (and empty) of row e, so no barrier is ever two phases
+// ahead of a waiter; a block sends for row e + 4 only after its ahead warp
+// finished row e + 2 with all pairs of that row, whose senders' ahead warps
+// had then finished row e: with four sets in rotation no set is overwritten
+// while it is read.
 template <typename T, int TH, bool GRAD>
-__global__ void __launch_bounds__(TH, 1024 / TH) k_distill_ring(const Distill a, const int C, const int slice_slots) {
-  using S = Slots<T>;
-  constexpr int GW = TH / 32, U = 4;
+__global__ void __launch_bounds__(TH + 32, 1024 / TH) k_distill_ring(const Distill a, const int log_c, const int slice_slots) {
+  constexpr int GW = TH / 32, U = 4, SETS = 4;
   extern __shared__ __align__(128) unsigned char sm[];
   uint4* buf = reinterpret_cast<uint4*>(sm);
-  int32_t* ids = reinterpret_cast<int32_t*>(sm + (size_t)slice_slots * 16);   // [2][top]: rows alternate
-  float* zis = reinterpret_cast<float*>(ids + 2 * a.top);                      // [2][top]
-  float* tl = zis + 2 * a.top;
-  float* p = tl + a.top;
-  __shared__ float2 pairs[2][GW * kMaxCluster];
-  __shared__ uint64_t full, xch[2];
+  __shared__ float2 pairs[SETS][GW * kMaxCluster];    // (m, s) of the row's warps
+  __shared__ float2 loss_parts[SETS][2 * kMaxCluster];
+  __shared__ uint64_t full, summed, listed, empty, xch[SETS], parts[SETS];
   __shared__ int gave_up;
+  __shared__ int32_t any[2];   // whether a slot of the row counts
   const int t = threadIdx.x, lane = t % 32, gw = t / 32;
+  const int C = 1 << log_c;
   const int rank = C == 1 ? 0 : (int)cluster_rank();
-  const int64_t clusters = gridDim.x / (unsigned)C;
-  int64_t row = blockIdx.x / (unsigned)C;
+  const int clusters = gridDim.x >> log_c;
+  int64_t row = blockIdx.x >> log_c;
   if (t == 0) {
     mbar_init(&full, 1);
-    mbar_init(&xch[0], 1);
-    mbar_init(&xch[1], 1);
+    mbar_init(&summed, GW);
+    mbar_init(&listed, 1);
+    mbar_init(&empty, GW);
+    for (int k = 0; k < SETS; ++k) {
+      mbar_init(&xch[k], 1);
+      mbar_init(&parts[k], 1);
+    }
     gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
   if (C > 1) cluster_sync();
-
-  // The whole slots of a row's slice, by one thread, once the buffer is free.
-  auto fetch = [&](int64_t r) {
-    const Slice<T> n(a, r, rank, C);
-    const int lo = n.first == 0 ? 1 : 0, hi = n.last >= 0 ? n.last : n.cnt;
-    const uint32_t bytes = hi > lo ? (uint32_t)(hi - lo) * 16 : 0;
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // after the block's reads of the last row
-    mbar_arrive_expect_tx(&full, bytes);
-    if (bytes) bulk_g2s(buf + lo, n.z16() + lo, bytes, &full);
-  };
   auto weight = [&](int64_t r) { return r >= a.rows ? 0.f : a.row_weight ? a.row_weight[r] : 1.f; };
-
+  auto wait = [&](uint64_t* bar, uint32_t phase) { mbar_wait_or_abort(bar, phase & 1, kWaitNs, &gave_up); };
   float w = weight(row);
-  int32_t next_id = -1;
-  float next_t = 0.f;
-  if (w != 0.f) {
-    if (t == 0) fetch(row);
-    if (t < a.top) load_top(a, row, t, rank == 0, next_id, next_t);
-  }
-  uint32_t fetched = 0, exchanged = 0;
+  uint32_t e = 0;   // rows of weight other than 0 so far
   const float c = a.log2e_t;
+
+  if (gw == GW) {   // the warp that works ahead
+    List l;
+    l.top = a.top;
+    l.log_size = table_log_size(a.top);
+    l.id = reinterpret_cast<int32_t*>(sm + (size_t)slice_slots * 16);
+    l.place = l.id + a.top;
+    l.e = reinterpret_cast<float*>(l.place + a.top);
+    l.z = l.e + a.top;
+    l.key = reinterpret_cast<int32_t*>(l.z + a.top);
+    l.sum = reinterpret_cast<float*>(l.key + (1 << l.log_size));
+    l.any = false;
+    // The whole slots of a row's slice, when all lanes are done with the last one's.
+    auto fetch = [&](const Slice<T>& n) {
+      __syncwarp();
+      if (lane == 0) {
+        const int lo = n.first == 0 ? 1 : 0, hi = n.last >= 0 ? n.last : n.cnt;
+        const uint32_t bytes = hi > lo ? (uint32_t)(hi - lo) * 16 : 0;
+        mbar_arrive_expect_tx(&full, bytes);
+        if (bytes) bulk_g2s(buf + lo, n.z16() + lo, bytes, &full);
+      }
+      __syncwarp();
+    };
+    ListAhead x;
+    auto list = [&](const Slice<T>& n, int64_t at, int par) {
+      make_list<T, GRAD>(a, n, at, rank == 0, x, l);
+      if (lane == 0) {
+        any[par] = l.any;
+        mbar_arrive(&listed);
+      }
+      __syncwarp();
+    };
+    load_list<T>(a, row, 0, x);
+    Slice<T> r(a, row, rank, log_c);
+    if (w != 0.f) {
+      fetch(r);
+      list(r, row, 0);
+    }
+    if (row + clusters < a.rows) load_list<T>(a, row + clusters, 0, x);
+    for (int par = 0; row < a.rows; par ^= 1) {
+      const int64_t next = row + clusters;
+      const float w_next = weight(next);
+      const Slice<T> r_next(a, next < a.rows ? next : row, rank, log_c);
+      if (w != 0.f) {
+        const int b = e & (SETS - 1);
+        const bool learn = l.any;
+        wait(&full, e);
+        if (learn) read_listed<T, true>(r, buf, l);
+        wait(&summed, e);
+        if (learn && (r.first >= 0 || r.last >= 0)) read_listed<T, false>(r, buf, l);
+        if (!GRAD && w_next != 0.f) fetch(r_next);
+        if (learn) {
+          float ref, pz, ps;
+          __syncwarp();
+          sum_listed(r, l, ref, pz, ps);
+          float2* mine = &loss_parts[b][2 * rank];
+          if (C > 1) {
+            if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&parts[b], (uint32_t)(2 * C * sizeof(float2)));
+            if (lane < 2) send_pair(mine + lane, &parts[b], 0, lane ? ps : ref, lane ? 0.f : pz);
+          } else if (lane < 2) {
+            mine[lane] = make_float2(lane ? ps : ref, lane ? 0.f : pz);
+          }
+          __syncwarp();
+        }
+        if (C > 1) wait(&xch[b], e / SETS);
+        float m, s;
+        join_pairs<GW * kMaxCluster>(pairs[b], GW * C, c, m, s);
+        if (rank == 0) {
+          float loss = 0.f;
+          if (learn) {
+            if (C > 1) wait(&parts[b], e / SETS);
+            float pz = 0.f;   // sum p (z - m)
+            if (lane < C) {
+              const float2 u = loss_parts[b][2 * lane], v = loss_parts[b][2 * lane + 1];
+              if (v.x != 0.f) pz = fmaf(v.x, u.x - m, u.y);
+            }
+            loss = w * a.temperature * a.temperature * (l.p_log_p - (warp_sum(pz) * a.inv_t - logf(s)));
+          }
+          if (lane == 0) a.loss[row] = loss;
+        }
+        if (GRAD) {
+          wait(&empty, e);
+          if (w_next != 0.f) fetch(r_next);
+          if (learn) {   // the listed classes of this slice, again
+            const float wt = w * a.temperature, f = wt / s, wp = wt * l.inv;
+            LOPT_LIST_SLOTS(k0, l.top) {
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const int k = k0 + u * 32 + lane;
+                const int h = k < l.top ? l.place[k] : -1;
+                if (h >= 0) r.g[l.id[k]] = from_f<T>(fmaf(ex2((l.z[k] - m) * c), f, -wp * l.sum[h]));
+              }
+            }
+          }
+          __syncwarp();
+        }
+        // A barrier that this row left unused keeps its phase with the others'.
+        if (C > 1 && rank == 0 && !learn && lane == 0) mbar_arrive(&parts[b]);
+        ++e;
+      } else {
+        if (w_next != 0.f) fetch(r_next);
+        if (rank == 0 && lane == 0) a.loss[row] = 0.f;
+      }
+      if (w_next != 0.f) list(r_next, next, par ^ 1);
+      if (next + clusters < a.rows) load_list<T>(a, next + clusters, 0, x);
+      r = r_next;
+      row = next;
+      w = w_next;
+    }
+    if (gave_up && lane == 0 && a.status) atomicOr(a.status, kStatusGaveUp);
+    return;
+  }
+
   for (int par = 0; row < a.rows; par ^= 1) {
     const int64_t next = row + clusters;
     const float w_next = weight(next);
-    const Slice<T> r(a, row, rank, C);
-    int32_t* id = ids + par * a.top;
-    float* zi = zis + par * a.top;
-    const float wt = w * a.temperature;
-    float m = 0.f, s = 1.f, f = 0.f;
-    bool learn = w != 0.f;
-    if (learn) {
-      for (int k = t; k < a.top; k += TH) {
-        if (k != t) load_top(a, row, k, rank == 0, next_id, next_t);
-        id[k] = next_id;
-        tl[k] = next_t;
-        if (next_id >= 0) zi[k] = to_f(r.z[next_id]);
+    const Slice<T> r(a, row, rank, log_c);
+    bool learn = false;
+    if (w != 0.f) {
+      // Slots that are not whole are read by the threads that use them (a
+      // slot of the buffer is the same thread's in every row), and stored
+      // when the copy is there: until then the ahead warp may still read
+      // the row before.
+      const bool edge_first = r.first == 0 && t == 0, edge_last = r.last >= 0 && r.last != r.first && t == r.last % TH;
+      uint4 edge = make_uint4(0, 0, 0, 0);
+      if (edge_first) edge = r.read_edge(0);
+      else if (edge_last) edge = r.read_edge(r.last);
+      wait(&full, e);
+      if (edge_first || edge_last) {
+        buf[edge_first ? 0 : r.last] = edge;
+        if (edge_first && edge_last) buf[r.last] = r.read_edge(r.last);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // a later row's copy may land there
       }
-      // Slots that are not whole, by the threads that will use them.
-      if (r.first == 0 && t == 0) r.read_edge(0, reinterpret_cast<uint32_t*>(buf));
-      if (r.last > 0 && t == r.last % TH) r.read_edge(r.last, reinterpret_cast<uint32_t*>(buf + r.last));
-      if (r.last == 0 && r.first != 0 && t == 0) r.read_edge(0, reinterpret_cast<uint32_t*>(buf));
-      mbar_wait_or_abort(&full, fetched++ & 1, kWaitNs, &gave_up);
       Partial<T> part;
-      for (int q0 = t; q0 < r.cnt; q0 += U * TH) {
+      int q = t;
+      for (; q + (U - 1) * TH < r.cnt; q += U * TH) {
         uint32_t v[U][4];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int q = q0 + u * TH;
-          const uint4 x = q < r.cnt ? buf[q] : make_uint4(S::kNegInf, S::kNegInf, S::kNegInf, S::kNegInf);
+          const uint4 x = buf[q + u * TH];
           v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
         }
         part.template add<U>(v, c);
       }
-      m = part.m;
-      s = part.s;
+      for (; q < r.cnt; q += TH) {
+        const uint4 x = buf[q];
+        const uint32_t v[1][4] = {{x.x, x.y, x.z, x.w}};
+        part.template add<1>(v, c);
+      }
+      float m = part.m, s = part.s;
       join_warp(m, s, c);
-      const float2* got = pairs[0];
+      const int b = e & (SETS - 1);
       if (C == 1) {
-        if (lane == 0) pairs[0][gw] = make_float2(m, s);
-        __syncthreads();
+        if (lane == 0) pairs[b][gw] = make_float2(m, s);
       } else {
-        const int b = exchanged & 1;
-        got = pairs[b];
         if (t == 0) mbar_arrive_expect_tx(&xch[b], (uint32_t)(GW * C * sizeof(float2)));
         if (lane < C) send_pair(&pairs[b][rank * GW + gw], &xch[b], lane, m, s);
-        __syncthreads();
-        mbar_wait_or_abort(&xch[b], exchanged++ >> 1 & 1, kWaitNs, &gave_up);
       }
-      // Every warp joins all pairs, in the same order.
-      Partial<T> all;
-#pragma unroll
-      for (int k = 0; k < GW * kMaxCluster; k += 32) {
-        if (k + lane >= GW * C) continue;
-        const float2 x = got[k + lane];
-        if (x.x == -INFINITY) {
-          all.s += x.y;
-        } else if (!(x.x <= all.m)) {
-          all.s = fmaf(all.s, all.m == -INFINITY ? 1.f : ex2((all.m - x.x) * c), x.y);
-          all.m = x.x;
-        } else {
-          all.s = fmaf(x.y, ex2((x.x - all.m) * c), all.s);
-        }
-      }
-      m = all.m;
-      s = all.s;
-      join_warp(m, s, c);
-      float tmax, ps;
-      learn = top_softmax(id, tl, a.top, c, tmax, ps);
-      if (learn) {
-        f = wt / s;
-        if (rank == 0 && gw == GW - 1) {
-          const float loss = top_loss(a, id, tl, zi, tmax, ps, m, s);
-          if (lane == 0) a.loss[row] = w * loss;
-        }
-        if (GRAD) {
-          const float inv_ps = 1.f / ps;
-          for (int k = t; k < a.top; k += TH) p[k] = id[k] < 0 ? 0.f : ex2((tl[k] - tmax) * c) * inv_ps;
-          const Dense<T> dense(m, c, f);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&summed);
+      if (GRAD) {
+        if (C > 1) wait(&xch[b], e / SETS);
+        else wait(&summed, e);
+        wait(&listed, e);
+        learn = any[par];
+        if (learn) {
+          join_pairs<GW * kMaxCluster>(pairs[b], GW * C, c, m, s);
+          const Dense<T> dense(m, c, w * a.temperature / s);
 #pragma unroll 4
-          for (int q = t; q < r.cnt; q += TH) {
-            const uint4 x = buf[q];
+          for (int k = t; k < r.cnt; k += TH) {
+            const uint4 x = buf[k];
             const uint32_t v[4] = {x.x, x.y, x.z, x.w};
             uint32_t o[4];
             dense.of(v, o);
-            r.write(q, o);
+            r.write(k, o);
           }
         }
       }
     }
-    if (!learn) {   // nothing to learn from this row
-      if (rank == 0 && t == 0) a.loss[row] = 0.f;
+    if (GRAD && !learn) {   // nothing to learn from this row
+      const uint32_t o[4] = {0, 0, 0, 0};
+      for (int q = t; q < r.cnt; q += TH) r.write(q, o);
+    }
+    if (w != 0.f) {
       if (GRAD) {
-        const uint32_t o[4] = {0, 0, 0, 0};
-        for (int q = t; q < r.cnt; q += TH) r.write(q, o);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty);
       }
-    }
-    __syncthreads();
-    if (w_next != 0.f) {
-      if (t == 0) fetch(next);
-      if (t < a.top) load_top(a, next, t, rank == 0, next_id, next_t);
-    }
-    if (GRAD && learn) {   // the listed classes of this slice, again
-      for (int k = t; k < a.top; k += TH) {
-        float g;
-        if (r.holds(id[k]) && top_grad(a, id, p, zi, k, m, f, wt, g)) r.g[id[k]] = from_f<T>(g);
-      }
+      ++e;
     }
     row = next;
     w = w_next;
   }
-  if (gave_up && t == 0 && a.status) atomicOr(a.status, kStatusGaveUp);
 }
 
 // Rows beyond a cluster's shared memory: one block per row, which is read for
@@ -665,6 +954,8 @@ __global__ void __launch_bounds__(512) k_distill_rows(const Distill a) {
   }
 }
 
+#undef LOPT_LIST_SLOTS
+
 // ---- choice of the kernel -------------------------------------------------------
 template <typename T, int NV>
 cudaError_t warp_as(const Distill& a, cudaStream_t s) {
@@ -675,14 +966,14 @@ cudaError_t warp_as(const Distill& a, cudaStream_t s) {
 }
 
 template <typename T, int TH, bool GRAD>
-cudaError_t ring_as(const Distill& a, int C, int slice_slots, size_t smem, int blocks, cudaStream_t s) {
+cudaError_t ring_as(const Distill& a, int log_c, int slice_slots, size_t smem, int blocks, cudaStream_t s) {
   auto* k = &k_distill_ring<T, TH, GRAD>;
   if (smem > 40 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  const int64_t clusters = std::min<int64_t>(a.rows, blocks / C);
-  return launch(k, dim3((unsigned)(clusters * C)), dim3(TH), smem, s, false, C, a, C, slice_slots);
+  const int64_t clusters = std::min<int64_t>(a.rows, blocks >> log_c);
+  return launch(k, dim3((unsigned)(clusters << log_c)), dim3(TH + 32), smem, s, false, 1 << log_c, a, log_c, slice_slots);
 }
 
 template <typename T>
@@ -700,23 +991,25 @@ cudaError_t distill_rows(const Distill& a, int sms, cudaStream_t s) {
     if (slots <= 32 * 6) return warp_as<T, 6>(a, s);
     return warp_as<T, 8>(a, s);
   }
-  // Shared memory of a block: its slice of the row and the lists; two blocks
-  // of 512 threads (four of 256) per SM while they fit, one at most beyond.
-  constexpr int64_t kFour = 54 * 1024, kTwo = 110 * 1024, kOne = 220 * 1024;
-  const int64_t list_bytes = (int64_t)a.top * 6 * 4;
-  auto bytes = [&](int64_t C) { return ceil(slots, C) * 16 + list_bytes; };
-  int64_t C = 1;
-  while (C < kMaxCluster && bytes(C) > kTwo) C *= 2;
-  if (bytes(C) <= kOne) {
+  // Shared memory of a block: its slice of the row and the lists.  Four blocks
+  // of 256 threads per SM while a cluster can hold the row so, else two of
+  // 512, else one.  (8192 x 50257 bf16: 286 us with four blocks, two to a
+  // row; 293 with two blocks, one to a row.)
+  constexpr int64_t kFour = 54528, kTwo = 107 * 1024, kOne = 216 * 1024;
+  const int64_t list_bytes = (int64_t)list_words(a.top) * 4;
+  auto bytes = [&](int lc) { return ceil(slots, 1 << lc) * 16 + list_bytes; };
+  int lc = 0;   // log2 of the blocks per row
+  while (1 << lc < kMaxCluster && bytes(lc) > kFour) ++lc;
+  if (bytes(lc) <= kOne) {
     // Few rows: more blocks for each, while a slice is 8 KB.
-    while (C < kMaxCluster && a.rows * C * 2 <= sms && ceil(slots, 2 * C) >= 512) C *= 2;
-    const bool small = bytes(C) <= kFour;
-    const int per_sm = small ? 4 : bytes(C) <= kTwo ? 2 : 1;
-    const int slice = (int)ceil(slots, C), blocks = sms * per_sm;
-    const size_t smem = (size_t)bytes(C);
+    while (1 << lc < kMaxCluster && (a.rows << lc) * 2 <= sms && ceil(slots, 2 << lc) >= 512) ++lc;
+    const bool small = bytes(lc) <= kFour;
+    const int per_sm = small ? 4 : bytes(lc) <= kTwo ? 2 : 1;
+    const int slice = (int)ceil(slots, 1 << lc), blocks = sms * per_sm;
+    const size_t smem = (size_t)bytes(lc);
     if (a.grad)
-      return small ? ring_as<T, 256, true>(a, (int)C, slice, smem, blocks, s) : ring_as<T, 512, true>(a, (int)C, slice, smem, blocks, s);
-    return small ? ring_as<T, 256, false>(a, (int)C, slice, smem, blocks, s) : ring_as<T, 512, false>(a, (int)C, slice, smem, blocks, s);
+      return small ? ring_as<T, 256, true>(a, lc, slice, smem, blocks, s) : ring_as<T, 512, true>(a, lc, slice, smem, blocks, s);
+    return small ? ring_as<T, 256, false>(a, lc, slice, smem, blocks, s) : ring_as<T, 512, false>(a, lc, slice, smem, blocks, s);
   }
   return launch(k_distill_rows<T>, dim3((unsigned)a.rows), dim3(512), 0, s, false, 1, a);
 }
