@@ -9,9 +9,9 @@
 // sorted list is cut into chunks of equal length, whatever the ids: no row of
 // the table is a block's fate, and every sum runs in position order, so the
 // result does not depend on timing.
-//   1. k_embed_sort: each block owns a range of ids and reads the whole index
-//      list (it stays in L2) to count and place its own: a stable counting
-//      sort with no exchange between blocks.  It also writes the zero rows.
+//   1. k_embed_sort: each block owns some ids and reads the whole index list
+//      (it stays in L2) to count and place its own: a stable counting sort
+//      with no exchange between blocks.  It also writes the zero rows.
 //   2. k_embed_sum: each block adds the rows of one chunk of the sorted list.
 //      A run of equal ids inside the chunk goes straight to its row; a run
 //      that crosses chunks leaves partial sums, which the last of its blocks
@@ -34,64 +34,88 @@ struct EmbedFwd {
   float scale;
 };
 
-// blockDim.x threads across the columns, blockIdx.y column blocks, blockDim.y
-// tokens at a time.
-template <typename TI, typename TO, int VEC>
+// blockDim.x threads across the columns, blockIdx.y column blocks; a thread
+// takes U tokens, blockDim.y apart, with their loads side by side.
+template <typename TI, typename TO, int VEC, int U>
 __global__ void __launch_bounds__(256) k_embed_fwd(const EmbedFwd a) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const int64_t i0 = (int64_t)blockIdx.x * (blockDim.y * U) + threadIdx.y;
   const int64_t j = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * VEC;
-  if (i >= a.n || j >= a.cols) return;
-  const int64_t id = load_index(a.index, i, a.itype);
-  const bool real = id >= 0 && id < a.rows;
-  if (id >= a.rows && a.status && j == 0) atomicOr(a.status, kStatusIndex);
-  Pack<TO, VEC> o;
-  if (real) {
-    const Pack<TI, VEC> p = *reinterpret_cast<const Pack<TI, VEC>*>(static_cast<const TI*>(a.table) + id * a.ts + j);
+  if (j >= a.cols) return;
+  int64_t id[U];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) o.v[e] = from_f<TO>(to_f(p.v[e]) * a.scale);
-  } else {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) o.v[e] = from_f<TO>(0.f);
+  for (int u = 0; u < U; ++u) {
+    const int64_t i = i0 + u * (int)blockDim.y;
+    id[u] = i < a.n ? load_index(a.index, i, a.itype) : -1;
   }
-  *reinterpret_cast<Pack<TO, VEC>*>(static_cast<TO*>(a.out) + i * a.os + j) = o;
+  Pack<TI, VEC> p[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (id[u] >= a.rows) {
+      if (a.status && j == 0) atomicOr(a.status, kStatusIndex);
+      id[u] = -1;
+    }
+    if (id[u] >= 0) p[u] = *reinterpret_cast<const Pack<TI, VEC>*>(static_cast<const TI*>(a.table) + id[u] * a.ts + j);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t i = i0 + u * (int)blockDim.y;
+    if (i >= a.n) break;
+    float v[VEC];
+    to_floats(p[u], v);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] = id[u] >= 0 ? v[e] * a.scale : 0.f;
+    *reinterpret_cast<Pack<TO, VEC>*>(static_cast<TO*>(a.out) + i * a.os + j) = from_floats<TO, VEC>(v);
+  }
 }
 
 // ---- backward: sort ------------------------------------------------------------
+// Block b of 2^log_blocks owns the ids v with v mod 2^log_blocks == b, at most
+// 1024 of them: ids are given out by frequency in most vocabularies, and so
+// the common ones (each of which keeps its block busy) fall to different
+// blocks.  In the sorted list the blocks follow each other, in a block its
+// ids ascend, and an id's positions ascend.
 constexpr int kSortThreads = 1024, kSortWarps = 32;
-constexpr int kMaxIdsPerBlock = 1024;   // 32 x 1024 counters: 128 KB of shared memory
+constexpr int kMinLogBlocks = 7;        // 128 blocks
+constexpr int kLogIds = 10;             // ids per block: at most 1024, 128 KB of counters
+constexpr int kFound = 192;             // entries a warp keeps of its part of the list
+constexpr int kZeroBytes = 8192;        // what one bulk store writes of a row of zeros
 
 struct EmbedSort {
   const void* index;
-  int itype;
-  int n, rows, ids_per_block;
+  int n, rows, log_blocks, ids_per_block;
   int64_t n_counters;
   int32_t *order, *key, *offsets, *counters, *status;
   float* grad;
   int64_t cols;
-  int zero_rows, zero_vec;
+  int zero_rows, zero_bulk;
 };
 
 template <typename IT>
 __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const EmbedSort a) {
-  extern __shared__ int32_t sh[];
+  extern __shared__ __align__(16) int32_t sh[];
   const int K = a.ids_per_block;
-  int32_t* cnt = sh;                       // [32 warps][K]
-  int32_t* tot = sh + kSortWarps * K;      // [K]
+  int32_t* zeros = sh;                                      // kZeroBytes
+  uint32_t* found = reinterpret_cast<uint32_t*>(sh) + kZeroBytes / 4;   // [32 warps][kFound]: id's number | place << kLogIds
+  int32_t* cnt = reinterpret_cast<int32_t*>(found) + kSortWarps * kFound;   // [32 warps][K]
+  int32_t* tot = cnt + kSortWarps * K;                      // [K]
   __shared__ int32_t wsum[kSortWarps];
   __shared__ int32_t below_sum;
   const int tid = threadIdx.x, lane = tid % 32, w = tid / 32;
-  const int lo = blockIdx.x * K, hi = min(lo + K, a.rows);
+  const unsigned lt = (1u << lane) - 1;
+  const int blk = blockIdx.x, mask = (1 << a.log_blocks) - 1;
   const IT* index = static_cast<const IT*>(a.index);
   let_next_start();
   for (int i = tid; i < kSortWarps * K; i += kSortThreads) cnt[i] = 0;
+  for (int i = tid; i < kZeroBytes / 4; i += kSortThreads) zeros[i] = 0;
   if (tid == 0) below_sum = 0;
-  for (int64_t i = (int64_t)blockIdx.x * kSortThreads + tid; i < a.n_counters; i += (int64_t)gridDim.x * kSortThreads)
+  for (int64_t i = (int64_t)blk * kSortThreads + tid; i < a.n_counters; i += (int64_t)gridDim.x * kSortThreads)
     a.counters[i] = 0;
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the zeros, before bulk stores read them
   __syncthreads();
-  // Warp w counts the ids of its contiguous part of the list.
+  // Warp w reads its contiguous part of the list and keeps what the block owns.
   const int per = ((a.n + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
   const int beg = min(w * per, a.n), end = min(beg + per, a.n);
-  int below = 0;
+  int below = 0, mine_n = 0;
   bool bad = false;
   constexpr int U = 8;
   for (int i0 = beg; i0 < end; i0 += 32 * U) {
@@ -103,18 +127,52 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const EmbedSort a) 
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      below += id[u] >= 0 && id[u] < lo;
+      const bool real = id[u] >= 0 && id[u] < a.rows;
       bad |= id[u] >= a.rows;
-      const bool mine = id[u] >= lo && id[u] < hi;
-      if (__any_sync(0xffffffffu, mine)) {
-        const int key = mine ? (int)id[u] - lo : -1;
-        const unsigned peers = __match_any_sync(0xffffffffu, key);
-        if (mine && lane == __ffs(peers) - 1) cnt[w * K + key] += __popc(peers);
-        __syncwarp();
+      const int b = (int)id[u] & mask;
+      below += real && b < blk;
+      const bool mine = real && b == blk;
+      const unsigned who = __ballot_sync(0xffffffffu, mine);
+      if (mine) {
+        const int at = mine_n + __popc(who & lt);
+        if (at < kFound) found[w * kFound + at] = (uint32_t)((int)id[u] >> a.log_blocks) | (uint32_t)(i0 - beg + u * 32 + lane) << kLogIds;
       }
+      mine_n += __popc(who);
     }
   }
-  if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, kStatusIndex);
+  __syncwarp();
+  // In list order, 32 at a time: f(number of the id in the block or -1, its
+  // place in the warp's part).  From what the warp kept, or, where that was
+  // not all, from the list again.
+  const bool kept = mine_n <= kFound && per <= 1 << (32 - kLogIds);
+  auto each = [&](auto f) {
+    if (kept) {
+      for (int c = 0; c < mine_n; c += 32) {
+        const uint32_t x = c + lane < mine_n ? found[w * kFound + c + lane] : 0;
+        f(c + lane < mine_n ? (int)(x & ((1 << kLogIds) - 1)) : -1, (int)(x >> kLogIds));
+      }
+    } else {
+      for (int i0 = beg; i0 < end; i0 += 32 * U) {
+        IT id[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = i0 + u * 32 + lane;
+          id[u] = i < end ? index[i] : (IT)-1;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const bool mine = id[u] >= 0 && id[u] < a.rows && ((int)id[u] & mask) == blk;
+          if (__any_sync(0xffffffffu, mine)) f(mine ? (int)id[u] >> a.log_blocks : -1, i0 - beg + u * 32 + lane);
+        }
+      }
+    }
+  };
+  each([&](int k, int) {
+    const unsigned peers = __match_any_sync(0xffffffffu, k);
+    if (k >= 0 && lane == __ffs(peers) - 1) cnt[w * K + k] += __popc(peers);
+    __syncwarp();
+  });
+  if (bad && blk == 0 && a.status) atomicOr(a.status, kStatusIndex);
   for (int o = 16; o > 0; o >>= 1) below += __shfl_xor_sync(0xffffffffu, below, o);
   if (lane == 0 && below) atomicAdd(&below_sum, below);   // integers: any order gives the same
   __syncthreads();
@@ -143,54 +201,55 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const EmbedSort a) 
     }
     wsum[lane] = t;
   }
+  // Rows no token has, while the positions are placed: bulk stores of zeros
+  // where rows are 16-byte aligned.
+  if (a.zero_rows) {
+    if (a.zero_bulk) {
+      const int64_t bytes = a.cols * 4;
+      for (int k = tid; k < K; k += kSortThreads) {
+        const int v = k << a.log_blocks | blk;
+        if (v >= a.rows || tot[k]) continue;
+        char* g = reinterpret_cast<char*>(a.grad + (int64_t)v * a.cols);
+        for (int64_t o = 0; o < bytes; o += kZeroBytes) {
+          const uint32_t size = (uint32_t)min((int64_t)kZeroBytes, bytes - o);
+          asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+                       :: "l"(g + o), "r"((uint32_t)__cvta_generic_to_shared(zeros)), "r"(size) : "memory");
+        }
+      }
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    } else {
+      for (int k = w; k < K; k += kSortWarps) {
+        const int v = k << a.log_blocks | blk;
+        if (v >= a.rows || tot[k]) continue;
+        float* g = a.grad + (int64_t)v * a.cols;
+        for (int64_t j = lane; j < a.cols; j += 32) g[j] = 0.f;
+      }
+    }
+  }
   __syncthreads();
   const int start = below_sum + (w ? wsum[w - 1] : 0) + incl - mine;
-  if (tid < K && lo + tid < a.rows) {
-    a.offsets[lo + tid] = start;
-    if (lo + tid == a.rows - 1) a.offsets[a.rows] = start + mine;
+  if (tid < K) {
+    a.offsets[blk * K + tid] = start;
+    if (blk == mask && tid == K - 1) a.offsets[blk * K + K] = start + mine;
     for (int k = 0; k < kSortWarps; ++k) cnt[k * K + tid] += start;
   }
-  // Rows no token has.  Their stores drain while the list is read again.
-  if (a.zero_rows) {
-    for (int v = w; v < hi - lo; v += kSortWarps) {
-      if (tot[v]) continue;
-      float* g = a.grad + (int64_t)(lo + v) * a.cols;
-      if (a.zero_vec) {
-        for (int64_t j = lane * 4; j < a.cols; j += 128) __stcs(reinterpret_cast<float4*>(g + j), make_float4(0, 0, 0, 0));
-      } else {
-        for (int64_t j = lane; j < a.cols; j += 32) __stcs(g + j, 0.f);
-      }
-    }
-  }
   __syncthreads();
-  for (int i0 = beg; i0 < end; i0 += 32 * U) {
-    IT id[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * 32 + lane;
-      id[u] = i < end ? index[i] : (IT)-1;
+  each([&](int k, int place) {
+    const unsigned peers = __match_any_sync(0xffffffffu, k);
+    if (k >= 0) {
+      const int at = cnt[w * K + k] + __popc(peers & lt);
+      a.order[at] = beg + place;
+      a.key[at] = k << a.log_blocks | blk;
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool in = id[u] >= lo && id[u] < hi;
-      if (__any_sync(0xffffffffu, in)) {
-        const int key = in ? (int)id[u] - lo : -1;
-        const unsigned peers = __match_any_sync(0xffffffffu, key);
-        if (in) {
-          const int at = cnt[w * K + key] + __popc(peers & ((1u << lane) - 1));
-          a.order[at] = i0 + u * 32 + lane;
-          a.key[at] = (int)id[u];
-        }
-        __syncwarp();
-        if (in && lane == __ffs(peers) - 1) cnt[w * K + key] += __popc(peers);
-        __syncwarp();
-      }
-    }
-  }
+    __syncwarp();
+    if (k >= 0 && lane == __ffs(peers) - 1) cnt[w * K + k] += __popc(peers);
+    __syncwarp();
+  });
+  if (a.zero_rows && a.zero_bulk) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // the zeros stay until read
 }
 
 // ---- backward: sums ----------------------------------------------------------------
-constexpr int kMaxChunk = 64;
+constexpr int kMaxChunk = 16;
 
 struct EmbedSum {
   const void* grad_out;
@@ -199,7 +258,7 @@ struct EmbedSum {
   float* part;             // [chunks][2][cols]: sums of a run entering / leaving the chunk
   float* grad;
   int64_t gs, cols;
-  int rows, chunk, accumulate;
+  int log_blocks, ids_per_block, last_offset, chunk, accumulate;
   float scale;
 };
 
@@ -231,13 +290,13 @@ __device__ __forceinline__ void add_sums(const float* p, float v[VEC]) {   // wr
 }
 
 template <typename T, int VEC>
-__global__ void __launch_bounds__(256) k_embed_sum(const EmbedSum a) {
+__global__ void __launch_bounds__(256, 4) k_embed_sum(const EmbedSum a) {
   __shared__ int32_t ord[kMaxChunk], key[kMaxChunk + 2];   // key[0]: before the chunk, key[len + 1]: after it
   __shared__ int32_t last_flag;
   const int64_t j = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * VEC;
   const bool live = j < a.cols;
   wait_for_previous();
-  const int total = a.offsets[a.rows];
+  const int total = a.offsets[a.last_offset];
   const int base = blockIdx.x * a.chunk;
   if (base >= total) return;
   const int len = min(a.chunk, total - base);
@@ -263,8 +322,10 @@ __global__ void __launch_bounds__(256) k_embed_sum(const EmbedSum a) {
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u;
       if (i >= len) break;
+      float v[VEC];
+      to_floats(p[u], v);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) acc[e] += to_f(p[u].v[e]);
+      for (int e = 0; e < VEC; ++e) acc[e] += v[e];
       if (i + 1 < len && key[i + 2] == key[i + 1]) continue;   // the run goes on
       if (live) {
         const bool from_before = run_start == 0 && head_open, goes_on = i + 1 == len && tail_open;
@@ -288,7 +349,8 @@ __global__ void __launch_bounds__(256) k_embed_sum(const EmbedSum a) {
   for (int side = 0; side < 2; ++side) {
     if (side == 0 ? !head_open : !tail_open) continue;
     const int v = side == 0 ? key[1] : key[len];
-    const int s0 = a.offsets[v], s1 = a.offsets[v + 1];
+    const int at = (v & ((1 << a.log_blocks) - 1)) * a.ids_per_block + (v >> a.log_blocks);
+    const int s0 = a.offsets[at], s1 = a.offsets[at + 1];
     const int first = s0 / a.chunk, last = (s1 - 1) / a.chunk;
     if (side == 1 && head_open && first < (int)blockIdx.x) continue;   // one run through the whole chunk: counted
     __threadfence();
@@ -314,7 +376,7 @@ __global__ void __launch_bounds__(256) k_embed_sum(const EmbedSum a) {
 
 // ---- host --------------------------------------------------------------------------
 struct Plan {
-  int chunk, chunks, ids_per_block, blocks;
+  int chunk, chunks, log_blocks, ids_per_block;
   int col_blocks;   // upper bound, for the counters
   int64_t o_order, o_key, o_offsets, o_counters, o_part, bytes;
 };
@@ -324,37 +386,44 @@ int64_t up(int64_t x) { return (x + 255) / 256 * 256; }
 // The layout of the workspace; a function of the sizes alone.
 Plan plan(int64_t n, int64_t rows, int64_t cols) {
   Plan p;
-  p.chunk = n >= 16384 ? 32 : 8;
+  p.chunk = n >= 16384 ? 16 : 8;
   p.chunks = (int)std::max<int64_t>((n + p.chunk - 1) / p.chunk, 1);
-  p.ids_per_block = (int)std::min<int64_t>(std::max<int64_t>((rows + 151) / 152, 1), kMaxIdsPerBlock);
-  p.blocks = (int)((rows + p.ids_per_block - 1) / p.ids_per_block);
+  p.log_blocks = kMinLogBlocks;
+  while (rows > (int64_t)1 << (p.log_blocks + kLogIds)) ++p.log_blocks;
+  p.ids_per_block = (int)((rows + ((int64_t)1 << p.log_blocks) - 1) >> p.log_blocks);
   p.col_blocks = (int)((cols + 255) / 256);
   p.o_order = 0;
   p.o_key = p.o_order + up(n * 4);
   p.o_offsets = p.o_key + up(n * 4);
-  p.o_counters = p.o_offsets + up((rows + 1) * 4);
+  p.o_counters = p.o_offsets + up((((int64_t)p.ids_per_block << p.log_blocks) + 1) * 4);
   p.o_part = p.o_counters + up((int64_t)p.chunks * p.col_blocks * 4);
   p.bytes = p.o_part + up((int64_t)p.chunks * 2 * cols * 4);
   return p;
 }
 
 template <typename TI, typename TO>
-cudaError_t fwd_as(const EmbedFwd& a, int vec, cudaStream_t s) {
+cudaError_t fwd_as(const EmbedFwd& a, int vec, int sms, cudaStream_t s) {
   const int64_t nv = (a.cols + vec - 1) / vec;
   const int tx = (int)std::min<int64_t>((nv + 31) / 32 * 32, 256);
   const int ty = std::max(1, 256 / tx);
-  const dim3 grid((unsigned)((a.n + ty - 1) / ty), (unsigned)((nv + tx - 1) / tx)), block(tx, ty);
-  if (vec == 8) return launch(k_embed_fwd<TI, TO, 8>, grid, block, 0, s, false, 1, a);
-  if (vec == 4) return launch(k_embed_fwd<TI, TO, 4>, grid, block, 0, s, false, 1, a);
-  return launch(k_embed_fwd<TI, TO, 1>, grid, block, 0, s, false, 1, a);
+  const unsigned gy = (unsigned)((nv + tx - 1) / tx);
+  // Four tokens per thread once that still fills every SM's eight blocks.
+  const bool many = a.n * gy >= (int64_t)sms * 8 * 4 * ty;
+  const int64_t per = many ? 4 * ty : ty;
+  const dim3 grid((unsigned)((a.n + per - 1) / per), gy), block(tx, ty);
+  if (vec == 8)
+    return many ? launch(k_embed_fwd<TI, TO, 8, 4>, grid, block, 0, s, false, 1, a) : launch(k_embed_fwd<TI, TO, 8, 1>, grid, block, 0, s, false, 1, a);
+  if (vec == 4)
+    return many ? launch(k_embed_fwd<TI, TO, 4, 4>, grid, block, 0, s, false, 1, a) : launch(k_embed_fwd<TI, TO, 4, 1>, grid, block, 0, s, false, 1, a);
+  return many ? launch(k_embed_fwd<TI, TO, 1, 4>, grid, block, 0, s, false, 1, a) : launch(k_embed_fwd<TI, TO, 1, 1>, grid, block, 0, s, false, 1, a);
 }
 
 template <typename TI>
-cudaError_t fwd_from(const EmbedFwd& a, int out_type, int vec, cudaStream_t s) {
+cudaError_t fwd_from(const EmbedFwd& a, int out_type, int vec, int sms, cudaStream_t s) {
   switch (out_type) {
-    case LOPT_F32: return fwd_as<TI, float>(a, vec, s);
-    case LOPT_F16: return fwd_as<TI, __half>(a, vec, s);
-    default: return fwd_as<TI, __nv_bfloat16>(a, vec, s);
+    case LOPT_F32: return fwd_as<TI, float>(a, vec, sms, s);
+    case LOPT_F16: return fwd_as<TI, __half>(a, vec, sms, s);
+    default: return fwd_as<TI, __nv_bfloat16>(a, vec, sms, s);
   }
 }
 
@@ -391,10 +460,11 @@ int lopt_embed_forward(const void* table, int table_type, int64_t rows, int64_t 
   if (cols % vec || !rows_aligned(mt, std::min(vec * ti, 32)) || !rows_aligned(mo, std::min(vec * to, 32))) vec = 1;
   const EmbedFwd a{table, index, out, status, rows, cols, table_stride, n, out_stride, index_type, scale};
   cudaStream_t s = (cudaStream_t)stream;
+  const int sms = sm_count();
   switch (table_type) {
-    case LOPT_F32: return done(fwd_from<float>(a, out_type, vec, s));
-    case LOPT_F16: return done(fwd_from<__half>(a, out_type, vec, s));
-    default: return done(fwd_from<__nv_bfloat16>(a, out_type, vec, s));
+    case LOPT_F32: return done(fwd_from<float>(a, out_type, vec, sms, s));
+    case LOPT_F16: return done(fwd_from<__half>(a, out_type, vec, sms, s));
+    default: return done(fwd_from<__nv_bfloat16>(a, out_type, vec, sms, s));
   }
 }
 
@@ -402,6 +472,7 @@ int lopt_embed_workspace(int64_t n, int64_t rows, int64_t cols, int64_t* bytes) 
   if (!bytes) return LOPT_E_ARG;
   if (rows < 1 || cols < 1 || n < 0 || rows >= kMaxRows || cols > kMaxCols || n >= kMaxRows)
     return LOPT_E_SHAPE;
+  if (rows > (int64_t)1 << 30) return LOPT_E_SHAPE;   // the sort numbers them in int32, rounded up per block
   *bytes = plan(n, rows, cols).bytes;
   return LOPT_OK;
 }
@@ -428,9 +499,9 @@ int lopt_embed_backward(const void* grad_out, int type, int64_t grad_out_stride,
   const bool v4 = cols % 4 == 0 && (uintptr_t)grad % 16 == 0;
   EmbedSort a{};
   a.index = index;
-  a.itype = index_type;
   a.n = (int)n;
   a.rows = (int)rows;
+  a.log_blocks = p.log_blocks;
   a.ids_per_block = p.ids_per_block;
   a.n_counters = (int64_t)p.chunks * p.col_blocks;
   a.order = (int32_t*)(w + p.o_order);
@@ -441,12 +512,12 @@ int lopt_embed_backward(const void* grad_out, int type, int64_t grad_out_stride,
   a.grad = grad;
   a.cols = cols;
   a.zero_rows = !accumulate;
-  a.zero_vec = v4;
-  const size_t smem = (size_t)(kSortWarps + 1) * p.ids_per_block * 4;
+  a.zero_bulk = v4;
+  const size_t smem = kZeroBytes + (size_t)kSortWarps * kFound * 4 + (size_t)(kSortWarps + 1) * p.ids_per_block * 4;
   auto* sort = index_type == LOPT_I32 ? &k_embed_sort<int32_t> : &k_embed_sort<int64_t>;
   cudaError_t e = cudaSuccess;
   if (smem > 40 * 1024) e = cudaFuncSetAttribute(sort, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e == cudaSuccess) e = launch(sort, dim3((unsigned)p.blocks), dim3(kSortThreads), smem, s, false, 1, a);
+  if (e == cudaSuccess) e = launch(sort, dim3(1u << p.log_blocks), dim3(kSortThreads), smem, s, false, 1, a);
   if (e != cudaSuccess) return done(e);
   EmbedSum b{};
   b.grad_out = grad_out;
@@ -458,7 +529,9 @@ int lopt_embed_backward(const void* grad_out, int type, int64_t grad_out_stride,
   b.grad = grad;
   b.gs = grad_out_stride;
   b.cols = cols;
-  b.rows = (int)rows;
+  b.log_blocks = p.log_blocks;
+  b.ids_per_block = p.ids_per_block;
+  b.last_offset = p.ids_per_block << p.log_blocks;
   b.chunk = p.chunk;
   b.accumulate = accumulate;
   b.scale = scale;

@@ -34,6 +34,47 @@ template <typename T, int VEC> struct alignas(VEC * sizeof(T)) Pack {
   T v[VEC];
 };
 
+// All its elements to and from float, two at a time where they are 16-bit.
+template <typename T, int VEC> __device__ __forceinline__ void to_floats(const Pack<T, VEC>& p, float (&f)[VEC]) {
+  if constexpr (sizeof(T) == 2 && VEC % 2 == 0) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&p);
+#pragma unroll
+    for (int k = 0; k < VEC / 2; ++k) {
+      float2 v;
+      if constexpr (__is_same(T, __nv_bfloat16)) {
+        v = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+      } else {
+        v = __half22float2(*reinterpret_cast<const __half2*>(w + k));
+      }
+      f[2 * k] = v.x;
+      f[2 * k + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) f[e] = to_f(p.v[e]);
+  }
+}
+template <typename T, int VEC> __device__ __forceinline__ Pack<T, VEC> from_floats(const float (&f)[VEC]) {
+  Pack<T, VEC> p;
+  if constexpr (sizeof(T) == 2 && VEC % 2 == 0) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&p);
+#pragma unroll
+    for (int k = 0; k < VEC / 2; ++k) {
+      if constexpr (__is_same(T, __nv_bfloat16)) {
+        const __nv_bfloat162 h = __float22bfloat162_rn(make_float2(f[2 * k], f[2 * k + 1]));
+        w[k] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const __half2 h = __float22half2_rn(make_float2(f[2 * k], f[2 * k + 1]));
+        w[k] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) p.v[e] = from_f<T>(f[e]);
+  }
+  return p;
+}
+
 // An element of a float-like array whose type is known at run time.
 __device__ __forceinline__ float load_as_f(const void* p, int64_t i, int type) {
   if (type == LOPT_F32) return static_cast<const float*>(p)[i];
