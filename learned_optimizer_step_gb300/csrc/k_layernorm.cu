@@ -9,6 +9,7 @@
 // blocks' sums go to the workspace and a second kernel adds them in block
 // order.  Both directions are bound by HBM bytes.
 #include <algorithm>
+#include <cstring>
 
 #include "train_common.cuh"
 
@@ -34,15 +35,14 @@ struct NormBwd {
   int wtype;
 };
 
-// Sum over the L threads of a row; L == 32: a warp, else the whole block.
+// Sum over the L threads of a row that are a whole block (L > 32), or a warp.
 template <int L>
 __device__ __forceinline__ float row_sum(float v, float* red) {
   v = warp_sum(v);
   if (L == 32) return v;
   constexpr int W = L / 32;
-  const int w = threadIdx.x / 32;
   __syncthreads();                      // the previous use of red is over
-  if (threadIdx.x % 32 == 0) red[w] = v;
+  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
   __syncthreads();
   float t = red[0];
 #pragma unroll
@@ -50,28 +50,27 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   return t;
 }
 
+// Two sums over the L threads of group `group` of a block; red alternates
+// between two areas from row to row, so one barrier does.
 template <int L>
-__device__ __forceinline__ float2 row_sum2(float a, float b, float2* red) {
-  a = warp_sum(a);
-  b = warp_sum(b);
-  if (L == 32) return make_float2(a, b);
+__device__ __forceinline__ float2 group_sum2(float2 v, float2* red, int group) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    v = __fadd2_rn(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
+  if (L == 32) return v;
   constexpr int W = L / 32;
-  const int w = threadIdx.x / 32;
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) red[w] = make_float2(a, b);
-  __syncthreads();
+  red += group * W;
+  if (threadIdx.x % 32 == 0) red[threadIdx.x % L / 32] = v;
+  asm volatile("bar.sync %0, %1;" :: "r"(1 + group), "n"(L) : "memory");
   float2 t = red[0];
 #pragma unroll
-  for (int k = 1; k < W; ++k) {
-    t.x += red[k].x;
-    t.y += red[k].y;
-  }
+  for (int k = 1; k < W; ++k) t = __fadd2_rn(t, red[k]);
   return t;
 }
 
 // VEC consecutive weights from column j on.
 template <typename T, int VEC>
-__device__ __forceinline__ void load_weights(const void* p, int wtype, int64_t j, float out[VEC]) {
+__device__ __forceinline__ void load_weights(const void* p, int wtype, int64_t j, float (&out)[VEC]) {
   if (wtype == LOPT_F32) {
     constexpr int V4 = VEC < 4 ? VEC : 4;
 #pragma unroll
@@ -81,87 +80,142 @@ __device__ __forceinline__ void load_weights(const void* p, int wtype, int64_t j
       for (int e = 0; e < V4; ++e) out[k + e] = q.v[e];
     }
   } else {
-    const Pack<T, VEC> q = *reinterpret_cast<const Pack<T, VEC>*>(static_cast<const T*>(p) + j);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) out[e] = to_f(q.v[e]);
+    to_floats(*reinterpret_cast<const Pack<T, VEC>*>(static_cast<const T*>(p) + j), out);
   }
 }
 
-__host__ __device__ constexpr int row_threads(int L) { return L == 32 ? 256 : L; }
+// Elementwise arithmetic on a lane's V elements: two at a time, by one
+// instruction for both, where V is even.
+__device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
+#define LOPT_EACH(V, PAIRS, SINGLE)                                     \
+  if constexpr ((V) % 2 == 0) {                                         \
+    _Pragma("unroll") for (int k = 0; k < (V); k += 2) { PAIRS; }       \
+  } else {                                                              \
+    _Pragma("unroll") for (int k = 0; k < (V); ++k) { SINGLE; }         \
+  }
+template <int V> __device__ __forceinline__ float2 at2(const float (&v)[V], int k) { return make_float2(v[k], v[k + 1]); }
+template <int V> __device__ __forceinline__ void set2(float (&v)[V], int k, float2 x) {
+  v[k] = x.x;
+  v[k + 1] = x.y;
+}
+// o = (x + a) * b
+template <int V> __device__ __forceinline__ void add_mul(const float (&x)[V], float a, float b, float (&o)[V]) {
+  LOPT_EACH(V, set2(o, k, __fmul2_rn(__fadd2_rn(at2(x, k), two(a)), two(b))), o[k] = (x[k] + a) * b)
+}
+// o += a;  o *= a
+template <int V> __device__ __forceinline__ void add_one(float a, float (&o)[V]) {
+  LOPT_EACH(V, set2(o, k, __fadd2_rn(at2(o, k), two(a))), o[k] += a)
+}
+template <int V> __device__ __forceinline__ void mul_one(float a, float (&o)[V]) {
+  LOPT_EACH(V, set2(o, k, __fmul2_rn(at2(o, k), two(a))), o[k] *= a)
+}
+// o = x * y
+template <int V> __device__ __forceinline__ void mul(const float (&x)[V], const float (&y)[V], float (&o)[V]) {
+  LOPT_EACH(V, set2(o, k, __fmul2_rn(at2(x, k), at2(y, k))), o[k] = x[k] * y[k])
+}
+// o += x
+template <int V> __device__ __forceinline__ void add_to(const float (&x)[V], float (&o)[V]) {
+  LOPT_EACH(V, set2(o, k, __fadd2_rn(at2(o, k), at2(x, k))), o[k] += x[k])
+}
+// o += x * y
+template <int V> __device__ __forceinline__ void fma_to(const float (&x)[V], const float (&y)[V], float (&o)[V]) {
+  LOPT_EACH(V, set2(o, k, __ffma2_rn(at2(x, k), at2(y, k), at2(o, k))), o[k] = fmaf(x[k], y[k], o[k]))
+}
+// o = x * a + (y * b + c)
+template <int V> __device__ __forceinline__ void fma_fma(const float (&x)[V], float a, const float (&y)[V], float b, float c, float (&o)[V]) {
+  LOPT_EACH(V, set2(o, k, __ffma2_rn(at2(x, k), two(a), __ffma2_rn(at2(y, k), two(b), two(c)))),
+            o[k] = fmaf(x[k], a, fmaf(y[k], b, c)))
+}
+template <int V> __device__ __forceinline__ float sum_of(const float (&x)[V]) {
+  if constexpr (V % 2 == 0) {
+    float2 t = at2(x, 0);
+#pragma unroll
+    for (int k = 2; k < V; k += 2) t = __fadd2_rn(t, at2(x, k));
+    return t.x + t.y;
+  } else {
+    float t = x[0];
+#pragma unroll
+    for (int k = 1; k < V; ++k) t += x[k];
+    return t;
+  }
+}
 
-// L threads per row, each with SLOTS accesses of VEC elements.
+__host__ __device__ constexpr int fwd_threads(int L) { return L == 32 ? 128 : L; }
+
+// L threads per row, each with SLOTS accesses of VEC elements.  Small blocks,
+// 32 warps per SM: with 16,421 rows of 768 a persistent form with the next
+// row's loads ahead takes 23.1 us, since its few rows per warp do not come
+// out even, this one 21.6.
 template <typename T, int VEC, int SLOTS, int L>
-__global__ void __launch_bounds__(row_threads(L)) k_norm_fwd(const NormFwd a) {
-  constexpr int R = row_threads(L) / L;
+__global__ void __launch_bounds__(fwd_threads(L), 1024 / fwd_threads(L)) k_norm_fwd(const NormFwd a) {
+  constexpr int TH = fwd_threads(L), R = TH / L;
   __shared__ float red[L / 32];
   const int lane = threadIdx.x % L;
+  const int cols = (int)a.cols;
+  const float inv = 1.f / (float)cols;
   const int64_t row = (int64_t)blockIdx.x * R + threadIdx.x / L;
   if (row >= a.rows) return;            // whole warps when L == 32, else never
   const T* x = static_cast<const T*>(a.x) + row * a.xs;
-  const T* r = a.residual ? static_cast<const T*>(a.residual) + row * a.rs : nullptr;
-  const int cols = (int)a.cols;
+  const T* r = static_cast<const T*>(a.residual) + row * a.rs;
   Pack<T, VEC> px[SLOTS], pr[SLOTS];
 #pragma unroll
   for (int s = 0; s < SLOTS; ++s) {
     const int j = (s * L + lane) * VEC;
-    if (j < cols) {
-      px[s] = *reinterpret_cast<const Pack<T, VEC>*>(x + j);
-      if (r) pr[s] = *reinterpret_cast<const Pack<T, VEC>*>(r + j);
-    }
+    if (j >= cols) continue;
+    px[s] = *reinterpret_cast<const Pack<T, VEC>*>(x + j);
+    if (a.residual) pr[s] = *reinterpret_cast<const Pack<T, VEC>*>(r + j);
   }
-  float v[SLOTS][VEC];
-  float sum = 0.f;
+  {
+    float v[SLOTS][VEC], sum[VEC];
 #pragma unroll
-  for (int s = 0; s < SLOTS; ++s) {
-    const bool in = (s * L + lane) * VEC < cols;
+    for (int k = 0; k < VEC; ++k) sum[k] = 0.f;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      v[s][e] = in ? to_f(px[s].v[e]) + (r ? to_f(pr[s].v[e]) : 0.f) : 0.f;
-      sum += v[s][e];
+    for (int s = 0; s < SLOTS; ++s) {
+      to_floats(px[s], v[s]);
+      if (a.residual) {
+        float t[VEC];
+        to_floats(pr[s], t);
+        add_to(t, v[s]);
+      }
+      if ((s * L + lane) * VEC < cols) add_to(v[s], sum);
     }
-  }
-  const float inv = 1.f / (float)cols;
-  const float mean = row_sum<L>(sum, red) * inv;
-  float sq = 0.f;
+    if (a.summed) {
+      T* sm = static_cast<T*>(a.summed) + row * a.ss;
 #pragma unroll
-  for (int s = 0; s < SLOTS; ++s) {
-    if ((s * L + lane) * VEC < cols) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float d = v[s][e] - mean;
-        sq = fmaf(d, d, sq);
+      for (int s = 0; s < SLOTS; ++s) {
+        const int j = (s * L + lane) * VEC;
+        if (j < cols) *reinterpret_cast<Pack<T, VEC>*>(sm + j) = from_floats<T, VEC>(v[s]);
       }
     }
-  }
-  const float rstd = rsqrtf(row_sum<L>(sq, red) * inv + a.eps);
-  if (lane == 0) {
-    a.mean[row] = mean;
-    a.rstd[row] = rstd;
-  }
-  T* y = static_cast<T*>(a.y) + row * a.ys;
-  T* sm = a.summed ? static_cast<T*>(a.summed) + row * a.ss : nullptr;
+    const float mean = row_sum<L>(sum_of(sum), red) * inv;
 #pragma unroll
-  for (int s = 0; s < SLOTS; ++s) {
-    const int j = (s * L + lane) * VEC;
-    if (j >= cols) continue;
-    float w[VEC], b[VEC];
-    load_weights<T, VEC>(a.weight, a.wtype, j, w);
-    if (a.bias) {
-      load_weights<T, VEC>(a.bias, a.wtype, j, b);
-    } else {
+    for (int k = 0; k < VEC; ++k) sum[k] = 0.f;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) b[e] = 0.f;
+    for (int s = 0; s < SLOTS; ++s) {
+      add_one(-mean, v[s]);
+      if ((s * L + lane) * VEC < cols) fma_to(v[s], v[s], sum);
     }
-    Pack<T, VEC> o;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) o.v[e] = from_f<T>(fmaf((v[s][e] - mean) * rstd, w[e], b[e]));
-    if (sm) {
-      Pack<T, VEC> q;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) q.v[e] = from_f<T>(v[s][e]);
-      *reinterpret_cast<Pack<T, VEC>*>(sm + j) = q;
+    const float rstd = rsqrtf(row_sum<L>(sum_of(sum), red) * inv + a.eps);
+    if (lane == 0) {
+      a.mean[row] = mean;
+      a.rstd[row] = rstd;
     }
-    *reinterpret_cast<Pack<T, VEC>*>(y + j) = o;
+    T* y = static_cast<T*>(a.y) + row * a.ys;
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+      const int j = (s * L + lane) * VEC;
+      if (j >= cols) continue;
+      float w[VEC];
+      load_weights<T, VEC>(a.weight, a.wtype, j, w);
+      mul_one(rstd, v[s]);
+      mul(v[s], w, w);
+      if (a.bias) {
+        float b[VEC];
+        load_weights<T, VEC>(a.bias, a.wtype, j, b);
+        add_to(b, w);
+      }
+      *reinterpret_cast<Pack<T, VEC>*>(y + j) = from_floats<T, VEC>(w);
+    }
   }
 }
 
@@ -192,111 +246,149 @@ __global__ void __launch_bounds__(512) k_norm_fwd_long(const NormFwd a) {
   }
   for (int64_t j = threadIdx.x; j < a.cols; j += L) {
     const float s = to_f(x[j]) + (r ? to_f(r[j]) : 0.f);
-    float w, b = 0.f;
-    load_weights<T, 1>(a.weight, a.wtype, j, &w);
-    if (a.bias) load_weights<T, 1>(a.bias, a.wtype, j, &b);
+    float w[1], b[1] = {0.f};
+    load_weights<T, 1>(a.weight, a.wtype, j, w);
+    if (a.bias) load_weights<T, 1>(a.bias, a.wtype, j, b);
     if (sm) sm[j] = from_f<T>(s);
-    y[j] = from_f<T>(fmaf((s - mean) * rstd, w, b));
+    y[j] = from_f<T>(fmaf((s - mean) * rstd, w[0], b[0]));
   }
 }
 
-// Persistent: a block's row groups take rows blockIdx.x * R + group,
-// striding by gridDim.x * R, and keep the column sums of their columns.
-template <typename T, int VEC, int SLOTS, int L>
-__global__ void __launch_bounds__(row_threads(L)) k_norm_bwd(const NormBwd a) {
-  constexpr int TH = row_threads(L), R = TH / L;
-  __shared__ float2 red[L / 32];
-  __shared__ float comb[R > 1 ? TH * VEC : 1];
+// Threads of a backward block, of which an SM takes one: 24 warps of lanes
+// with 8 elements, else 16 (128 registers).
+__host__ __device__ constexpr int bwd_threads(int E, int L, int es) {
+  return L == 1024 || (E <= 8 && es == 2 && L == 512) ? 1024 : E <= 8 && es == 2 ? 768 : 512;
+}
+
+// Persistent: a block's groups of L threads take rows blockIdx.x * R + group,
+// striding by gridDim.x * R, and keep the column sums of their columns.  With
+// AHEAD, the next row's x and dy are loaded before the current row is reduced;
+// with KEEP, xhat and g stay in registers over the reduction, else they are
+// made again.
+template <typename T, int VEC, int SLOTS, int L, bool AHEAD, bool KEEP>
+__global__ void __launch_bounds__(bwd_threads(VEC * SLOTS, L, sizeof(T)), 1) k_norm_bwd(const NormBwd a) {
+  constexpr int E = VEC * SLOTS, TH = bwd_threads(E, L, sizeof(T)), R = TH / L, W = L * E;
+  using P = Pack<T, VEC>;
+  __shared__ float2 red[2][TH / 32];
+  extern __shared__ __align__(16) float comb[];   // the groups' sums, at the end: [2][R][W]
   const int lane = threadIdx.x % L, group = threadIdx.x / L;
   const int cols = (int)a.cols;
   const float inv = 1.f / (float)cols;
+  const int64_t stride = (int64_t)gridDim.x * R;
+  const bool res = a.dres != nullptr;
+  let_next_start();
+  auto in = [&](int s) { return (s * L + lane) * VEC < cols; };
   float dw[SLOTS][VEC], db[SLOTS][VEC];
 #pragma unroll
   for (int s = 0; s < SLOTS; ++s)
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) dw[s][e] = db[s][e] = 0.f;
-  for (int64_t row = (int64_t)blockIdx.x * R + group; row < a.rows; row += (int64_t)gridDim.x * R) {
-    const T* x = static_cast<const T*>(a.x) + row * a.xs;
-    const T* dy = static_cast<const T*>(a.dy) + row * a.dys;
-    Pack<T, VEC> px[SLOTS], pd[SLOTS];
+    for (int k = 0; k < VEC; ++k) dw[s][k] = db[s][k] = 0.f;
+  P px[SLOTS], pd[SLOTS];
+  float mean = 0.f, rstd = 0.f;
+  auto load = [&](int64_t r, P (&x)[SLOTS], P (&d)[SLOTS], float& m, float& rs) {
+    const T* xp = static_cast<const T*>(a.x) + r * a.xs + lane * VEC;
+    const T* dp = static_cast<const T*>(a.dy) + r * a.dys + lane * VEC;
+    m = a.mean[r];
+    rs = a.rstd[r];
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
-      const int j = (s * L + lane) * VEC;
-      if (j < cols) {
-        px[s] = *reinterpret_cast<const Pack<T, VEC>*>(x + j);
-        pd[s] = *reinterpret_cast<const Pack<T, VEC>*>(dy + j);
-      }
+      if (!in(s)) continue;
+      x[s] = *reinterpret_cast<const P*>(xp + s * L * VEC);
+      d[s] = *reinterpret_cast<const P*>(dp + s * L * VEC);
     }
-    const float mean = a.mean[row], rstd = a.rstd[row];
+  };
+  int64_t row = (int64_t)blockIdx.x * R + group;
+  if (row < a.rows) load(row, px, pd, mean, rstd);
+  for (int par = 0; row < a.rows; row += stride, par ^= 1) {
+    P pr[SLOTS];
+    if (res) {
+      const T* rp = static_cast<const T*>(a.dres) + row * a.drs + lane * VEC;
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s)
+        if (in(s)) pr[s] = *reinterpret_cast<const P*>(rp + s * L * VEC);
+    }
+    P nx[SLOTS], nd[SLOTS];
+    float nmean = 0.f, nrstd = 0.f;
+    if (AHEAD && row + stride < a.rows) load(row + stride, nx, nd, nmean, nrstd);
+    float kx[SLOTS][VEC], kg[SLOTS][VEC];
+    auto make = [&](int s, float (&d)[VEC]) {
+      float w[VEC];
+      load_weights<T, VEC>(a.weight, a.wtype, (s * L + lane) * VEC, w);
+      to_floats(px[s], kx[s]);
+      to_floats(pd[s], d);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        kx[s][k] = (kx[s][k] - mean) * rstd;
+        kg[s][k] = d[k] * w[k];
+      }
+    };
     float sg = 0.f, sgx = 0.f;
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
-      const int j = (s * L + lane) * VEC;
-      if (j >= cols) continue;
-      float w[VEC];
-      load_weights<T, VEC>(a.weight, a.wtype, j, w);
+      if (!in(s)) continue;
+      float d[VEC];
+      make(s, d);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float d = to_f(pd[s].v[e]);
-        const float xh = (to_f(px[s].v[e]) - mean) * rstd;
-        const float g = d * w[e];
-        sg += g;
-        sgx = fmaf(g, xh, sgx);
-        dw[s][e] = fmaf(d, xh, dw[s][e]);
-        db[s][e] += d;
+      for (int k = 0; k < VEC; ++k) {
+        sg += kg[s][k];
+        sgx = fmaf(kg[s][k], kx[s][k], sgx);
+        dw[s][k] = fmaf(d[k], kx[s][k], dw[s][k]);
+        db[s][k] += d[k];
       }
     }
-    const float2 t = row_sum2<L>(sg, sgx, red);
-    const float mg = t.x * inv, mgx = t.y * inv;
-    T* dx = static_cast<T*>(a.dx) + row * a.dxs;
-    const T* dr = a.dres ? static_cast<const T*>(a.dres) + row * a.drs : nullptr;
+    const float2 t = group_sum2<L>(make_float2(sg, sgx), red[par], group);
+    const float c1 = -rstd * (t.x * inv), c2 = -rstd * (t.y * inv);
+    T* op = static_cast<T*>(a.dx) + row * a.dxs + lane * VEC;
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
-      const int j = (s * L + lane) * VEC;
-      if (j >= cols) continue;
-      float w[VEC];
-      load_weights<T, VEC>(a.weight, a.wtype, j, w);
-      Pack<T, VEC> o, q;
-      if (dr) q = *reinterpret_cast<const Pack<T, VEC>*>(dr + j);
+      if (!in(s)) continue;
+      float o[VEC];
+      if (!KEEP) make(s, o);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float xh = (to_f(px[s].v[e]) - mean) * rstd;
-        const float g = to_f(pd[s].v[e]) * w[e];
-        const float v = rstd * (g - mg - xh * mgx);
-        o.v[e] = from_f<T>(dr ? v + to_f(q.v[e]) : v);
+      for (int k = 0; k < VEC; ++k) o[k] = fmaf(kx[s][k], c2, fmaf(kg[s][k], rstd, c1));
+      if (res) {
+        float q[VEC];
+        to_floats(pr[s], q);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) o[k] += q[k];
       }
-      *reinterpret_cast<Pack<T, VEC>*>(dx + j) = o;
+      *reinterpret_cast<P*>(op + s * L * VEC) = from_floats<T, VEC>(o);
+    }
+    if (AHEAD) {
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s) {
+        px[s] = nx[s];
+        pd[s] = nd[s];
+      }
+      mean = nmean;
+      rstd = nrstd;
+    } else if (row + stride < a.rows) {
+      load(row + stride, px, pd, mean, rstd);
     }
   }
-  // The block's sums: over its row groups in order.
+  // The block's sums: over its groups in order.
   float* pw = a.part + (int64_t)blockIdx.x * cols;
-  float* pb = a.part + ((int64_t)gridDim.x + blockIdx.x) * cols;
+  const int64_t pb = (int64_t)gridDim.x * cols;   // the bias's sums lie so far behind the weight's
+  float* to_w = R == 1 ? pw : comb + group * W;
+  float* to_b = R == 1 ? pw + pb : comb + (R + group) * W;
 #pragma unroll
   for (int s = 0; s < SLOTS; ++s) {
-    const int j = (s * L + lane) * VEC;
-    if (R == 1) {
-      if (j < cols) {
+    if (!in(s)) continue;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          pw[j + e] = dw[s][e];
-          pb[j + e] = db[s][e];
-        }
-      }
-    } else {
+    for (int k = 0; k < VEC; ++k) {
+      to_w[(s * L + lane) * VEC + k] = dw[s][k];
+      to_b[(s * L + lane) * VEC + k] = db[s][k];
+    }
+  }
+  if (R > 1) {
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * W; c += TH) {
+      const int h = c / W, j = c % W;
+      if (j >= cols) continue;
+      float t = 0.f;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) comb[group * L * VEC + e * L + lane] = h ? db[s][e] : dw[s][e];
-        __syncthreads();
-        for (int c = threadIdx.x; c < L * VEC; c += TH) {   // c = e * L + lane of the column
-          float t = 0.f;
-#pragma unroll
-          for (int g = 0; g < R; ++g) t += comb[g * L * VEC + c];
-          const int col = (s * L + c % L) * VEC + c / L;
-          if (col < cols) (h ? pb : pw)[col] = t;
-        }
-      }
+      for (int g = 0; g < R; ++g) t += comb[(h * R + g) * W + j];
+      pw[h * pb + j] = t;
     }
   }
 }
@@ -315,18 +407,18 @@ __global__ void __launch_bounds__(512) k_norm_bwd_long(const NormBwd a) {
   const float mean = a.mean[row], rstd = a.rstd[row];
   float sg = 0.f, sgx = 0.f;
   for (int64_t j = threadIdx.x; j < a.cols; j += L) {
-    float w;
-    load_weights<T, 1>(a.weight, a.wtype, j, &w);
-    const float g = to_f(dy[j]) * w;
+    float w[1];
+    load_weights<T, 1>(a.weight, a.wtype, j, w);
+    const float g = to_f(dy[j]) * w[0];
     sg += g;
     sgx = fmaf(g, (to_f(x[j]) - mean) * rstd, sgx);
   }
-  const float2 t = row_sum2<L>(sg, sgx, red);
+  const float2 t = group_sum2<L>(make_float2(sg, sgx), red, 0);
   const float inv = 1.f / (float)a.cols;
   for (int64_t j = threadIdx.x; j < a.cols; j += L) {
-    float w;
-    load_weights<T, 1>(a.weight, a.wtype, j, &w);
-    const float v = rstd * (to_f(dy[j]) * w - t.x * inv - (to_f(x[j]) - mean) * rstd * (t.y * inv));
+    float w[1];
+    load_weights<T, 1>(a.weight, a.wtype, j, w);
+    const float v = rstd * (to_f(dy[j]) * w[0] - t.x * inv - (to_f(x[j]) - mean) * rstd * (t.y * inv));
     dx[j] = from_f<T>(dr ? v + to_f(dr[j]) : v);
   }
 }
@@ -349,87 +441,104 @@ __global__ void __launch_bounds__(256) k_norm_cols_long(const NormBwd a) {
   a.part[((int64_t)gridDim.y + blockIdx.y) * a.cols + j] = db;
 }
 
-// The blocks' sums of 32 columns: warp w adds blocks w, w + 32, ..., then one
-// warp the 32 sums in order.  blockIdx.y: 0 the weight's, 1 the bias's.
-__global__ void __launch_bounds__(1024) k_norm_finish(const float* part, int blocks, int64_t cols, float* dw, float* db,
-                                                      int accumulate) {
-  __shared__ float red[32][33];
-  wait_for_previous();
+// The blocks' sums of 32 columns: warp w adds blocks w, w + 8, ..., then one
+// warp the eight sums in order.  blockIdx.y: 0 the weight's, 1 the bias's.
+__global__ void __launch_bounds__(256) k_norm_finish(const float* part, int blocks, int64_t cols, float* dw, float* db,
+                                                     int accumulate) {
+  __shared__ float red[8][32];
   float* out = blockIdx.y ? db : dw;
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
   const int64_t j = (int64_t)blockIdx.x * 32 + lane;
-  const float* p = part + (int64_t)blockIdx.y * blocks * cols;
+  const float* p = part + (int64_t)blockIdx.y * blocks * cols + j;
+  wait_for_previous();
   float t = 0.f;
-  if (j < cols)
-    for (int b = w; b < blocks; b += 32) t += p[(int64_t)b * cols + j];
+  if (j < cols) {
+    constexpr int U = 20;   // 152 blocks in one go
+    for (int b0 = w; b0 < blocks; b0 += 8 * U) {
+      float v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = b0 + 8 * u < blocks ? __ldcg(p + (int64_t)(b0 + 8 * u) * cols) : 0.f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) t += v[u];
+    }
+  }
   red[w][lane] = t;
   __syncthreads();
   if (w == 0 && j < cols) {
     t = red[0][lane];
 #pragma unroll
-    for (int k = 1; k < 32; ++k) t += red[k][lane];
+    for (int k = 1; k < 8; ++k) t += red[k][lane];
     out[j] = accumulate ? out[j] + t : t;
   }
 }
 
 // ---- choice of the kernel -------------------------------------------------------
-// nvec accesses of VEC elements per row.  A warp per row while a lane holds
-// at most 32 elements, then 256 and 512 threads; longer rows read again.
-constexpr int kMaxBlocks = 1216;   // partial sums in the workspace
+constexpr int kMaxBlocks = 192;   // blocks' sums in the workspace
+
+template <typename K> cudaError_t allow_smem(K* k, size_t smem) {
+  if (smem <= 40 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+}
 
 template <typename T, int VEC, int SLOTS, int L>
 cudaError_t fwd_as(const NormFwd& a, cudaStream_t s) {
-  constexpr int R = row_threads(L) / L;
+  constexpr int R = fwd_threads(L) / L;
   const int64_t grid = (a.rows + R - 1) / R;
-  return launch(k_norm_fwd<T, VEC, SLOTS, L>, dim3((unsigned)grid), dim3(row_threads(L)), 0, s, false, 1, a);
+  return launch(k_norm_fwd<T, VEC, SLOTS, L>, dim3((unsigned)grid), dim3(fwd_threads(L)), 0, s, false, 1, a);
 }
 
 template <typename T, int VEC, int SLOTS, int L>
 cudaError_t bwd_as(const NormBwd& a, int sms, cudaStream_t s, int* blocks) {
-  constexpr int R = row_threads(L) / L;
-  int per_sm = 1;
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_norm_bwd<T, VEC, SLOTS, L>, row_threads(L), 0);
+  constexpr int E = VEC * SLOTS, TH = bwd_threads(E, L, sizeof(T)), R = TH / L;
+  constexpr bool kAhead = VEC > 1 && E <= 16, kKeep = VEC > 1 && E <= 8;   // what the registers hold beside the sums
+  const size_t smem = R > 1 ? (size_t)TH * E * 8 : 0;
+  auto* k = &k_norm_bwd<T, VEC, SLOTS, L, kAhead, kKeep>;
+  const cudaError_t e = allow_smem(k, smem);
   if (e != cudaSuccess) return e;
-  const int64_t grid = std::min<int64_t>({(a.rows + R - 1) / R, (int64_t)sms * std::max(per_sm, 1), kMaxBlocks});
-  *blocks = (int)grid;
-  return launch(k_norm_bwd<T, VEC, SLOTS, L>, dim3((unsigned)grid), dim3(row_threads(L)), 0, s, false, 1, a);
+  *blocks = (int)std::min<int64_t>({(a.rows + R - 1) / R, (int64_t)sms, kMaxBlocks});
+  return launch(k, dim3((unsigned)*blocks), dim3(TH), smem, s, false, 1, a);
 }
 
-// f.template operator()<VEC, SLOTS, L>() for the shape of a row.
+// Threads and slots for rows of nvec accesses of VEC elements: a warp per row
+// while a lane holds at most 24 elements, then groups with 16 (8 in float32)
+// elements a thread, up to 512 threads with 32 elements each; longer rows are
+// read again.
 #define LOPT_NORM_CASE(V, S, L_) if (nvec <= (int64_t)(S) * (L_)) return f.template run<V, S, L_>()
 template <int FULL, typename F>
 cudaError_t pick(int64_t cols, bool vec, F f) {
   if (vec) {
     const int64_t nvec = (cols + FULL - 1) / FULL;
+    constexpr int B = 8 / FULL;   // slots of 8 elements
     LOPT_NORM_CASE(FULL, 1, 32);
-    LOPT_NORM_CASE(FULL, 2, 32);
-    LOPT_NORM_CASE(FULL, 3, 32);
-    LOPT_NORM_CASE(FULL, 4, 32);
-    if constexpr (FULL == 4) {
-      LOPT_NORM_CASE(FULL, 6, 32);
-      LOPT_NORM_CASE(FULL, 8, 32);
+    if constexpr (F::kForward) {
+      LOPT_NORM_CASE(FULL, 2, 32);
+      LOPT_NORM_CASE(FULL, 3, 32);
+      LOPT_NORM_CASE(FULL, 2, 64);
+    } else {
+      LOPT_NORM_CASE(FULL, B, 32);
+      LOPT_NORM_CASE(FULL, B, 64);
+      LOPT_NORM_CASE(FULL, B, 128);
     }
-    LOPT_NORM_CASE(FULL, 1, 256);
-    LOPT_NORM_CASE(FULL, 2, 256);
-    LOPT_NORM_CASE(FULL, 4, 256);
-    if constexpr (FULL == 4) {
-      LOPT_NORM_CASE(FULL, 8, 256);
-    }
-    LOPT_NORM_CASE(FULL, 32 / FULL, 512);
+    LOPT_NORM_CASE(FULL, B, 256);
+    LOPT_NORM_CASE(FULL, B, 512);
+    LOPT_NORM_CASE(FULL, B, 1024);
+    LOPT_NORM_CASE(FULL, 4 * B, 512);
   } else {
     const int64_t nvec = cols;
     LOPT_NORM_CASE(1, 4, 32);
     LOPT_NORM_CASE(1, 8, 32);
     LOPT_NORM_CASE(1, 16, 32);
-    LOPT_NORM_CASE(1, 4, 256);
+    LOPT_NORM_CASE(1, 8, 128);
     LOPT_NORM_CASE(1, 8, 256);
-    LOPT_NORM_CASE(1, 16, 256);
+    LOPT_NORM_CASE(1, 8, 512);
+    LOPT_NORM_CASE(1, 16, 512);
     LOPT_NORM_CASE(1, 32, 512);
   }
   return f.long_rows();
 }
 
 template <typename T> struct FwdRun {
+  static constexpr bool kForward = true;
   const NormFwd& a;
   cudaStream_t s;
   template <int V, int S, int L> cudaError_t run() { return fwd_as<T, V, S, L>(a, s); }
@@ -439,6 +548,7 @@ template <typename T> struct FwdRun {
 };
 
 template <typename T> struct BwdRun {
+  static constexpr bool kForward = false;
   const NormBwd& a;
   int sms;
   cudaStream_t s;
@@ -573,7 +683,7 @@ int lopt_layernorm_backward(const void* grad_out, int type, int64_t rows, int64_
     default: e = pick<8>(cols, vec, BwdRun<__nv_bfloat16>{a, sms, s, &blocks}); break;
   }
   if (e != cudaSuccess) return done(e);
-  return done(launch(k_norm_finish, dim3((unsigned)((cols + 31) / 32), grad_bias ? 2u : 1u), dim3(1024), 0, s, true, 1,
+  return done(launch(k_norm_finish, dim3((unsigned)((cols + 31) / 32), grad_bias ? 2u : 1u), dim3(256), 0, s, true, 1,
                      (const float*)workspace, blocks, cols, grad_weight, grad_bias, accumulate));
 }
 
