@@ -84,12 +84,17 @@ __global__ void __launch_bounds__(256) k_embed_fwd(const EmbedFwd a) {
 constexpr int kMinLogBlocks = 7;        // 128 blocks
 constexpr int kLogIds = 10;             // ids per block: at most 1024, 128 KB of counters
 constexpr int kLogCluster = 3, kCluster = 1 << kLogCluster;
-constexpr int kFound = 256;             // entries a warp keeps of its part of the list
+// Entries a warp keeps of its part of the list: all of a short list's, at
+// most what shared memory has beside the counters.
+inline int found_of(int warps, int n) {
+  const int per_warp = (n + kCluster * warps - 1) / (kCluster * warps);
+  return std::min((per_warp + 31) / 32 * 64, warps == 16 ? 1024 : 256);
+}
 constexpr int kLogPlace = 32 - kLogIds - kLogCluster;
 
 struct EmbedSort {
   const void* index;
-  int n, rows, log_blocks, ids_per_block;
+  int n, rows, log_blocks, ids_per_block, found;
   int64_t n_counters;
   int32_t *order, *key, *offsets, *counters, *status;
 };
@@ -111,13 +116,14 @@ __device__ __forceinline__ void cluster_sync() {
 
 template <typename IT, int kSortWarps>
 __global__ void __launch_bounds__(32 * kSortWarps) k_embed_sort(const EmbedSort a) {
-  constexpr int kSortThreads = 32 * kSortWarps, kKept = kSortWarps * kFound;
+  constexpr int kSortThreads = 32 * kSortWarps;
+  const int keep = a.found;
   extern __shared__ int32_t sh[];
   const int K = a.ids_per_block;
   // An entry: block in the cluster | id's number in its block | place in this block's part.
-  uint32_t* list = reinterpret_cast<uint32_t*>(sh);                          // [kKept]: the block's
-  uint32_t* found = list + kKept;                                            // [32 warps][kFound]
-  int32_t* cnt = reinterpret_cast<int32_t*>(found) + kSortWarps * kFound;    // [32 warps][K]
+  uint32_t* list = reinterpret_cast<uint32_t*>(sh);                          // [warps x keep]: the block's
+  uint32_t* found = list + kSortWarps * keep;                                            // [warps][keep]
+  int32_t* cnt = reinterpret_cast<int32_t*>(found) + kSortWarps * keep;    // [warps][K]
   __shared__ int32_t found_n[kSortWarps];
   __shared__ int32_t list_n;   // -1: not all kept
   __shared__ int32_t wsum[kSortWarps];
@@ -128,7 +134,6 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_embed_sort(const EmbedSort 
   const int log_clusters = a.log_blocks - kLogCluster, mask = (1 << log_clusters) - 1;
   const unsigned rows = (unsigned)a.rows;
   const IT* index = static_cast<const IT*>(a.index);
-  let_next_start();
   for (int i = tid; i < kSortWarps * K; i += kSortThreads) cnt[i] = 0;
   if (tid == 0) below_cluster = below_block = 0;
   for (int64_t i = (int64_t)blk * kSortThreads + tid; i < a.n_counters; i += (int64_t)gridDim.x * kSortThreads)
@@ -161,8 +166,8 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_embed_sort(const EmbedSort 
     const unsigned who = __ballot_sync(0xffffffffu, b == cluster);
     if (!who) return;
     const int at = mine_n + __popc(who & lt);
-    if (b == cluster && at < kFound)   // the id without its cluster: block in the cluster, then number in the block
-      found[w * kFound + at] = (uint32_t)((int)id >> log_clusters) | (uint32_t)(i - first) << (kLogIds + kLogCluster);
+    if (b == cluster && at < keep)   // the id without its cluster: block in the cluster, then number in the block
+      found[w * keep + at] = (uint32_t)((int)id >> log_clusters) | (uint32_t)(i - first) << (kLogIds + kLogCluster);
     mine_n += __popc(who);
   });
   if (bad && a.status) atomicOr(a.status, kStatusIndex);
@@ -179,67 +184,62 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_embed_sort(const EmbedSort 
       const int t = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += t;
     }
-    const bool kept = !__any_sync(0xffffffffu, n > kFound) && per_block <= 1 << kLogPlace;
+    const bool kept = !__any_sync(0xffffffffu, n > keep) && per_block <= 1 << kLogPlace;
     const int off = __shfl_sync(0xffffffffu, incl - n, w), total = __shfl_sync(0xffffffffu, incl, 31);
     if (kept)
-      for (int i = lane; i < mine_n; i += 32) list[off + i] = found[w * kFound + i];
+      for (int i = lane; i < mine_n; i += 32) list[off + i] = found[w * keep + i];
     if (tid == 0) list_n = kept ? total : -1;
   }
   cluster_sync();
-  int size[kCluster], all = 0;   // where each of the cluster's lists begins; their entries
-  bool kept = true;
-#pragma unroll
-  for (int r = 0; r < kCluster; ++r) size[r] = *of_block(&list_n, r);
-#pragma unroll
-  for (int r = 0; r < kCluster; ++r) {
-    kept &= size[r] >= 0;
-    const int n = size[r];
-    size[r] = all;
-    all += n;
-  }
   // f(number of the id in this block or -1, position, whether a lower block of
-  // the cluster has it) over warp w's share of the cluster's entries, in list
-  // order; of the index itself where one list was not all kept.
+  // the cluster has it) over warp w's share of one of the cluster's lists, or,
+  // where that was not all kept, of the positions it stands for.
+  constexpr int kShares = kSortWarps / kCluster;   // warps to a list
+  const int from = w / kShares, part = w % kShares;
+  const int size = *of_block(&list_n, from);
+  const uint32_t* theirs = of_block(list, from);
   auto each = [&](auto f) {
-    if (kept) {
-      const int share = (all + 32 * kSortWarps - 1) / (32 * kSortWarps) * 32, end = min((w + 1) * share, all);
-      constexpr int V = 4;
-      for (int g0 = w * share; g0 < end; g0 += 32 * V) {
+    const int base = min(from * per_block, a.n);
+    if (size >= 0) {
+      const int share = (size + 32 * kShares - 1) / (32 * kShares) * 32, end = min((part + 1) * share, size);
+      constexpr int V = 8;
+      for (int g0 = part * share; g0 < end; g0 += 32 * V) {
         uint32_t x[V];
-        int base[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const int g = g0 + v * 32 + lane;
-          int r = 0, from = 0;
-#pragma unroll
-          for (int k = 1; k < kCluster; ++k) {
-            r += g >= size[k];
-            if (g >= size[k]) from = size[k];
-          }
-          base[v] = r * per_block;
-          x[v] = g < end ? of_block(list, r)[g - from] : 0;
-        }
+        for (int v = 0; v < V; ++v) x[v] = g0 + v * 32 + lane < end ? theirs[g0 + v * 32 + lane] : 0;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           if (g0 + v * 32 >= end) break;
           const int b = g0 + v * 32 + lane < end ? (int)(x[v] & (kCluster - 1)) : kCluster;
-          f(b == rank ? (int)(x[v] >> kLogCluster & ((1 << kLogIds) - 1)) : -1, base[v] + (int)(x[v] >> (kLogIds + kLogCluster)),
+          f(b == rank ? (int)(x[v] >> kLogCluster & ((1 << kLogIds) - 1)) : -1, base + (int)(x[v] >> (kLogIds + kLogCluster)),
             b < rank);
         }
       }
     } else {
-      const int per = (a.n + kSortWarps - 1) / kSortWarps;
-      scan(min(w * per, a.n), min(w * per + per, a.n), [&](int b, IT id, int i) {
+      const int stop = min(base + per_block, a.n), share = (per_block + kShares - 1) / kShares;
+      scan(min(base + part * share, stop), min(base + (part + 1) * share, stop), [&](int b, IT id, int i) {
         const int in = (int)id >> log_clusters & (kCluster - 1);
         f(b == cluster && in == rank ? (int)id >> a.log_blocks : -1, i, b == cluster && in < rank);
       });
     }
   };
-  int lower = 0;
-  each([&](int k, int, bool low) {
+  // Counts, and the block's own entries of the warp's share, for the second
+  // time (number in the block, position), in the place of what it found.
+  int lower = 0, own_n = 0;
+  const int own_keep = keep / 2;
+  uint2* own = reinterpret_cast<uint2*>(found + w * keep);
+  each([&](int k, int pos, bool low) {
     lower += low;
-    if (k >= 0) atomicAdd(cnt + w * K + k, 1);
+    const unsigned who = __ballot_sync(0xffffffffu, k >= 0);
+    if (!who) return;
+    const int at = own_n + __popc(who & lt);
+    if (k >= 0) {
+      atomicAdd(cnt + w * K + k, 1);
+      if (at < own_keep) own[at] = make_uint2(k, pos);
+    }
+    own_n += __popc(who);
   });
+  __syncwarp();
   for (int o = 16; o > 0; o >>= 1) lower += __shfl_xor_sync(0xffffffffu, lower, o);
   if (lane == 0 && lower) atomicAdd(&below_block, lower);
   __syncthreads();
@@ -279,8 +279,7 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_embed_sort(const EmbedSort 
     for (int k = 0; k < kSortWarps; ++k) cnt[k * K + tid] += start;
   }
   __syncthreads();
-  each([&](int k, int pos, bool) {
-    if (!__any_sync(0xffffffffu, k >= 0)) return;
+  auto put = [&](int k, int pos) {
     const unsigned peers = __match_any_sync(0xffffffffu, k);
     if (k >= 0) {
       const int at = cnt[w * K + k] + __popc(peers & lt);
@@ -290,7 +289,18 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_embed_sort(const EmbedSort 
     __syncwarp();
     if (k >= 0 && lane == __ffs(peers) - 1) cnt[w * K + k] += __popc(peers);
     __syncwarp();
-  });
+  };
+  if (own_n <= own_keep) {
+    for (int c = 0; c < own_n; c += 32) {
+      const bool in = c + lane < own_n;
+      const uint2 x = in ? own[c + lane] : make_uint2(0xffffffffu, 0);
+      put((int)x.x, (int)x.y);
+    }
+  } else {
+    each([&](int k, int pos, bool) {
+      if (__any_sync(0xffffffffu, k >= 0)) put(k, pos);
+    });
+  }
   cluster_sync();   // no block leaves while another reads its lists
 }
 
@@ -513,8 +523,9 @@ cudaError_t fwd_from(const EmbedFwd& a, int out_type, int vec, int sms, cudaStre
 }
 
 template <typename IT, int WARPS>
-cudaError_t sort_as(const EmbedSort& a, cudaStream_t s) {
-  const size_t smem = (size_t)WARPS * (2 * kFound + a.ids_per_block) * 4;
+cudaError_t sort_as(EmbedSort a, cudaStream_t s) {
+  a.found = found_of(WARPS, a.n);
+  const size_t smem = (size_t)WARPS * (2 * a.found + a.ids_per_block) * 4;
   auto* k = &k_embed_sort<IT, WARPS>;
   if (smem > 40 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
