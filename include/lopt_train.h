@@ -58,7 +58,9 @@ extern "C" {
  * Indices.  A negative index stands for "none": padding, an unused slot.
  * An index at or above the limit is an error that only the device can see:
  * it is treated as "none", and the kernels set bit 0 of *status (a device
- * int32 the caller zeroes and reads when it likes; NULL: not reported).
+ * int32 the caller zeroes and reads when it likes; NULL: not reported).  Bit 1
+ * says that a bounded wait inside lopt_distill() ran out and its results are
+ * not valid.
  */
 
 /*
@@ -126,7 +128,7 @@ int lopt_layernorm_backward(const void* grad_out, int type, int64_t rows, int64_
  *   loss[r] = w * T^2 * sum_k p_k * (log p_k - log q[i_k]),
  *   grad[r][j] = w * T * (q[j] - sum over k with i_k == j of p_k),
  * w = row_weight[r] (NULL: 1).  A row with w == 0, or with no slot that
- * counts, has loss 0 and gradient 0, and its logits are not read.  One slot
+ * counts, has loss 0 and gradient 0, whatever its logits hold.  One slot
  * with any finite t_k is the cross entropy with class i_k.  grad (type of the
  * logits) may be NULL: the loss alone.  In place: grad on logits.
  * top_type: LOPT_F32 or `type`.  1 <= top <= LOPT_MAX_TOP, 1e-30 <= T <= 1e30.

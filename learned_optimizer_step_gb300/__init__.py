@@ -6,7 +6,7 @@ from .lopt import (LearnedOptimizer, LoptError, PreparedList, TensorState,  # no
                    load_library, schedule_info, weight_set_size, zeros_state, MLP_FP32, MLP_TC)
 
 _TRAIN_OPS = ("check_indices", "distill_forward", "distill_forward_backward", "embedding_backward",
-              "embedding_forward", "layernorm_backward", "layernorm_forward")
+              "embedding_forward", "layernorm_backward", "layernorm_forward", "release_workspaces")
 
 
 def __getattr__(name):

@@ -9,6 +9,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "tc_layout.cuh"
 #include "train_common.cuh"
@@ -282,131 +283,6 @@ template <typename T> struct Slice {
   }
 };
 
-// One slot of the teacher's list: its class (-1: does not count) and logit.
-__device__ __forceinline__ void load_top(const Distill& a, int64_t row, int k, bool report, int32_t& id, float& t) {
-  const int64_t i = load_index(a.top_index, row * a.is + k, a.itype);
-  t = load_as_f(a.top_logits, row * a.ts + k, a.ttype);
-  if (i >= a.cols && a.status && report) atomicOr(a.status, kStatusIndex);
-  id = i >= 0 && i < a.cols && t != -INFINITY ? (int32_t)i : -1;
-}
-
-// The teacher's maximum and sum over a list in shared memory, by one warp;
-// false if no slot counts.
-__device__ __forceinline__ bool top_softmax(const int32_t* id, const float* tl, int top, float c, float& tmax, float& ps) {
-  const int lane = threadIdx.x % 32;
-  bool any = false;
-  tmax = -INFINITY;
-  ps = 0.f;
-  for (int k = lane; k < top; k += 32) {
-    if (id[k] < 0) continue;
-    any = true;
-    tmax = fmaxf(tmax, tl[k]);
-  }
-  if (!__any_sync(0xffffffffu, any)) return false;
-  tmax = warp_max(tmax);
-  for (int k = lane; k < top; k += 32)
-    if (id[k] >= 0) ps += ex2((tl[k] - tmax) * c);
-  ps = warp_sum(ps);
-  return true;
-}
-
-// The row's loss, by one warp.
-__device__ __forceinline__ float top_loss(const Distill& a, const int32_t* id, const float* tl, const float* zi, float tmax,
-                                          float ps, float m, float s) {
-  const float log_s = logf(s), log_ps = logf(ps), inv_ps = 1.f / ps;
-  float kl = 0.f;
-  for (int k = threadIdx.x % 32; k < a.top; k += 32) {
-    if (id[k] < 0) continue;
-    const float d = tl[k] - tmax, pk = ex2(d * a.log2e_t) * inv_ps;
-    if (pk == 0.f) continue;   // 0 log 0 = 0
-    kl += pk * ((d * a.inv_t - log_ps) - ((zi[k] - m) * a.inv_t - log_s));
-  }
-  return warp_sum(kl) * a.temperature * a.temperature;
-}
-
-// The gradient of slot k's class, if slot k is the first that lists it.
-__device__ __forceinline__ bool top_grad(const Distill& a, const int32_t* id, const float* p, const float* zi, int k, float m,
-                                         float f, float wt, float& v) {
-  const int j = id[k];
-  bool first = true;
-  float pk = 0.f;
-#pragma unroll 4
-  for (int o = 0; o < a.top; ++o) {
-    const bool alike = id[o] == j;
-    first &= !alike || o >= k;
-    pk += alike ? p[o] : 0.f;
-  }
-  v = fmaf(ex2((zi[k] - m) * a.log2e_t), f, -wt * pk);
-  return first;
-}
-
-// ---- short rows: a warp per row ----------------------------------------------------
-// The row stays in registers, NV slots per lane.
-template <typename T, int NV, bool GRAD>
-__global__ void __launch_bounds__(256) k_distill_warp(const Distill a) {
-  using S = Slots<T>;
-  extern __shared__ int32_t lists[];                    // per warp: class, p, z, teacher's logit of the slots
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int64_t row = (int64_t)blockIdx.x * 8 + warp;
-  if (row >= a.rows) return;
-  int32_t* id = lists + warp * a.top * 4;
-  float* p = reinterpret_cast<float*>(id + a.top);
-  float* zi = p + a.top;
-  float* tl = zi + a.top;
-  const Slice<T> r(a, row, 0, 0);
-  const float w = a.row_weight ? a.row_weight[row] : 1.f;
-  uint32_t v[NV][4];
-  float tmax, ps;
-  bool learn = w != 0.f;
-  if (learn) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int q = i * 32 + lane;
-      uint4 x = make_uint4(S::kNegInf, S::kNegInf, S::kNegInf, S::kNegInf);
-      if (q < r.cnt) x = r.whole(q) ? r.z16()[q] : r.read_edge(q);
-      v[i][0] = x.x; v[i][1] = x.y; v[i][2] = x.z; v[i][3] = x.w;
-    }
-    for (int k = lane; k < a.top; k += 32) {
-      load_top(a, row, k, true, id[k], tl[k]);
-      if (id[k] >= 0) zi[k] = to_f(r.z[id[k]]);
-    }
-    __syncwarp();
-    learn = top_softmax(id, tl, a.top, a.log2e_t, tmax, ps);
-  }
-  if (!learn) {
-    if (lane == 0) a.loss[row] = 0.f;
-    if (GRAD) {
-      const uint32_t o[4] = {0, 0, 0, 0};
-      for (int q = lane; q < r.cnt; q += 32) r.write(q, o);
-    }
-    return;
-  }
-  const float c = a.log2e_t;
-  Partial<T> part;
-  part.template add<NV>(v, c);
-  float m = part.m, s = part.s;
-  join_warp(m, s, c);
-  const float loss = top_loss(a, id, tl, zi, tmax, ps, m, s);
-  if (lane == 0) a.loss[row] = w * loss;
-  if (!GRAD) return;
-  const float wt = w * a.temperature, f = wt / s, inv_ps = 1.f / ps;
-  const Dense<T> dense(m, c, f);
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int q = i * 32 + lane;
-    if (q >= r.cnt) continue;
-    uint32_t o[4];
-    dense.of(v[i], o);
-    r.write(q, o);
-  }
-  for (int k = lane; k < a.top; k += 32) p[k] = id[k] < 0 ? 0.f : ex2((tl[k] - tmax) * c) * inv_ps;
-  __syncwarp();
-  for (int k = lane; k < a.top; k += 32) {
-    float g;
-    if (id[k] >= 0 && top_grad(a, id, p, zi, k, m, f, wt, g)) r.g[id[k]] = from_f<T>(g);
-  }
-}
-
 // ---- long rows: a block, or a cluster of blocks, per row -----------------------------
 constexpr int kMaxCluster = 8;
 constexpr uint64_t kWaitNs = 1000000000ull;   // 1 s: a wait that long has failed
@@ -439,6 +315,7 @@ struct List {
   // Of the whole list: 1 / sum of e, sum of p log p; whether any slot counts.
   float inv, p_log_p;
   bool any;
+  __device__ __forceinline__ List(int32_t* words, int top_);
 };
 __host__ __device__ inline int table_log_size(int top) {
   int n = 5;
@@ -446,6 +323,14 @@ __host__ __device__ inline int table_log_size(int top) {
   return n;
 }
 __host__ __device__ inline int list_words(int top) { return 4 * top + 2 * (1 << table_log_size(top)); }
+__device__ __forceinline__ List::List(int32_t* words, int top_) : top(top_), log_size(table_log_size(top_)), any(false) {
+  id = words;
+  place = id + top;
+  e = reinterpret_cast<float*>(place + top);
+  z = e + top;
+  key = reinterpret_cast<int32_t*>(z + top);
+  sum = reinterpret_cast<float*>(key + (1 << log_size));
+}
 
 // Slots are taken 128 at a time, four of a lane's side by side: the list is
 // a chain of short steps, and its warp has latency to lose, not work.
@@ -570,35 +455,180 @@ __device__ __forceinline__ void read_listed(const Slice<T>& r, const uint4* buf,
   }
 }
 
-// The slice's part of sum p z, as (ref, sum of p (z - ref)) and sum of p: exact
-// about any row maximum.
+// This lane's part of sum p (z - m) over the slots of the slice.
 template <typename T>
-__device__ __forceinline__ void sum_listed(const Slice<T>& r, const List& l, float& ref, float& pz, float& ps) {
-  const int lane = threadIdx.x % 32;
-  ref = -INFINITY;
+__device__ __forceinline__ float sum_listed(const Slice<T>& r, const List& l, float m) {
+  float pz = 0.f;
   LOPT_LIST_SLOTS(k0, l.top) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int k = k0 + u * 32 + lane;
-      if (k < l.top && r.holds(l.id[k]) && l.e[k] != 0.f) ref = fmaxf(ref, l.z[k]);
-    }
-  }
-  ref = warp_max(ref);
-  if (ref == -INFINITY) ref = 0.f;
-  pz = ps = 0.f;
-  LOPT_LIST_SLOTS(k0, l.top) {
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int k = k0 + u * 32 + lane;
+      const int k = k0 + u * 32 + (int)(threadIdx.x % 32);
       if (k >= l.top || !r.holds(l.id[k])) continue;
       const float p = l.e[k] * l.inv;
-      if (p == 0.f) continue;   // 0 log 0 = 0
-      pz = fmaf(p, l.z[k] - ref, pz);
-      ps += p;
+      if (p != 0.f) pz = fmaf(p, l.z[k] - m, pz);   // 0 log 0 = 0
     }
   }
-  pz = warp_sum(pz);
-  ps = warp_sum(ps);
+  return pz;
+}
+
+// A list of at most 128 slots whose gradient is not wanted (or at most 32, in
+// a lane each): registers hold it.
+template <int U> struct SlotRegs {
+  int32_t id[U];
+  float e[U], z[U];
+  float inv, p_log_p;
+  bool any;
+};
+template <typename T, int U>
+__device__ __forceinline__ void make_slots(const Distill& a, const ListAhead& x, bool report, SlotRegs<U>& l) {
+  float tmax = -INFINITY;
+  bool any = false, bad = false;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    l.e[u] = top_logit<T>(a, x.t[u]);
+    bad |= x.id[u] >= a.cols;
+    const bool counts = x.id[u] >= 0 && x.id[u] < a.cols && l.e[u] != -INFINITY;
+    l.id[u] = counts ? (int32_t)x.id[u] : -1;
+    if (counts) tmax = fmaxf(tmax, l.e[u]);
+    any |= counts;
+  }
+  if (bad && report && a.status) atomicOr(a.status, kStatusIndex);
+  l.any = __any_sync(0xffffffffu, any);
+  tmax = warp_max(tmax);
+  float2 sums = make_float2(0.f, 0.f);   // of e, of e (t - max)
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const float d = l.e[u] - tmax, e = l.id[u] < 0 ? 0.f : ex2(d * a.log2e_t);
+    l.e[u] = e;
+    sums.x += e;
+    if (e != 0.f) sums.y = fmaf(e, d, sums.y);   // 0 log 0 = 0
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    sums = __fadd2_rn(sums, make_float2(__shfl_xor_sync(0xffffffffu, sums.x, o), __shfl_xor_sync(0xffffffffu, sums.y, o)));
+  l.inv = 1.f / sums.x;
+  l.p_log_p = sums.y * l.inv * a.inv_t - logf(sums.x);   // sum p (d / T - log es), sum p = 1
+}
+template <typename T, bool WHOLE, int U>
+__device__ __forceinline__ void read_slots(const Slice<T>& r, const uint4* buf, SlotRegs<U>& l) {
+  const T* z = reinterpret_cast<const T*>(buf) + (r.mis - r.beg * Slice<T>::N);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (r.holds(l.id[u]) && r.whole((l.id[u] + r.mis) / Slice<T>::N - r.beg) == WHOLE) l.z[u] = to_f(z[l.id[u]]);
+}
+template <typename T, int U>
+__device__ __forceinline__ float sum_slots(const Slice<T>& r, const SlotRegs<U>& l, float m) {
+  float pz = 0.f;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const float p = l.e[u] * l.inv;
+    if (p != 0.f && r.holds(l.id[u])) pz = fmaf(p, l.z[u] - m, pz);
+  }
+  return pz;
+}
+
+// The gradient of the listed classes, over what the dense part wrote.
+template <typename T>
+__device__ __forceinline__ void write_listed(const Slice<T>& r, const List& l, float c, float m, float f, float wt) {
+  const float wp = wt * l.inv;
+  LOPT_LIST_SLOTS(k0, l.top) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int k = k0 + u * 32 + (int)(threadIdx.x % 32);
+      const int h = k < l.top ? l.place[k] : -1;
+      if (h >= 0) r.g[l.id[k]] = from_f<T>(fmaf(ex2((l.z[k] - m) * c), f, -wp * l.sum[h]));
+    }
+  }
+}
+
+// ---- short rows: a warp per row ----------------------------------------------------
+// The row stays in registers, NV slots per lane.  Its loads go out before
+// its weight is known: a short row is a chain of latencies.
+constexpr int kWarpRows = 4;   // rows of a block: small blocks even out the last wave
+
+template <typename T, int NV, bool GRAD>
+__global__ void __launch_bounds__(32 * kWarpRows, 8) k_distill_warp(const Distill a) {
+  using S = Slots<T>;
+  extern __shared__ int32_t words[];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int64_t row = (int64_t)blockIdx.x * kWarpRows + warp;
+  if (row >= a.rows) return;
+  ListAhead x;
+  load_list<T>(a, row, 0, x);
+  const Slice<T> r(a, row, 0, 0);
+  uint32_t v[NV][4];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int q = i * 32 + lane;
+    uint4 y = make_uint4(S::kNegInf, S::kNegInf, S::kNegInf, S::kNegInf);
+    if (q < r.cnt) y = r.whole(q) ? r.z16()[q] : r.read_edge(q);
+    v[i][0] = y.x; v[i][1] = y.y; v[i][2] = y.z; v[i][3] = y.w;
+  }
+  const float w = a.row_weight ? a.row_weight[row] : 1.f;
+  float z[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (x.id[u] >= 0 && x.id[u] < a.cols) z[u] = to_f(r.z[x.id[u]]);
+  const float c = a.log2e_t;
+  Partial<T> part;
+  part.template add<NV>(v, c);
+  float m = part.m, s = part.s;
+  join_warp(m, s, c);
+  const float wt = w * a.temperature, f = wt / s;
+  // The loss, or a row of zeros; whether there is a gradient to write.
+  auto finish = [&](bool any, float p_log_p, float pz) {
+    if (lane == 0) a.loss[row] = any ? wt * a.temperature * (p_log_p - (pz * a.inv_t - logf(s))) : 0.f;
+    if (!GRAD) return false;
+    if (!any) {   // nothing to learn from this row
+      const uint32_t o[4] = {0, 0, 0, 0};
+      for (int q = lane; q < r.cnt; q += 32) r.write(q, o);
+      return false;
+    }
+    const Dense<T> dense(m, c, f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int q = i * 32 + lane;
+      if (q >= r.cnt) continue;
+      uint32_t o[4];
+      dense.of(v[i], o);
+      r.write(q, o);
+    }
+    __syncwarp();
+    return true;
+  };
+  if (a.top <= 32) {   // a slot in each lane
+    SlotRegs<1> l;
+    make_slots<T>(a, x, w != 0.f, l);
+    l.z[0] = z[0];
+    const bool any = w != 0.f && l.any;
+    if (!finish(any, l.p_log_p, warp_sum(sum_slots(r, l, m)))) return;
+    // The listed classes again: by the first slot of a class, the repeats added
+    // in slot order.
+    const unsigned alike = __match_any_sync(0xffffffffu, l.id[0]);
+    float e = l.e[0];
+    if (__any_sync(0xffffffffu, l.id[0] >= 0 && alike != 1u << lane)) {
+      e = 0.f;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        const float ek = __shfl_sync(0xffffffffu, l.e[0], k);
+        if (alike >> k & 1) e += ek;
+      }
+    }
+    if (l.id[0] >= 0 && lane == __ffs(alike) - 1)
+      r.g[l.id[0]] = from_f<T>(fmaf(ex2((l.z[0] - m) * c), f, -wt * l.inv * e));
+    return;
+  }
+  List l(words + warp * list_words(a.top), a.top);
+  if (w != 0.f) {
+    make_list<T, GRAD>(a, r, row, true, x, l);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (u * 32 + lane < l.top) l.z[u * 32 + lane] = z[u];
+    for (int k = 128 + lane; k < l.top; k += 32)
+      if (l.id[k] >= 0) l.z[k] = to_f(r.z[l.id[k]]);
+    __syncwarp();
+  }
+  if (finish(l.any, l.p_log_p, warp_sum(l.any ? sum_listed(r, l, m) : 0.f))) write_listed(r, l, c, m, f, wt);
 }
 
 // The row's (m, s) from all its warps' pairs, by one warp, in a fixed order.
@@ -655,7 +685,7 @@ __global__ void __launch_bounds__(TH + 32, 1024 / TH) k_distill_ring(const Disti
   extern __shared__ __align__(128) unsigned char sm[];
   uint4* buf = reinterpret_cast<uint4*>(sm);
   __shared__ float2 pairs[SETS][GW * kMaxCluster];    // (m, s) of the row's warps
-  __shared__ float2 loss_parts[SETS][2 * kMaxCluster];
+  __shared__ float2 loss_parts[SETS][kMaxCluster];    // (sum of p (z - m), 0) of the blocks
   __shared__ uint64_t full, summed, listed, empty, xch[SETS], parts[SETS];
   __shared__ int gave_up;
   __shared__ int32_t any[2];   // whether a slot of the row counts
@@ -685,16 +715,7 @@ __global__ void __launch_bounds__(TH + 32, 1024 / TH) k_distill_ring(const Disti
   const float c = a.log2e_t;
 
   if (gw == GW) {   // the warp that works ahead
-    List l;
-    l.top = a.top;
-    l.log_size = table_log_size(a.top);
-    l.id = reinterpret_cast<int32_t*>(sm + (size_t)slice_slots * 16);
-    l.place = l.id + a.top;
-    l.e = reinterpret_cast<float*>(l.place + a.top);
-    l.z = l.e + a.top;
-    l.key = reinterpret_cast<int32_t*>(l.z + a.top);
-    l.sum = reinterpret_cast<float*>(l.key + (1 << l.log_size));
-    l.any = false;
+    List l(reinterpret_cast<int32_t*>(sm + (size_t)slice_slots * 16), a.top);
     // The whole slots of a row's slice, when all lanes are done with the last one's.
     auto fetch = [&](const Slice<T>& n) {
       __syncwarp();
@@ -707,13 +728,20 @@ __global__ void __launch_bounds__(TH + 32, 1024 / TH) k_distill_ring(const Disti
       __syncwarp();
     };
     ListAhead x;
+    SlotRegs<4> lr;
+    const bool regs = !GRAD && a.top <= 128;
     auto list = [&](const Slice<T>& n, int64_t at, int par) {
-      make_list<T, GRAD>(a, n, at, rank == 0, x, l);
+      if (regs) make_slots<T>(a, x, rank == 0, lr);
+      else make_list<T, GRAD>(a, n, at, rank == 0, x, l);
       if (lane == 0) {
-        any[par] = l.any;
+        any[par] = regs ? lr.any : l.any;
         mbar_arrive(&listed);
       }
       __syncwarp();
+    };
+    auto read = [&](const Slice<T>& n, auto whole) {
+      if (regs) read_slots<T, decltype(whole)::value>(n, buf, lr);
+      else read_listed<T, decltype(whole)::value>(n, buf, l);
     };
     load_list<T>(a, row, 0, x);
     Slice<T> r(a, row, rank, log_c);
@@ -728,54 +756,36 @@ __global__ void __launch_bounds__(TH + 32, 1024 / TH) k_distill_ring(const Disti
       const Slice<T> r_next(a, next < a.rows ? next : row, rank, log_c);
       if (w != 0.f) {
         const int b = e & (SETS - 1);
-        const bool learn = l.any;
+        const bool learn = regs ? lr.any : l.any;
         wait(&full, e);
-        if (learn) read_listed<T, true>(r, buf, l);
+        if (learn) read(r, std::true_type());
         wait(&summed, e);
-        if (learn && (r.first >= 0 || r.last >= 0)) read_listed<T, false>(r, buf, l);
+        if (learn && (r.first >= 0 || r.last >= 0)) read(r, std::false_type());
         if (!GRAD && w_next != 0.f) fetch(r_next);
-        if (learn) {
-          float ref, pz, ps;
-          __syncwarp();
-          sum_listed(r, l, ref, pz, ps);
-          float2* mine = &loss_parts[b][2 * rank];
-          if (C > 1) {
-            if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&parts[b], (uint32_t)(2 * C * sizeof(float2)));
-            if (lane < 2) send_pair(mine + lane, &parts[b], 0, lane ? ps : ref, lane ? 0.f : pz);
-          } else if (lane < 2) {
-            mine[lane] = make_float2(lane ? ps : ref, lane ? 0.f : pz);
-          }
-          __syncwarp();
-        }
         if (C > 1) wait(&xch[b], e / SETS);
         float m, s;
         join_pairs<GW * kMaxCluster>(pairs[b], GW * C, c, m, s);
-        if (rank == 0) {
-          float loss = 0.f;
-          if (learn) {
-            if (C > 1) wait(&parts[b], e / SETS);
-            float pz = 0.f;   // sum p (z - m)
-            if (lane < C) {
-              const float2 u = loss_parts[b][2 * lane], v = loss_parts[b][2 * lane + 1];
-              if (v.x != 0.f) pz = fmaf(v.x, u.x - m, u.y);
+        float loss = 0.f;
+        if (learn) {
+          float pz = warp_sum(regs ? sum_slots(r, lr, m) : sum_listed(r, l, m));
+          if (C > 1) {   // the first block adds the blocks' parts
+            if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&parts[b], (uint32_t)(C * sizeof(float2)));
+            __syncwarp();
+            if (lane == 0) send_pair(&loss_parts[b][rank], &parts[b], 0, pz, 0.f);
+            if (rank == 0) {
+              wait(&parts[b], e / SETS);
+              pz = warp_sum(lane < C ? loss_parts[b][lane].x : 0.f);
             }
-            loss = w * a.temperature * a.temperature * (l.p_log_p - (warp_sum(pz) * a.inv_t - logf(s)));
           }
-          if (lane == 0) a.loss[row] = loss;
+          loss = w * a.temperature * a.temperature * ((regs ? lr.p_log_p : l.p_log_p) - (pz * a.inv_t - logf(s)));
         }
+        if (rank == 0 && lane == 0) a.loss[row] = loss;
         if (GRAD) {
           wait(&empty, e);
           if (w_next != 0.f) fetch(r_next);
           if (learn) {   // the listed classes of this slice, again
-            const float wt = w * a.temperature, f = wt / s, wp = wt * l.inv;
-            LOPT_LIST_SLOTS(k0, l.top) {
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                const int k = k0 + u * 32 + lane;
-                const int h = k < l.top ? l.place[k] : -1;
-                if (h >= 0) r.g[l.id[k]] = from_f<T>(fmaf(ex2((l.z[k] - m) * c), f, -wp * l.sum[h]));
-              }
-            }
+            const float wt = w * a.temperature;
+            write_listed(r, l, c, m, wt / s, wt);
           }
           __syncwarp();
         }
@@ -959,8 +969,8 @@ __global__ void __launch_bounds__(512) k_distill_rows(const Distill a) {
 // ---- choice of the kernel -------------------------------------------------------
 template <typename T, int NV>
 cudaError_t warp_as(const Distill& a, cudaStream_t s) {
-  const dim3 grid((unsigned)((a.rows + 7) / 8)), block(256);
-  const size_t smem = (size_t)8 * a.top * 4 * 4;
+  const dim3 grid((unsigned)((a.rows + kWarpRows - 1) / kWarpRows)), block(32 * kWarpRows);
+  const size_t smem = a.top <= 32 ? 0 : (size_t)kWarpRows * list_words(a.top) * 4;
   if (a.grad) return launch(k_distill_warp<T, NV, true>, grid, block, smem, s, false, 1, a);
   return launch(k_distill_warp<T, NV, false>, grid, block, smem, s, false, 1, a);
 }
@@ -968,10 +978,8 @@ cudaError_t warp_as(const Distill& a, cudaStream_t s) {
 template <typename T, int TH, bool GRAD>
 cudaError_t ring_as(const Distill& a, int log_c, int slice_slots, size_t smem, int blocks, cudaStream_t s) {
   auto* k = &k_distill_ring<T, TH, GRAD>;
-  if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem);
+  if (e != cudaSuccess) return e;
   const int64_t clusters = std::min<int64_t>(a.rows, blocks >> log_c);
   return launch(k, dim3((unsigned)(clusters << log_c)), dim3(TH + 32), smem, s, false, 1 << log_c, a, log_c, slice_slots);
 }

@@ -527,10 +527,8 @@ cudaError_t sort_as(EmbedSort a, cudaStream_t s) {
   a.found = found_of(WARPS, a.n);
   const size_t smem = (size_t)WARPS * (2 * a.found + a.ids_per_block) * 4;
   auto* k = &k_embed_sort<IT, WARPS>;
-  if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem);
+  if (e != cudaSuccess) return e;
   return launch(k, dim3(1u << a.log_blocks), dim3(32 * WARPS), smem, s, false, kCluster, a);
 }
 

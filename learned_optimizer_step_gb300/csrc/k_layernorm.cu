@@ -475,11 +475,6 @@ __global__ void __launch_bounds__(256) k_norm_finish(const float* part, int bloc
 // ---- choice of the kernel -------------------------------------------------------
 constexpr int kMaxBlocks = 192;   // blocks' sums in the workspace
 
-template <typename K> cudaError_t allow_smem(K* k, size_t smem) {
-  if (smem <= 40 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-}
-
 template <typename T, int VEC, int SLOTS, int L>
 cudaError_t fwd_as(const NormFwd& a, cudaStream_t s) {
   constexpr int R = fwd_threads(L) / L;
@@ -493,7 +488,7 @@ cudaError_t bwd_as(const NormBwd& a, int sms, cudaStream_t s, int* blocks) {
   constexpr bool kAhead = VEC > 1 && E <= 16, kKeep = VEC > 1 && E <= 8;   // what the registers hold beside the sums
   const size_t smem = R > 1 ? (size_t)TH * E * 8 : 0;
   auto* k = &k_norm_bwd<T, VEC, SLOTS, L, kAhead, kKeep>;
-  const cudaError_t e = allow_smem(k, smem);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem);
   if (e != cudaSuccess) return e;
   *blocks = (int)std::min<int64_t>({(a.rows + R - 1) / R, (int64_t)sms, kMaxBlocks});
   return launch(k, dim3((unsigned)*blocks), dim3(TH), smem, s, false, 1, a);

@@ -3,6 +3,7 @@
 // argument checks and launches.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -132,6 +133,37 @@ cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
   cfg.attrs = at;
   cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+// Lets `kernel` have all the dynamic shared memory of a block on the current
+// device.  The runtime calls cost more than a small launch can spare, so which
+// (kernel, device) have it is remembered in a table without locks; two threads
+// that both find it missing set the same value.
+inline cudaError_t allow_smem(const void* kernel, size_t smem) {
+  if (smem <= 40 * 1024) return cudaSuccess;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  constexpr int kSlots = 1024;
+  static std::atomic<uintptr_t> done[kSlots];
+  const uintptr_t key = (uintptr_t)kernel * 64 + (uintptr_t)(dev & 63) + 1;
+  size_t h = (key * 0x9e3779b97f4a7c15ull) >> 54;
+  for (int n = 0; n < kSlots; ++n, h = (h + 1) & (kSlots - 1)) {
+    const uintptr_t k = done[h].load(std::memory_order_acquire);
+    if (k == key) return cudaSuccess;
+    if (k == 0) break;
+  }
+  cudaFuncAttributes at;
+  int most = 0;
+  if ((e = cudaFuncGetAttributes(&at, kernel)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)at.sharedSizeBytes);
+  if (e != cudaSuccess) return e;
+  for (int n = 0; n < kSlots; ++n, h = (h + 1) & (kSlots - 1)) {
+    uintptr_t k = 0;
+    if (done[h].compare_exchange_strong(k, key) || k == key) break;
+  }
+  return cudaSuccess;
 }
 
 inline int done(cudaError_t e) { return e == cudaSuccess ? LOPT_OK : record_cuda_error(e); }

@@ -18,6 +18,8 @@ only the device sees it.
 from __future__ import annotations
 
 import ctypes
+import functools
+import threading
 from typing import Optional
 
 import torch
@@ -36,7 +38,10 @@ TRAIN_EXPORTED = ("lopt_embed_forward", "lopt_embed_workspace", "lopt_embed_back
 
 _TYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 _INDEX = {torch.int32: I32, torch.int64: I64}
+_E_TIMEOUT = -7
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 _fns = None
 
 
@@ -115,23 +120,26 @@ def _index(t, what):
 class _Call:
     """Device and stream of one call; new tensors are allocated for them."""
 
-    __slots__ = ("dev", "handle", "stream", "guard")
+    __slots__ = ("dev", "handle", "stream")
 
     def __init__(self, first, others, stream):
-        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        try:
+            dev = self.dev = first.get_device()
+            for t in others:
+                if t is not None and t.get_device() != dev:
+                    raise TypeError("all tensors of a call must be on the same CUDA device")
+        except AttributeError:
+            raise TypeError("the operators take torch tensors") from None
+        if dev < 0 or not first.is_cuda:
             raise TypeError("the operators take CUDA tensors")
-        self.dev = first.get_device()
-        for t in others:
-            if t is not None and (not isinstance(t, torch.Tensor) or t.get_device() != self.dev):
-                raise TypeError("all tensors of a call must be on the same CUDA device")
         self.stream = None
         if stream is None:
-            self.handle = torch._C._cuda_getCurrentRawStream(self.dev)
+            self.handle = _raw_stream(dev)
         else:
             self.handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-            if self.handle != torch._C._cuda_getCurrentRawStream(self.dev):
+            if self.handle != _raw_stream(dev):
                 self.stream = (stream if hasattr(stream, "cuda_stream")
-                               else torch.cuda.ExternalStream(self.handle, device=self.dev))
+                               else torch.cuda.ExternalStream(self.handle, device=dev))
 
     def empty(self, shape, dtype):
         if self.stream is None:
@@ -141,15 +149,47 @@ class _Call:
         with torch.cuda.stream(self.stream):
             return torch.empty(shape, dtype=dtype, device=torch.device("cuda", self.dev))
 
+    def workspace(self, size):
+        """(tensor, address) of scratch memory for one call.  Calls of one
+        thread on one stream follow each other and share it; it grows to the
+        largest asked for.  A captured call gets memory of its own graph's."""
+        if self.stream is not None or torch.cuda.is_current_stream_capturing():
+            t = self.empty((size,), torch.uint8)
+            return t, t.data_ptr()
+        key = (self.dev, self.handle, threading.get_ident())
+        got = _workspaces.get(key)
+        if got is None or got[2] < size:
+            t = self.empty((size,), torch.uint8)
+            got = _workspaces[key] = (t, t.data_ptr(), size)
+        return got[0], got[1]
+
     def run(self, name, *args):
-        fn = _load()[name]
-        if self.dev == torch._C._cuda_getDevice():
+        fn = (_fns or _load())[name]
+        if self.dev == _current_device():
             code = fn(*args, self.handle)
         else:
             with torch.cuda.device(self.dev):
                 code = fn(*args, self.handle)
         if code:
             _lopt._check(name, code)
+
+
+_workspaces = {}
+
+
+def release_workspaces() -> None:
+    """Give the operators' scratch memory back to torch's allocator."""
+    _workspaces.clear()
+
+
+@functools.lru_cache(maxsize=1024)
+def _size_of(name, *sizes):
+    """What a workspace function of the library says for these sizes."""
+    need = ctypes.c_int64()
+    code = _load()[name](*sizes, need)
+    if code:
+        _lopt._check(name, code)
+    return need.value
 
 
 _status = {}
@@ -171,16 +211,18 @@ def _status_ptr(dev):
 
 def check_indices(device: Optional[int] = None) -> None:
     """Wait for the device and raise LoptError (LOPT_E_INDEX) if an index of
-    any call since the last check was at or above its limit."""
+    any call since the last check was at or above its limit (or
+    LOPT_E_TIMEOUT if a kernel's bounded wait ran out)."""
     dev = torch.cuda.current_device() if device is None else torch.device("cuda", device).index
     t = _status.get(dev)
     if t is None:
         return
     torch.cuda.synchronize(dev)
-    if int(t.item()):
+    flags = int(t.item())
+    if flags:
         t.zero_()
         torch.cuda.synchronize(dev)
-        _lopt._check("check_indices", E_INDEX)
+        _lopt._check("check_indices", _E_TIMEOUT if flags & 2 else E_INDEX)
 
 
 # ---- embedding ------------------------------------------------------------------
@@ -223,13 +265,10 @@ def embedding_backward(grad_out, index, rows: int, scale: float = 1.0, *, out=No
             raise ValueError("accumulate needs out")
         out = c.empty((rows, cols), torch.float32)
     ptr = _vector(out, rows * cols, "out")
-    need = ctypes.c_int64()
-    code = _load()["lopt_embed_workspace"](n, rows, cols, need)
-    if code:
-        _lopt._check("lopt_embed_workspace", code)
-    ws = c.empty((need.value,), torch.uint8)
+    need = _size_of("lopt_embed_workspace", n, rows, cols)
+    ws, ws_ptr = c.workspace(need)
     c.run("lopt_embed_backward", grad_out.data_ptr(), _type(grad_out, "grad_out"), gs, index.data_ptr(), kind, n, rows,
-          cols, scale, 1 if accumulate else 0, ptr, ws.data_ptr(), need.value, _status_ptr(c.dev))
+          cols, scale, 1 if accumulate else 0, ptr, ws_ptr, need, _status_ptr(c.dev))
     return out
 
 
@@ -306,15 +345,12 @@ def layernorm_backward(grad_out, x, mean, rstd, weight, *, grad_residual=None, n
         grad_bias = None
     elif grad_bias is None:
         grad_bias = c.empty((cols,), torch.float32)
-    need = ctypes.c_int64()
-    code = _load()["lopt_layernorm_workspace"](rows, cols, need)
-    if code:
-        _lopt._check("lopt_layernorm_workspace", code)
-    ws = c.empty((need.value,), torch.uint8)
+    need = _size_of("lopt_layernorm_workspace", rows, cols)
+    ws, ws_ptr = c.workspace(need)
     c.run("lopt_layernorm_backward", grad_out.data_ptr(), kind, rows, cols, ds, xp, xs, _vector(mean, rows, "mean"),
           _vector(rstd, rows, "rstd"), w, wt, r, rs, gx, gs, _vector(grad_weight, cols, "grad_weight"),
-          0 if grad_bias is None else _vector(grad_bias, cols, "grad_bias"), 1 if accumulate else 0, ws.data_ptr(),
-          need.value)
+          0 if grad_bias is None else _vector(grad_bias, cols, "grad_bias"), 1 if accumulate else 0, ws_ptr,
+          need)
     return grad_x, grad_weight, grad_bias
 
 
@@ -353,8 +389,8 @@ def distill_forward(logits, top_logits, top_index, temperature: float = 1.0, *, 
 
     logits: [..., classes]; top_logits, top_index: [..., top], top <= 1024;
     slots with a negative index or a logit of -inf do not count.  A row of
-    weight 0, or without slots that count, has loss 0 and is not read.  With
-    one slot per row it is the cross entropy with that class."""
+    weight 0, or without slots that count, has loss 0 whatever its logits
+    hold.  With one slot per row it is the cross entropy with that class."""
     return _distill(logits, top_logits, top_index, temperature, row_weight, loss, None, False, stream)[0]
 
 
