@@ -368,8 +368,72 @@ __device__ __forceinline__ float top_logit(const Distill& a, uint32_t raw) {
   }
 }
 
-template <typename T, bool GRAD>
-__device__ __forceinline__ void make_list(const Distill& a, const Slice<T>& r, int64_t row, bool report, ListAhead x, List& l) {
+// Where a list's slots come from: slot k, the u-th of four, as loaded.
+// From registers (the first 128 slots), the rest from memory ...
+template <typename T> struct FromRegs {
+  const Distill& a;
+  int64_t row;
+  ListAhead x;
+  __device__ __forceinline__ void block(int k0) {
+    if (k0 > 0) load_list<T>(a, row, k0, x);
+  }
+  __device__ __forceinline__ int64_t id(int k, int u) const { return x.id[u]; }
+  __device__ __forceinline__ float t(int k, int u) const { return top_logit<T>(a, x.t[u]); }
+};
+// ... or from shared memory, where asynchronous copies put them a row ahead
+// (a lane's slots by the lane itself: no other thread waits for them).  16-bit
+// logits are too narrow for such copies and wait in registers, the first 128.
+template <typename T> struct FromShared {
+  const Distill& a;
+  char* ids;       // [top] of the index type
+  float* logits;   // [top] if float32
+  uint32_t raw[4];
+  int64_t row;
+  __device__ __forceinline__ FromShared(const Distill& a_, void* at) : a(a_), ids(static_cast<char*>(at)), row(0) {
+    logits = reinterpret_cast<float*>(ids + (size_t)a.top * (a.itype == LOPT_I32 ? 4 : 8));
+  }
+  static __device__ __forceinline__ uint32_t addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+  __device__ __forceinline__ void fetch(int64_t row_) {
+    row = row_;
+    const int lane = threadIdx.x % 32;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");   // a list that no one wanted may still be landing here
+    for (int k = lane; k < a.top; k += 32) {
+      if (a.itype == LOPT_I32)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;"
+                     :: "r"(addr(ids + k * 4)), "l"(static_cast<const int32_t*>(a.top_index) + row * a.is + k) : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;"
+                     :: "r"(addr(ids + k * 8)), "l"(static_cast<const int64_t*>(a.top_index) + row * a.is + k) : "memory");
+      if (a.ttype == LOPT_F32)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;"
+                     :: "r"(addr(logits + k)), "l"(static_cast<const float*>(a.top_logits) + row * a.ts + k) : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (a.ttype != LOPT_F32) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        raw[u] = u * 32 + lane < a.top ? static_cast<const uint16_t*>(a.top_logits)[row * a.ts + u * 32 + lane] : 0;
+    }
+  }
+  __device__ __forceinline__ void block(int k0) {
+    if (k0 == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  }
+  __device__ __forceinline__ int64_t id(int k, int u) const {
+    if (k >= a.top) return -1;
+    return a.itype == LOPT_I32 ? (int64_t)reinterpret_cast<const int32_t*>(ids)[k] : reinterpret_cast<const int64_t*>(ids)[k];
+  }
+  __device__ __forceinline__ float t(int k, int u) const {
+    if (k >= a.top) return 0.f;
+    if (a.ttype == LOPT_F32) return logits[k];
+    return k < 128 ? top_logit<T>(a, raw[u]) : load_as_f(a.top_logits, row * a.ts + k, a.ttype);
+  }
+};
+inline int64_t shared_list_bytes(const Distill& a) {   // a multiple of 8
+  return ((int64_t)a.top * ((a.itype == LOPT_I32 ? 4 : 8) + (a.ttype == LOPT_F32 ? 4 : 0)) + 7) / 8 * 8;
+}
+
+template <typename T, bool GRAD, typename From>
+__device__ __forceinline__ void make_list(const Distill& a, const Slice<T>& r, bool report, From& from, List& l) {
   const int lane = threadIdx.x % 32, size = 1 << l.log_size;
   if (GRAD) {
     for (int h = lane; h < size; h += 32) {
@@ -380,15 +444,16 @@ __device__ __forceinline__ void make_list(const Distill& a, const Slice<T>& r, i
   float tmax = -INFINITY;
   bool any = false, bad = false;
   LOPT_LIST_SLOTS(k0, l.top) {
-    if (k0 > 0) load_list<T>(a, row, k0, x);
+    from.block(k0);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int k = k0 + u * 32 + lane;
-      const float t = top_logit<T>(a, x.t[u]);
-      bad |= x.id[u] >= a.cols;
-      const bool counts = x.id[u] >= 0 && x.id[u] < a.cols && t != -INFINITY;
+      const float t = from.t(k, u);
+      const int64_t i = from.id(k, u);
+      bad |= i >= a.cols;
+      const bool counts = i >= 0 && i < a.cols && t != -INFINITY;
       if (k < l.top) {
-        l.id[k] = counts ? (int32_t)x.id[u] : -1;
+        l.id[k] = counts ? (int32_t)i : -1;
         l.e[k] = t;
       }
       if (counts) tmax = fmaxf(tmax, t);
@@ -479,16 +544,19 @@ template <int U> struct SlotRegs {
   float inv, p_log_p;
   bool any;
 };
-template <typename T, int U>
-__device__ __forceinline__ void make_slots(const Distill& a, const ListAhead& x, bool report, SlotRegs<U>& l) {
+template <int U, typename From>
+__device__ __forceinline__ void make_slots(const Distill& a, From& from, bool report, SlotRegs<U>& l) {
+  from.block(0);
   float tmax = -INFINITY;
   bool any = false, bad = false;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    l.e[u] = top_logit<T>(a, x.t[u]);
-    bad |= x.id[u] >= a.cols;
-    const bool counts = x.id[u] >= 0 && x.id[u] < a.cols && l.e[u] != -INFINITY;
-    l.id[u] = counts ? (int32_t)x.id[u] : -1;
+    const int k = u * 32 + (int)(threadIdx.x % 32);
+    l.e[u] = from.t(k, u);
+    const int64_t i = from.id(k, u);
+    bad |= i >= a.cols;
+    const bool counts = i >= 0 && i < a.cols && l.e[u] != -INFINITY;
+    l.id[u] = counts ? (int32_t)i : -1;
     if (counts) tmax = fmaxf(tmax, l.e[u]);
     any |= counts;
   }
@@ -553,8 +621,9 @@ __global__ void __launch_bounds__(32 * kWarpRows, 8) k_distill_warp(const Distil
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int64_t row = (int64_t)blockIdx.x * kWarpRows + warp;
   if (row >= a.rows) return;
-  ListAhead x;
-  load_list<T>(a, row, 0, x);
+  FromRegs<T> from{a, row, {}};
+  load_list<T>(a, row, 0, from.x);
+  const ListAhead& x = from.x;
   const Slice<T> r(a, row, 0, 0);
   uint32_t v[NV][4];
 #pragma unroll
@@ -598,7 +667,7 @@ __global__ void __launch_bounds__(32 * kWarpRows, 8) k_distill_warp(const Distil
   };
   if (a.top <= 32) {   // a slot in each lane
     SlotRegs<1> l;
-    make_slots<T>(a, x, w != 0.f, l);
+    make_slots(a, from, w != 0.f, l);
     l.z[0] = z[0];
     const bool any = w != 0.f && l.any;
     if (!finish(any, l.p_log_p, warp_sum(sum_slots(r, l, m)))) return;
@@ -620,7 +689,7 @@ __global__ void __launch_bounds__(32 * kWarpRows, 8) k_distill_warp(const Distil
   }
   List l(words + warp * list_words(a.top), a.top);
   if (w != 0.f) {
-    make_list<T, GRAD>(a, r, row, true, x, l);
+    make_list<T, GRAD>(a, r, true, from, l);
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       if (u * 32 + lane < l.top) l.z[u * 32 + lane] = z[u];
@@ -680,7 +749,7 @@ __device__ __forceinline__ void join_pairs(const float2* got, int n, float c, fl
 // had then finished row e: with four sets in rotation no set is overwritten
 // while it is read.
 template <typename T, int TH, bool GRAD>
-__global__ void __launch_bounds__(TH + 32, 1024 / TH) k_distill_ring(const Distill a, const int log_c, const int slice_slots) {
+__global__ void __launch_bounds__(TH + 32, 1024 / TH) k_distill_ring(const Distill a, const int log_c, const int slice_slots, const int ahead_bytes) {
   constexpr int GW = TH / 32, U = 4, SETS = 4;
   extern __shared__ __align__(128) unsigned char sm[];
   uint4* buf = reinterpret_cast<uint4*>(sm);
@@ -715,7 +784,8 @@ __global__ void __launch_bounds__(TH + 32, 1024 / TH) k_distill_ring(const Disti
   const float c = a.log2e_t;
 
   if (gw == GW) {   // the warp that works ahead
-    List l(reinterpret_cast<int32_t*>(sm + (size_t)slice_slots * 16), a.top);
+    FromShared<T> from(a, sm + (size_t)slice_slots * 16);
+    List l(reinterpret_cast<int32_t*>(sm + (size_t)slice_slots * 16 + ahead_bytes), a.top);
     // The whole slots of a row's slice, when all lanes are done with the last one's.
     auto fetch = [&](const Slice<T>& n) {
       __syncwarp();
@@ -727,12 +797,11 @@ __global__ void __launch_bounds__(TH + 32, 1024 / TH) k_distill_ring(const Disti
       }
       __syncwarp();
     };
-    ListAhead x;
     SlotRegs<4> lr;
     const bool regs = !GRAD && a.top <= 128;
-    auto list = [&](const Slice<T>& n, int64_t at, int par) {
-      if (regs) make_slots<T>(a, x, rank == 0, lr);
-      else make_list<T, GRAD>(a, n, at, rank == 0, x, l);
+    auto list = [&](const Slice<T>& n, int par) {
+      if (regs) make_slots(a, from, rank == 0, lr);
+      else make_list<T, GRAD>(a, n, rank == 0, from, l);
       if (lane == 0) {
         any[par] = regs ? lr.any : l.any;
         mbar_arrive(&listed);
@@ -743,13 +812,13 @@ __global__ void __launch_bounds__(TH + 32, 1024 / TH) k_distill_ring(const Disti
       if (regs) read_slots<T, decltype(whole)::value>(n, buf, lr);
       else read_listed<T, decltype(whole)::value>(n, buf, l);
     };
-    load_list<T>(a, row, 0, x);
+    from.fetch(row);
     Slice<T> r(a, row, rank, log_c);
     if (w != 0.f) {
       fetch(r);
-      list(r, row, 0);
+      list(r, 0);
     }
-    if (row + clusters < a.rows) load_list<T>(a, row + clusters, 0, x);
+    if (row + clusters < a.rows) from.fetch(row + clusters);
     for (int par = 0; row < a.rows; par ^= 1) {
       const int64_t next = row + clusters;
       const float w_next = weight(next);
@@ -796,8 +865,8 @@ __global__ void __launch_bounds__(TH + 32, 1024 / TH) k_distill_ring(const Disti
         if (w_next != 0.f) fetch(r_next);
         if (rank == 0 && lane == 0) a.loss[row] = 0.f;
       }
-      if (w_next != 0.f) list(r_next, next, par ^ 1);
-      if (next + clusters < a.rows) load_list<T>(a, next + clusters, 0, x);
+      if (w_next != 0.f) list(r_next, par ^ 1);
+      if (next + clusters < a.rows) from.fetch(next + clusters);
       r = r_next;
       row = next;
       w = w_next;
@@ -981,7 +1050,7 @@ cudaError_t ring_as(const Distill& a, int log_c, int slice_slots, size_t smem, i
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem);
   if (e != cudaSuccess) return e;
   const int64_t clusters = std::min<int64_t>(a.rows, blocks >> log_c);
-  return launch(k, dim3((unsigned)(clusters << log_c)), dim3(TH + 32), smem, s, false, 1 << log_c, a, log_c, slice_slots);
+  return launch(k, dim3((unsigned)(clusters << log_c)), dim3(TH + 32), smem, s, false, 1 << log_c, a, log_c, slice_slots, (int)shared_list_bytes(a));
 }
 
 template <typename T>
@@ -1003,8 +1072,8 @@ cudaError_t distill_rows(const Distill& a, int sms, cudaStream_t s) {
   // of 256 threads per SM while a cluster can hold the row so, else two of
   // 512, else one.  (8192 x 50257 bf16: 286 us with four blocks, two to a
   // row; 293 with two blocks, one to a row.)
-  constexpr int64_t kFour = 54528, kTwo = 107 * 1024, kOne = 216 * 1024;
-  const int64_t list_bytes = (int64_t)list_words(a.top) * 4;
+  constexpr int64_t kFour = 54912, kTwo = 107 * 1024, kOne = 216 * 1024;
+  const int64_t list_bytes = (int64_t)list_words(a.top) * 4 + shared_list_bytes(a);
   auto bytes = [&](int lc) { return ceil(slots, 1 << lc) * 16 + list_bytes; };
   int lc = 0;   // log2 of the blocks per row
   while (1 << lc < kMaxCluster && bytes(lc) > kFour) ++lc;
