@@ -74,13 +74,15 @@ __global__ void __launch_bounds__(256) k_embed_fwd(const EmbedFwd a) {
 // Of 2^log_blocks blocks, the cluster v mod 2^(log_blocks - 3) and in it the
 // block (v / 2^(log_blocks - 3)) mod 8 own the id v, at most 1024 ids a block:
 // ids are given out by frequency in most vocabularies, and so the common ones
-// (each of which keeps its block busy) fall to different clusters.  In the sorted list the blocks follow each other, in a block its
-// ids ascend, and an id's positions ascend.
+// (each of which keeps its block busy) fall to different clusters.  In the
+// sorted list the blocks follow each other, in a block its ids ascend, and an
+// id's positions ascend.
 //
-// The eight blocks of a cluster read the index list together, an eighth each
-// (every block reading all of it took 22 us for 65,536 ids, most of them L2
-// traffic) and keep what belongs to the cluster, in list order; each block
-// then picks its own entries from the cluster's eight lists.
+// The eight blocks of a cluster read the index list together, an eighth each,
+// and keep what belongs to the cluster, in list order; each block then picks
+// its own entries from the cluster's eight lists.  Bound by the chain of those
+// steps: 12 us for 65,536 ids, 9 for 4,099 (every block reading the whole list
+// took 22 us for 65,536, most of it L2 traffic).
 constexpr int kMinLogBlocks = 7;        // 128 blocks
 constexpr int kLogIds = 10;             // ids per block: at most 1024, 128 KB of counters
 constexpr int kLogCluster = 3, kCluster = 1 << kLogCluster;
@@ -355,9 +357,10 @@ __device__ __forceinline__ int place_of(const EmbedSum& a, int v) {
 }
 
 // Zeros into the rows without tokens among the kZeroRows from b * kZeroRows
-// on, a warp per row; streaming stores, since no one reads zeros soon (4099
-// tokens, 50257 x 768: 33.1 us, 37.1 with plain stores; bulk stores from
-// shared memory 35.7).
+// on, a warp per row; streaming stores, since no one reads zeros soon (the
+// whole gradient of 4,099 tokens, 50,257 x 768: 32.3 us, of which a plain fill
+// of as many bytes takes 25; 4 us more with plain stores, 2.6 with bulk stores
+// from shared memory).
 __device__ __forceinline__ void zero_rows(const EmbedSum& a, int b) {
   const int lane = threadIdx.x % 32, warps = blockDim.x / 32;
   wait_for_previous();
@@ -375,8 +378,11 @@ __device__ __forceinline__ void zero_rows(const EmbedSum& a, int b) {
   }
 }
 
+// 80 registers, for eight rows' loads side by side: 24 warps per SM take 122 us
+// for 65,536 tokens of 2048 bfloat16 into 50,304 rows (726 MB, 5.95 TB/s), 32
+// warps with 64 registers 134, 16 warps 134, 40 warps 162.
 template <typename T, int VEC>
-__global__ void __launch_bounds__(256, 4) k_embed_sum(const EmbedSum a) {
+__global__ void __launch_bounds__(256, 3) k_embed_sum(const EmbedSum a) {
   __shared__ int32_t ord[kMaxChunk], key[kMaxChunk + 2];   // key[0]: before the chunk, key[len + 1]: after it
   __shared__ int32_t last_flag;
   // Blocks of the two kinds alternate evenly over the grid.

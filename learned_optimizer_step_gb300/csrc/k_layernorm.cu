@@ -35,12 +35,14 @@ struct NormBwd {
   int wtype;
 };
 
-// Sum over the L threads of a row that are a whole block (L > 32), or a warp.
+// Sum over the L threads of a row that are a whole block (L > 32), a warp or
+// half of one.
 template <int L>
 __device__ __forceinline__ float row_sum(float v, float* red) {
-  v = warp_sum(v);
-  if (L == 32) return v;
-  constexpr int W = L / 32;
+#pragma unroll
+  for (int o = (L < 32 ? L : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (L <= 32) return v;
+  constexpr int W = L <= 32 ? 1 : L / 32;
   __syncthreads();                      // the previous use of red is over
   if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
   __syncthreads();
@@ -55,10 +57,10 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
 template <int L>
 __device__ __forceinline__ float2 group_sum2(float2 v, float2* red, int group) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+  for (int o = (L < 32 ? L : 32) / 2; o > 0; o >>= 1)
     v = __fadd2_rn(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
-  if (L == 32) return v;
-  constexpr int W = L / 32;
+  if (L <= 32) return v;
+  constexpr int W = L <= 32 ? 1 : L / 32;
   red += group * W;
   if (threadIdx.x % 32 == 0) red[threadIdx.x % L / 32] = v;
   asm volatile("bar.sync %0, %1;" :: "r"(1 + group), "n"(L) : "memory");
@@ -140,30 +142,35 @@ template <int V> __device__ __forceinline__ float sum_of(const float (&x)[V]) {
   }
 }
 
-__host__ __device__ constexpr int fwd_threads(int L) { return L == 32 ? 128 : L; }
+__host__ __device__ constexpr int fwd_threads(int L) { return L <= 32 ? 128 : L; }
 
-// L threads per row, each with SLOTS accesses of VEC elements.  Small blocks,
-// 32 warps per SM: with 16,421 rows of 768 a persistent form with the next
-// row's loads ahead takes 23.1 us, since its few rows per warp do not come
-// out even, this one 21.6.
-template <typename T, int VEC, int SLOTS, int L>
+// L threads per row, each with SLOTS accesses of VEC elements.  Bound by HBM
+// bytes: 33.5M float32 elements with a residual take 84.6 us at any width from
+// 64 to 2048 (6.3 TB/s, what an elementwise sum of three such arrays takes);
+// 16,421 rows of 768 bfloat16 with a residual 21.0 us (4.8 TB/s: launch, first
+// loads and last stores are a sixth of it).  Small blocks that take one row
+// and end: a persistent form with the next row's loads ahead took 23.1 us
+// there, since its few rows per warp do not come out even.
+template <typename T, int VEC, int SLOTS, int L, bool RES>
 __global__ void __launch_bounds__(fwd_threads(L), 1024 / fwd_threads(L)) k_norm_fwd(const NormFwd a) {
   constexpr int TH = fwd_threads(L), R = TH / L;
-  __shared__ float red[L / 32];
+  __shared__ float red[L <= 32 ? 1 : L / 32];
   const int lane = threadIdx.x % L;
   const int cols = (int)a.cols;
   const float inv = 1.f / (float)cols;
-  const int64_t row = (int64_t)blockIdx.x * R + threadIdx.x / L;
-  if (row >= a.rows) return;            // whole warps when L == 32, else never
+  int64_t row = (int64_t)blockIdx.x * R + threadIdx.x / L;
+  const bool live = row < a.rows;
+  if (L >= 32 && !live) return;         // whole warps when L == 32, else never
+  if (!live) row = a.rows - 1;          // half a warp: reads, and writes nothing
   const T* x = static_cast<const T*>(a.x) + row * a.xs;
-  const T* r = static_cast<const T*>(a.residual) + row * a.rs;
+  const T* r = RES ? static_cast<const T*>(a.residual) + row * a.rs : nullptr;
   Pack<T, VEC> px[SLOTS], pr[SLOTS];
 #pragma unroll
   for (int s = 0; s < SLOTS; ++s) {
     const int j = (s * L + lane) * VEC;
     if (j >= cols) continue;
     px[s] = *reinterpret_cast<const Pack<T, VEC>*>(x + j);
-    if (a.residual) pr[s] = *reinterpret_cast<const Pack<T, VEC>*>(r + j);
+    if (RES) pr[s] = *reinterpret_cast<const Pack<T, VEC>*>(r + j);
   }
   {
     float v[SLOTS][VEC], sum[VEC];
@@ -172,14 +179,14 @@ __global__ void __launch_bounds__(fwd_threads(L), 1024 / fwd_threads(L)) k_norm_
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
       to_floats(px[s], v[s]);
-      if (a.residual) {
+      if (RES) {
         float t[VEC];
         to_floats(pr[s], t);
         add_to(t, v[s]);
       }
       if ((s * L + lane) * VEC < cols) add_to(v[s], sum);
     }
-    if (a.summed) {
+    if (RES && a.summed && live) {
       T* sm = static_cast<T*>(a.summed) + row * a.ss;
 #pragma unroll
       for (int s = 0; s < SLOTS; ++s) {
@@ -196,10 +203,11 @@ __global__ void __launch_bounds__(fwd_threads(L), 1024 / fwd_threads(L)) k_norm_
       if ((s * L + lane) * VEC < cols) fma_to(v[s], v[s], sum);
     }
     const float rstd = rsqrtf(row_sum<L>(sum_of(sum), red) * inv + a.eps);
-    if (lane == 0) {
+    if (lane == 0 && live) {
       a.mean[row] = mean;
       a.rstd[row] = rstd;
     }
+    if (!live) return;
     T* y = static_cast<T*>(a.y) + row * a.ys;
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
@@ -255,16 +263,25 @@ __global__ void __launch_bounds__(512) k_norm_fwd_long(const NormFwd a) {
 }
 
 // Threads of a backward block, of which an SM takes one: 24 warps of lanes
-// with 8 elements, else 16 (128 registers).
+// with 8 elements of 16 bits (80 registers) where rows take 32 to 256 threads,
+// else 16 warps (128 registers): with 64 or 80 registers the others spill
+// (bfloat16 with a residual gradient, 8,192 rows of 4096: 74 us with one group
+// of 512 threads, 107 with two; 524,288 rows of 64: 130 us with 16 warps, 197
+// with 24).
 __host__ __device__ constexpr int bwd_threads(int E, int L, int es) {
-  return L == 1024 || (E <= 8 && es == 2 && L == 512) ? 1024 : E <= 8 && es == 2 ? 768 : 512;
+  return L == 1024 ? 1024 : L % 96 == 0 ? (es == 2 ? 768 : 480) : E <= 8 && es == 2 && L >= 32 && L <= 256 ? 768 : 512;
 }
 
 // Persistent: a block's groups of L threads take rows blockIdx.x * R + group,
 // striding by gridDim.x * R, and keep the column sums of their columns.  With
 // AHEAD, the next row's x and dy are loaded before the current row is reduced;
 // with KEEP, xhat and g stay in registers over the reduction, else they are
-// made again.
+// made again.  32,768 rows of 2048 bfloat16 with a residual gradient: 98 us
+// (5.5 TB/s; 85 us is what an elementwise operation on as many arrays takes).
+// Not the loads bound it but a row's chain of sum, barrier and store: rows
+// copied to shared memory five ahead 104 to 108 us, pairs of elements per
+// instruction 106 to 113 (fewer instructions, more conversions between pairs),
+// two groups with all weights in registers 111, 16 elements a thread 118.
 template <typename T, int VEC, int SLOTS, int L, bool AHEAD, bool KEEP>
 __global__ void __launch_bounds__(bwd_threads(VEC * SLOTS, L, sizeof(T)), 1) k_norm_bwd(const NormBwd a) {
   constexpr int E = VEC * SLOTS, TH = bwd_threads(E, L, sizeof(T)), R = TH / L, W = L * E;
@@ -285,7 +302,16 @@ __global__ void __launch_bounds__(bwd_threads(VEC * SLOTS, L, sizeof(T)), 1) k_n
     for (int k = 0; k < VEC; ++k) dw[s][k] = db[s][k] = 0.f;
   P px[SLOTS], pd[SLOTS];
   float mean = 0.f, rstd = 0.f;
+  // A warp that holds two rows goes on while the first is one: the other's
+  // lanes then see a row of zeros and write nothing.
+  const int second = L < 32 ? group % 2 : 0;
   auto load = [&](int64_t r, P (&x)[SLOTS], P (&d)[SLOTS], float& m, float& rs) {
+    if (L < 32 && r >= a.rows) {
+      m = rs = 0.f;
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s) x[s] = d[s] = P{};
+      return;
+    }
     const T* xp = static_cast<const T*>(a.x) + r * a.xs + lane * VEC;
     const T* dp = static_cast<const T*>(a.dy) + r * a.dys + lane * VEC;
     m = a.mean[r];
@@ -298,10 +324,11 @@ __global__ void __launch_bounds__(bwd_threads(VEC * SLOTS, L, sizeof(T)), 1) k_n
     }
   };
   int64_t row = (int64_t)blockIdx.x * R + group;
-  if (row < a.rows) load(row, px, pd, mean, rstd);
-  for (int par = 0; row < a.rows; row += stride, par ^= 1) {
+  if (row - second < a.rows) load(row, px, pd, mean, rstd);
+  for (int par = 0; row - second < a.rows; row += stride, par ^= 1) {
+    const bool live = L >= 32 || row < a.rows;
     P pr[SLOTS];
-    if (res) {
+    if (res && live) {
       const T* rp = static_cast<const T*>(a.dres) + row * a.drs + lane * VEC;
 #pragma unroll
       for (int s = 0; s < SLOTS; ++s)
@@ -309,7 +336,7 @@ __global__ void __launch_bounds__(bwd_threads(VEC * SLOTS, L, sizeof(T)), 1) k_n
     }
     P nx[SLOTS], nd[SLOTS];
     float nmean = 0.f, nrstd = 0.f;
-    if (AHEAD && row + stride < a.rows) load(row + stride, nx, nd, nmean, nrstd);
+    if (AHEAD && row - second + stride < a.rows) load(row + stride, nx, nd, nmean, nrstd);
     float kx[SLOTS][VEC], kg[SLOTS][VEC];
     auto make = [&](int s, float (&d)[VEC]) {
       float w[VEC];
@@ -341,7 +368,7 @@ __global__ void __launch_bounds__(bwd_threads(VEC * SLOTS, L, sizeof(T)), 1) k_n
     T* op = static_cast<T*>(a.dx) + row * a.dxs + lane * VEC;
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
-      if (!in(s)) continue;
+      if (!in(s) || !live) continue;
       float o[VEC];
       if (!KEEP) make(s, o);
 #pragma unroll
@@ -362,7 +389,7 @@ __global__ void __launch_bounds__(bwd_threads(VEC * SLOTS, L, sizeof(T)), 1) k_n
       }
       mean = nmean;
       rstd = nrstd;
-    } else if (row + stride < a.rows) {
+    } else if (row - second + stride < a.rows) {
       load(row + stride, px, pd, mean, rstd);
     }
   }
@@ -479,7 +506,8 @@ template <typename T, int VEC, int SLOTS, int L>
 cudaError_t fwd_as(const NormFwd& a, cudaStream_t s) {
   constexpr int R = fwd_threads(L) / L;
   const int64_t grid = (a.rows + R - 1) / R;
-  return launch(k_norm_fwd<T, VEC, SLOTS, L>, dim3((unsigned)grid), dim3(fwd_threads(L)), 0, s, false, 1, a);
+  return launch(a.residual ? k_norm_fwd<T, VEC, SLOTS, L, true> : k_norm_fwd<T, VEC, SLOTS, L, false>, dim3((unsigned)grid),
+                dim3(fwd_threads(L)), 0, s, false, 1, a);
 }
 
 template <typename T, int VEC, int SLOTS, int L>
@@ -494,24 +522,38 @@ cudaError_t bwd_as(const NormBwd& a, int sms, cudaStream_t s, int* blocks) {
   return launch(k, dim3((unsigned)*blocks), dim3(TH), smem, s, false, 1, a);
 }
 
-// Threads and slots for rows of nvec accesses of VEC elements: a warp per row
-// while a lane holds at most 24 elements, then groups with 16 (8 in float32)
-// elements a thread, up to 512 threads with 32 elements each; longer rows are
-// read again.
+// Threads and slots for rows of nvec accesses of VEC elements: half a warp
+// for the shortest, then as few threads as keep 8 elements each (the forward
+// direction in 16 bits: a warp up to 24), up to 1024 threads; then 512 threads
+// with 32 elements each; longer rows are read again.  33.5M elements with a
+// residual: rows of 128 bfloat16 forward 47.8 us by half warps, 74.4 by whole
+// ones; rows of 768 float32 forward 84.6 us by 96 threads, 117 by 256, backward
+// in bfloat16 62 by 96, 69 by 128.
 #define LOPT_NORM_CASE(V, S, L_) if (nvec <= (int64_t)(S) * (L_)) return f.template run<V, S, L_>()
 template <int FULL, typename F>
 cudaError_t pick(int64_t cols, bool vec, F f) {
   if (vec) {
     const int64_t nvec = (cols + FULL - 1) / FULL;
     constexpr int B = 8 / FULL;   // slots of 8 elements
-    LOPT_NORM_CASE(FULL, 1, 32);
-    if constexpr (F::kForward) {
+    if constexpr (F::kForward && FULL == 8) {
+      LOPT_NORM_CASE(FULL, 1, 16);
+      LOPT_NORM_CASE(FULL, 1, 32);
       LOPT_NORM_CASE(FULL, 2, 32);
       LOPT_NORM_CASE(FULL, 3, 32);
       LOPT_NORM_CASE(FULL, 2, 64);
-    } else {
+    } else if constexpr (F::kForward) {
+      LOPT_NORM_CASE(FULL, 1, 16);
+      LOPT_NORM_CASE(FULL, 1, 32);
       LOPT_NORM_CASE(FULL, B, 32);
       LOPT_NORM_CASE(FULL, B, 64);
+      LOPT_NORM_CASE(FULL, B, 96);
+      LOPT_NORM_CASE(FULL, B, 128);
+    } else {
+      LOPT_NORM_CASE(FULL, 1, 16);
+      LOPT_NORM_CASE(FULL, 1, 32);
+      LOPT_NORM_CASE(FULL, B, 32);
+      LOPT_NORM_CASE(FULL, B, 64);
+      LOPT_NORM_CASE(FULL, B, 96);
       LOPT_NORM_CASE(FULL, B, 128);
     }
     LOPT_NORM_CASE(FULL, B, 256);
@@ -559,11 +601,10 @@ template <typename T> struct BwdRun {
 };
 
 // Vector accesses need whole vectors in a row and aligned rows.
-bool vec_ok(int64_t cols, int es, std::initializer_list<Span> ms, const void* w, const void* b, int wsize) {
+bool vec_ok(int64_t cols, int es, std::initializer_list<Span> ms, const void* w, const void* b) {
   if ((cols * es) % 16) return false;
   for (const Span& m : ms)
     if (!rows_aligned(m, 16)) return false;
-  (void)wsize;
   return (uintptr_t)w % 16 == 0 && (uintptr_t)b % 16 == 0;
 }
 
@@ -610,7 +651,7 @@ int lopt_layernorm_forward(const void* x, int type, int64_t rows, int64_t cols, 
   }
   const NormFwd a{x, residual, weight, bias, y, summed, mean, rstd, rows, cols, x_stride, residual_stride,
                   y_stride, summed_stride, weight_type, eps};
-  const bool vec = vec_ok(cols, es, {mx, mr, my, ms}, weight, bias, type_size(weight_type));
+  const bool vec = vec_ok(cols, es, {mx, mr, my, ms}, weight, bias);
   cudaStream_t s = (cudaStream_t)stream;
   switch (type) {
     case LOPT_F32: return done(pick<4>(cols, vec, FwdRun<float>{a, s}));
@@ -668,7 +709,7 @@ int lopt_layernorm_backward(const void* grad_out, int type, int64_t rows, int64_
   }
   const NormBwd a{grad_out, x, weight, grad_residual, mean, rstd, grad_x, (float*)workspace, rows, cols,
                   grad_out_stride, x_stride, grad_residual_stride, grad_x_stride, weight_type};
-  const bool vec = vec_ok(cols, es, {md, mx, mr, mo}, weight, nullptr, type_size(weight_type));
+  const bool vec = vec_ok(cols, es, {md, mx, mr, mo}, weight, nullptr);
   const int sms = sm_count();
   int blocks = 0;
   cudaError_t e;
