@@ -609,6 +609,25 @@ __device__ __forceinline__ void write_listed(const Slice<T>& r, const List& l, f
   }
 }
 
+// The same for a list of a slot in each lane.
+template <typename T>
+__device__ __forceinline__ void write_slots(const Slice<T>& r, const SlotRegs<1>& l, float c, float m, float f, float wt) {
+  const int lane = threadIdx.x % 32;
+  // By the first slot of a class, the repeats added in slot order.
+  const unsigned alike = __match_any_sync(0xffffffffu, l.id[0]);
+  float e = l.e[0];
+  if (__any_sync(0xffffffffu, l.id[0] >= 0 && alike != 1u << lane)) {
+    e = 0.f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const float ek = __shfl_sync(0xffffffffu, l.e[0], k);
+      if (alike >> k & 1) e += ek;
+    }
+  }
+  if (l.id[0] >= 0 && lane == __ffs(alike) - 1)
+    r.g[l.id[0]] = from_f<T>(fmaf(ex2((l.z[0] - m) * c), f, -wt * l.inv * e));
+}
+
 // ---- short rows: a warp per row ----------------------------------------------------
 // The row stays in registers, NV slots per lane.  Its loads go out before
 // its weight is known: a short row is a chain of latencies.
@@ -671,20 +690,7 @@ __global__ void __launch_bounds__(32 * kWarpRows, 8) k_distill_warp(const Distil
     l.z[0] = z[0];
     const bool any = w != 0.f && l.any;
     if (!finish(any, l.p_log_p, warp_sum(sum_slots(r, l, m)))) return;
-    // The listed classes again: by the first slot of a class, the repeats added
-    // in slot order.
-    const unsigned alike = __match_any_sync(0xffffffffu, l.id[0]);
-    float e = l.e[0];
-    if (__any_sync(0xffffffffu, l.id[0] >= 0 && alike != 1u << lane)) {
-      e = 0.f;
-#pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        const float ek = __shfl_sync(0xffffffffu, l.e[0], k);
-        if (alike >> k & 1) e += ek;
-      }
-    }
-    if (l.id[0] >= 0 && lane == __ffs(alike) - 1)
-      r.g[l.id[0]] = from_f<T>(fmaf(ex2((l.z[0] - m) * c), f, -wt * l.inv * e));
+    write_slots(r, l, c, m, f, wt);
     return;
   }
   List l(words + warp * list_words(a.top), a.top);
@@ -698,6 +704,87 @@ __global__ void __launch_bounds__(32 * kWarpRows, 8) k_distill_warp(const Distil
     __syncwarp();
   }
   if (finish(l.any, l.p_log_p, warp_sum(l.any ? sum_listed(r, l, m) : 0.f))) write_listed(r, l, c, m, f, wt);
+}
+
+// ---- rows of up to 16 KB: a block per row ---------------------------------------------
+// The row stays in registers, kBlockSlots slots per thread; the first warp has
+// the list.  A block takes one row and ends: the SM's other blocks run through
+// its waits.
+constexpr int kBlockSlots = 4, kBlockThreads = 256;
+
+template <typename T, bool GRAD>
+__global__ void __launch_bounds__(kBlockThreads, 4) k_distill_block(const Distill a) {
+  using S = Slots<T>;
+  constexpr int NV = kBlockSlots;
+  const int TH = blockDim.x, W = TH / 32;
+  extern __shared__ int32_t words[];
+  __shared__ float2 pairs[kBlockThreads / 32];   // (m, s) of the warps
+  __shared__ int any_slot;
+  const int t = threadIdx.x, lane = t % 32, warp = t / 32;
+  const int64_t row = blockIdx.x;
+  FromRegs<T> from{a, row, {}};
+  if (warp == 0) load_list<T>(a, row, 0, from.x);
+  const Slice<T> r(a, row, 0, 0);
+  uint32_t v[NV][4];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int q = i * TH + t;
+    uint4 y = make_uint4(S::kNegInf, S::kNegInf, S::kNegInf, S::kNegInf);
+    if (q < r.cnt) y = r.whole(q) ? r.z16()[q] : r.read_edge(q);
+    v[i][0] = y.x; v[i][1] = y.y; v[i][2] = y.z; v[i][3] = y.w;
+  }
+  const float w = a.row_weight ? a.row_weight[row] : 1.f;
+  const float c = a.log2e_t;
+  const bool slots = a.top <= 32;   // a slot in each lane
+  SlotRegs<1> lr;
+  List l(words, a.top);
+  if (warp == 0 && w != 0.f) {
+    if (slots) {
+      make_slots(a, from, true, lr);
+      if (lr.id[0] >= 0) lr.z[0] = to_f(r.z[lr.id[0]]);
+    } else {
+      make_list<T, GRAD>(a, r, true, from, l);
+      for (int k = lane; k < l.top; k += 32)
+        if (l.id[k] >= 0) l.z[k] = to_f(r.z[l.id[k]]);
+    }
+    if (lane == 0) any_slot = slots ? lr.any : l.any;
+  }
+  Partial<T> part;
+  part.template add<NV>(v, c);
+  float m = part.m, s = part.s;
+  join_warp(m, s, c);
+  if (lane == 0) pairs[warp] = make_float2(m, s);
+  __syncthreads();
+  if (w == 0.f || !any_slot) {   // nothing to learn from this row
+    if (t == 0) a.loss[row] = 0.f;
+    const uint32_t o[4] = {0, 0, 0, 0};
+    if (GRAD)
+      for (int q = t; q < r.cnt; q += TH) r.write(q, o);
+    return;
+  }
+  const float2 x = lane < W ? pairs[lane] : make_float2(-INFINITY, 0.f);
+  m = x.x;
+  s = x.y;
+  join_warp(m, s, c);
+  const float wt = w * a.temperature, f = wt / s;
+  if (warp == 0) {
+    const float pz = warp_sum(slots ? sum_slots(r, lr, m) : sum_listed(r, l, m));
+    if (lane == 0) a.loss[row] = wt * a.temperature * ((slots ? lr.p_log_p : l.p_log_p) - (pz * a.inv_t - logf(s)));
+  }
+  if (!GRAD) return;
+  const Dense<T> dense(m, c, f);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int q = i * TH + t;
+    if (q >= r.cnt) break;
+    uint32_t o[4];
+    dense.of(v[i], o);
+    r.write(q, o);
+  }
+  __syncthreads();
+  if (warp != 0) return;
+  if (slots) write_slots(r, lr, c, m, f, wt);
+  else write_listed(r, l, c, m, f, wt);
 }
 
 // The row's (m, s) from all its warps' pairs, by one warp, in a fixed order.
@@ -1044,6 +1131,13 @@ cudaError_t warp_as(const Distill& a, cudaStream_t s) {
   return launch(k_distill_warp<T, NV, false>, grid, block, smem, s, false, 1, a);
 }
 
+template <typename T>
+cudaError_t block_as(const Distill& a, int threads, cudaStream_t s) {
+  const size_t smem = a.top <= 32 ? 0 : (size_t)list_words(a.top) * 4;
+  return launch(a.grad ? k_distill_block<T, true> : k_distill_block<T, false>, dim3((unsigned)a.rows), dim3(threads), smem, s,
+                false, 1, a);
+}
+
 template <typename T, int TH, bool GRAD>
 cudaError_t ring_as(const Distill& a, int log_c, int slice_slots, size_t smem, int blocks, cudaStream_t s) {
   auto* k = &k_distill_ring<T, TH, GRAD>;
@@ -1068,20 +1162,27 @@ cudaError_t distill_rows(const Distill& a, int sms, cudaStream_t s) {
     if (slots <= 32 * 6) return warp_as<T, 6>(a, s);
     return warp_as<T, 8>(a, s);
   }
-  // Shared memory of a block: its slice of the row and the lists.  Four blocks
-  // of 256 threads per SM while a cluster can hold the row so, else two of
-  // 512, else one.  (8192 x 50257 bf16: 286 us with four blocks, two to a
-  // row; 293 with two blocks, one to a row.)
-  constexpr int64_t kFour = 54912, kTwo = 107 * 1024, kOne = 216 * 1024;
+  // Up to 16 KB.  (64M elements with gradient: rows of 4000 bfloat16 64 us,
+  // 132 by the persistent blocks; rows of 2000 float32 105, 244.  A little
+  // above it is the other way round, rows of 5003 float32 178 us with 512
+  // threads to a block, 119.)
+  if (slots <= kBlockSlots * kBlockThreads)
+    return block_as<T>(a, (int)std::max<int64_t>(ceil(slots, kBlockSlots * 32) * 32, 64), s);
+  // Shared memory of a block: its slice of the row and the lists.  The fewest
+  // blocks to a row of which three still fit an SM (64M float32 elements in
+  // rows of 131,072 with gradient: 131 us with slices of 64 KB so, 163 with two
+  // larger blocks per SM; rows of 32,000: 97 in two slices, 136 in four), or
+  // four where they do; else two blocks of 512 threads, else one.
+  constexpr int64_t kFour = 54912, kThree = 74368, kTwo = 107 * 1024, kOne = 216 * 1024;
   const int64_t list_bytes = (int64_t)list_words(a.top) * 4 + shared_list_bytes(a);
   auto bytes = [&](int lc) { return ceil(slots, 1 << lc) * 16 + list_bytes; };
   int lc = 0;   // log2 of the blocks per row
-  while (1 << lc < kMaxCluster && bytes(lc) > kFour) ++lc;
+  while (1 << lc < kMaxCluster && bytes(lc) > kThree) ++lc;
   if (bytes(lc) <= kOne) {
     // Few rows: more blocks for each, while a slice is 8 KB.
     while (1 << lc < kMaxCluster && (a.rows << lc) * 2 <= sms && ceil(slots, 2 << lc) >= 512) ++lc;
-    const bool small = bytes(lc) <= kFour;
-    const int per_sm = small ? 4 : bytes(lc) <= kTwo ? 2 : 1;
+    const bool small = bytes(lc) <= kThree;
+    const int per_sm = bytes(lc) <= kFour ? 4 : small ? 3 : bytes(lc) <= kTwo ? 2 : 1;
     const int slice = (int)ceil(slots, 1 << lc), blocks = sms * per_sm;
     const size_t smem = (size_t)bytes(lc);
     if (a.grad)
