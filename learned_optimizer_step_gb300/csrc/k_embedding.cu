@@ -81,8 +81,8 @@ __global__ void __launch_bounds__(256) k_embed_fwd(const EmbedFwd a) {
 // The eight blocks of a cluster read the index list together, an eighth each,
 // and keep what belongs to the cluster, in list order; each block then picks
 // its own entries from the cluster's eight lists.  Bound by the chain of those
-// steps: 12 us for 65,536 ids, 9 for 4,099 (every block reading the whole list
-// took 22 us for 65,536, most of it L2 traffic).
+// steps: 19 us for 65,536 ids, 8.5 for 4,099 (every block reading the whole
+// list took 22 us for 65,536, most of it L2 traffic).
 constexpr int kMinLogBlocks = 7;        // 128 blocks
 constexpr int kLogIds = 10;             // ids per block: at most 1024, 128 KB of counters
 constexpr int kLogCluster = 3, kCluster = 1 << kLogCluster;
@@ -378,9 +378,9 @@ __device__ __forceinline__ void zero_rows(const EmbedSum& a, int b) {
   }
 }
 
-// 80 registers, for eight rows' loads side by side: 24 warps per SM take 122 us
-// for 65,536 tokens of 2048 bfloat16 into 50,304 rows (726 MB, 5.95 TB/s), 32
-// warps with 64 registers 134, 16 warps 134, 40 warps 162.
+// 80 registers, for eight rows' loads side by side: 24 warps per SM take 114 us
+// for 65,536 tokens of 2048 bfloat16 into 50,304 rows (5.7 TB/s), 32 warps with
+// 64 registers 126, 16 warps 126, 40 warps 154.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256, 3) k_embed_sum(const EmbedSum a) {
   __shared__ int32_t ord[kMaxChunk], key[kMaxChunk + 2];   // key[0]: before the chunk, key[len + 1]: after it
