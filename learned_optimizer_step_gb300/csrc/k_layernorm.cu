@@ -175,9 +175,10 @@ __global__ void __launch_bounds__(fwd_threads(L), 1024 / fwd_threads(L)) k_norm_
     px[s] = *reinterpret_cast<const Pack<T, VEC>*>(x + j);
     if (RES) pr[s] = *reinterpret_cast<const Pack<T, VEC>*>(r + j);
   }
-  // The weights are wanted after two sums: the first blocks fetch them from HBM
-  // meanwhile (16 rows of 768 float32, all cold: 5.3 us, 5.9 without).
-  if (blockIdx.x < kFetchBlocks) {
+  // The weights are wanted after two sums: a small call fetches them from HBM
+  // meanwhile (16 rows of 768 float32, all cold: 5.3 us, 5.9 without; 16,421
+  // rows, had their first blocks fetched: 22.6 us, 21.1 without).
+  if (gridDim.x <= kFetchBlocks) {
     const size_t size = a.wtype == LOPT_F32 ? 4 : sizeof(T);
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
