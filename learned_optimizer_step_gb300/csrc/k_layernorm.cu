@@ -540,11 +540,16 @@ cudaError_t bwd_as(const NormBwd& a, int sms, cudaStream_t s, int* blocks) {
 
 // Threads and slots for rows of nvec accesses of VEC elements: half a warp
 // for the shortest, then as few threads as keep 8 elements each (the forward
-// direction in 16 bits: a warp up to 24), up to 1024 threads; then 512 threads
-// with 32 elements each; longer rows are read again.  33.5M elements with a
-// residual: rows of 128 bfloat16 forward 47.8 us by half warps, 74.4 by whole
-// ones; rows of 768 float32 forward 84.6 us by 96 threads, 117 by 256, backward
-// in bfloat16 62 by 96, 69 by 128.
+// direction in 16 bits: a warp up to 24), for wide rows 16 where that leaves an
+// SM several rows (forward, and backward in float32: in 16 bits its loads a row
+// ahead and xhat in registers count for more); then 512 threads with 32
+// elements each; longer rows are read again.  33.5M elements with a residual,
+// us: forward, rows of 128 bfloat16 by half warps 48, by warps 74; of 768
+// float32 by 96 threads 85, by 256 117; of 4512 by 384 threads with 16 elements
+// 60 bfloat16, 91 float32, by 1024 with 8 136, 158; backward, rows of 768
+// bfloat16 by 96 threads 62, by 128 69; of 3000 by 384 68, by 512 83; of 4512
+// by 768 threads with 8 elements 88, by 512 with 16 117 (float32: 137 with 16,
+// 178 with 8).
 #define LOPT_NORM_CASE(V, S, L_) if (nvec <= (int64_t)(S) * (L_)) return f.template run<V, S, L_>()
 template <int FULL, typename F>
 cudaError_t pick(int64_t cols, bool vec, F f) {
@@ -573,8 +578,20 @@ cudaError_t pick(int64_t cols, bool vec, F f) {
       LOPT_NORM_CASE(FULL, B, 128);
     }
     LOPT_NORM_CASE(FULL, B, 256);
-    LOPT_NORM_CASE(FULL, B, 512);
-    LOPT_NORM_CASE(FULL, B, 1024);
+    if constexpr (F::kForward) {
+      LOPT_NORM_CASE(FULL, 2 * B, 192);
+      LOPT_NORM_CASE(FULL, 2 * B, 256);
+      LOPT_NORM_CASE(FULL, 2 * B, 384);
+      LOPT_NORM_CASE(FULL, 2 * B, 512);
+    } else if constexpr (FULL == 8) {
+      LOPT_NORM_CASE(FULL, B, 384);
+      LOPT_NORM_CASE(FULL, B, 512);
+      LOPT_NORM_CASE(FULL, B, 768);
+      LOPT_NORM_CASE(FULL, B, 1024);
+    } else {
+      LOPT_NORM_CASE(FULL, 2 * B, 256);
+      LOPT_NORM_CASE(FULL, 2 * B, 512);
+    }
     LOPT_NORM_CASE(FULL, 4 * B, 512);
   } else {
     const int64_t nvec = cols;

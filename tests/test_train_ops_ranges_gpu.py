@@ -42,7 +42,7 @@ def test_embedding_backward_ranges(n, rows, cols):
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=ids)
 @pytest.mark.parametrize("rows,cols", [(1300, 64), (901, 256), (640, 1024), (500, 2048), (330, 4096), (321, 5001),
-                                       (310, 8200), (305, 2050), (40, 17000)])
+                                       (310, 8200), (305, 2050), (40, 17000), (160, 1032), (310, 2056), (170, 6000), (1001, 16)])
 def test_layernorm_many_rows(dtype, rows, cols):
     g = gen(rows * 7 + cols)
     x, w, b = norm_inputs(g, rows, cols, dtype, torch.float32)
