@@ -37,11 +37,13 @@ struct EmbedFwd {
 };
 
 // blockDim.x threads across the columns, blockIdx.y column blocks; a thread
-// takes U tokens, blockDim.y apart, with their loads side by side.
-template <typename TI, typename TO, int VEC, int U>
+// takes U tokens, blockDim.y apart, and of each of their rows C accesses,
+// blockDim.x apart, with all their loads side by side.
+template <typename TI, typename TO, int VEC, int U, int C>
 __global__ void __launch_bounds__(256) k_embed_fwd(const EmbedFwd a) {
   const int64_t i0 = (int64_t)blockIdx.x * (blockDim.y * U) + threadIdx.y;
-  const int64_t j = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * VEC;
+  const int64_t j = ((int64_t)blockIdx.y * (blockDim.x * C) + threadIdx.x) * VEC;
+  const int step = blockDim.x * VEC;
   if (j >= a.cols) return;
   int64_t id[U];
 #pragma unroll
@@ -49,24 +51,32 @@ __global__ void __launch_bounds__(256) k_embed_fwd(const EmbedFwd a) {
     const int64_t i = i0 + u * (int)blockDim.y;
     id[u] = i < a.n ? load_index(a.index, i, a.itype) : -1;
   }
-  Pack<TI, VEC> p[U];
+  Pack<TI, VEC> p[U][C];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (id[u] >= a.rows) {
       if (a.status && j == 0) atomicOr(a.status, kStatusIndex);
       id[u] = -1;
     }
-    if (id[u] >= 0) p[u] = *reinterpret_cast<const Pack<TI, VEC>*>(static_cast<const TI*>(a.table) + id[u] * a.ts + j);
+    const TI* row = static_cast<const TI*>(a.table) + id[u] * a.ts + j;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (id[u] >= 0 && j + c * step < a.cols) p[u][c] = *reinterpret_cast<const Pack<TI, VEC>*>(row + c * step);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t i = i0 + u * (int)blockDim.y;
     if (i >= a.n) break;
-    float v[VEC];
-    to_floats(p[u], v);
+    TO* to = static_cast<TO*>(a.out) + i * a.os + j;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) v[e] = id[u] >= 0 ? v[e] * a.scale : 0.f;
-    *reinterpret_cast<Pack<TO, VEC>*>(static_cast<TO*>(a.out) + i * a.os + j) = from_floats<TO, VEC>(v);
+    for (int c = 0; c < C; ++c) {
+      if (j + c * step >= a.cols) break;
+      float v[VEC];
+      to_floats(p[u][c], v);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[e] = id[u] >= 0 ? v[e] * a.scale : 0.f;
+      *reinterpret_cast<Pack<TO, VEC>*>(to + c * step) = from_floats<TO, VEC>(v);
+    }
   }
 }
 
@@ -523,21 +533,25 @@ Plan plan(int64_t n, int64_t rows, int64_t cols) {
   return p;
 }
 
-template <typename TI, typename TO>
-cudaError_t fwd_as(const EmbedFwd& a, int vec, int sms, cudaStream_t s) {
-  const int64_t nv = (a.cols + vec - 1) / vec;
+template <typename TI, typename TO, int VEC, int C>
+cudaError_t fwd_as(const EmbedFwd& a, int sms, cudaStream_t s) {
+  const int64_t nv = (a.cols + VEC * C - 1) / (VEC * C);
   const int tx = (int)std::min<int64_t>((nv + 31) / 32 * 32, 256);
   const int ty = std::max(1, 256 / tx);
   const unsigned gy = (unsigned)((nv + tx - 1) / tx);
   // Four tokens per thread once that still fills every SM's eight blocks.
   const bool many = a.n * gy >= (int64_t)sms * 8 * 4 * ty;
   const int64_t per = many ? 4 * ty : ty;
-  const dim3 grid((unsigned)((a.n + per - 1) / per), gy), block(tx, ty);
-  if (vec == 8)
-    return many ? launch(k_embed_fwd<TI, TO, 8, 4>, grid, block, 0, s, false, 1, a) : launch(k_embed_fwd<TI, TO, 8, 1>, grid, block, 0, s, false, 1, a);
-  if (vec == 4)
-    return many ? launch(k_embed_fwd<TI, TO, 4, 4>, grid, block, 0, s, false, 1, a) : launch(k_embed_fwd<TI, TO, 4, 1>, grid, block, 0, s, false, 1, a);
-  return many ? launch(k_embed_fwd<TI, TO, 1, 4>, grid, block, 0, s, false, 1, a) : launch(k_embed_fwd<TI, TO, 1, 1>, grid, block, 0, s, false, 1, a);
+  return launch(many ? k_embed_fwd<TI, TO, VEC, 4, C> : k_embed_fwd<TI, TO, VEC, 1, C>, dim3((unsigned)((a.n + per - 1) / per), gy),
+                dim3(tx, ty), 0, s, false, 1, a);
+}
+template <typename TI, typename TO>
+cudaError_t fwd_as(const EmbedFwd& a, int vec, int sms, cudaStream_t s) {
+  if constexpr (sizeof(TI) + sizeof(TO) < 8)
+    if (vec == 8) return fwd_as<TI, TO, 8, 1>(a, sms, s);
+  if (vec == 4) return fwd_as<TI, TO, 4, 1>(a, sms, s);
+  // Single elements, four of a row (33.5M elements, rows of 1001: 38 us; 62 with one).
+  return fwd_as<TI, TO, 1, 4>(a, sms, s);
 }
 
 template <typename TI>
@@ -587,9 +601,9 @@ int lopt_embed_forward(const void* table, int table_type, int64_t rows, int64_t 
   if ((rc = check_matrix(mt, false)) || (rc = check_matrix(mo, true)) || (rc = check_matrix(mi, false))) return rc;
   if (overlap(mo, mt) || overlap(mo, mi)) return LOPT_E_ALIAS;
   if (status && (uintptr_t)status % 4) return LOPT_E_ALIGN;
-  // 8 elements per thread when either side is 16-bit, 4 between fp32 sides.
-  int vec = ti == 4 && to == 4 ? 4 : 8;
-  if (cols % vec || !rows_aligned(mt, std::min(vec * ti, 32)) || !rows_aligned(mo, std::min(vec * to, 32))) vec = 1;
+  // 8 elements per thread when either side is 16-bit, else 4, as the rows allow.
+  auto fits = [&](int v) { return cols % v == 0 && rows_aligned(mt, v * ti) && rows_aligned(mo, v * to); };
+  const int vec = ti + to < 8 && fits(8) ? 8 : fits(4) ? 4 : 1;
   const EmbedFwd a{table, index, out, status, rows, cols, table_stride, n, out_stride, index_type, scale};
   cudaStream_t s = (cudaStream_t)stream;
   const int sms = sm_count();
