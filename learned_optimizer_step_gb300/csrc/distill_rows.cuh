@@ -138,11 +138,13 @@ template <> struct Slots<__nv_bfloat16> {
 
 // Sums of 2^((z - m) c) over slots, m a running maximum: one thread's part.
 //
-// The exponent is fma(z, c, -mc) with mc = m c rounded once; `fix` takes off
-// what that rounding left, so the sum is about m exactly.  Where m c could
-// overflow (rows of the type's lowest value), (z - m) c is taken instead,
-// which is slower by an addition.
-constexpr float kSafe = 1e38f;
+// The exponent is fma(z, c, -mc) with mc = m c rounded once; a factor takes off
+// what that rounding left, so the sum is about m exactly.  What it left is at
+// most half a unit in the last place of mc: up to 2^24 that is 1/2, and all
+// terms stay below 2.  Beyond (rows, or a thread's first classes, that are
+// masked by -1e10 or the type's lowest value) it would grow past what 2^x can
+// hold, so (z - m) c is taken there, which is slower by an addition.
+constexpr float kSafe = 16777216.f;
 
 template <typename T> struct Partial {
   float m = -INFINITY, s = 0.f;
