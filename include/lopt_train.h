@@ -59,8 +59,8 @@ extern "C" {
  * An index at or above the limit is an error that only the device can see:
  * it is treated as "none", and the kernels set bit 0 of *status (a device
  * int32 the caller zeroes and reads when it likes; NULL: not reported).  Bit 1
- * says that a bounded wait inside lopt_distill() ran out and its results are
- * not valid.
+ * says that a bounded wait (1 s) inside lopt_distill() ran out: rows whose
+ * loss is then NaN are not whole, neither is their gradient.
  */
 
 /*
@@ -138,6 +138,17 @@ int lopt_distill(const void* logits, int type, int64_t rows, int64_t cols, int64
                  const void* top_index, int index_type, int64_t top_index_stride, int64_t top,
                  float temperature, const float* row_weight,
                  float* loss, void* grad, int64_t grad_stride, int32_t* status, void* stream);
+
+/*
+ * Self-test of the bounded waits: lopt_distill() whose waits run out after
+ * limit_ns (0 to 10^9) instead of 1 s.  Nothing hangs or faults: rows that it
+ * did not finish have a NaN loss, and bit 1 of *status is set.
+ */
+int lopt_selftest_distill(int64_t limit_ns, const void* logits, int type, int64_t rows, int64_t cols,
+                          int64_t logits_stride, const void* top_logits, int top_type, int64_t top_logits_stride,
+                          const void* top_index, int index_type, int64_t top_index_stride, int64_t top,
+                          float temperature, const float* row_weight, float* loss, void* grad, int64_t grad_stride,
+                          int32_t* status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -28,9 +28,10 @@ struct Distill {
 };
 
 // One per element type, each in a source of its own (they compile side by side).
-cudaError_t distill_f32(const Distill& a, int sms, cudaStream_t s);
-cudaError_t distill_f16(const Distill& a, int sms, cudaStream_t s);
-cudaError_t distill_bf16(const Distill& a, int sms, cudaStream_t s);
+// A wait that lasts longer than wait_ns has failed.
+cudaError_t distill_f32(const Distill& a, uint64_t wait_ns, int sms, cudaStream_t s);
+cudaError_t distill_f16(const Distill& a, uint64_t wait_ns, int sms, cudaStream_t s);
+cudaError_t distill_bf16(const Distill& a, uint64_t wait_ns, int sms, cudaStream_t s);
 
 #ifdef LOPT_DISTILL_KERNELS
 namespace {
@@ -287,7 +288,7 @@ template <typename T> struct Slice {
 
 // ---- long rows: a block, or a cluster of blocks, per row -----------------------------
 constexpr int kMaxCluster = 8;
-constexpr uint64_t kWaitNs = 1000000000ull;   // 1 s: a wait that long has failed
+constexpr uint64_t kDrainNs = 1000000000ull;   // 1 s: for what is on its way when a block gives up
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -296,6 +297,12 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A shared-memory address of another block of the cluster.
+template <typename P> __device__ __forceinline__ P* of_block(P* p, int rank) {
+  uint64_t out;
+  asm("mapa.u64 %0, %1, %2;" : "=l"(out) : "l"((uint64_t)p), "r"(rank));
+  return reinterpret_cast<P*>(out);
 }
 // (m, s) into block `rank` of the cluster, counted on its barrier.
 __device__ __forceinline__ void send_pair(const float2* at, const uint64_t* bar, int rank, float m, float s) {
@@ -840,21 +847,31 @@ __device__ __forceinline__ void join_pairs(const float2* got, int n, float c, fl
 // had then finished row e: with four sets in rotation no set is overwritten
 // while it is read.
 //
+// Every wait is bounded.  A warp whose wait runs out sets gave_up in all
+// blocks of the cluster, which ends their other waits too, and leaves at the
+// row it is in.  No block goes before all are here; if one gave up, they then
+// agree on how far the stores to each other have come, send what is missing
+// (nobody reads it), wait until all of it and the copies have landed, and mark
+// the rows that are not whole: their loss is NaN, and the caller's status says
+// so.  A warp's answer in common and the last barrier cost 1 % (250.7 us for
+// the first case below, 247.6 when waits that ran out went unnoticed).
+//
 // Bound by HBM bytes: 8,192 rows of 50,257 bfloat16 (two blocks to a row) with
-// gradient 247 us, 6.25 TB/s; the loss alone of 2,048 rows of 50,304 float16
-// 36 us, 5.0 TB/s, since a block has six rows and nothing covers the first
+// gradient 251 us, 6.17 TB/s; the loss alone of 2,048 rows of 50,304 float16
+// 37 us, 5.0 TB/s, since a block has six rows and nothing covers the first
 // one's load.  Copying the next row chunk by chunk, as the current one's are
 // done with, was slower (264 and 64 us), and so was a row in the registers of a
 // cluster (469).
 template <typename T, int TH, bool GRAD>
-__global__ void __launch_bounds__(TH + 32, 1024 / TH) k_distill_ring(const Distill a, const int log_c, const int slice_slots, const int ahead_bytes) {
+__global__ void __launch_bounds__(TH + 32, 1024 / TH) k_distill_ring(const Distill a, const int log_c, const int slice_slots,
+                                                                     const int ahead_bytes, const uint64_t wait_ns) {
   constexpr int GW = TH / 32, U = 4, SETS = 4;
   extern __shared__ __align__(128) unsigned char sm[];
   uint4* buf = reinterpret_cast<uint4*>(sm);
   __shared__ float2 pairs[SETS][GW * kMaxCluster];    // (m, s) of the row's warps
   __shared__ float2 loss_parts[SETS][kMaxCluster];    // (sum of p (z - m), 0) of the blocks
   __shared__ uint64_t full, summed, listed, empty, xch[SETS], parts[SETS];
-  __shared__ int gave_up;
+  __shared__ int gave_up;                             // here or in another block of the cluster
   __shared__ int32_t any[2];   // whether a slot of the row counts
   const int t = threadIdx.x, lane = t % 32, gw = t / 32;
   const int C = 1 << log_c;
@@ -876,14 +893,31 @@ __global__ void __launch_bounds__(TH + 32, 1024 / TH) k_distill_ring(const Disti
   __syncthreads();
   if (C > 1) cluster_sync();
   auto weight = [&](int64_t r) { return r >= a.rows ? 0.f : a.row_weight ? a.row_weight[r] : 1.f; };
-  auto wait = [&](uint64_t* bar, uint32_t phase) { mbar_wait_or_abort(bar, phase & 1, kWaitNs, &gave_up); };
+  // By a whole warp, with one answer.
+  auto wait = [&](uint64_t* bar, uint32_t phase) {
+    return __all_sync(0xffffffffu, mbar_wait_or_abort(bar, phase & 1, wait_ns, &gave_up));
+  };
+  // The pairs of a computing warp for the n-th row, and the ahead warp's part.
+  auto send_pairs = [&](uint32_t n, float m, float s) {
+    const int b = n & (SETS - 1);
+    if (t == 0) mbar_arrive_expect_tx(&xch[b], (uint32_t)(GW * C * sizeof(float2)));
+    if (lane < C) send_pair(&pairs[b][rank * GW + gw], &xch[b], lane, m, s);
+  };
+  auto send_part = [&](uint32_t n, float pz) {
+    const int b = n & (SETS - 1);
+    if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&parts[b], (uint32_t)(C * sizeof(float2)));
+    __syncwarp();
+    if (lane == 0) send_pair(&loss_parts[b][rank], &parts[b], 0, pz, 0.f);
+  };
   float w = weight(row);
-  uint32_t e = 0;   // rows of weight other than 0 so far
+  uint32_t e = 0;         // rows of weight other than 0 so far; a warp that gives up counts one whose pairs or part it sent
+  uint32_t fetched = 0;   // the ahead warp's copies
   const float c = a.log2e_t;
+  int32_t* const words = reinterpret_cast<int32_t*>(sm + (size_t)slice_slots * 16 + ahead_bytes);
 
   if (gw == GW) {   // the warp that works ahead
     FromShared<T> from(a, sm + (size_t)slice_slots * 16);
-    List l(reinterpret_cast<int32_t*>(sm + (size_t)slice_slots * 16 + ahead_bytes), a.top);
+    List l(words, a.top);
     // The whole slots of a row's slice, when all lanes are done with the last one's.
     auto fetch = [&](const Slice<T>& n) {
       __syncwarp();
@@ -893,6 +927,7 @@ __global__ void __launch_bounds__(TH + 32, 1024 / TH) k_distill_ring(const Disti
         mbar_arrive_expect_tx(&full, bytes);
         if (bytes) bulk_g2s(buf + lo, n.z16() + lo, bytes, &full);
       }
+      ++fetched;
       __syncwarp();
     };
     SlotRegs<4> lr;
@@ -924,31 +959,33 @@ __global__ void __launch_bounds__(TH + 32, 1024 / TH) k_distill_ring(const Disti
       if (w != 0.f) {
         const int b = e & (SETS - 1);
         const bool learn = regs ? lr.any : l.any;
-        wait(&full, e);
+        if (!wait(&full, e)) break;
         if (learn) read(r, std::true_type());
-        wait(&summed, e);
+        if (!wait(&summed, e)) break;
         if (learn && (r.first >= 0 || r.last >= 0)) read(r, std::false_type());
         if (!GRAD && w_next != 0.f) fetch(r_next);
-        if (C > 1) wait(&xch[b], e / SETS);
+        if (C > 1 && !wait(&xch[b], e / SETS)) break;
         float m, s;
         join_pairs<GW * kMaxCluster>(pairs[b], GW * C, c, m, s);
-        float loss = 0.f;
-        if (learn) {
-          float pz = warp_sum(regs ? sum_slots(r, lr, m) : sum_listed(r, l, m));
-          if (C > 1) {   // the first block adds the blocks' parts
-            if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&parts[b], (uint32_t)(C * sizeof(float2)));
-            __syncwarp();
-            if (lane == 0) send_pair(&loss_parts[b][rank], &parts[b], 0, pz, 0.f);
-            if (rank == 0) {
-              wait(&parts[b], e / SETS);
-              pz = warp_sum(lane < C ? loss_parts[b][lane].x : 0.f);
+        float pz = learn ? warp_sum(regs ? sum_slots(r, lr, m) : sum_listed(r, l, m)) : 0.f;
+        if (C > 1) {   // the first block adds the blocks' parts
+          send_part(e, pz);
+          if (rank == 0) {
+            if (!wait(&parts[b], e / SETS)) {
+              ++e;
+              break;
             }
+            pz = warp_sum(lane < C ? loss_parts[b][lane].x : 0.f);
           }
-          loss = w * a.temperature * a.temperature * ((regs ? lr.p_log_p : l.p_log_p) - (pz * a.inv_t - logf(s)));
         }
+        float loss = 0.f;
+        if (learn) loss = w * a.temperature * a.temperature * ((regs ? lr.p_log_p : l.p_log_p) - (pz * a.inv_t - logf(s)));
         if (rank == 0 && lane == 0) a.loss[row] = loss;
         if (GRAD) {
-          wait(&empty, e);
+          if (!wait(&empty, e)) {
+            ++e;
+            break;
+          }
           if (w_next != 0.f) fetch(r_next);
           if (learn) {   // the listed classes of this slice, again
             const float wt = w * a.temperature;
@@ -956,8 +993,6 @@ __global__ void __launch_bounds__(TH + 32, 1024 / TH) k_distill_ring(const Disti
           }
           __syncwarp();
         }
-        // A barrier that this row left unused keeps its phase with the others'.
-        if (C > 1 && rank == 0 && !learn && lane == 0) mbar_arrive(&parts[b]);
         ++e;
       } else {
         if (w_next != 0.f) fetch(r_next);
@@ -969,90 +1004,128 @@ __global__ void __launch_bounds__(TH + 32, 1024 / TH) k_distill_ring(const Disti
       row = next;
       w = w_next;
     }
-    if (gave_up && lane == 0 && a.status) atomicOr(a.status, kStatusGaveUp);
-    return;
-  }
-
-  for (int par = 0; row < a.rows; par ^= 1) {
-    const int64_t next = row + clusters;
-    const float w_next = weight(next);
-    const Slice<T> r(a, row, rank, log_c);
-    bool learn = false;
-    if (w != 0.f) {
-      // Slots that are not whole are read by the threads that use them (a
-      // slot of the buffer is the same thread's in every row), and stored
-      // when the copy is there: until then the ahead warp may still read
-      // the row before.
-      const bool edge_first = r.first == 0 && t == 0, edge_last = r.last >= 0 && r.last != r.first && t == r.last % TH;
-      uint4 edge = make_uint4(0, 0, 0, 0);
-      if (edge_first) edge = r.read_edge(0);
-      else if (edge_last) edge = r.read_edge(r.last);
-      wait(&full, e);
-      if (edge_first || edge_last) {
-        buf[edge_first ? 0 : r.last] = edge;
-        if (edge_first && edge_last) buf[r.last] = r.read_edge(r.last);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // a later row's copy may land there
-      }
-      Partial<T> part;
-      int q = t;
-      for (; q + (U - 1) * TH < r.cnt; q += U * TH) {
-        uint32_t v[U][4];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const uint4 x = buf[q + u * TH];
-          v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");   // a list that no one wanted
+  } else {
+    for (int par = 0; row < a.rows; par ^= 1) {
+      const int64_t next = row + clusters;
+      const float w_next = weight(next);
+      const Slice<T> r(a, row, rank, log_c);
+      bool learn = false;
+      if (w != 0.f) {
+        // Slots that are not whole are read by the threads that use them (a
+        // slot of the buffer is the same thread's in every row), and stored
+        // when the copy is there: until then the ahead warp may still read
+        // the row before.
+        const bool edge_first = r.first == 0 && t == 0, edge_last = r.last >= 0 && r.last != r.first && t == r.last % TH;
+        uint4 edge = make_uint4(0, 0, 0, 0);
+        if (edge_first) edge = r.read_edge(0);
+        else if (edge_last) edge = r.read_edge(r.last);
+        if (!wait(&full, e)) break;
+        if (edge_first || edge_last) {
+          buf[edge_first ? 0 : r.last] = edge;
+          if (edge_first && edge_last) buf[r.last] = r.read_edge(r.last);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // a later row's copy may land there
         }
-        part.template add<U>(v, c);
-      }
-      for (; q < r.cnt; q += TH) {
-        const uint4 x = buf[q];
-        const uint32_t v[1][4] = {{x.x, x.y, x.z, x.w}};
-        part.template add<1>(v, c);
-      }
-      float m = part.m, s = part.s;
-      join_warp(m, s, c);
-      const int b = e & (SETS - 1);
-      if (C == 1) {
-        if (lane == 0) pairs[b][gw] = make_float2(m, s);
-      } else {
-        if (t == 0) mbar_arrive_expect_tx(&xch[b], (uint32_t)(GW * C * sizeof(float2)));
-        if (lane < C) send_pair(&pairs[b][rank * GW + gw], &xch[b], lane, m, s);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&summed);
-      if (GRAD) {
-        if (C > 1) wait(&xch[b], e / SETS);
-        else wait(&summed, e);
-        wait(&listed, e);
-        learn = any[par];
-        if (learn) {
-          join_pairs<GW * kMaxCluster>(pairs[b], GW * C, c, m, s);
-          const Dense<T> dense(m, c, w * a.temperature / s);
+        Partial<T> part;
+        int q = t;
+        for (; q + (U - 1) * TH < r.cnt; q += U * TH) {
+          uint32_t v[U][4];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const uint4 x = buf[q + u * TH];
+            v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
+          }
+          part.template add<U>(v, c);
+        }
+        for (; q < r.cnt; q += TH) {
+          const uint4 x = buf[q];
+          const uint32_t v[1][4] = {{x.x, x.y, x.z, x.w}};
+          part.template add<1>(v, c);
+        }
+        float m = part.m, s = part.s;
+        join_warp(m, s, c);
+        const int b = e & (SETS - 1);
+        if (C == 1) {
+          if (lane == 0) pairs[b][gw] = make_float2(m, s);
+        } else {
+          send_pairs(e, m, s);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&summed);
+        if (GRAD) {
+          if (!(C > 1 ? wait(&xch[b], e / SETS) : wait(&summed, e)) || !wait(&listed, e)) {
+            ++e;
+            break;
+          }
+          learn = any[par];
+          if (learn) {
+            join_pairs<GW * kMaxCluster>(pairs[b], GW * C, c, m, s);
+            const Dense<T> dense(m, c, w * a.temperature / s);
 #pragma unroll 4
-          for (int k = t; k < r.cnt; k += TH) {
-            const uint4 x = buf[k];
-            const uint32_t v[4] = {x.x, x.y, x.z, x.w};
-            uint32_t o[4];
-            dense.of(v, o);
-            r.write(k, o);
+            for (int k = t; k < r.cnt; k += TH) {
+              const uint4 x = buf[k];
+              const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+              uint32_t o[4];
+              dense.of(v, o);
+              r.write(k, o);
+            }
           }
         }
       }
-    }
-    if (GRAD && !learn) {   // nothing to learn from this row
-      const uint32_t o[4] = {0, 0, 0, 0};
-      for (int q = t; q < r.cnt; q += TH) r.write(q, o);
-    }
-    if (w != 0.f) {
-      if (GRAD) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty);
+      if (GRAD && !learn) {   // nothing to learn from this row
+        const uint32_t o[4] = {0, 0, 0, 0};
+        for (int q = t; q < r.cnt; q += TH) r.write(q, o);
       }
-      ++e;
+      if (w != 0.f) {
+        if (GRAD) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty);
+        }
+        ++e;
+      }
+      row = next;
+      w = w_next;
     }
-    row = next;
-    w = w_next;
   }
+
+  // Leaving; `row` is the first row that this warp has not finished.
+  if (row < a.rows) {
+    if (C == 1) gave_up = 1;
+    else if (lane < C) *of_block(&gave_up, lane) = 1;
+  }
+  __syncwarp();
+  if (C == 1) __syncthreads();
+  else cluster_sync();
+  if (*(volatile int*)&gave_up == 0) return;
+  // Some warp gave up.
+  if (C > 1) {
+    // How far the cluster's computing warps (its ahead warps) came: no one is
+    // more than two rows behind.  The lists are not wanted any more.
+    uint32_t* sent_n = reinterpret_cast<uint32_t*>(words);   // [GW + 1]
+    if (lane == 0) sent_n[gw] = e;
+    __syncwarp();
+    cluster_sync();
+    const int n = gw == GW ? 1 : GW;
+    uint32_t most = 0;
+    for (int k = lane; k < n * C; k += 32) most = max(most, of_block(sent_n, k / n)[gw == GW ? GW : k % n]);
+    most = __reduce_max_sync(0xffffffffu, most);
+    for (; e < most; ++e) {
+      if (gw == GW) send_part(e, 0.f);
+      else send_pairs(e, 0.f, 0.f);
+    }
+    __syncwarp();
+    cluster_sync();   // all is sent, and no one reads another block's memory any more
+    if (gw == 0 || (gw == GW && rank == 0)) {
+      uint64_t* bars = gw == GW ? parts : xch;
+      for (uint32_t k = most > SETS ? most - SETS : 0; k < most; ++k)
+        mbar_wait_bounded(bars + (k & (SETS - 1)), k / SETS & 1, kDrainNs);
+    }
+  }
+  if (gw != GW) return;
+  if (fetched) mbar_wait_bounded(&full, (fetched - 1) & 1, kDrainNs);
+  // The ahead warp finishes a row last of its block's.
+  if (row < a.rows && lane == 0 && a.status) atomicOr(a.status, kStatusGaveUp);
+  for (int64_t k = row + (int64_t)lane * clusters; k < a.rows; k += (int64_t)32 * clusters) a.loss[k] = NAN;
 }
 
 // Rows beyond a cluster's shared memory: one block per row, which is read for
@@ -1152,16 +1225,18 @@ cudaError_t block_as(const Distill& a, int threads, cudaStream_t s) {
 }
 
 template <typename T, int TH, bool GRAD>
-cudaError_t ring_as(const Distill& a, int log_c, int slice_slots, size_t smem, int blocks, cudaStream_t s) {
+cudaError_t ring_as(const Distill& a, int log_c, int slice_slots, size_t smem, int blocks, uint64_t wait_ns,
+                    cudaStream_t s) {
   auto* k = &k_distill_ring<T, TH, GRAD>;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem);
   if (e != cudaSuccess) return e;
   const int64_t clusters = std::min<int64_t>(a.rows, blocks >> log_c);
-  return launch(k, dim3((unsigned)(clusters << log_c)), dim3(TH + 32), smem, s, false, 1 << log_c, a, log_c, slice_slots, (int)shared_list_bytes(a));
+  return launch(k, dim3((unsigned)(clusters << log_c)), dim3(TH + 32), smem, s, false, 1 << log_c, a, log_c, slice_slots,
+                (int)shared_list_bytes(a), wait_ns);
 }
 
 template <typename T>
-cudaError_t distill_rows(const Distill& a, int sms, cudaStream_t s) {
+cudaError_t distill_rows(const Distill& a, uint64_t wait_ns, int sms, cudaStream_t s) {
   constexpr int N = Slots<T>::N;
   // Most slots that cover a row, wherever it starts.
   const bool aligned = (uintptr_t)a.logits % 16 == 0 && (a.rows == 1 || (a.ls * (int64_t)sizeof(T)) % 16 == 0);
@@ -1199,8 +1274,10 @@ cudaError_t distill_rows(const Distill& a, int sms, cudaStream_t s) {
     const int slice = (int)ceil(slots, 1 << lc), blocks = sms * per_sm;
     const size_t smem = (size_t)bytes(lc);
     if (a.grad)
-      return small ? ring_as<T, 256, true>(a, lc, slice, smem, blocks, s) : ring_as<T, 512, true>(a, lc, slice, smem, blocks, s);
-    return small ? ring_as<T, 256, false>(a, lc, slice, smem, blocks, s) : ring_as<T, 512, false>(a, lc, slice, smem, blocks, s);
+      return small ? ring_as<T, 256, true>(a, lc, slice, smem, blocks, wait_ns, s)
+               : ring_as<T, 512, true>(a, lc, slice, smem, blocks, wait_ns, s);
+    return small ? ring_as<T, 256, false>(a, lc, slice, smem, blocks, wait_ns, s)
+             : ring_as<T, 512, false>(a, lc, slice, smem, blocks, wait_ns, s);
   }
   return launch(k_distill_rows<T>, dim3((unsigned)a.rows), dim3(512), 0, s, false, 1, a);
 }

@@ -3,11 +3,14 @@
 
 using namespace lopt::train;
 
-extern "C" int lopt_distill(const void* logits, int type, int64_t rows, int64_t cols, int64_t logits_stride,
-                            const void* top_logits, int top_type, int64_t top_logits_stride, const void* top_index,
-                            int index_type, int64_t top_index_stride, int64_t top, float temperature,
-                            const float* row_weight, float* loss, void* grad, int64_t grad_stride, int32_t* status,
-                            void* stream) {
+namespace {
+
+constexpr uint64_t kWaitNs = 1000000000ull;   // 1 s
+
+int distill(const void* logits, int type, int64_t rows, int64_t cols, int64_t logits_stride,
+            const void* top_logits, int top_type, int64_t top_logits_stride, const void* top_index, int index_type,
+            int64_t top_index_stride, int64_t top, float temperature, const float* row_weight, float* loss, void* grad,
+            int64_t grad_stride, int32_t* status, uint64_t wait_ns, void* stream) {
   const int es = type_size(type), ts = type_size(top_type), is = index_size(index_type);
   if (!es || !ts || !is || (top_type != LOPT_F32 && top_type != type)) return LOPT_E_ARG;
   // T, 1 / T and log2(e) / T are finite and not zero.
@@ -34,8 +37,32 @@ extern "C" int lopt_distill(const void* logits, int type, int64_t rows, int64_t 
   cudaStream_t s = (cudaStream_t)stream;
   const int sms = sm_count();
   switch (type) {
-    case LOPT_F32: return done(distill_f32(a, sms, s));
-    case LOPT_F16: return done(distill_f16(a, sms, s));
-    default: return done(distill_bf16(a, sms, s));
+    case LOPT_F32: return done(distill_f32(a, wait_ns, sms, s));
+    case LOPT_F16: return done(distill_f16(a, wait_ns, sms, s));
+    default: return done(distill_bf16(a, wait_ns, sms, s));
   }
 }
+
+}  // namespace
+
+extern "C" {
+
+int lopt_distill(const void* logits, int type, int64_t rows, int64_t cols, int64_t logits_stride, const void* top_logits,
+                 int top_type, int64_t top_logits_stride, const void* top_index, int index_type,
+                 int64_t top_index_stride, int64_t top, float temperature, const float* row_weight, float* loss,
+                 void* grad, int64_t grad_stride, int32_t* status, void* stream) {
+  return distill(logits, type, rows, cols, logits_stride, top_logits, top_type, top_logits_stride, top_index, index_type,
+                 top_index_stride, top, temperature, row_weight, loss, grad, grad_stride, status, kWaitNs, stream);
+}
+
+int lopt_selftest_distill(int64_t limit_ns, const void* logits, int type, int64_t rows, int64_t cols,
+                          int64_t logits_stride, const void* top_logits, int top_type, int64_t top_logits_stride,
+                          const void* top_index, int index_type, int64_t top_index_stride, int64_t top,
+                          float temperature, const float* row_weight, float* loss, void* grad, int64_t grad_stride,
+                          int32_t* status, void* stream) {
+  if (limit_ns < 0 || limit_ns > (int64_t)kWaitNs) return LOPT_E_ARG;
+  return distill(logits, type, rows, cols, logits_stride, top_logits, top_type, top_logits_stride, top_index, index_type,
+                 top_index_stride, top, temperature, row_weight, loss, grad, grad_stride, status, (uint64_t)limit_ns, stream);
+}
+
+}  // extern "C"

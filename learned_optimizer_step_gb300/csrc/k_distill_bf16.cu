@@ -4,6 +4,8 @@
 
 namespace lopt {
 namespace train {
-cudaError_t distill_bf16(const Distill& a, int sms, cudaStream_t s) { return distill_rows<__nv_bfloat16>(a, sms, s); }
+cudaError_t distill_bf16(const Distill& a, uint64_t wait_ns, int sms, cudaStream_t s) {
+  return distill_rows<__nv_bfloat16>(a, wait_ns, sms, s);
+}
 }  // namespace train
 }  // namespace lopt

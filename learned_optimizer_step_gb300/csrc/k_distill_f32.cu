@@ -4,6 +4,8 @@
 
 namespace lopt {
 namespace train {
-cudaError_t distill_f32(const Distill& a, int sms, cudaStream_t s) { return distill_rows<float>(a, sms, s); }
+cudaError_t distill_f32(const Distill& a, uint64_t wait_ns, int sms, cudaStream_t s) {
+  return distill_rows<float>(a, wait_ns, sms, s);
+}
 }  // namespace train
 }  // namespace lopt

@@ -34,7 +34,7 @@ E_INDEX = -10
 _lopt.ERRORS.setdefault(E_INDEX, "LOPT_E_INDEX")
 
 TRAIN_EXPORTED = ("lopt_embed_forward", "lopt_embed_workspace", "lopt_embed_backward", "lopt_layernorm_forward",
-                  "lopt_layernorm_workspace", "lopt_layernorm_backward", "lopt_distill")
+                  "lopt_layernorm_workspace", "lopt_layernorm_backward", "lopt_distill", "lopt_selftest_distill")
 
 _TYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 _INDEX = {torch.int32: I32, torch.int64: I64}
@@ -62,6 +62,7 @@ def _load():
                                         i32, vp, i64, vp],
             "lopt_distill": [vp, i32, i64, i64, i64, vp, i32, i64, vp, i32, i64, i64, f, vp, vp, vp, i64, vp, vp],
         }
+        sig["lopt_selftest_distill"] = [i64] + sig["lopt_distill"]
         for name, args in sig.items():
             fn = getattr(lib, name)
             fn.argtypes, fn.restype = args, i32
