@@ -64,6 +64,17 @@ extern "C" {
  */
 
 /*
+ * A status word of the library's own, one per device, for callers that keep
+ * none: zero before the first call, at the same address as long as the
+ * device's context lives.  lopt_status_word() gives its address on the current
+ * device, to any thread, also while a stream is being captured.
+ * lopt_status_take() waits for the current device, gives the bits set since
+ * the last time and clears them.
+ */
+int lopt_status_word(int32_t** word);
+int lopt_status_take(int32_t* flags);
+
+/*
  * out[i] = scale * table[index[i]],  i < n;  zeros where the index is none.
  *   table  [rows x cols] of table_type;  index  [n];  out  [n x cols].
  */

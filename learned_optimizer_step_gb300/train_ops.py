@@ -34,7 +34,8 @@ E_INDEX = -10
 _lopt.ERRORS.setdefault(E_INDEX, "LOPT_E_INDEX")
 
 TRAIN_EXPORTED = ("lopt_embed_forward", "lopt_embed_workspace", "lopt_embed_backward", "lopt_layernorm_forward",
-                  "lopt_layernorm_workspace", "lopt_layernorm_backward", "lopt_distill", "lopt_selftest_distill")
+                  "lopt_layernorm_workspace", "lopt_layernorm_backward", "lopt_distill", "lopt_selftest_distill",
+                  "lopt_status_word", "lopt_status_take")
 
 _TYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 _INDEX = {torch.int32: I32, torch.int64: I64}
@@ -62,6 +63,8 @@ def _load():
                                         i32, vp, i64, vp],
             "lopt_distill": [vp, i32, i64, i64, i64, vp, i32, i64, vp, i32, i64, i64, f, vp, vp, vp, i64, vp, vp],
         }
+        sig["lopt_status_word"] = [ctypes.POINTER(vp)]
+        sig["lopt_status_take"] = [ctypes.POINTER(ctypes.c_int32)]
         sig["lopt_selftest_distill"] = [i64] + sig["lopt_distill"]
         for name, args in sig.items():
             fn = getattr(lib, name)
@@ -197,33 +200,33 @@ _status = {}
 
 
 def _status_ptr(dev):
-    """Address of the device's word for bad indices (0 while a graph capture
-    comes before any call that could make it)."""
-    t = _status.get(dev)
-    if t is None:
-        if torch.cuda.is_current_stream_capturing():
-            return 0
+    """Address of the library's status word on a device: the same for every
+    thread, and there before the first call, be it a captured one."""
+    ptr = _status.get(dev)
+    if ptr is None:
+        word = ctypes.c_void_p()
         with torch.cuda.device(dev):
-            t = torch.zeros(1, dtype=torch.int32, device="cuda")
-            torch.cuda.synchronize()   # zero before another stream's kernels can see it
-        _status[dev] = t
-    return t.data_ptr()
+            code = _load()["lopt_status_word"](word)
+        if code:
+            _lopt._check("lopt_status_word", code)
+        ptr = _status[dev] = word.value
+    return ptr
 
 
 def check_indices(device: Optional[int] = None) -> None:
     """Wait for the device and raise LoptError (LOPT_E_INDEX) if an index of
-    any call since the last check was at or above its limit (or
-    LOPT_E_TIMEOUT if a kernel's bounded wait ran out)."""
+    any call since the last check, replayed graphs among them, was at or above
+    its limit (or LOPT_E_TIMEOUT if a kernel's bounded wait ran out)."""
     dev = torch.cuda.current_device() if device is None else torch.device("cuda", device).index
-    t = _status.get(dev)
-    if t is None:
+    if dev not in _status:
         return
-    torch.cuda.synchronize(dev)
-    flags = int(t.item())
-    if flags:
-        t.zero_()
-        torch.cuda.synchronize(dev)
-        _lopt._check("check_indices", _E_TIMEOUT if flags & 2 else E_INDEX)
+    flags = ctypes.c_int32()
+    with torch.cuda.device(dev):
+        code = _load()["lopt_status_take"](flags)
+    if code:
+        _lopt._check("lopt_status_take", code)
+    if flags.value:
+        _lopt._check("check_indices", _E_TIMEOUT if flags.value & 2 else E_INDEX)
 
 
 # ---- embedding ------------------------------------------------------------------
