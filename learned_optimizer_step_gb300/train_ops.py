@@ -10,6 +10,12 @@ dimensions are flattened; the distance between rows is free.  There is no
 fallback: a tensor that is not on the GPU, or a shape that does not fit,
 raises.
 
+The operators record nothing for autograd: the backward passes are calls of
+their own.  With gradients enabled, a tensor that requires one is refused; call
+under torch.no_grad() or from a torch.autograd.Function.  Tensors that are
+written count as changed in place, so that autograd notices if it had saved
+them.
+
 Indices: a negative one stands for none (padding, an unused slot).  One at or
 above the limit is treated the same and reported by ``check_indices()``, since
 only the device sees it.
@@ -41,7 +47,10 @@ _TYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 _INDEX = {torch.int32: I32, torch.int64: I64}
 _E_TIMEOUT = -7
 
+_increment_version = torch._C._increment_version
+_is_grad_enabled = torch.is_grad_enabled
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_is_capturing = torch._C._cuda_isCurrentStreamCapturing
 _current_device = torch._C._cuda_getDevice
 _fns = None
 
@@ -78,13 +87,16 @@ def _load():
 
 def _matrix(t, what):
     """(rows, cols, row stride) of a tensor with its leading dimensions flattened."""
-    if t.dim() == 2:
-        rows, cols = t.shape
+    shape = t.shape
+    if len(shape) == 2:
+        rows, cols = shape
+        if t.is_contiguous():
+            return rows, cols, cols
         rs, cs = t.stride()
-    elif t.dim() == 0:
+    elif not shape:
         raise ValueError("%s must have at least one dimension" % what)
     else:
-        cols = t.shape[-1]
+        cols = shape[-1]
         rows = t.numel() // cols if cols else 0
         try:
             rs, cs = t.view(rows, cols).stride()
@@ -121,21 +133,35 @@ def _index(t, what):
     return kind
 
 
+_DEVICES = "all tensors of a call must be on the same CUDA device"
+
+
 class _Call:
     """Device and stream of one call; new tensors are allocated for them."""
 
     __slots__ = ("dev", "handle", "stream")
 
-    def __init__(self, first, others, stream):
+    def __init__(self, first, inputs, others, stream):
+        """`others`: integers and outputs, of which only the device matters."""
         try:
             dev = self.dev = first.get_device()
+            grad = first.requires_grad
+            for t in inputs:
+                if t is not None:
+                    if t.get_device() != dev:
+                        raise TypeError(_DEVICES)
+                    if t.requires_grad:
+                        grad = True
             for t in others:
                 if t is not None and t.get_device() != dev:
-                    raise TypeError("all tensors of a call must be on the same CUDA device")
+                    raise TypeError(_DEVICES)
         except AttributeError:
             raise TypeError("the operators take torch tensors") from None
         if dev < 0 or not first.is_cuda:
             raise TypeError("the operators take CUDA tensors")
+        if grad and _is_grad_enabled():
+            raise RuntimeError("the operators are not recorded by autograd: with a tensor that requires a gradient, "
+                               "call them under torch.no_grad() or from a torch.autograd.Function")
         self.stream = None
         if stream is None:
             self.handle = _raw_stream(dev)
@@ -157,7 +183,7 @@ class _Call:
         """(tensor, address) of scratch memory for one call.  Calls of one
         thread on one stream follow each other and share it; it grows to the
         largest asked for.  A captured call gets memory of its own graph's."""
-        if self.stream is not None or torch.cuda.is_current_stream_capturing():
+        if self.stream is not None or _is_capturing():
             t = self.empty((size,), torch.uint8)
             return t, t.data_ptr()
         key = (self.dev, self.handle, threading.get_ident())
@@ -167,15 +193,17 @@ class _Call:
             got = _workspaces[key] = (t, t.data_ptr(), size)
         return got[0], got[1]
 
-    def run(self, name, *args):
+    def run(self, name, written, *args):
+        """The library's call; `written`: the tensors that it writes."""
         fn = (_fns or _load())[name]
         if self.dev == _current_device():
-            code = fn(*args, self.handle)
+            code = fn(*args)
         else:
             with torch.cuda.device(self.dev):
-                code = fn(*args, self.handle)
+                code = fn(*args)
         if code:
             _lopt._check(name, code)
+        _increment_version(written)
 
 
 _workspaces = {}
@@ -238,7 +266,7 @@ def embedding_forward(table, index, scale: float = 1.0, *, out=None, out_dtype=N
     table: [rows, cols], float32, float16 or bfloat16; index: int32 or int64
     of any shape, contiguous; out: [*index.shape, cols] (default: new, of
     ``out_dtype`` or the table's type)."""
-    c = _Call(table, (index, out), stream)
+    c = _Call(table, (), (index, out), stream)
     if table.dim() != 2:
         raise ValueError("table must have two dimensions")
     rows, cols, ts = _matrix(table, "table")
@@ -248,8 +276,8 @@ def embedding_forward(table, index, scale: float = 1.0, *, out=None, out_dtype=N
     n_out, cols_out, os = _matrix(out, "out")
     if n_out != n or cols_out != cols:
         raise ValueError("out must be %s" % ((*index.shape, cols),))
-    c.run("lopt_embed_forward", table.data_ptr(), _type(table, "table"), rows, cols, ts, index.data_ptr(), kind, n,
-          scale, out.data_ptr(), _type(out, "out"), os, _status_ptr(c.dev))
+    c.run("lopt_embed_forward", (out,), table.data_ptr(), _type(table, "table"), rows, cols, ts, index.data_ptr(),
+          kind, n, scale, out.data_ptr(), _type(out, "out"), os, _status_ptr(c.dev), c.handle)
     return out
 
 
@@ -259,7 +287,7 @@ def embedding_backward(grad_out, index, rows: int, scale: float = 1.0, *, out=No
     ``scale * grad_out[i]`` over the i with index[i] == v, in that order.
     ``out``: the parameter's gradient buffer; ``accumulate`` adds to it (a
     table tied to the output projection) instead of writing every row."""
-    c = _Call(grad_out, (index, out), stream)
+    c = _Call(grad_out, (), (index, out), stream)
     n, cols, gs = _matrix(grad_out, "grad_out")
     kind = _index(index, "index")
     if index.numel() != n:
@@ -271,8 +299,8 @@ def embedding_backward(grad_out, index, rows: int, scale: float = 1.0, *, out=No
     ptr = _vector(out, rows * cols, "out")
     need = _size_of("lopt_embed_workspace", n, rows, cols)
     ws, ws_ptr = c.workspace(need)
-    c.run("lopt_embed_backward", grad_out.data_ptr(), _type(grad_out, "grad_out"), gs, index.data_ptr(), kind, n, rows,
-          cols, scale, 1 if accumulate else 0, ptr, ws_ptr, need, _status_ptr(c.dev))
+    c.run("lopt_embed_backward", (out,), grad_out.data_ptr(), _type(grad_out, "grad_out"), gs, index.data_ptr(),
+          kind, n, rows, cols, scale, 1 if accumulate else 0, ptr, ws_ptr, need, _status_ptr(c.dev), c.handle)
     return out
 
 
@@ -304,7 +332,7 @@ def layernorm_forward(x, weight, bias=None, eps: float = 1e-5, *, residual=None,
     summed is x + residual, what the residual stream goes on with; mean and
     rstd (float32, one per row) are what the backward pass wants.  weight and
     bias: float32 or the type of x."""
-    c = _Call(x, (weight, bias, residual, out, summed, mean, rstd), stream)
+    c = _Call(x, (weight, bias, residual), (out, summed, mean, rstd), stream)
     rows, cols, xs = _matrix(x, "x")
     kind = _type(x, "x")
     w, b, wt = _weight_type(weight, bias, x, cols)
@@ -319,9 +347,10 @@ def layernorm_forward(x, weight, bias=None, eps: float = 1e-5, *, residual=None,
         mean = c.empty(x.shape[:-1], torch.float32)
     if rstd is None:
         rstd = c.empty(x.shape[:-1], torch.float32)
-    c.run("lopt_layernorm_forward", x.data_ptr(), kind, rows, cols, xs, r, rs, w, b, wt, eps, y, ys, s, ss,
-          _vector(mean, rows, "mean"), _vector(rstd, rows, "rstd"))
-    return (out, mean, rstd) if residual is None else (out, summed, mean, rstd)
+    written = (out, mean, rstd) if residual is None else (out, summed, mean, rstd)
+    c.run("lopt_layernorm_forward", written, x.data_ptr(), kind, rows, cols, xs, r, rs, w, b, wt, eps, y, ys, s, ss,
+          _vector(mean, rows, "mean"), _vector(rstd, rows, "rstd"), c.handle)
+    return written
 
 
 def layernorm_backward(grad_out, x, mean, rstd, weight, *, grad_residual=None, need_bias: bool = True, grad_x=None,
@@ -332,7 +361,7 @@ def layernorm_backward(grad_out, x, mean, rstd, weight, *, grad_residual=None, n
     that reaches x past the norm, added to grad_x; grad_weight and grad_bias:
     float32 [cols], the parameters' gradient buffers (``accumulate`` adds to
     them)."""
-    c = _Call(grad_out, (x, mean, rstd, weight, grad_residual, grad_x, grad_weight, grad_bias), stream)
+    c = _Call(grad_out, (x, weight, grad_residual), (mean, rstd, grad_x, grad_weight, grad_bias), stream)
     rows, cols, ds = _matrix(grad_out, "grad_out")
     kind = _type(grad_out, "grad_out")
     x, xp, xs = _like(c, x, grad_out, (rows, cols), "x")
@@ -351,10 +380,11 @@ def layernorm_backward(grad_out, x, mean, rstd, weight, *, grad_residual=None, n
         grad_bias = c.empty((cols,), torch.float32)
     need = _size_of("lopt_layernorm_workspace", rows, cols)
     ws, ws_ptr = c.workspace(need)
-    c.run("lopt_layernorm_backward", grad_out.data_ptr(), kind, rows, cols, ds, xp, xs, _vector(mean, rows, "mean"),
-          _vector(rstd, rows, "rstd"), w, wt, r, rs, gx, gs, _vector(grad_weight, cols, "grad_weight"),
-          0 if grad_bias is None else _vector(grad_bias, cols, "grad_bias"), 1 if accumulate else 0, ws_ptr,
-          need)
+    written = (grad_x, grad_weight) if grad_bias is None else (grad_x, grad_weight, grad_bias)
+    c.run("lopt_layernorm_backward", written, grad_out.data_ptr(), kind, rows, cols, ds, xp, xs,
+          _vector(mean, rows, "mean"), _vector(rstd, rows, "rstd"), w, wt, r, rs, gx, gs,
+          _vector(grad_weight, cols, "grad_weight"), 0 if grad_bias is None else _vector(grad_bias, cols, "grad_bias"),
+          1 if accumulate else 0, ws_ptr, need, c.handle)
     return grad_x, grad_weight, grad_bias
 
 
@@ -362,7 +392,7 @@ def layernorm_backward(grad_out, x, mean, rstd, weight, *, grad_residual=None, n
 
 
 def _distill(logits, top_logits, top_index, temperature, row_weight, loss, grad, need_grad, stream):
-    c = _Call(logits, (top_logits, top_index, row_weight, loss, grad), stream)
+    c = _Call(logits, (top_logits, row_weight), (top_index, loss, grad), stream)
     rows, cols, zs = _matrix(logits, "logits")
     kind = _type(logits, "logits")
     t_rows, top, ts = _matrix(top_logits, "top_logits")
@@ -380,8 +410,9 @@ def _distill(logits, top_logits, top_index, temperature, row_weight, loss, grad,
     g = gs = 0
     if need_grad:
         grad, g, gs = _like(c, grad, logits, (rows, cols), "grad")
-    c.run("lopt_distill", logits.data_ptr(), kind, rows, cols, zs, top_logits.data_ptr(), _TYPES[top_logits.dtype], ts,
-          top_index.data_ptr(), ik, i_s, top, temperature, w, _vector(loss, rows, "loss"), g, gs, _status_ptr(c.dev))
+    c.run("lopt_distill", (loss, grad) if need_grad else (loss,), logits.data_ptr(), kind, rows, cols, zs,
+          top_logits.data_ptr(), _TYPES[top_logits.dtype], ts, top_index.data_ptr(), ik, i_s, top, temperature, w,
+          _vector(loss, rows, "loss"), g, gs, _status_ptr(c.dev), c.handle)
     return loss, grad
 
 
