@@ -10,6 +10,11 @@ dimensions are flattened; the distance between rows is free.  There is no
 fallback: a tensor that is not on the GPU, or a shape that does not fit,
 raises.
 
+With a ``stream`` other than the current one, the call does not wait for work
+of the current one, and new results belong to ``stream``.  Its tensors may be
+dropped at once if ``stream`` is one of torch's own; with a raw handle or an
+ExternalStream the caller keeps them until that stream is done with them.
+
 The operators record nothing for autograd: the backward passes are calls of
 their own.  With gradients enabled, a tensor that requires one is refused; call
 under torch.no_grad() or from a torch.autograd.Function.  Tensors that are
@@ -168,8 +173,14 @@ class _Call:
         else:
             self.handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
             if self.handle != _raw_stream(dev):
-                self.stream = (stream if hasattr(stream, "cuda_stream")
-                               else torch.cuda.ExternalStream(self.handle, device=dev))
+                if not isinstance(stream, torch.cuda.Stream):
+                    stream = torch.cuda.ExternalStream(self.handle, device=dev)
+                self.stream = stream
+                # Not for streams of others' making, which may be gone when a tensor is freed.
+                if not isinstance(stream, torch.cuda.ExternalStream):
+                    for t in (first, *inputs, *others):
+                        if t is not None:
+                            t.record_stream(stream)
 
     def empty(self, shape, dtype):
         if self.stream is None:
