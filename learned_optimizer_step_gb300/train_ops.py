@@ -31,6 +31,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import threading
+import weakref
 from typing import Optional
 
 import torch
@@ -193,15 +194,20 @@ class _Call:
     def workspace(self, size):
         """(tensor, address) of scratch memory for one call.  Calls of one
         thread on one stream follow each other and share it; it grows to the
-        largest asked for.  A captured call gets memory of its own graph's."""
+        largest asked for and goes with its thread.  A captured call gets memory
+        of its own graph's."""
         if self.stream is not None or _is_capturing():
             t = self.empty((size,), torch.uint8)
             return t, t.data_ptr()
-        key = (self.dev, self.handle, threading.get_ident())
-        got = _workspaces.get(key)
+        try:
+            mine = _local.scratch
+        except AttributeError:
+            mine = _local.scratch = _Scratch()
+        key = (self.dev, self.handle)
+        got = mine.get(key)
         if got is None or got[2] < size:
             t = self.empty((size,), torch.uint8)
-            got = _workspaces[key] = (t, t.data_ptr(), size)
+            got = mine[key] = (t, t.data_ptr(), size)
         return got[0], got[1]
 
     def run(self, name, written, *args):
@@ -217,12 +223,26 @@ class _Call:
         _increment_version(written)
 
 
-_workspaces = {}
+_local = threading.local()
+_scratches, _scratches_lock = weakref.WeakValueDictionary(), threading.Lock()
+
+
+class _Scratch(dict):
+    """A thread's scratch memory: (device, stream) to (tensor, address, size)."""
+
+    __slots__ = ("__weakref__",)
+
+    def __init__(self):
+        with _scratches_lock:
+            _scratches[id(self)] = self
 
 
 def release_workspaces() -> None:
-    """Give the operators' scratch memory back to torch's allocator."""
-    _workspaces.clear()
+    """Give the operators' scratch memory, of all threads, back to torch's allocator."""
+    with _scratches_lock:
+        scratches = list(_scratches.values())
+    for scratch in scratches:
+        scratch.clear()
 
 
 @functools.lru_cache(maxsize=1024)
