@@ -199,15 +199,12 @@ class _Call:
         if self.stream is not None or _is_capturing():
             t = self.empty((size,), torch.uint8)
             return t, t.data_ptr()
-        try:
-            mine = _local.scratch
-        except AttributeError:
-            mine = _local.scratch = _Scratch()
-        key = (self.dev, self.handle)
-        got = mine.get(key)
+        key = (self.dev, self.handle, threading.get_ident())
+        got = _workspaces.get(key)
         if got is None or got[2] < size:
             t = self.empty((size,), torch.uint8)
-            got = mine[key] = (t, t.data_ptr(), size)
+            _drop_with_thread(key[2])
+            got = _workspaces[key] = (t, t.data_ptr(), size)
         return got[0], got[1]
 
     def run(self, name, written, *args):
@@ -223,26 +220,29 @@ class _Call:
         _increment_version(written)
 
 
+_workspaces = {}         # (device, stream, thread): (tensor, address, size)
 _local = threading.local()
-_scratches, _scratches_lock = weakref.WeakValueDictionary(), threading.Lock()
 
 
-class _Scratch(dict):
-    """A thread's scratch memory: (device, stream) to (tensor, address, size)."""
+class _End:
+    """Goes with the thread it is a local of."""
 
-    __slots__ = ("__weakref__",)
 
-    def __init__(self):
-        with _scratches_lock:
-            _scratches[id(self)] = self
+def _drop(thread):
+    for key in [k for k in list(_workspaces) if k[2] == thread]:
+        _workspaces.pop(key, None)
+
+
+def _drop_with_thread(thread):
+    """Scratch memory of the calling thread goes when it ends."""
+    if not hasattr(_local, "end"):
+        _local.end = _End()
+        weakref.finalize(_local.end, _drop, thread).atexit = False
 
 
 def release_workspaces() -> None:
     """Give the operators' scratch memory, of all threads, back to torch's allocator."""
-    with _scratches_lock:
-        scratches = list(_scratches.values())
-    for scratch in scratches:
-        scratch.clear()
+    _workspaces.clear()
 
 
 @functools.lru_cache(maxsize=1024)
