@@ -142,7 +142,9 @@ int lopt_layernorm_backward(const void* grad_out, int type, int64_t rows, int64_
  * counts, has loss 0 and gradient 0, whatever its logits hold.  One slot
  * with any finite t_k is the cross entropy with class i_k.  grad (type of the
  * logits) may be NULL: the loss alone.  In place: grad on logits.
- * top_type: LOPT_F32 or `type`.  1 <= top <= LOPT_MAX_TOP, 1e-30 <= T <= 1e30.
+ * top_type: LOPT_F32 or `type`.  1 <= top <= LOPT_MAX_TOP, 1e-30 <= T <= 1e3.
+ * The loss is off by about 2^-20 w T^2 (1 + log cols), from the logarithms, and
+ * 2^-22 w T times the differences t_k - max t and z - max z that it weighs.
  */
 int lopt_distill(const void* logits, int type, int64_t rows, int64_t cols, int64_t logits_stride,
                  const void* top_logits, int top_type, int64_t top_logits_stride,

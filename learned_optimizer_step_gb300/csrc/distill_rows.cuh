@@ -4,6 +4,9 @@
 // With m = max z and s = sum exp((z - m) / T), log q_j = (z_j - m) / T - log s.
 // The exponents are taken of z - m, not of z / T - m / T: masks of the type's
 // lowest value stay finite that way, and the terms near the maximum exact.
+// The loss, with d = t - max t and es = sum 2^(d log2e / T) over the slots, is
+//   w T (sum p d - sum p (z - m) + T (log s - log es)):
+// no quotient by T, which could overflow for a small one, and no T^2.
 // The dense part of the gradient, w T q_j, is written for every column and
 // the listed columns are then written again with their p taken off.
 #pragma once
@@ -24,7 +27,7 @@ struct Distill {
   int32_t* status;
   int64_t rows, cols, ls, ts, is, gs;
   int top, ttype, itype;
-  float temperature, inv_t, log2e_t;   // T, 1 / T, log2(e) / T
+  float temperature, log2e_t;   // T, log2(e) / T
 };
 
 // One per element type, each in a source of its own (they compile side by side).
@@ -71,6 +74,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
+}
+
+// The loss of a row from the sums over its slots and its own; wt = w T.
+__device__ __forceinline__ float loss_of(const Distill& a, float wt, float p_d, float log_e, float pz, float s) {
+  return wt * fmaf(a.temperature, logf(s) - log_e, p_d - pz);
 }
 
 // ---- 16 bytes of a row ---------------------------------------------------------
@@ -321,8 +329,8 @@ struct List {
   int32_t *id, *place, *key;
   float *e, *z, *sum;
   int top, log_size;
-  // Of the whole list: 1 / sum of e, sum of p log p; whether any slot counts.
-  float inv, p_log_p;
+  // Of the whole list: 1 / sum of e, its logarithm, sum of p (t - max); whether any slot counts.
+  float inv, log_e, p_d;
   bool any;
   __device__ __forceinline__ List(int32_t* words, int top_);
 };
@@ -488,7 +496,8 @@ __device__ __forceinline__ void make_list(const Distill& a, const Slice<T>& r, b
     es = warp_sum(es);
     ed = warp_sum(ed);
     l.inv = 1.f / es;
-    l.p_log_p = ed * l.inv * a.inv_t - logf(es);   // sum p (d / T - log es), sum p = 1
+    l.log_e = logf(es);
+    l.p_d = __fmul_rn(ed, l.inv);   // rounded here in every form of the kernels: the loss has the same bits
     __syncwarp();
     if (GRAD) {
       for (int k0 = 0; k0 < l.top; k0 += 32) {
@@ -550,7 +559,7 @@ __device__ __forceinline__ float sum_listed(const Slice<T>& r, const List& l, fl
 template <int U> struct SlotRegs {
   int32_t id[U];
   float e[U], z[U];
-  float inv, p_log_p;
+  float inv, log_e, p_d;
   bool any;
 };
 template <int U, typename From>
@@ -584,7 +593,8 @@ __device__ __forceinline__ void make_slots(const Distill& a, From& from, bool re
   for (int o = 16; o > 0; o >>= 1)
     sums = __fadd2_rn(sums, make_float2(__shfl_xor_sync(0xffffffffu, sums.x, o), __shfl_xor_sync(0xffffffffu, sums.y, o)));
   l.inv = 1.f / sums.x;
-  l.p_log_p = sums.y * l.inv * a.inv_t - logf(sums.x);   // sum p (d / T - log es), sum p = 1
+  l.log_e = logf(sums.x);
+  l.p_d = __fmul_rn(sums.y, l.inv);
 }
 template <typename T, bool WHOLE, int U>
 __device__ __forceinline__ void read_slots(const Slice<T>& r, const uint4* buf, SlotRegs<U>& l) {
@@ -675,8 +685,8 @@ __global__ void __launch_bounds__(32 * kWarpRows, 8) k_distill_warp(const Distil
   join_warp(m, s, c);
   const float wt = w * a.temperature, f = wt / s;
   // The loss, or a row of zeros; whether there is a gradient to write.
-  auto finish = [&](bool any, float p_log_p, float pz) {
-    if (lane == 0) a.loss[row] = any ? wt * a.temperature * (p_log_p - (pz * a.inv_t - logf(s))) : 0.f;
+  auto finish = [&](bool any, float p_d, float log_e, float pz) {
+    if (lane == 0) a.loss[row] = any ? loss_of(a, wt, p_d, log_e, pz, s) : 0.f;
     if (!GRAD) return false;
     if (!any) {   // nothing to learn from this row
       const uint32_t o[4] = {0, 0, 0, 0};
@@ -700,7 +710,7 @@ __global__ void __launch_bounds__(32 * kWarpRows, 8) k_distill_warp(const Distil
     make_slots(a, from, w != 0.f, l);
     l.z[0] = z[0];
     const bool any = w != 0.f && l.any;
-    if (!finish(any, l.p_log_p, warp_sum(sum_slots(r, l, m)))) return;
+    if (!finish(any, l.p_d, l.log_e, warp_sum(sum_slots(r, l, m)))) return;
     write_slots(r, l, c, m, f, wt);
     return;
   }
@@ -714,7 +724,7 @@ __global__ void __launch_bounds__(32 * kWarpRows, 8) k_distill_warp(const Distil
       if (l.id[k] >= 0) l.z[k] = to_f(r.z[l.id[k]]);
     __syncwarp();
   }
-  if (finish(l.any, l.p_log_p, warp_sum(l.any ? sum_listed(r, l, m) : 0.f))) write_listed(r, l, c, m, f, wt);
+  if (finish(l.any, l.p_d, l.log_e, warp_sum(l.any ? sum_listed(r, l, m) : 0.f))) write_listed(r, l, c, m, f, wt);
 }
 
 // ---- rows of up to 16 KB: a block per row ---------------------------------------------
@@ -780,7 +790,7 @@ __global__ void __launch_bounds__(kBlockThreads, 4) k_distill_block(const Distil
   const float wt = w * a.temperature, f = wt / s;
   if (warp == 0) {
     const float pz = warp_sum(slots ? sum_slots(r, lr, m) : sum_listed(r, l, m));
-    if (lane == 0) a.loss[row] = wt * a.temperature * ((slots ? lr.p_log_p : l.p_log_p) - (pz * a.inv_t - logf(s)));
+    if (lane == 0) a.loss[row] = slots ? loss_of(a, wt, lr.p_d, lr.log_e, pz, s) : loss_of(a, wt, l.p_d, l.log_e, pz, s);
   }
   if (!GRAD) return;
   const Dense<T> dense(m, c, f);
@@ -979,7 +989,10 @@ __global__ void __launch_bounds__(TH + 32, 1024 / TH) k_distill_ring(const Disti
           }
         }
         float loss = 0.f;
-        if (learn) loss = w * a.temperature * a.temperature * ((regs ? lr.p_log_p : l.p_log_p) - (pz * a.inv_t - logf(s)));
+        if (learn) {
+          const float wt = w * a.temperature;
+          loss = regs ? loss_of(a, wt, lr.p_d, lr.log_e, pz, s) : loss_of(a, wt, l.p_d, l.log_e, pz, s);
+        }
         if (rank == 0 && lane == 0) a.loss[row] = loss;
         if (GRAD) {
           if (!wait(&empty, e)) {
@@ -1177,20 +1190,23 @@ __global__ void __launch_bounds__(512) k_distill_rows(const Distill a) {
   float s = 0.f;
   for (int64_t j = tid; j < a.cols; j += L) s += ex2((to_f(z[j]) - m) * a.log2e_t);
   s = block_sum<W>(s, red);
-  const float log_s = logf(s), log_ps = logf(ps), inv_ps = 1.f / ps;
-  float kl = 0.f;
+  const float inv_ps = 1.f / ps;
+  float p_d = 0.f, pz = 0.f;
   for (int k = tid; k < a.top; k += L) {
     if (id[k] < 0) continue;
     const float d = p[k] - tmax;
     const float pk = ex2(d * a.log2e_t) * inv_ps;
-    const float term = pk * ((d * a.inv_t - log_ps) - ((zi[k] - m) * a.inv_t - log_s));
-    if (pk != 0.f) kl += term;   // 0 log 0 = 0
+    if (pk != 0.f) {   // 0 log 0 = 0
+      p_d = fmaf(pk, d, p_d);
+      pz = fmaf(pk, zi[k] - m, pz);
+    }
     p[k] = pk;
   }
-  kl = block_sum<W>(kl, red);
-  if (tid == 0) a.loss[row] = w * a.temperature * a.temperature * kl;
-  if (!g) return;
+  p_d = block_sum<W>(p_d, red);
+  pz = block_sum<W>(pz, red);
   const float wt = w * a.temperature, f = wt / s;
+  if (tid == 0) a.loss[row] = loss_of(a, wt, p_d, logf(ps), pz, s);
+  if (!g) return;
   for (int64_t j = tid; j < a.cols; j += L) g[j] = from_f<T>(ex2((to_f(z[j]) - m) * a.log2e_t) * f);
   __syncthreads();
   // A class listed more than once is written by its first slot.

@@ -13,8 +13,10 @@ int distill(const void* logits, int type, int64_t rows, int64_t cols, int64_t lo
             int64_t grad_stride, int32_t* status, uint64_t wait_ns, void* stream) {
   const int es = type_size(type), ts = type_size(top_type), is = index_size(index_type);
   if (!es || !ts || !is || (top_type != LOPT_F32 && top_type != type)) return LOPT_E_ARG;
-  // T, 1 / T and log2(e) / T are finite and not zero.
-  if (!(temperature >= 1e-30f && temperature <= 1e30f)) return LOPT_E_ARG;
+  // log2(e) / T is finite.  Above, T^2 times the rounding of the logarithms (some
+  // 1e-6) is larger than the loss of a list of all classes, which no longer
+  // grows with T.
+  if (!(temperature >= 1e-30f && temperature <= 1e3f)) return LOPT_E_ARG;
   if (rows < 0 || cols < 1 || rows >= kMaxRows || cols > kMaxCols || top < 1 || top > LOPT_MAX_TOP) return LOPT_E_SHAPE;
   if (rows == 0) return LOPT_OK;
   const Span mz{logits, rows, cols, logits_stride, es}, mt{top_logits, rows, top, top_logits_stride, ts};
@@ -33,7 +35,7 @@ int distill(const void* logits, int type, int64_t rows, int64_t cols, int64_t lo
   if (overlap(ml, mz)) return LOPT_E_ALIAS;
   const Distill a{logits, top_logits, top_index, row_weight, loss, grad, status, rows, cols, logits_stride,
                   top_logits_stride, top_index_stride, grad_stride, (int)top, top_type, index_type, temperature,
-                  1.f / temperature, 1.4426950408889634f / temperature};
+                  1.4426950408889634f / temperature};
   cudaStream_t s = (cudaStream_t)stream;
   const int sms = sm_count();
   switch (type) {

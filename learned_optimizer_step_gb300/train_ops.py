@@ -451,7 +451,7 @@ def distill_forward(logits, top_logits, top_index, temperature: float = 1.0, *, 
                     stream=None):
     """The loss of each row (float32): row_weight * T^2 * KL(p || q), p the
     teacher's softmax over the listed classes, q the softmax of the logits,
-    both at temperature T.
+    both at temperature T (1e-30 to 1e3).
 
     logits: [..., classes]; top_logits, top_index: [..., top], top <= 1024;
     slots with a negative index or a logit of -inf do not count.  A row of
