@@ -88,8 +88,9 @@ int lopt_embed_forward(const void* table, int table_type, int64_t rows, int64_t 
  * grad is contiguous fp32 [rows x cols], as lopt_step() reads it.  With
  * accumulate = 0 every row is written (zeros where no token has it); with 1
  * the sums are added to what grad holds, and rows without tokens are left.
- * The tokens are sorted and their sums cut into pieces of equal length, so
- * the association of a long sum depends on n and cols alone.
+ * The tokens are sorted by id and the sorted list is cut into pieces of equal
+ * length, whose sums are then added in order: the same index list and sizes
+ * give the same bits, but where a row's sum is cut depends on the other ids too.
  * workspace: lopt_embed_workspace() bytes, 256-byte aligned, any contents.
  */
 int lopt_embed_workspace(int64_t n, int64_t rows, int64_t cols, int64_t* bytes);
