@@ -863,11 +863,12 @@ __device__ __forceinline__ void join_pairs(const float2* got, int n, float c, fl
 // agree on how far the stores to each other have come, send what is missing
 // (nobody reads it), wait until all of it and the copies have landed, and mark
 // the rows that are not whole: their loss is NaN, and the caller's status says
-// so.  A warp's answer in common and the last barrier cost 1 % (250.7 us for
-// the first case below, 247.6 when waits that ran out went unnoticed).
+// so.  A warp's answer in common and the last barrier cost 0.6 % of the first
+// case below and 2 % of the second (247.6 and 36.0 us when waits that ran out
+// went unnoticed), and of 7 rows of 50,257 in a graph 4 % (6.4 us, 6.15).
 //
 // Bound by HBM bytes: 8,192 rows of 50,257 bfloat16 (two blocks to a row) with
-// gradient 251 us, 6.17 TB/s; the loss alone of 2,048 rows of 50,304 float16
+// gradient 249 us, 6.21 TB/s; the loss alone of 2,048 rows of 50,304 float16
 // 37 us, 5.0 TB/s, since a block has six rows and nothing covers the first
 // one's load.  Copying the next row chunk by chunk, as the current one's are
 // done with, was slower (264 and 64 us), and so was a row in the registers of a
@@ -905,7 +906,8 @@ __global__ void __launch_bounds__(TH + 32, 1024 / TH) k_distill_ring(const Disti
   auto weight = [&](int64_t r) { return r >= a.rows ? 0.f : a.row_weight ? a.row_weight[r] : 1.f; };
   // By a whole warp, with one answer.
   auto wait = [&](uint64_t* bar, uint32_t phase) {
-    return __all_sync(0xffffffffu, mbar_wait_or_abort(bar, phase & 1, wait_ns, &gave_up));
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, phase & 1))) return true;
+    return __all_sync(0xffffffffu, mbar_wait_slow(bar, phase & 1, wait_ns, &gave_up)) != 0;
   };
   // The pairs of a computing warp for the n-th row, and the ahead warp's part.
   auto send_pairs = [&](uint32_t n, float m, float s) {
@@ -1143,7 +1145,7 @@ __global__ void __launch_bounds__(TH + 32, 1024 / TH) k_distill_ring(const Disti
 
 // Rows beyond a cluster's shared memory: one block per row, which is read for
 // each of the three passes.  304 rows of 500,009 float32 with gradient: 722 us,
-// 2.4 TB/s of the four passes' bytes; each pass waits for the one before, and
+// 3.4 TB/s of the four passes' bytes; each pass waits for the one before, and
 // rows this long come few at a time.
 template <typename T>
 __global__ void __launch_bounds__(512) k_distill_rows(const Distill a) {
@@ -1191,21 +1193,18 @@ __global__ void __launch_bounds__(512) k_distill_rows(const Distill a) {
   for (int64_t j = tid; j < a.cols; j += L) s += ex2((to_f(z[j]) - m) * a.log2e_t);
   s = block_sum<W>(s, red);
   const float inv_ps = 1.f / ps;
-  float p_d = 0.f, pz = 0.f;
+  const float log_q = a.temperature * (logf(s) - logf(ps));
+  float kl = 0.f;
   for (int k = tid; k < a.top; k += L) {
     if (id[k] < 0) continue;
     const float d = p[k] - tmax;
     const float pk = ex2(d * a.log2e_t) * inv_ps;
-    if (pk != 0.f) {   // 0 log 0 = 0
-      p_d = fmaf(pk, d, p_d);
-      pz = fmaf(pk, zi[k] - m, pz);
-    }
+    if (pk != 0.f) kl += pk * ((d - (zi[k] - m)) + log_q);   // 0 log 0 = 0
     p[k] = pk;
   }
-  p_d = block_sum<W>(p_d, red);
-  pz = block_sum<W>(pz, red);
+  kl = block_sum<W>(kl, red);
   const float wt = w * a.temperature, f = wt / s;
-  if (tid == 0) a.loss[row] = loss_of(a, wt, p_d, logf(ps), pz, s);
+  if (tid == 0) a.loss[row] = wt * kl;
   if (!g) return;
   for (int64_t j = tid; j < a.cols; j += L) g[j] = from_f<T>(ex2((to_f(z[j]) - m) * a.log2e_t) * f);
   __syncthreads();
