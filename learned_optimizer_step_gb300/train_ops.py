@@ -142,6 +142,16 @@ def _index(t, what):
 _DEVICES = "all tensors of a call must be on the same CUDA device"
 
 
+def _same_lead(lead, **tensors):
+    """Tensors that are not flat have the leading dimensions of the one they go with."""
+    want = [d for d in lead if d != 1]
+    if len(want) < 2:
+        return
+    for what, (t, tail) in tensors.items():
+        if t is not None and t.dim() - tail > 1 and [d for d in t.shape[:t.dim() - tail] if d != 1] != want:
+            raise ValueError("%s is %s, expected leading dimensions %s" % (what, tuple(t.shape), tuple(lead)))
+
+
 class _Call:
     """Device and stream of one call; new tensors are allocated for them."""
 
@@ -307,6 +317,8 @@ def embedding_forward(table, index, scale: float = 1.0, *, out=None, out_dtype=N
     n_out, cols_out, os = _matrix(out, "out")
     if n_out != n or cols_out != cols:
         raise ValueError("out must be %s" % ((*index.shape, cols),))
+    if index.dim() > 1:
+        _same_lead(index.shape, out=(out, 1))
     c.run("lopt_embed_forward", (out,), table.data_ptr(), _type(table, "table"), rows, cols, ts, index.data_ptr(),
           kind, n, scale, out.data_ptr(), _type(out, "out"), os, _status_ptr(c.dev), c.handle)
     return out
@@ -323,10 +335,14 @@ def embedding_backward(grad_out, index, rows: int, scale: float = 1.0, *, out=No
     kind = _index(index, "index")
     if index.numel() != n:
         raise ValueError("grad_out has %d rows for %d indices" % (n, index.numel()))
+    if index.dim() > 1:
+        _same_lead(index.shape, grad_out=(grad_out, 1))
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
         out = c.empty((rows, cols), torch.float32)
+    elif out.shape != (rows, cols) and out.dim() != 1:
+        raise ValueError("out must be %s" % ((rows, cols),))
     ptr = _vector(out, rows * cols, "out")
     need = _size_of("lopt_embed_workspace", n, rows, cols)
     ws, ws_ptr = c.workspace(need)
@@ -365,6 +381,9 @@ def layernorm_forward(x, weight, bias=None, eps: float = 1e-5, *, residual=None,
     bias: float32 or the type of x."""
     c = _Call(x, (weight, bias, residual), (out, summed, mean, rstd), stream)
     rows, cols, xs = _matrix(x, "x")
+    if x.dim() > 2:
+        _same_lead(x.shape[:-1], residual=(residual, 1), out=(out, 1), summed=(summed, 1), mean=(mean, 0),
+                   rstd=(rstd, 0))
     kind = _type(x, "x")
     w, b, wt = _weight_type(weight, bias, x, cols)
     out, y, ys = _like(c, out, x, (rows, cols), "out")
@@ -394,6 +413,9 @@ def layernorm_backward(grad_out, x, mean, rstd, weight, *, grad_residual=None, n
     them)."""
     c = _Call(grad_out, (x, weight, grad_residual), (mean, rstd, grad_x, grad_weight, grad_bias), stream)
     rows, cols, ds = _matrix(grad_out, "grad_out")
+    if grad_out.dim() > 2:
+        _same_lead(grad_out.shape[:-1], x=(x, 1), mean=(mean, 0), rstd=(rstd, 0), grad_residual=(grad_residual, 1),
+                   grad_x=(grad_x, 1))
     kind = _type(grad_out, "grad_out")
     x, xp, xs = _like(c, x, grad_out, (rows, cols), "x")
     w, _, wt = _weight_type(weight, None, grad_out, cols)
@@ -425,6 +447,9 @@ def layernorm_backward(grad_out, x, mean, rstd, weight, *, grad_residual=None, n
 def _distill(logits, top_logits, top_index, temperature, row_weight, loss, grad, need_grad, stream):
     c = _Call(logits, (top_logits, row_weight), (top_index, loss, grad), stream)
     rows, cols, zs = _matrix(logits, "logits")
+    if logits.dim() > 2:
+        _same_lead(logits.shape[:-1], top_logits=(top_logits, 1), top_index=(top_index, 1), row_weight=(row_weight, 0),
+                   loss=(loss, 0), grad=(grad, 1))
     kind = _type(logits, "logits")
     t_rows, top, ts = _matrix(top_logits, "top_logits")
     i_rows, i_top, i_s = _matrix(top_index, "top_index")
