@@ -317,6 +317,8 @@ def embedding_forward(table, index, scale: float = 1.0, *, out=None, out_dtype=N
     n_out, cols_out, os = _matrix(out, "out")
     if n_out != n or cols_out != cols:
         raise ValueError("out must be %s" % ((*index.shape, cols),))
+    if out_dtype is not None and out.dtype is not out_dtype:
+        raise TypeError("out is %s, out_dtype %s" % (out.dtype, out_dtype))
     if index.dim() > 1:
         _same_lead(index.shape, out=(out, 1))
     c.run("lopt_embed_forward", (out,), table.data_ptr(), _type(table, "table"), rows, cols, ts, index.data_ptr(),

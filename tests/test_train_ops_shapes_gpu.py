@@ -66,3 +66,11 @@ def test_the_tables_gradient_has_the_tables_shape():
     for shape in ((8, 5), (10, 4), (1, 5, 8)):
         with pytest.raises(ValueError):
             L.embedding_backward(dy, index, 5, out=torch.zeros(*shape, device="cuda"))
+
+
+def test_out_and_out_dtype_agree():
+    table, index = torch.ones(5, 8, device="cuda"), torch.zeros(4, dtype=torch.int64, device="cuda")
+    out = torch.empty(4, 8, dtype=torch.bfloat16, device="cuda")
+    L.embedding_forward(table, index, out=out, out_dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        L.embedding_forward(table, index, out=out, out_dtype=torch.float32)
