@@ -76,9 +76,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// The loss of a row from the sums over its slots and its own; wt = w T.
+// The loss of a row from the sums over its slots and its own; wt = w T.  pz is
+// half the sum of p (z - m): z = -3.4e38 and p rounded up to more than 1 in
+// total would overflow where the loss, for w T < 1, does not.
+__device__ __forceinline__ float half_distance(float z, float m) { return 0.5f * z - 0.5f * m; }
 __device__ __forceinline__ float loss_of(const Distill& a, float wt, float p_d, float log_e, float pz, float s) {
-  return wt * fmaf(a.temperature, logf(s) - log_e, p_d - pz);
+  return 2.f * (wt * fmaf(0.5f * a.temperature, logf(s) - log_e, fmaf(0.5f, p_d, -pz)));
 }
 
 // ---- 16 bytes of a row ---------------------------------------------------------
@@ -538,7 +541,7 @@ __device__ __forceinline__ void read_listed(const Slice<T>& r, const uint4* buf,
   }
 }
 
-// This lane's part of sum p (z - m) over the slots of the slice.
+// This lane's part of half the sum of p (z - m) over the slots of the slice.
 template <typename T>
 __device__ __forceinline__ float sum_listed(const Slice<T>& r, const List& l, float m) {
   float pz = 0.f;
@@ -548,7 +551,7 @@ __device__ __forceinline__ float sum_listed(const Slice<T>& r, const List& l, fl
       const int k = k0 + u * 32 + (int)(threadIdx.x % 32);
       if (k >= l.top || !r.holds(l.id[k])) continue;
       const float p = l.e[k] * l.inv;
-      if (p != 0.f) pz = fmaf(p, l.z[k] - m, pz);   // 0 log 0 = 0
+      if (p != 0.f) pz = fmaf(p, half_distance(l.z[k], m), pz);   // 0 log 0 = 0
     }
   }
   return pz;
@@ -609,7 +612,7 @@ __device__ __forceinline__ float sum_slots(const Slice<T>& r, const SlotRegs<U>&
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const float p = l.e[u] * l.inv;
-    if (p != 0.f && r.holds(l.id[u])) pz = fmaf(p, l.z[u] - m, pz);
+    if (p != 0.f && r.holds(l.id[u])) pz = fmaf(p, half_distance(l.z[u], m), pz);
   }
   return pz;
 }
@@ -880,7 +883,7 @@ __global__ void __launch_bounds__(TH + 32, 1024 / TH) k_distill_ring(const Disti
   extern __shared__ __align__(128) unsigned char sm[];
   uint4* buf = reinterpret_cast<uint4*>(sm);
   __shared__ float2 pairs[SETS][GW * kMaxCluster];    // (m, s) of the row's warps
-  __shared__ float2 loss_parts[SETS][kMaxCluster];    // (sum of p (z - m), 0) of the blocks
+  __shared__ float2 loss_parts[SETS][kMaxCluster];    // (half the sum of p (z - m), 0) of the blocks
   __shared__ uint64_t full, summed, listed, empty, xch[SETS], parts[SETS];
   __shared__ int gave_up;                             // here or in another block of the cluster
   __shared__ int32_t any[2];   // whether a slot of the row counts
@@ -1193,18 +1196,18 @@ __global__ void __launch_bounds__(512) k_distill_rows(const Distill a) {
   for (int64_t j = tid; j < a.cols; j += L) s += ex2((to_f(z[j]) - m) * a.log2e_t);
   s = block_sum<W>(s, red);
   const float inv_ps = 1.f / ps;
-  const float log_q = a.temperature * (logf(s) - logf(ps));
+  const float log_q = 0.5f * a.temperature * (logf(s) - logf(ps));
   float kl = 0.f;
   for (int k = tid; k < a.top; k += L) {
     if (id[k] < 0) continue;
     const float d = p[k] - tmax;
     const float pk = ex2(d * a.log2e_t) * inv_ps;
-    if (pk != 0.f) kl += pk * ((d - (zi[k] - m)) + log_q);   // 0 log 0 = 0
+    if (pk != 0.f) kl += pk * ((0.5f * d - half_distance(zi[k], m)) + log_q);   // 0 log 0 = 0
     p[k] = pk;
   }
   kl = block_sum<W>(kl, red);
   const float wt = w * a.temperature, f = wt / s;
-  if (tid == 0) a.loss[row] = wt * kl;
+  if (tid == 0) a.loss[row] = 2.f * (wt * kl);
   if (!g) return;
   for (int64_t j = tid; j < a.cols; j += L) g[j] = from_f<T>(ex2((to_f(z[j]) - m) * a.log2e_t) * f);
   __syncthreads();

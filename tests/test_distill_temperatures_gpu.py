@@ -47,6 +47,25 @@ def test_a_wanted_class_at_the_lowest_value(dtype):
             check_distill(z, t, i, float(torch.tensor(T)), None, loss, grad, "%d classes, T=%g" % (cols, T))
 
 
+def test_a_sum_of_probabilities_that_rounds_up_does_not_overflow():
+    """Float32 slots all at the lowest value: their p add up to 1 and a bit in
+    some rows, the loss is half or a quarter of the largest number."""
+    g = gen(9)
+    low = torch.finfo(torch.float32).min
+    for cols in (64, 3001, 50257, 500009):
+        rows = 300 if cols < 4000 else 40
+        z = normal(g, rows, cols)
+        z[:, :40] = low
+        for top in (5, 23, 40):
+            i = torch.argsort(torch.rand(rows, 40, generator=g, device="cuda"), 1)[:, :top].contiguous()
+            t = normal(g, rows, top)
+            for T in (0.5, 0.25):
+                loss, grad = L.distill_forward_backward(z, t, i, T)
+                assert torch.isfinite(loss).all(), (cols, top, T)
+                check_distill(z, t, i, T, None, loss, grad, "%d classes, T=%g" % (cols, T))
+                assert torch.equal(loss, L.distill_forward(z, t, i, T))
+
+
 def test_temperatures_beyond_are_refused():
     z, t = torch.zeros(2, 8, device="cuda"), torch.zeros(2, 1, device="cuda")
     i = torch.zeros(2, 1, dtype=torch.int64, device="cuda")
