@@ -357,10 +357,11 @@ def embedding_backward(grad_out, index, rows: int, scale: float = 1.0, *, out=No
 
 
 def _weight_type(weight, bias, x, cols):
-    if weight.dtype is not x.dtype and weight.dtype is not torch.float32:
+    dtype = weight.dtype
+    if dtype is not torch.float32 and dtype is not x.dtype:
         raise TypeError("weight must be float32 or of the type of x")
-    w = _vector(weight, cols, "weight", weight.dtype)
-    return w, 0 if bias is None else _vector(bias, cols, "bias", weight.dtype), _TYPES[weight.dtype]
+    w = _vector(weight, cols, "weight", dtype)
+    return w, 0 if bias is None else _vector(bias, cols, "bias", dtype), _TYPES[dtype]
 
 
 def _like(c, t, x, shape, what):
