@@ -7,12 +7,17 @@ from .lopt import (LearnedOptimizer, LoptError, PreparedList, TensorState,  # no
 
 _TRAIN_OPS = ("check_indices", "distill_forward", "distill_forward_backward", "embedding_backward",
               "embedding_forward", "layernorm_backward", "layernorm_forward", "release_workspaces")
+_LM_OPS = ("AdamW", "AdamWTensor", "block_norm_backward", "block_norm_forward")
 
 
 def __getattr__(name):
-    """The training operators, whose module imports torch, on first use."""
+    """The operators, whose modules import torch, on first use."""
     if name in _TRAIN_OPS:
         from . import train_ops
         globals().update({n: getattr(train_ops, n) for n in _TRAIN_OPS})
+        return globals()[name]
+    if name in _LM_OPS:
+        from . import lm_ops
+        globals().update({n: getattr(lm_ops, n) for n in _LM_OPS})
         return globals()[name]
     raise AttributeError("module %r has no attribute %r" % (__name__, name))

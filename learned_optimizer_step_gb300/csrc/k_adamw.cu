@@ -1,0 +1,609 @@
+// AdamW over a list of tensors (see lopt_lm.h for the formulas).
+//
+// One pass over param, grad and the moments; bound by HBM bytes (28 a float32
+// element, 30 with a 16-bit copy, 16 with 8-bit moments and 16-bit gradients).
+// The list travels in the kernel's parameters, so a step copies nothing to the
+// device and may be captured.  A warp takes 256 consecutive elements, eight a
+// lane: they are one block of 8-bit moments, whose largest value is a few
+// shuffles away.
+//
+// Every operation is rounded on its own (the __f*_rn intrinsics are not fused),
+// so that the codes of 8-bit moments are those of the formulas bit for bit.
+#include <algorithm>
+#include <cmath>
+#include <vector>
+
+#include "lopt_lm.h"
+#include "train_common.cuh"
+
+namespace lopt {
+namespace train {
+namespace {
+
+constexpr int kUnit = LOPT_ADAMW_BLOCK;   // elements of a warp
+constexpr int kWarps = 8;
+
+struct Desc {
+  float* param;
+  const void* grad;
+  void *m, *v;
+  float *m_scale, *v_scale;
+  void* copy;
+  int64_t n;
+  uint32_t key;
+  int32_t first;      // its first chunk in the launch
+  uint8_t grad_type, copy_type, decay, vec;
+  int32_t pad;
+};
+static_assert(sizeof(Desc) == 80, "");
+
+// Kernel parameters hold up to 32,764 bytes; small lists take the small form,
+// whose parameters are quicker to send.
+template <int N> struct List {
+  Desc d[N];
+};
+constexpr int kSmall = 24, kLarge = 400;
+
+struct Hyper {
+  float b1, nb1, b2, nb2, c1, c2, eps, keep;   // nb = 1 - b; c1 = lr / (1 - b1^t); c2 = 1 / sqrt(1 - b2^t); keep = 1 - lr * decay
+  const float* clip;                           // the clip factor, below 0: change nothing; NULL: none
+  int count, units;                            // tensors; warp units of a chunk
+};
+
+__host__ __device__ inline uint32_t mix(uint32_t h) {
+  h ^= h >> 16;
+  h *= 0x85ebca6bu;
+  h ^= h >> 13;
+  h *= 0xc2b2ae35u;
+  return h ^ (h >> 16);
+}
+
+// The tensor of a chunk: the last whose first chunk is not behind it.
+template <int N>
+__device__ __forceinline__ int find(const List<N>& list, int count, int chunk) {
+  int lo = 0, hi = count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (list.d[mid].first <= chunk) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// A lane's eight elements of a unit.  In vectors: four from lane * 4 on and
+// four more 128 behind; one by one: every 32nd.
+__device__ __forceinline__ int place(bool vec, int lane, int k) {
+  return vec ? (k / 4) * 128 + lane * 4 + k % 4 : k * 32 + lane;
+}
+
+template <typename T, typename F>
+__device__ __forceinline__ void load8(const T* p, bool vec, int lane, int left, F put) {
+  if (vec) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const Pack<T, 4> q = *reinterpret_cast<const Pack<T, 4>*>(p + j * 128 + lane * 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) put(j * 4 + e, q.v[e]);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) put(k, k * 32 + lane < left ? p[k * 32 + lane] : T(0));
+  }
+}
+template <typename T, typename F>
+__device__ __forceinline__ void store8(T* p, bool vec, int lane, int left, F get) {
+  if (vec) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      Pack<T, 4> q;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q.v[e] = get(j * 4 + e);
+      *reinterpret_cast<Pack<T, 4>*>(p + j * 128 + lane * 4) = q;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k * 32 + lane < left) p[k * 32 + lane] = get(k);
+  }
+}
+
+__device__ __forceinline__ void load_grad(const Desc& d, int64_t at, bool vec, int lane, int left, float (&g)[8]) {
+  if (d.grad_type == LOPT_F32)
+    load8(static_cast<const float*>(d.grad) + at, vec, lane, left, [&](int k, float x) { g[k] = x; });
+  else if (d.grad_type == LOPT_F16)
+    load8(static_cast<const __half*>(d.grad) + at, vec, lane, left, [&](int k, __half x) { g[k] = __half2float(x); });
+  else
+    load8(static_cast<const __nv_bfloat16*>(d.grad) + at, vec, lane, left,
+          [&](int k, __nv_bfloat16 x) { g[k] = __bfloat162float(x); });
+}
+
+__device__ __forceinline__ float decode(int q, float scale) { return __fmul_rn((float)(q * abs(q)), scale); }
+
+// Largest |x| of a warp, as bits: NaN is above infinity.
+__device__ __forceinline__ float largest(const float (&x)[8]) {
+  uint32_t most = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) most = max(most, __float_as_uint(x[k]) & 0x7fffffffu);
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, most));
+}
+
+// The code of |x| = y / inv units, 0 to top: floor(sqrt(y)), or one more.
+template <int TOP>
+__device__ __forceinline__ int encode(float x, float inv, uint32_t bits) {
+  const float y = fminf(__fmul_rn(fabsf(x), inv), (float)(TOP * TOP));
+  // The root's last bits do not matter: the two lines behind it make it the floor.
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(y));
+  float low = floorf(r);
+  if (__fmul_rn(low, low) > y) low -= 1.f;
+  if (__fmul_rn(low + 1.f, low + 1.f) <= y) low += 1.f;
+  const float share = __fsub_rn(y, __fmul_rn(low, low));
+  const float step = __fadd_rn(__fmul_rn(2.f, low), 1.f);
+  return (int)low + (share > __fmul_rn(__fmul_rn((float)bits, 1.f / 65536.f), step) ? 1 : 0);
+}
+
+template <int N, bool EIGHT>
+__global__ void __launch_bounds__(kWarps * 32) k_adamw(const __grid_constant__ List<N> list, const Hyper h) {
+  const int lane = threadIdx.x % 32;
+  float clip = 1.f;
+  wait_for_previous();
+  if (h.clip) {
+    clip = *h.clip;
+    if (clip < 0.f) return;
+  }
+  const Desc& d = list.d[find(list, h.count, blockIdx.x)];
+  const int64_t first = (int64_t)(blockIdx.x - d.first) * h.units;
+  for (int u = threadIdx.x / 32; u < h.units; u += kWarps) {
+    const int64_t unit = first + u, at = unit * kUnit;
+    if (at >= d.n) return;
+    const int left = (int)min((int64_t)kUnit, d.n - at);
+    const bool vec = d.vec && left == kUnit;
+    float p[8], g[8], m[8], v[8];
+    load_grad(d, at, vec, lane, left, g);
+    load8(d.param + at, vec, lane, left, [&](int k, float x) { p[k] = x; });
+    if (EIGHT) {
+      const float ms = d.m_scale[unit], vs = d.v_scale[unit];
+      load8(static_cast<const int8_t*>(d.m) + at, vec, lane, left, [&](int k, int8_t x) { m[k] = decode(x, ms); });
+      load8(static_cast<const uint8_t*>(d.v) + at, vec, lane, left, [&](int k, uint8_t x) {
+        const float r = decode(x, vs);
+        v[k] = __fmul_rn(r, r);
+      });
+    } else {
+      load8(static_cast<const float*>(d.m) + at, vec, lane, left, [&](int k, float x) { m[k] = x; });
+      load8(static_cast<const float*>(d.v) + at, vec, lane, left, [&](int k, float x) { v[k] = x; });
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float x = __fmul_rn(g[k], clip);
+      m[k] = __fadd_rn(__fmul_rn(h.b1, m[k]), __fmul_rn(h.nb1, x));
+      v[k] = __fadd_rn(__fmul_rn(h.b2, v[k]), __fmul_rn(__fmul_rn(h.nb2, x), x));
+      const float root = __fsqrt_rn(v[k]);
+      const float step = __fdiv_rn(m[k], __fadd_rn(__fmul_rn(root, h.c2), h.eps));
+      if (d.decay) p[k] = __fmul_rn(p[k], h.keep);
+      p[k] = __fsub_rn(p[k], __fmul_rn(h.c1, step));
+      if (EIGHT) v[k] = root;
+    }
+    store8(d.param + at, vec, lane, left, [&](int k) { return p[k]; });
+    if (d.copy) {
+      if (d.copy_type == LOPT_F16)
+        store8(static_cast<__half*>(d.copy) + at, vec, lane, left, [&](int k) { return __float2half_rn(p[k]); });
+      else
+        store8(static_cast<__nv_bfloat16*>(d.copy) + at, vec, lane, left, [&](int k) { return __float2bfloat16_rn(p[k]); });
+    }
+    if (EIGHT) {
+      constexpr float kM = 127.f * 127.f, kV = 255.f * 255.f;
+      const float am = largest(m), av = largest(v);
+      // NaN passes both tests and makes the block's scale NaN.
+      const float im = am <= 1e-30f ? 0.f : __fdiv_rn(kM, am), iv = av <= 1e-30f ? 0.f : __fdiv_rn(kV, av);
+      const uint32_t key = d.key ^ ((uint32_t)(at >> 32) * 0x85ebca6bu);
+      int qm[8], qv[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t bits = mix((uint32_t)(at + place(vec, lane, k)) ^ key);
+        const int q = encode<127>(m[k], im, bits >> 16);
+        qm[k] = m[k] < 0.f ? -q : q;
+        qv[k] = encode<255>(v[k], iv, bits & 0xffffu);
+      }
+      store8(static_cast<int8_t*>(d.m) + at, vec, lane, left, [&](int k) { return (int8_t)qm[k]; });
+      store8(static_cast<uint8_t*>(d.v) + at, vec, lane, left, [&](int k) { return (uint8_t)qv[k]; });
+      if (lane == 0) {
+        d.m_scale[unit] = __fmul_rn(am, (float)(1.0 / (127 * 127)));
+        d.v_scale[unit] = __fmul_rn(av, (float)(1.0 / (255 * 255)));
+      }
+    } else {
+      store8(static_cast<float*>(d.m) + at, vec, lane, left, [&](int k) { return m[k]; });
+      store8(static_cast<float*>(d.v) + at, vec, lane, left, [&](int k) { return v[k]; });
+    }
+  }
+}
+
+// ---- the gradients' norm ----------------------------------------------------------
+constexpr int kNormBlocks = 608;       // most blocks of a launch
+constexpr int kMaxPartials = 16 * kNormBlocks;
+
+// The sum of squares in about 48 bits: s the running sum, c the roundings of
+// the squares and of the sums (two-sum and fused multiply-add residuals).
+struct Sum {
+  float s = 0.f, c = 0.f;
+  uint32_t any = 0;
+  __device__ __forceinline__ void add(float x) {
+    const float p = __fmul_rn(x, x), e = __fmaf_rn(x, x, -p);
+    const float t = __fadd_rn(s, p), b = __fsub_rn(t, s);
+    c += __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(p, b)) + e;
+    s = t;
+    any |= __float_as_uint(x);
+  }
+  // Squares that overflow or vanish in fp32: the caller adds again in fp64.
+  __device__ __forceinline__ bool lost() const { return !(s < 1e38f) || (s < 1e-20f && (any << 1)); }
+};
+
+template <int N>
+__global__ void __launch_bounds__(kWarps * 32) k_adamw_norm(const __grid_constant__ List<N> list, int count, int units,
+                                                            int chunks, double* part) {
+  __shared__ double red[kWarps];
+  const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
+  wait_for_previous();
+  let_next_start();
+  double total = 0.0;
+  for (int chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
+    const Desc& d = list.d[find(list, count, chunk)];
+    const int64_t first = (int64_t)(chunk - d.first) * units;
+    Sum sum;
+    for (int u = w; u < units; u += kWarps) {
+      const int64_t at = (first + u) * kUnit;
+      if (at >= d.n) break;
+      const int left = (int)min((int64_t)kUnit, d.n - at);
+      float g[8];
+      load_grad(d, at, d.vec && left == kUnit, lane, left, g);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum.add(g[k]);
+    }
+    if (!sum.lost()) {
+      total += (double)sum.s + (double)sum.c;
+      continue;
+    }
+    for (int u = w; u < units; u += kWarps) {
+      const int64_t at = (first + u) * kUnit;
+      if (at >= d.n) break;
+      const int left = (int)min((int64_t)kUnit, d.n - at);
+      float g[8];
+      load_grad(d, at, d.vec && left == kUnit, lane, left, g);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) total += (double)g[k] * (double)g[k];
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (lane == 0) red[w] = total;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int k = 1; k < kWarps; ++k) total += red[k];
+    part[blockIdx.x] = total;
+  }
+}
+
+// part[0 .. count) in a fixed order; out: the norm, and the clip factor or -1.
+__global__ void __launch_bounds__(256) k_adamw_clip(const double* part, int count, double max_norm, float* norm, float* clip) {
+  __shared__ double red[8];
+  wait_for_previous();
+  let_next_start();
+  double t = 0.0;
+  for (int k = threadIdx.x; k < count; k += 256) t += part[k];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = t;
+  __syncthreads();
+  if (threadIdx.x) return;
+  for (int k = 1; k < 8; ++k) t += red[k];
+  t = sqrt(t);
+  const float n = (float)t;
+  *norm = n;
+  *clip = !(n <= 3.4028235e38f) ? -1.f : (float)fmin(1.0, max_norm / (t + 1e-6));
+}
+
+// ---- the moments as values ----------------------------------------------------------
+struct Out {
+  const void *m, *v;
+  const float *m_scale, *v_scale;
+  float *to_m, *to_v;
+  int64_t n;
+  int32_t first;
+  uint8_t eight, vec;
+};
+template <int N> struct Outs {
+  Out d[N];
+};
+constexpr int kOuts = 400;
+
+__global__ void __launch_bounds__(kWarps * 32) k_adamw_moments(const __grid_constant__ Outs<kOuts> list, int count, int units) {
+  const int lane = threadIdx.x % 32;
+  const int chunk = blockIdx.x;
+  int lo = 0, hi = count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (list.d[mid].first <= chunk) lo = mid; else hi = mid - 1;
+  }
+  const Out& d = list.d[lo];
+  const int64_t first = (int64_t)(chunk - d.first) * units;
+  for (int u = threadIdx.x / 32; u < units; u += kWarps) {
+    const int64_t unit = first + u, at = unit * kUnit;
+    if (at >= d.n) return;
+    const int left = (int)min((int64_t)kUnit, d.n - at);
+    const bool vec = d.vec && left == kUnit;
+    float m[8], v[8];
+    if (d.eight) {
+      const float ms = d.m_scale[unit], vs = d.v_scale[unit];
+      load8(static_cast<const int8_t*>(d.m) + at, vec, lane, left, [&](int k, int8_t x) { m[k] = decode(x, ms); });
+      load8(static_cast<const uint8_t*>(d.v) + at, vec, lane, left, [&](int k, uint8_t x) {
+        const float r = decode(x, vs);
+        v[k] = __fmul_rn(r, r);
+      });
+    } else {
+      load8(static_cast<const float*>(d.m) + at, vec, lane, left, [&](int k, float x) { m[k] = x; });
+      load8(static_cast<const float*>(d.v) + at, vec, lane, left, [&](int k, float x) { v[k] = x; });
+    }
+    store8(d.to_m + at, vec, lane, left, [&](int k) { return m[k]; });
+    store8(d.to_v + at, vec, lane, left, [&](int k) { return v[k]; });
+  }
+}
+
+// ---- host ------------------------------------------------------------------------
+constexpr int64_t kMaxElements = (int64_t)1 << 40;
+
+struct Range {
+  uintptr_t lo, hi;
+  bool in;      // read only
+};
+
+// A tensor's arrays.
+int ranges(const lopt_adamw_tensor& t, Range (&r)[7], int* count) {
+  const int gs = type_size(t.grad_type), cs = t.copy_type == LOPT_F32 ? 0 : type_size(t.copy_type);
+  if (!gs || (t.moments != 32 && t.moments != 8) || (t.decay != 0 && t.decay != 1)) return LOPT_E_ARG;
+  if (t.copy && !cs) return LOPT_E_ARG;
+  if (t.n < 0 || t.n > kMaxElements) return LOPT_E_SHAPE;
+  *count = 0;
+  if (t.n == 0) return LOPT_OK;
+  const bool eight = t.moments == 8;
+  if (!t.param || !t.grad || !t.m || !t.v || (eight && (!t.m_scale || !t.v_scale))) return LOPT_E_ARG;
+  const int64_t blocks = (t.n + kUnit - 1) / kUnit;
+  const struct { const void* p; int64_t n; int size; } a[7] = {
+      {t.param, t.n, 4}, {t.grad, t.n, gs}, {t.m, t.n, eight ? 1 : 4}, {t.v, t.n, eight ? 1 : 4},
+      {t.copy, t.n, cs}, {eight ? t.m_scale : nullptr, blocks, 4}, {eight ? t.v_scale : nullptr, blocks, 4}};
+  for (int k = 0; k < 7; ++k) {
+    if (!a[k].p) continue;
+    if ((uintptr_t)a[k].p % a[k].size) return LOPT_E_ALIGN;
+    r[(*count)++] = Range{(uintptr_t)a[k].p, (uintptr_t)a[k].p + (uintptr_t)(a[k].n * a[k].size), k == 1};
+  }
+  return LOPT_OK;
+}
+
+bool all_aligned(const lopt_adamw_tensor& t) {
+  const uintptr_t es = t.moments == 8 ? 4 : 16;
+  return (uintptr_t)t.param % 16 == 0 && (uintptr_t)t.grad % (t.grad_type == LOPT_F32 ? 16 : 8) == 0 &&
+         (uintptr_t)t.m % es == 0 && (uintptr_t)t.v % es == 0 && (uintptr_t)t.copy % 8 == 0;
+}
+
+// Warp units of a chunk: lists that would not fill the GPU otherwise get
+// small chunks.
+int chunk_units(int64_t units, int sms) { return units > (int64_t)sms * 8 * 4 * kWarps ? 4 * kWarps : kWarps; }
+
+template <int N, bool EIGHT>
+cudaError_t launch_step(const List<N>& list, const Hyper& h, int chunks, cudaStream_t s) {
+  return launch(k_adamw<N, EIGHT>, dim3((unsigned)chunks), dim3(kWarps * 32), 0, s, true, 1, list, h);
+}
+
+struct Part {     // tensors of one launch
+  std::vector<int> index;
+  int chunks = 0;
+};
+
+// The list in launches of at most kLarge tensors and 2^30 chunks.
+std::vector<Part> parts(const lopt_adamw_tensor* t, int n, int bits, int units) {
+  std::vector<Part> out;
+  for (int i = 0; i < n; ++i) {
+    if (t[i].n == 0 || (bits && t[i].moments != bits)) continue;
+    const int64_t chunk = (int64_t)units * kUnit;
+    const int chunks = (int)((t[i].n + chunk - 1) / chunk);
+    if (out.empty() || out.back().index.size() == (size_t)kLarge || (int64_t)out.back().chunks + chunks > (1 << 30))
+      out.emplace_back();
+    out.back().index.push_back(i);
+    out.back().chunks += chunks;
+  }
+  return out;
+}
+
+template <int N>
+void fill(List<N>& list, const lopt_adamw_tensor* t, const Part& part, int units, uint32_t seed) {
+  int at = 0;
+  for (size_t k = 0; k < part.index.size(); ++k) {
+    const lopt_adamw_tensor& x = t[part.index[k]];
+    Desc& d = list.d[k];
+    d = Desc{x.param, x.grad, x.m, x.v, x.m_scale, x.v_scale, x.copy, x.n,
+             mix(seed ^ ((uint32_t)(part.index[k] + 1) * 0x9e3779b9u)), at, (uint8_t)x.grad_type, (uint8_t)x.copy_type,
+             (uint8_t)x.decay, (uint8_t)all_aligned(x), 0};
+    const int64_t chunk = (int64_t)units * kUnit;
+    at += (int)((x.n + chunk - 1) / chunk);
+  }
+}
+
+// The list, as large as it has to be, to `f`.
+template <typename F>
+cudaError_t with_list(const lopt_adamw_tensor* t, const Part& part, int units, uint32_t seed, F f) {
+  if (part.index.size() <= (size_t)kSmall) {
+    List<kSmall> list{};
+    fill(list, t, part, units, seed);
+    return f(list);
+  }
+  List<kLarge> list{};
+  fill(list, t, part, units, seed);
+  return f(list);
+}
+
+int check_each(const lopt_adamw_tensor* t, int32_t n, std::vector<Range>* all) {
+  if (n < 0 || (n && !t)) return LOPT_E_ARG;
+  for (int32_t i = 0; i < n; ++i) {
+    Range r[7];
+    int count = 0;
+    const int rc = ranges(t[i], r, &count);
+    if (rc) return rc;
+    for (int a = 0; a < count; ++a)
+      for (int b = a + 1; b < count; ++b)
+        if (r[a].lo < r[b].hi && r[b].lo < r[a].hi) return LOPT_E_ALIAS;
+    if (all) all->insert(all->end(), r, r + count);
+  }
+  return LOPT_OK;
+}
+
+int step(const lopt_adamw_tensor* tensors, int32_t n, int64_t t, double lr, double beta1, double beta2, double eps,
+         double weight_decay, double max_norm, uint32_t seed, float* norm, void* workspace, int64_t workspace_bytes,
+         cudaStream_t s) {
+  if (t < 1 || !(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1) || !(eps >= 0) || !std::isfinite(eps) ||
+      !std::isfinite(lr) || !std::isfinite(weight_decay) || !(max_norm >= 0))
+    return LOPT_E_ARG;
+  int rc = check_each(tensors, n, nullptr);
+  if (rc) return rc;
+  const bool clipped = max_norm > 0;
+  double* part = static_cast<double*>(workspace);
+  if (clipped) {
+    int64_t need = 0;
+    lopt_adamw_workspace(&need);
+    if (!norm || !workspace || workspace_bytes < need) return LOPT_E_ARG;
+    if ((uintptr_t)workspace % 256 || (uintptr_t)norm % 4) return LOPT_E_ALIGN;
+    const uintptr_t lo = (uintptr_t)workspace, hi = lo + (uintptr_t)need, nl = (uintptr_t)norm, nh = nl + 4;
+    if (nl < hi && lo < nh) return LOPT_E_ALIAS;
+    for (int32_t i = 0; i < n; ++i) {
+      Range r[7];
+      int count = 0;
+      ranges(tensors[i], r, &count);
+      for (int k = 0; k < count; ++k)
+        if ((r[k].lo < hi && lo < r[k].hi) || (r[k].lo < nh && nl < r[k].hi)) return LOPT_E_ALIAS;
+    }
+  }
+  const int sms = sm_count();
+  int64_t units = 0;
+  for (int32_t i = 0; i < n; ++i) units += (tensors[i].n + kUnit - 1) / kUnit;
+  const int per = chunk_units(units, sms);
+  Hyper h;
+  h.b1 = (float)beta1, h.nb1 = (float)(1.0 - beta1), h.b2 = (float)beta2, h.nb2 = (float)(1.0 - beta2);
+  h.c1 = (float)(lr / (1.0 - std::pow(beta1, (double)t)));
+  h.c2 = (float)(1.0 / std::sqrt(1.0 - std::pow(beta2, (double)t)));
+  h.eps = (float)eps, h.keep = (float)(1.0 - lr * weight_decay), h.clip = nullptr, h.units = per;
+  cudaError_t e = cudaSuccess;
+  if (clipped) {
+    int count = 0;
+    const std::vector<Part> ps = parts(tensors, n, 0, per);
+    if (ps.size() > kMaxPartials / kNormBlocks) return LOPT_E_TOO_LARGE;
+    for (const Part& p : ps) {
+      const int blocks = std::min(p.chunks, kNormBlocks);
+      e = with_list(tensors, p, per, seed, [&](const auto& list) {
+        constexpr int N = sizeof(list.d) / sizeof(list.d[0]);
+        return launch(k_adamw_norm<N>, dim3((unsigned)blocks), dim3(kWarps * 32), 0, s, true, 1, list,
+                      (int)p.index.size(), per, p.chunks, part + count);
+      });
+      if (e != cudaSuccess) return done(e);
+      count += blocks;
+    }
+    float* clip = reinterpret_cast<float*>(part + kMaxPartials);
+    h.clip = clip;
+    e = launch(k_adamw_clip, dim3(1), dim3(256), 0, s, true, 1, (const double*)part, count, max_norm, norm, clip);
+    if (e != cudaSuccess) return done(e);
+  }
+  for (int bits : {32, 8}) {
+    for (const Part& p : parts(tensors, n, bits, per)) {
+      h.count = (int)p.index.size();
+      e = with_list(tensors, p, per, seed, [&](const auto& list) {
+        return bits == 8 ? launch_step<sizeof(list.d) / sizeof(list.d[0]), true>(list, h, p.chunks, s)
+                         : launch_step<sizeof(list.d) / sizeof(list.d[0]), false>(list, h, p.chunks, s);
+      });
+      if (e != cudaSuccess) return done(e);
+    }
+  }
+  return LOPT_OK;
+}
+
+}  // namespace
+}  // namespace train
+}  // namespace lopt
+
+using namespace lopt::train;
+
+extern "C" {
+
+int lopt_adamw_check(const lopt_adamw_tensor* tensors, int32_t n) try {
+  std::vector<Range> all;
+  const int rc = check_each(tensors, n, &all);
+  if (rc) return rc;
+  // Arrays in order of their address: one that is written may not reach into
+  // the next.  Gradients may share memory among themselves.
+  std::sort(all.begin(), all.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+  uintptr_t end = 0, end_written = 0;
+  for (const Range& r : all) {
+    if (r.lo < (r.in ? end_written : end)) return LOPT_E_ALIAS;
+    end = std::max(end, r.hi);
+    if (!r.in) end_written = std::max(end_written, r.hi);
+  }
+  return LOPT_OK;
+} catch (...) {
+  return LOPT_E_OOM;
+}
+
+int lopt_adamw_workspace(int64_t* bytes) {
+  if (!bytes) return LOPT_E_ARG;
+  *bytes = kMaxPartials * 8 + 256;   // partial sums, then the clip factor
+  return LOPT_OK;
+}
+
+int lopt_adamw_step(const lopt_adamw_tensor* tensors, int32_t n, int64_t t, double lr, double beta1, double beta2,
+                    double eps, double weight_decay, double max_norm, uint32_t seed, float* norm, void* workspace,
+                    int64_t workspace_bytes, void* stream) try {
+  return step(tensors, n, t, lr, beta1, beta2, eps, weight_decay, max_norm, seed, norm, workspace, workspace_bytes,
+              (cudaStream_t)stream);
+} catch (...) {
+  return LOPT_E_OOM;
+}
+
+int lopt_adamw_moments(const lopt_adamw_tensor* tensors, int32_t n, float* const* m, float* const* v, void* stream) try {
+  std::vector<Range> all;
+  int rc = check_each(tensors, n, &all);
+  if (rc) return rc;
+  if (n && (!m || !v)) return LOPT_E_ARG;
+  for (Range& r : all) r.in = true;
+  int64_t units = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    if (tensors[i].n == 0) continue;
+    for (float* p : {m[i], v[i]}) {
+      if (!p) return LOPT_E_ARG;
+      if ((uintptr_t)p % 4) return LOPT_E_ALIGN;
+      all.push_back(Range{(uintptr_t)p, (uintptr_t)(p + tensors[i].n), false});
+    }
+    units += (tensors[i].n + kUnit - 1) / kUnit;
+  }
+  std::sort(all.begin(), all.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+  uintptr_t end = 0, end_written = 0;
+  for (const Range& r : all) {
+    if (r.lo < (r.in ? end_written : end)) return LOPT_E_ALIAS;
+    end = std::max(end, r.hi);
+    if (!r.in) end_written = std::max(end_written, r.hi);
+  }
+  const int per = chunk_units(units, sm_count());
+  for (const Part& p : parts(tensors, n, 0, per)) {
+    Outs<kOuts> list{};
+    int at = 0;
+    for (size_t k = 0; k < p.index.size(); ++k) {
+      const int i = p.index[k];
+      const lopt_adamw_tensor& x = tensors[i];
+      const uintptr_t es = x.moments == 8 ? 4 : 16;
+      const bool vec = (uintptr_t)x.m % es == 0 && (uintptr_t)x.v % es == 0 && (uintptr_t)m[i] % 16 == 0 && (uintptr_t)v[i] % 16 == 0;
+      list.d[k] = Out{x.m, x.v, x.m_scale, x.v_scale, m[i], v[i], x.n, at, (uint8_t)(x.moments == 8), (uint8_t)vec};
+      const int64_t chunk = (int64_t)per * kUnit;
+      at += (int)((x.n + chunk - 1) / chunk);
+    }
+    const cudaError_t e = launch(k_adamw_moments, dim3((unsigned)p.chunks), dim3(kWarps * 32), 0, (cudaStream_t)stream,
+                                 false, 1, list, (int)p.index.size(), per);
+    if (e != cudaSuccess) return done(e);
+  }
+  return LOPT_OK;
+} catch (...) {
+  return LOPT_E_OOM;
+}
+
+}  // extern "C"
