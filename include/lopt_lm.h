@@ -63,6 +63,44 @@ int lopt_block_norm_backward(const void* grad_y, int type, int64_t rows, int64_t
                              int accumulate, void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
+ * Linear cross entropy.  x: [rows x cols] hidden states, weight: [classes x
+ * cols], the output table, both of `type` (LOPT_F16 or LOPT_BF16); target: an
+ * index per row, none where it is negative (padding; see lopt_train.h for those
+ * at or above `classes`).  With logits z = x weight^T, which are never stored:
+ *   lse[r] = log sum exp z[r],   loss[r] = row_weight[r] * (lse[r] - z[r][target[r]])
+ * row_weight may be NULL (1).  A row without a target or with weight 0 has loss
+ * 0; its lse is that of its logits, whatever they are.  loss and lse: fp32 [rows].
+ * Products are exact, sums fp32.
+ *
+ * Backward, for the sum of the rows' losses, with lse as the forward pass gave it:
+ *   G[r][j] = row_weight[r] * (exp(z[r][j] - lse[r]) - [j == target[r]])
+ *   grad_x = G weight,   grad_weight = G^T x
+ * Rows that do not count give zeros and add nothing, whatever they hold.  grad_x
+ * (of `type`) or grad_weight may be NULL.  grad_weight is of LOPT_F32, which
+ * accumulate = 1 adds to, or of `type`; G is rounded to 16 bits for the products
+ * (relative to 2^-15 of the largest row_weight at least), for an fp32 grad_weight
+ * to twice as many.
+ *
+ * Bit 1 of *status: a bounded wait (1 s) ran out; losses, lse and grad_x are then
+ * NaN and grad_weight is not valid.
+ * workspace: lopt_linear_ce_workspace() bytes for the direction, 256-byte aligned,
+ * any contents; aligned = 1 where the rows of x and weight start on 16-byte
+ * boundaries (others are copied first), grad_weight_type LOPT_F32 or other.
+ * rows and classes up to 2^22, cols up to 2^16.
+ */
+int lopt_linear_ce_workspace(int64_t rows, int64_t classes, int64_t cols, int aligned, int backward,
+                             int grad_weight_type, int64_t* bytes);
+int lopt_linear_ce_forward(const void* x, int type, int64_t rows, int64_t cols, int64_t x_stride, const void* weight,
+                           int64_t classes, int64_t weight_stride, const void* target, int index_type,
+                           const float* row_weight, float* loss, float* lse, void* workspace, int64_t workspace_bytes,
+                           int32_t* status, void* stream);
+int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols, int64_t x_stride, const void* weight,
+                            int64_t classes, int64_t weight_stride, const void* target, int index_type,
+                            const float* row_weight, const float* lse, void* grad_x, int64_t grad_x_stride,
+                            void* grad_weight, int grad_weight_type, int64_t grad_weight_stride, int accumulate,
+                            void* workspace, int64_t workspace_bytes, int32_t* status, void* stream);
+
+/*
  * AdamW.  For every element of every tensor, in fp32, each operation rounded
  * once (no fused multiply-add), with g the gradient times the clip factor:
  *   m = beta1 * m + (1 - beta1) * g

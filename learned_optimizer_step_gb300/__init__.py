@@ -7,7 +7,8 @@ from .lopt import (LearnedOptimizer, LoptError, PreparedList, TensorState,  # no
 
 _TRAIN_OPS = ("check_indices", "distill_forward", "distill_forward_backward", "embedding_backward",
               "embedding_forward", "layernorm_backward", "layernorm_forward", "release_workspaces")
-_LM_OPS = ("AdamW", "AdamWTensor", "block_norm_backward", "block_norm_forward")
+_LM_OPS = ("AdamW", "AdamWTensor", "block_norm_backward", "block_norm_forward", "linear_cross_entropy_backward",
+           "linear_cross_entropy_forward")
 
 
 def __getattr__(name):

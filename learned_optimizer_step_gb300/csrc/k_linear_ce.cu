@@ -1,0 +1,990 @@
+// Linear cross entropy: softmax cross entropy of hidden states x [N x D] against
+// an output table W [V x D] (see lopt_lm.h for the formulas).
+//
+// Three matrix products by one persistent kernel on the tensor cores, with what
+// surrounds them in its epilogues, so that logits never leave the SM:
+//
+//   loss     tile of x W^T  ->  each row's maximum, sum of exponentials and
+//                               target logit over the tile's classes
+//   grad     tile of x W^T  ->  G = (exp(logit - lse) - [target]) * weight, 16-bit
+//   grad_x   tile of G W        (sum over classes, in pieces of the vocabulary)
+//   grad_w   tile of G^T x      (sum over tokens)
+//
+// The backward pass goes over the vocabulary in chunks whose G fits a bounded
+// workspace; the chunk's grad_x is added to fp32 sums, its rows of grad_w are
+// written.  For a 32-bit grad_w, G is held as the sum of two 16-bit numbers
+// (16 bits of bfloat16, 22 of float16): rounded once to bfloat16 it would be off by
+// 2^-9, which is what a 16-bit grad_w is rounded by anyway.
+//
+// A pair of CTAs (cta_group::2) computes a 256 x 256 tile: each holds 128 rows of
+// A and 128 of B per 64-wide step of K in shared memory (TMA, 128-byte swizzle) and
+// 128 rows of the accumulator in its tensor memory, twice, so that a tile's
+// epilogue runs beside the next tile's product.  Roles: warp 0 loads, warp 1 of the
+// pair's first CTA issues, warps 4 to 11 are the epilogue.
+#include <algorithm>
+#include <cmath>
+#include <cuda.h>
+
+#include "lopt_lm.h"
+#include "tc_layout.cuh"
+#include "train_common.cuh"
+
+namespace lopt {
+namespace train {
+namespace {
+
+constexpr int kTile = 256;                       // rows and columns of a pair's tile
+constexpr int kHalf = 128;                       // ... of one CTA's part of an operand
+constexpr int kStep = 64;                        // K elements of a stage: 128 bytes
+constexpr int kStages = 6;
+constexpr int kOperand = kHalf * kStep * 2;      // bytes of one operand of a stage
+constexpr int kThreads = 384;
+constexpr int kEpilogueWarps = 8;
+constexpr size_t kSmem = (size_t)kStages * 2 * kOperand + 1024 + 256;
+constexpr int kRowGroup = 32;                    // tiles of rows that share the classes' operand in L2
+constexpr uint64_t kLimitNs = 1000000000ull;
+constexpr float kLog2e = 1.4426950408889634f;
+
+enum Mode { kLoss = 0, kGrad = 1, kGradX = 2, kGradW = 3 };
+
+// One kind of tiles of a launch.
+struct Job {
+  int mode, first, tiles;      // its tiles are [first, first + tiles) of the launch
+  int m_tiles, n_tiles, splits;
+  int k_steps;                 // of the whole product
+  int buffer;                  // which G
+  int v0, v1;                  // classes of the chunk
+  int add;                     // grad_x: add to the sums
+};
+constexpr int kJobs = 3;
+
+struct Maps {
+  CUtensorMap x_k, x_m, w_k, w_m, g_k[2], g_m[2], g_low[2];
+};
+
+struct Args {
+  int rows, classes, cols;
+  int planes;                  // 2: G in two parts
+  int is_bf16;
+  const void* target;
+  int index_type;
+  const float* row_weight;     // NULL: 1
+  const float* lse;
+  float2* part;                // [2 * class tiles][rows]: maximum, sum
+  float* chosen;               // [rows] target logits
+  void* g[2][2];               // [buffer][part]
+  int64_t g_stride;
+  const int* exponent;         // G is scaled by 2^(15 - *exponent)
+  float* dx;
+  int64_t dx_stride, dx_slice;
+  void* dw;
+  int dw_type, accumulate;
+  int64_t dw_stride;
+  int* gave_up;                // one word per CTA
+  int32_t* status;
+  Job job[kJobs];
+  int jobs, tiles;
+};
+
+// ---- PTX -----------------------------------------------------------------------
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A box of a matrix to this CTA's shared memory; its bytes count on the
+// barrier of the pair's first CTA.
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
+      :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n"
+      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+// Arrives on the barrier at this offset of both CTAs once the products issued so far are done.
+__device__ __forceinline__ void pair_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+               :: "r"(bar), "h"((uint16_t)3) : "memory");
+}
+__device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+// Bounded: gives up after a second, or when another warp of the CTA has.
+static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort) {
+  const uint64_t t0 = global_ns();
+  for (uint32_t it = 0; it < (1u << 30); ++it) {
+    if (try_wait(bar, parity)) return true;
+    if ((it & 15) == 15) {
+      if (*abort) return false;
+      if (global_ns() - t0 > kLimitNs) break;
+    }
+  }
+  *abort = 1;
+  return false;
+}
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return try_wait(bar, parity) || wait_slow(bar, parity, abort);
+}
+__device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               :: "l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Shared-memory descriptors, 128-byte swizzle, groups of eight 128-byte rows 1024
+// bytes apart.  K along the rows: the operand is one box of 128 rows.  K across
+// them: two boxes of 64 columns each, 8192 bytes apart.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool k_rows) {
+  return (uint64_t)((addr >> 4) & 0x3fff) | (uint64_t)(k_rows ? 1 : 8192 >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// ---- tiles ---------------------------------------------------------------------
+struct Tile {
+  int m, n, split, k0, k1;   // K steps [k0, k1)
+};
+
+__device__ __forceinline__ Tile tile_of(const Job& j, int t) {
+  Tile r;
+  if (j.mode <= kGrad) {
+    // Rows fastest, in groups that stay in L2 while the classes pass by.
+    const int group = t / (kRowGroup * j.n_tiles), left = t - group * kRowGroup * j.n_tiles;
+    const int in_group = min(kRowGroup, j.m_tiles - group * kRowGroup);
+    r.n = left / in_group;
+    r.m = group * kRowGroup + left - r.n * in_group;
+    r.split = 0;
+  } else {
+    r.n = t % j.n_tiles;
+    t /= j.n_tiles;
+    r.split = t % j.splits;
+    r.m = t / j.splits;
+  }
+  r.k0 = (int)((int64_t)j.k_steps * r.split / j.splits);
+  r.k1 = (int)((int64_t)j.k_steps * (r.split + 1) / j.splits);
+  return r;
+}
+__device__ __forceinline__ const Job& job_of(const Args& a, int t) {
+  int k = 0;
+  while (k + 1 < a.jobs && t >= a.job[k + 1].first) ++k;
+  return a.job[k];
+}
+
+// ---- epilogues: 32 columns of a row at a time ------------------------------------
+__device__ __forceinline__ void as_floats(const uint32_t (&r)[32], float (&v)[32]) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
+}
+
+// `get(c)` gives the 32 columns from 32 * c on, c < 4.
+template <typename Get>
+__device__ __forceinline__ void loss_tile(const Args& a, const Job& j, const Tile& t, int row, int col, int half, Get get) {
+  int64_t target = -1;
+  if (row < a.rows) target = load_index(a.target, row, a.index_type);
+  float most = -INFINITY, sum = 0.f;
+  for (int c = 0; c < 4; ++c) {
+    float v[32];
+    get(c, v);
+    const int c0 = col + 32 * c;
+    if (c0 + 32 > a.classes) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (c0 + k >= a.classes) v[k] = -INFINITY;
+    }
+    const int64_t at = target - c0;
+    if (at >= 0 && at < 32 && target < a.classes) {
+      float x = 0.f;
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (at == k) x = v[k];
+      a.chosen[row] = x;
+    }
+    float m = most;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) m = fmaxf(m, v[k]);
+    // Nothing but -inf so far: 0 keeps exponents of it at 0.
+    const float base = m == -INFINITY ? 0.f : m;
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+      s0 += exp2_fast((v[k] - base) * kLog2e);
+      s1 += exp2_fast((v[k + 1] - base) * kLog2e);
+    }
+    sum = fmaf(sum, exp2_fast((most - base) * kLog2e), s0 + s1);
+    most = m;
+  }
+  if (row < a.rows) a.part[(int64_t)(2 * t.n + half) * a.rows + row] = make_float2(most, sum);
+}
+
+template <typename T, typename Get>
+__device__ __forceinline__ void grad_tile(const Args& a, const Job& j, const Tile& t, int row, int col, Get get) {
+  int64_t target = -1;
+  float lse = 0.f, scale = 0.f;
+  const bool live = row < a.rows;
+  if (live) {
+    target = load_index(a.target, row, a.index_type);
+    if (target >= 0 && target < a.classes) scale = a.row_weight ? a.row_weight[row] : 1.f;
+    lse = a.lse[row];
+    scale = scalbnf(scale, 15 - *a.exponent);
+  }
+  const int64_t out = (int64_t)row * a.g_stride + (col - j.v0);
+  for (int c = 0; c < 4; ++c) {
+    float v[32];
+    get(c, v);
+    const int c0 = col + 32 * c;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = exp2_fast((v[k] - lse) * kLog2e);
+    const int64_t at = target - c0;
+    if (at >= 0 && at < 32) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (at == k) v[k] -= 1.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] *= scale;
+    // Rows that do not count, whatever their logits hold, and classes past the last.
+    if (scale == 0.f || c0 + 32 > a.classes) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (scale == 0.f || c0 + k >= a.classes) v[k] = 0.f;
+    }
+    if (!live) continue;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t hi[8], lo[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float x = v[16 * h + 2 * k], y = v[16 * h + 2 * k + 1];
+        Pack<T, 2> p, q;
+        p.v[0] = from_f<T>(x);
+        p.v[1] = from_f<T>(y);
+        q.v[0] = from_f<T>(x - to_f(p.v[0]));
+        q.v[1] = from_f<T>(y - to_f(p.v[1]));
+        hi[k] = *reinterpret_cast<const uint32_t*>(&p);
+        lo[k] = *reinterpret_cast<const uint32_t*>(&q);
+      }
+      store32(static_cast<T*>(a.g[j.buffer][0]) + out + 32 * c + 16 * h, hi);
+      if (a.planes == 2) store32(static_cast<T*>(a.g[j.buffer][1]) + out + 32 * c + 16 * h, lo);
+    }
+  }
+}
+
+template <typename Get>
+__device__ __forceinline__ void grad_x_tile(const Args& a, const Job& j, const Tile& t, int row, int col, Get get) {
+  float* out = a.dx + t.split * a.dx_slice + (int64_t)row * a.dx_stride + col;
+  for (int c = 0; c < 4; ++c) {
+    float v[32];
+    get(c, v);
+    if (row >= a.rows) continue;
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+      if (col + 32 * c + k >= a.dx_stride) continue;
+      float4* p = reinterpret_cast<float4*>(out + 32 * c + k);
+      float4 x = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+      if (j.add) {
+        const float4 o = *p;
+        x = make_float4(x.x + o.x, x.y + o.y, x.z + o.z, x.w + o.w);
+      }
+      *p = x;
+    }
+  }
+}
+
+template <typename O, int VEC>
+__device__ __forceinline__ void put(O* p, int left, bool add, float f1, float f2, const float (&v)[32]) {
+#pragma unroll
+  for (int k = 0; k < 32; k += VEC) {
+    if (k >= left) continue;
+    float o[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) o[e] = v[k + e] * f1 * f2;
+    Pack<O, VEC>* q = reinterpret_cast<Pack<O, VEC>*>(p + k);
+    if (add) {
+      float b[VEC];
+      to_floats(*q, b);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) o[e] += b[e];
+    }
+    *q = from_floats<O, VEC>(o);
+  }
+}
+// As many elements at a time as the rows' alignment allows: 16 bytes or one.
+template <typename O, typename Get>
+__device__ __forceinline__ void grad_w_tile(const Args& a, const Job& j, int v, int col, Get get) {
+  const int down = *a.exponent - 15, d1 = down / 2;
+  const float f1 = scalbnf(1.f, d1), f2 = scalbnf(1.f, down - d1);
+  constexpr int VEC = 16 / sizeof(O);
+  O* out = static_cast<O*>(a.dw) + (int64_t)v * a.dw_stride + col;
+  const bool vec = (a.cols % VEC == 0) && (a.dw_stride % VEC == 0) && (reinterpret_cast<uintptr_t>(a.dw) % 16 == 0);
+  for (int c = 0; c < 4; ++c) {
+    float x[32];
+    get(c, x);
+    if (v >= j.v1) continue;
+    const int left = a.cols - (col + 32 * c);
+    if (vec) put<O, VEC>(out + 32 * c, left, a.accumulate, f1, f2, x);
+    else put<O, 1>(out + 32 * c, left, a.accumulate, f1, f2, x);
+  }
+}
+
+// ---- the kernel ------------------------------------------------------------------
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    k_linear_ce(const __grid_constant__ Maps maps, const __grid_constant__ Args a) {
+  extern __shared__ uint8_t raw[];
+  __shared__ uint64_t s_full[kStages], s_empty[kStages], s_acc_full[2], s_acc_empty[2];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cta_rank();
+  const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  const uint32_t stages = (smem_u32(raw) + 1023) & ~1023u;
+  volatile int* abort = &s_abort;
+  if (threadIdx.x == 0) {
+    s_abort = 0;
+    for (int k = 0; k < kStages; ++k) {
+      mbar_init(&s_full[k], 1);
+      mbar_init(&s_empty[k], 1);
+    }
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(&s_acc_full[k], 1);
+      mbar_init(&s_acc_empty[k], 2 * kEpilogueWarps);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(smem_u32(&s_tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  __syncwarp();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  wait_for_previous();
+  let_next_start();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int t = pair; t < a.tiles; t += pairs) {
+        const Job& j = job_of(a, t);
+        const Tile x = tile_of(j, t - j.first);
+        const int m0 = x.m * kTile + rank * kHalf, n0 = x.n * kTile + rank * kHalf;
+        for (int k = x.k0; k < x.k1; ++k) {
+          if (!wait_for(smem_u32(&s_empty[stage]), phase ^ 1, abort)) break;
+          const uint32_t sa = stages + stage * 2 * kOperand, sb = sa + kOperand;
+          const uint32_t bar = in_cta(smem_u32(&s_full[stage]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&s_full[stage], 4 * kOperand);
+          const int kk = k * kStep;
+          if (j.mode <= kGrad) {
+            load_box(sa, &maps.x_k, kk, m0, bar);
+            load_box(sb, &maps.w_k, kk, j.v0 + n0, bar);
+          } else if (j.mode == kGradX) {
+            load_box(sa, &maps.g_k[j.buffer], kk, m0, bar);
+            load_box(sb, &maps.w_m, n0, j.v0 + kk, bar);
+            load_box(sb + kOperand / 2, &maps.w_m, n0 + 64, j.v0 + kk, bar);
+          } else {
+            // Both parts of G against the same tokens, one after the other.
+            const int y = (a.planes == 2 ? k >> 1 : k) * kStep;
+            const CUtensorMap* g = a.planes == 2 && (k & 1) ? &maps.g_low[j.buffer] : &maps.g_m[j.buffer];
+            load_box(sa, g, m0, y, bar);
+            load_box(sa + kOperand / 2, g, m0 + 64, y, bar);
+            load_box(sb, &maps.x_m, n0, y, bar);
+            load_box(sb + kOperand / 2, &maps.x_m, n0 + 64, y, bar);
+          }
+          if (++stage == kStages) stage = 0, phase ^= 1;
+        }
+        if (*abort) break;
+      }
+      // No stage is left with the pair's barriers still to be told of it.
+      for (int k = 0; k < kStages && !*abort; ++k) {
+        wait_for(smem_u32(&s_empty[stage]), phase ^ 1, abort);
+        if (++stage == kStages) stage = 0, phase ^= 1;
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      for (int t = pair; t < a.tiles; t += pairs) {
+        const Job& j = job_of(a, t);
+        const Tile x = tile_of(j, t - j.first);
+        const bool ak = j.mode != kGradW, bk = j.mode <= kGrad;   // K along the rows of A, B
+        const uint32_t idesc = (1u << 4) | ((uint32_t)a.is_bf16 << 7) | ((uint32_t)a.is_bf16 << 10) | (ak ? 0u : 1u << 15) |
+                               (bk ? 0u : 1u << 16) | ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+        // 16 of K further: 32 bytes along the rows, two groups of eight rows across.
+        const uint32_t step_a = (ak ? 32 : 2048) >> 4, step_b = (bk ? 32 : 2048) >> 4;
+        if (!wait_for(smem_u32(&s_acc_empty[buf]), acc_phase ^ 1, abort)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + buf * kTile;
+        for (int k = x.k0; k < x.k1; ++k) {
+          if (!wait_for(smem_u32(&s_full[stage]), phase, abort)) break;
+          tc_fence_after();
+          const uint32_t sa = stages + stage * 2 * kOperand;
+          const uint64_t da = operand_desc(sa, ak), db = operand_desc(sa + kOperand, bk);
+#pragma unroll
+          for (int q = 0; q < kStep / 16; ++q) pair_mma(d, da + q * step_a, db + q * step_b, idesc, k > x.k0 || q > 0);
+          pair_commit(smem_u32(&s_empty[stage]));
+          if (++stage == kStages) stage = 0, phase ^= 1;
+        }
+        if (*abort) break;
+        pair_commit(smem_u32(&s_acc_full[buf]));
+        if (++buf == 2) buf = 0, acc_phase ^= 1;
+      }
+    }
+  } else if (warp >= 4) {
+    const int quarter = warp % 4, half = (warp - 4) / 4;
+    int buf = 0;
+    uint32_t phase = 0;
+    for (int t = pair; t < a.tiles; t += pairs) {
+      const Job& j = job_of(a, t);
+      const Tile x = tile_of(j, t - j.first);
+      const bool ok = wait_for(smem_u32(&s_acc_full[buf]), phase, abort);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTile + half * kHalf;
+      auto get = [&](int c, float (&v)[32]) {
+        if (x.k0 == x.k1) {      // a slice without classes: nothing was issued
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = 0.f;
+          return;
+        }
+        uint32_t r[32];
+        __syncwarp();
+        tmem_ld32(src + 32 * c, r);
+        tmem_wait_ld();
+        as_floats(r, v);
+      };
+      const int row = x.m * kTile + rank * kHalf + quarter * 32 + lane;
+      const int col = x.n * kTile + half * kHalf;
+      if (j.mode == kLoss) {
+        loss_tile(a, j, x, row, j.v0 + col, half, get);
+      } else if (j.mode == kGrad) {
+        if (a.is_bf16) grad_tile<__nv_bfloat16>(a, j, x, row, j.v0 + col, get);
+        else grad_tile<__half>(a, j, x, row, j.v0 + col, get);
+      } else if (j.mode == kGradX) {
+        grad_x_tile(a, j, x, row, col, get);
+      } else if (a.dw_type == LOPT_F32) {
+        grad_w_tile<float>(a, j, j.v0 + row, col, get);
+      } else if (a.dw_type == LOPT_F16) {
+        grad_w_tile<__half>(a, j, j.v0 + row, col, get);
+      } else {
+        grad_w_tile<__nv_bfloat16>(a, j, j.v0 + row, col, get);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_at(in_cta(smem_u32(&s_acc_empty[buf]), 0));
+      if (++buf == 2) buf = 0, phase ^= 1;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    // A forward launch says so either way, a backward one into cleared words.
+    if (s_abort || a.lse == nullptr) a.gave_up[blockIdx.x] = s_abort;
+    if (s_abort) {
+      if (a.status) atomicOr(a.status, kStatusGaveUp);
+      // Copies and products in flight end long before this.
+      const uint64_t t0 = global_ns();
+      for (uint32_t it = 0; it < (1u << 28) && global_ns() - t0 < 100000000ull; ++it) __nanosleep(1000);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  __syncwarp();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
+}
+
+// ---- the rows' losses from the tiles' statistics -----------------------------------
+__global__ void __launch_bounds__(512) k_linear_ce_rows(const float2* part, int parts, const float* chosen, const int* gave_up,
+                                                        int ctas, int64_t rows, int classes, const void* target,
+                                                        int index_type, const float* row_weight, float* loss,
+                                                        float* lse, int32_t* status) {
+  __shared__ float2 red[16][32];
+  __shared__ int s_bad;
+  const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
+  const int64_t row = (int64_t)blockIdx.x * 32 + lane;
+  if (threadIdx.x == 0) s_bad = 0;
+  wait_for_previous();
+  __syncthreads();
+  if (threadIdx.x < ctas && gave_up[threadIdx.x]) s_bad = 1;
+  float m = -INFINITY, s = 0.f;
+  auto join = [&](float2 p) {
+    const float top = fmaxf(m, p.x), base = top == -INFINITY ? 0.f : top;
+    s = s * exp2_fast((m - base) * kLog2e) + p.y * exp2_fast((p.x - base) * kLog2e);
+    m = top;
+  };
+  if (row < rows) {
+#pragma unroll 4
+    for (int k = w; k < parts; k += 16) join(part[(int64_t)k * rows + row]);
+  }
+  red[w][lane] = make_float2(m, s);
+  __syncthreads();
+  if (w || row >= rows) return;
+  m = -INFINITY, s = 0.f;
+  for (int k = 0; k < 16; ++k) join(red[k][lane]);
+  const float all = m == -INFINITY && s == 0.f ? -INFINITY : m + logf(s);
+  const int64_t t = load_index(target, row, index_type);
+  const float weight = row_weight ? row_weight[row] : 1.f;
+  if (t >= classes && status) atomicOr(status, kStatusIndex);
+  float l = 0.f;
+  if (t >= 0 && t < classes && weight != 0.f) l = weight * (all - chosen[row]);
+  loss[row] = s_bad ? NAN : l;
+  lse[row] = s_bad ? NAN : all;
+}
+
+// ---- before and after the backward products ------------------------------------------
+// Rows of 16-bit elements to rows that TMA can read.  With targets, rows that
+// do not count become zeros, whatever they hold, and the largest weight's
+// exponent is found.
+__global__ void __launch_bounds__(256) k_linear_ce_copy(const uint16_t* x, int64_t stride, int64_t rows, int cols, uint16_t* out,
+                                                        int64_t out_stride, const void* target, int index_type,
+                                                        int classes, const float* row_weight, int* exponent,
+                                                        int32_t* status) {
+  const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  wait_for_previous();
+  if (row >= rows) return;
+  bool live = true;
+  if (target) {
+    const int64_t t = load_index(target, row, index_type);
+    const float w = row_weight ? row_weight[row] : 1.f;
+    live = t >= 0 && t < classes && w != 0.f;
+    if (lane == 0) {
+      if (t >= classes && status) atomicOr(status, kStatusIndex);
+      // The least e with |w| < 2^e.
+      if (live && isfinite(w)) atomicMax(exponent, ilogbf(w) + 1);
+    }
+  }
+  const uint16_t* p = x + row * stride;
+  uint16_t* q = out + row * out_stride;
+  if (cols % 8 == 0 && stride % 8 == 0 && (uintptr_t)x % 16 == 0) {
+    for (int j = lane * 8; j < cols; j += 256)
+      *reinterpret_cast<uint4*>(q + j) = live ? *reinterpret_cast<const uint4*>(p + j) : make_uint4(0, 0, 0, 0);
+  } else {
+    for (int j = lane; j < cols; j += 32) q[j] = live ? p[j] : 0;
+  }
+}
+
+__global__ void k_linear_ce_start(int* exponent, int* gave_up) {
+  if (threadIdx.x == 0) *exponent = -200;
+  gave_up[threadIdx.x] = 0;
+}
+
+// grad_x from the sums of its slices, in order.
+template <typename T>
+__global__ void __launch_bounds__(256) k_linear_ce_grad_x(const float* dx, int64_t dx_stride, int64_t slice, int slices,
+                                                          int64_t rows, int cols, const int* exponent, const void* target,
+                                                          int index_type, int classes, const float* row_weight,
+                                                          const int* gave_up, int ctas, T* out, int64_t out_stride) {
+  __shared__ int s_bad;
+  if (threadIdx.x == 0) s_bad = 0;
+  wait_for_previous();
+  __syncthreads();
+  if (threadIdx.x < ctas && gave_up[threadIdx.x]) s_bad = 1;
+  __syncthreads();
+  const int64_t row = (int64_t)blockIdx.x;
+  const int64_t t = load_index(target, row, index_type);
+  const float w = row_weight ? row_weight[row] : 1.f;
+  const bool live = t >= 0 && t < classes && w != 0.f;
+  const int down = *exponent - 15, d1 = down / 2;
+  const float f1 = scalbnf(1.f, d1), f2 = scalbnf(1.f, down - d1);
+  const float* p = dx + row * dx_stride;
+  T* q = out + row * out_stride;
+  const bool vec = cols % 4 == 0 && out_stride % 4 == 0 && (uintptr_t)out % (4 * sizeof(T)) == 0;
+  if (vec) {
+    for (int j = (blockIdx.y * 256 + threadIdx.x) * 4; j < cols; j += 1024 * gridDim.y) {
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      if (live) {
+        for (int s = 0; s < slices; ++s) {
+          const float4 x = *reinterpret_cast<const float4*>(p + s * slice + j);
+          v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = s_bad ? NAN : v[e] * f1 * f2;
+      *reinterpret_cast<Pack<T, 4>*>(q + j) = from_floats<T, 4>(v);
+    }
+  } else {
+    for (int j = blockIdx.y * 256 + threadIdx.x; j < cols; j += 256 * gridDim.y) {
+      float v = 0.f;
+      if (live)
+        for (int s = 0; s < slices; ++s) v += p[s * slice + j];
+      q[j] = from_f<T>(s_bad ? NAN : v * f1 * f2);
+    }
+  }
+}
+
+// ---- host ----------------------------------------------------------------------
+constexpr int64_t kMaxTokens = (int64_t)1 << 22, kMaxClasses = (int64_t)1 << 22, kMaxWidth = (int64_t)1 << 16;
+constexpr int64_t kLossRows = 32768;               // most rows of a forward launch
+constexpr int64_t kPartBytes = (int64_t)256 << 20;    // of its statistics
+constexpr int kPairs = 76;                         // of a GB300: what a split of the classes counts on
+constexpr int64_t kChunkBytes = (int64_t)256 << 20;   // of one G
+constexpr int kMaxSplits = 64;
+constexpr int kMaxCtas = 256;
+
+int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+
+// Rows that TMA reads in place.
+bool tma_rows(const Span& s) {
+  return s.lo() % 16 == 0 && (s.rows == 1 || (s.stride * 2 % 16 == 0 && s.stride >= s.cols && s.stride < (int64_t)1 << 38));
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encoder() {
+  static const EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+// A matrix of 16-bit elements, read in boxes of 64 columns and `box` rows.
+bool make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64_t stride, int box, bool bf16) {
+  const EncodeTiled fn = encoder();
+  if (!fn) return false;
+  if (rows == 1) stride = up(cols, 8);
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
+  const cuuint32_t boxes[2] = {kStep, (cuuint32_t)box}, steps[2] = {1, 1};
+  return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(p), dims,
+            strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Pairs of CTAs that run at once on this device.
+int pair_count() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
+  int n = known[dev & 63].load(std::memory_order_relaxed);
+  if (n) return n;
+  allow_smem(reinterpret_cast<const void*>(&k_linear_ce), kSmem);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = 2;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, k_linear_ce, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = sm_count() / 2;
+  }
+  n = std::min(std::max(n, 1), kMaxCtas / 2);
+  known[dev & 63].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+cudaError_t launch_tiles(const Maps& maps, Args& a, int pairs, cudaStream_t s) {
+  a.tiles = a.job[a.jobs - 1].first + a.job[a.jobs - 1].tiles;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&k_linear_ce), kSmem);
+  if (e != cudaSuccess) return e;
+  return launch(k_linear_ce, dim3(2 * (unsigned)std::min(pairs, a.tiles)), dim3(kThreads), kSmem, s, true, 1, maps, a);
+}
+
+// Where things are in the workspace, in bytes from its start.
+struct Plan {
+  int64_t x = 0, w = 0, part = 0, chosen = 0, g = 0, g_plane = 0, dx = 0, flags = 0, exponent = 0, size = 0;
+  int64_t x_stride, w_stride, chunk = 0, dx_stride = 0, slice = 0;
+  int splits = 1, buffers = 1;
+};
+
+int64_t take(Plan& p, int64_t bytes) {
+  const int64_t at = p.size;
+  p.size += up(bytes, 1024);
+  return at;
+}
+
+// copy: also room for rows that TMA cannot read.
+Plan plan_loss(int64_t rows, int64_t classes, int64_t cols, bool copy) {
+  Plan p;
+  p.x_stride = p.w_stride = up(cols, 8);
+  const int64_t parts = 2 * up(classes, kTile) / kTile;
+  p.chunk = std::min(rows, std::min(kLossRows, std::max<int64_t>(kPartBytes / (parts * 8) / kTile, 1) * kTile));
+  p.flags = take(p, kMaxCtas * 4);
+  p.part = take(p, parts * p.chunk * 8);
+  p.chosen = take(p, p.chunk * 4);
+  if (copy) {
+    p.x = take(p, rows * p.x_stride * 2);
+    p.w = take(p, classes * p.w_stride * 2);
+  }
+  return p;
+}
+
+Plan plan_grad(int64_t rows, int64_t classes, int64_t cols, int planes, bool copy) {
+  Plan p;
+  p.x_stride = p.w_stride = up(cols, 8);
+  p.flags = take(p, kMaxCtas * 4);
+  p.exponent = take(p, 4);
+  p.x = take(p, rows * p.x_stride * 2);
+  if (copy) p.w = take(p, classes * p.w_stride * 2);
+  const int64_t all = up(classes, kTile);
+  p.chunk = std::min(all, std::max<int64_t>(kChunkBytes / (rows * 2 * planes) / kTile, 1) * kTile);
+  p.buffers = p.chunk < all ? 2 : 1;
+  p.g_plane = up(rows * p.chunk * 2, 1024);
+  p.g = take(p, p.g_plane * planes * p.buffers);
+  p.dx_stride = up(cols, 8);
+  p.slice = up(rows * p.dx_stride, 256);
+  // Few tiles of grad_x: the classes are split over slices, added in order at the end.
+  const int64_t tiles = up(rows, kTile) / kTile * (up(cols, kTile) / kTile), steps = p.chunk / kStep;
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({kPairs / tiles, steps / 4, kMaxSplits}));
+  p.dx = take(p, p.slice * p.splits * 4);
+  return p;
+}
+
+struct Call {
+  const void *x, *w, *target;
+  const float* row_weight;
+  int type, index_type;
+  int64_t rows, classes, cols;
+  Span mx, mw;
+};
+
+int check_call(const Call& c) {
+  if (c.type != LOPT_F16 && c.type != LOPT_BF16) return LOPT_E_ARG;
+  if (!index_size(c.index_type)) return LOPT_E_ARG;
+  if (c.rows < 0 || c.rows > kMaxTokens || c.classes < 1 || c.classes > kMaxClasses || c.cols < 1 || c.cols > kMaxWidth)
+    return LOPT_E_SHAPE;
+  int rc;
+  if ((rc = check_matrix(c.mw, false))) return rc;
+  if (c.rows == 0) return LOPT_OK;
+  if ((rc = check_matrix(c.mx, false))) return rc;
+  if (!c.target) return LOPT_E_ARG;
+  if ((uintptr_t)c.target % index_size(c.index_type) || (uintptr_t)c.row_weight % 4) return LOPT_E_ALIGN;
+  return LOPT_OK;
+}
+
+int check_alias(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (auto o = outs.begin(); o != outs.end(); ++o) {
+    for (auto p = o + 1; p != outs.end(); ++p)
+      if (overlap(*o, *p)) return LOPT_E_ALIAS;
+    for (const Span& i : ins)
+      if (overlap(*o, i)) return LOPT_E_ALIAS;
+  }
+  return LOPT_OK;
+}
+
+}  // namespace
+}  // namespace train
+}  // namespace lopt
+
+using namespace lopt::train;
+
+extern "C" {
+
+int lopt_linear_ce_workspace(int64_t rows, int64_t classes, int64_t cols, int aligned, int backward,
+                             int grad_weight_type, int64_t* bytes) {
+  if (!bytes || (aligned != 0 && aligned != 1) || (backward != 0 && backward != 1) || (backward && !type_size(grad_weight_type))) return LOPT_E_ARG;
+  if (rows < 0 || rows > kMaxTokens || classes < 1 || classes > kMaxClasses || cols < 1 || cols > kMaxWidth) return LOPT_E_SHAPE;
+  const int64_t n = std::max<int64_t>(rows, 1);
+  *bytes = backward ? plan_grad(n, classes, cols, grad_weight_type == LOPT_F32 ? 2 : 1, !aligned).size
+                    : plan_loss(n, classes, cols, !aligned).size;
+  return LOPT_OK;
+}
+
+int lopt_linear_ce_forward(const void* x, int type, int64_t rows, int64_t cols, int64_t x_stride, const void* weight,
+                           int64_t classes, int64_t weight_stride, const void* target, int index_type,
+                           const float* row_weight, float* loss, float* lse, void* workspace, int64_t workspace_bytes,
+                           int32_t* status, void* stream) {
+  const Call c{x, weight, target, row_weight, type, index_type, rows, classes, cols,
+               Span{x, rows, cols, x_stride, 2}, Span{weight, classes, cols, weight_stride, 2}};
+  int rc = check_call(c);
+  if (rc || rows == 0) return rc;
+  const Plan p = plan_loss(rows, classes, cols, !tma_rows(c.mx) || !tma_rows(c.mw));
+  if (!loss || !lse || !workspace || workspace_bytes < p.size) return LOPT_E_ARG;
+  if ((uintptr_t)loss % 4 || (uintptr_t)lse % 4 || (uintptr_t)status % 4 || (uintptr_t)workspace % 256) return LOPT_E_ALIGN;
+  const Span so{loss, 1, rows, rows, 4}, sl{lse, 1, rows, rows, 4}, sw{workspace, 1, p.size, p.size, 1};
+  const Span st{target, 1, rows, rows, index_size(index_type)}, sr{row_weight, 1, rows, rows, 4};
+  if ((rc = check_alias({so, sl, sw}, {c.mx, c.mw, st, sr}))) return rc;
+  cudaStream_t s = (cudaStream_t)stream;
+  char* ws = static_cast<char*>(workspace);
+  const bool bf16 = type == LOPT_BF16;
+  cudaError_t e;
+  const void *xp = x, *wp = weight;
+  int64_t xs = x_stride, wst = weight_stride;
+  if (!tma_rows(c.mx)) {
+    xp = ws + p.x, xs = p.x_stride;
+    e = launch(k_linear_ce_copy, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, true, 1, (const uint16_t*)x, x_stride, rows,
+               (int)cols, (uint16_t*)xp, xs, (const void*)nullptr, 0, 0, (const float*)nullptr, (int*)nullptr, (int32_t*)nullptr);
+    if (e != cudaSuccess) return done(e);
+  }
+  if (!tma_rows(c.mw)) {
+    wp = ws + p.w, wst = p.w_stride;
+    e = launch(k_linear_ce_copy, dim3((unsigned)((classes + 7) / 8)), dim3(256), 0, s, true, 1, (const uint16_t*)weight, weight_stride,
+               classes, (int)cols, (uint16_t*)wp, wst, (const void*)nullptr, 0, 0, (const float*)nullptr, (int*)nullptr,
+               (int32_t*)nullptr);
+    if (e != cudaSuccess) return done(e);
+  }
+  const int pairs = pair_count();
+  const int n_tiles = (int)(up(classes, kTile) / kTile);
+  for (int64_t r0 = 0; r0 < rows; r0 += p.chunk) {
+    const int64_t n = std::min(p.chunk, rows - r0);
+    Maps maps{};
+    Args a{};
+    if (!make_map(&maps.x_k, static_cast<const uint16_t*>(xp) + r0 * xs, n, cols, xs, kHalf, bf16) ||
+        !make_map(&maps.w_k, wp, classes, cols, wst, kHalf, bf16))
+      return LOPT_E_UNSUPPORTED;
+    a.rows = (int)n, a.classes = (int)classes, a.cols = (int)cols, a.is_bf16 = bf16, a.planes = 1;
+    a.target = static_cast<const char*>(target) + r0 * index_size(index_type), a.index_type = index_type;
+    a.part = reinterpret_cast<float2*>(ws + p.part), a.chosen = reinterpret_cast<float*>(ws + p.chosen);
+    a.gave_up = reinterpret_cast<int*>(ws + p.flags), a.status = status;
+    const int m_tiles = (int)(up(n, kTile) / kTile);
+    a.jobs = 1;
+    a.job[0] = Job{kLoss, 0, m_tiles * n_tiles, m_tiles, n_tiles, 1, (int)(up(cols, kStep) / kStep), 0, 0, (int)classes, 0};
+    if ((e = launch_tiles(maps, a, pairs, s)) != cudaSuccess) return done(e);
+    const float* rw = row_weight ? row_weight + r0 : nullptr;
+    e = launch(k_linear_ce_rows, dim3((unsigned)((n + 31) / 32)), dim3(512), 0, s, true, 1, (const float2*)a.part, 2 * n_tiles,
+               (const float*)a.chosen, (const int*)a.gave_up, 2 * std::min(pairs, a.tiles), n, (int)classes, a.target,
+               index_type, rw, loss + r0, lse + r0, status);
+    if (e != cudaSuccess) return done(e);
+  }
+  return LOPT_OK;
+}
+
+int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols, int64_t x_stride, const void* weight,
+                            int64_t classes, int64_t weight_stride, const void* target, int index_type,
+                            const float* row_weight, const float* lse, void* grad_x, int64_t grad_x_stride,
+                            void* grad_weight, int grad_weight_type, int64_t grad_weight_stride, int accumulate,
+                            void* workspace, int64_t workspace_bytes, int32_t* status, void* stream) {
+  const Call c{x, weight, target, row_weight, type, index_type, rows, classes, cols,
+               Span{x, rows, cols, x_stride, 2}, Span{weight, classes, cols, weight_stride, 2}};
+  int rc = check_call(c);
+  if (rc) return rc;
+  if ((accumulate != 0 && accumulate != 1) || (grad_weight && grad_weight_type != LOPT_F32 && grad_weight_type != type) ||
+      (accumulate && grad_weight && grad_weight_type != LOPT_F32))
+    return LOPT_E_ARG;
+  const int gs = grad_weight ? type_size(grad_weight_type) : 4;
+  const Span mg{grad_weight, classes, cols, grad_weight_stride, gs};
+  if (grad_weight && (rc = check_matrix(mg, true))) return rc;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (rows == 0) {
+    if (!grad_weight || accumulate) return LOPT_OK;
+    return done(cudaMemset2DAsync(grad_weight, grad_weight_stride * gs, 0, cols * gs, classes, s));
+  }
+  const Span mo{grad_x, rows, cols, grad_x_stride, 2};
+  if (grad_x && (rc = check_matrix(mo, true))) return rc;
+  if (!grad_x && !grad_weight) return LOPT_OK;
+  const int planes = grad_weight && grad_weight_type == LOPT_F32 ? 2 : 1;
+  const int pairs = pair_count();
+  const Plan p = plan_grad(rows, classes, cols, planes, !tma_rows(c.mw));
+  if (!lse || !workspace || workspace_bytes < p.size) return LOPT_E_ARG;
+  if ((uintptr_t)lse % 4 || (uintptr_t)status % 4 || (uintptr_t)workspace % 256) return LOPT_E_ALIGN;
+  const Span sl{lse, 1, rows, rows, 4}, sw{workspace, 1, p.size, p.size, 1};
+  const Span st{target, 1, rows, rows, index_size(index_type)}, sr{row_weight, 1, rows, rows, 4};
+  if ((rc = check_alias({mo, mg, sw}, {c.mx, c.mw, st, sr, sl}))) return rc;
+  char* ws = static_cast<char*>(workspace);
+  const bool bf16 = type == LOPT_BF16;
+  int* exponent = reinterpret_cast<int*>(ws + p.exponent);
+  cudaError_t e = launch(k_linear_ce_start, dim3(1), dim3(kMaxCtas), 0, s, false, 1, exponent, reinterpret_cast<int*>(ws + p.flags));
+  if (e != cudaSuccess) return done(e);
+  uint16_t* xp = reinterpret_cast<uint16_t*>(ws + p.x);
+  e = launch(k_linear_ce_copy, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, true, 1, (const uint16_t*)x, x_stride, rows,
+             (int)cols, xp, p.x_stride, target, index_type, (int)classes, row_weight, exponent, status);
+  if (e != cudaSuccess) return done(e);
+  const void* wp = weight;
+  int64_t wst = weight_stride;
+  if (!tma_rows(c.mw)) {
+    wp = ws + p.w, wst = p.w_stride;
+    e = launch(k_linear_ce_copy, dim3((unsigned)((classes + 7) / 8)), dim3(256), 0, s, true, 1, (const uint16_t*)weight, weight_stride,
+               classes, (int)cols, (uint16_t*)wp, wst, (const void*)nullptr, 0, 0, (const float*)nullptr, (int*)nullptr,
+               (int32_t*)nullptr);
+    if (e != cudaSuccess) return done(e);
+  }
+  Maps maps{};
+  Args a{};
+  bool ok = make_map(&maps.x_k, xp, rows, cols, p.x_stride, kHalf, bf16) && make_map(&maps.x_m, xp, rows, cols, p.x_stride, kStep, bf16) &&
+            make_map(&maps.w_k, wp, classes, cols, wst, kHalf, bf16) && make_map(&maps.w_m, wp, classes, cols, wst, kStep, bf16);
+  for (int b = 0; b < p.buffers; ++b) {
+    for (int k = 0; k < planes; ++k) a.g[b][k] = ws + p.g + (b * planes + k) * p.g_plane;
+    ok = ok && make_map(&maps.g_k[b], a.g[b][0], rows, p.chunk, p.chunk, kHalf, bf16) &&
+         make_map(&maps.g_m[b], a.g[b][0], rows, p.chunk, p.chunk, kStep, bf16);
+    if (planes == 2) ok = ok && make_map(&maps.g_low[b], a.g[b][1], rows, p.chunk, p.chunk, kStep, bf16);
+  }
+  if (!ok) return LOPT_E_UNSUPPORTED;
+  a.rows = (int)rows, a.classes = (int)classes, a.cols = (int)cols, a.planes = planes, a.is_bf16 = bf16;
+  a.target = target, a.index_type = index_type, a.row_weight = row_weight, a.lse = lse;
+  a.g_stride = p.chunk, a.exponent = exponent;
+  a.dx = reinterpret_cast<float*>(ws + p.dx), a.dx_stride = p.dx_stride, a.dx_slice = p.slice;
+  a.dw = grad_weight, a.dw_type = grad_weight_type, a.dw_stride = grad_weight_stride, a.accumulate = accumulate;
+  a.gave_up = reinterpret_cast<int*>(ws + p.flags), a.status = status;
+  const int m_tiles = (int)(up(rows, kTile) / kTile), d_tiles = (int)(up(cols, kTile) / kTile);
+  const int64_t chunks = (up(classes, kTile) + p.chunk - 1) / p.chunk;
+  auto grad_job = [&](int64_t k) {
+    const int64_t v0 = k * p.chunk, v1 = std::min(classes, v0 + p.chunk);
+    const int n_tiles = (int)(up(v1 - v0, kTile) / kTile);
+    return Job{kGrad, 0, m_tiles * n_tiles, m_tiles, n_tiles, 1, (int)(up(cols, kStep) / kStep), (int)(k % p.buffers), (int)v0, (int)v1, 0};
+  };
+  // Launch k makes chunk k's G beside the products of chunk k - 1: the long
+  // tiles first, the short ones of G fill the last round.
+  for (int64_t k = 0; k <= chunks; ++k) {
+    a.jobs = 0;
+    int first = 0;
+    auto add = [&](Job j) {
+      j.first = first;
+      first += j.tiles;
+      a.job[a.jobs++] = j;
+    };
+    if (k > 0) {
+      Job g = grad_job(k - 1);
+      if (grad_weight)
+        add(Job{kGradW, 0, g.n_tiles * d_tiles, g.n_tiles, d_tiles, 1, (int)(up(rows, kStep) / kStep) * planes, g.buffer, g.v0, g.v1, 0});
+      if (grad_x)
+        add(Job{kGradX, 0, m_tiles * d_tiles * p.splits, m_tiles, d_tiles, p.splits, (int)(up(g.v1 - g.v0, kStep) / kStep), g.buffer,
+                g.v0, g.v1, k > 1});
+    }
+    if (k < chunks) add(grad_job(k));
+    if ((e = launch_tiles(maps, a, pairs, s)) != cudaSuccess) return done(e);
+  }
+  if (!grad_x) return LOPT_OK;
+  const dim3 grid((unsigned)rows, (unsigned)((cols + 1023) / 1024));
+  const int ctas = 2 * std::min(pairs, a.tiles);
+  if (bf16)
+    e = launch(k_linear_ce_grad_x<__nv_bfloat16>, grid, dim3(256), 0, s, true, 1, (const float*)a.dx, p.dx_stride, p.slice, p.splits,
+               rows, (int)cols, (const int*)exponent, target, index_type, (int)classes, row_weight, (const int*)a.gave_up, ctas,
+               (__nv_bfloat16*)grad_x, grad_x_stride);
+  else
+    e = launch(k_linear_ce_grad_x<__half>, grid, dim3(256), 0, s, true, 1, (const float*)a.dx, p.dx_stride, p.slice, p.splits, rows,
+               (int)cols, (const int*)exponent, target, index_type, (int)classes, row_weight, (const int*)a.gave_up, ctas,
+               (__half*)grad_x, grad_x_stride);
+  return done(e);
+}
+
+}  // extern "C"

@@ -24,6 +24,7 @@ from .lopt import load_library
 from .train_ops import BF16, F16, F32, _Call, _index, _like, _matrix, _same_lead, _type, _TYPES, _vector
 
 LM_EXPORTED = ("lopt_block_norm_forward", "lopt_block_norm_workspace", "lopt_block_norm_backward",
+               "lopt_linear_ce_workspace", "lopt_linear_ce_forward", "lopt_linear_ce_backward",
                "lopt_adamw_check", "lopt_adamw_workspace", "lopt_adamw_step", "lopt_adamw_moments")
 
 ADAMW_BLOCK = 256
@@ -53,6 +54,10 @@ def _load():
             "lopt_block_norm_workspace": [i64, i64, pi64],
             "lopt_block_norm_backward": [vp, i32, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i32, f,
                                          vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, i32, vp, i64, vp],
+            "lopt_linear_ce_workspace": [i64, i64, i64, i32, i32, i32, pi64],
+            "lopt_linear_ce_forward": [vp, i32, i64, i64, i64, vp, i64, i64, vp, i32, vp, vp, vp, vp, i64, vp, vp],
+            "lopt_linear_ce_backward": [vp, i32, i64, i64, i64, vp, i64, i64, vp, i32, vp, vp, vp, i64, vp, i32, i64,
+                                        i32, vp, i64, vp, vp],
             "lopt_adamw_check": [pt, i32],
             "lopt_adamw_workspace": [pi64],
             "lopt_adamw_step": [pt, i32, i64, d, d, d, d, d, d, ctypes.c_uint32, vp, vp, i64, vp],
@@ -190,6 +195,107 @@ def block_norm_backward(grad_out, h, summed, rstd_post, rstd_pre, w_post, w_pre,
          gr, grs, gg, ggs, _vector(grad_w_post, cols, "grad_w_post"), _vector(grad_w_pre, cols, "grad_w_pre"),
          1 if accumulate else 0, ws_ptr, need, c.handle)
     return grad_h, grad_residual, grad_gate, grad_w_post, grad_w_pre
+
+
+# ---- linear cross entropy ------------------------------------------------------------
+
+
+def _hidden(c, x, weight, target, row_weight):
+    """What both directions say of their inputs: (type, rows, cols, x stride,
+    classes, weight stride, index type, row_weight's address, rows aligned)."""
+    rows, cols, xs = _matrix(x, "x")
+    if x.dtype is not torch.float16 and x.dtype is not torch.bfloat16:
+        raise TypeError("x must be float16 or bfloat16, not %s" % x.dtype)
+    if weight.dim() != 2 or weight.shape[1] != cols:
+        raise ValueError("weight must be [classes, %d]" % cols)
+    if weight.dtype is not x.dtype:
+        raise TypeError("weight must be of the type of x")
+    classes, _, ws = _matrix(weight, "weight")
+    kind = _index(target, "target")
+    if target.numel() != rows:
+        raise ValueError("x has %d rows for %d targets" % (rows, target.numel()))
+    if x.dim() > 2:
+        _same_lead(x.shape[:-1], target=(target, 0), row_weight=(row_weight, 0))
+    w = 0 if row_weight is None else _vector(row_weight, rows, "row_weight")
+    aligned = all(t.data_ptr() % 16 == 0 and (n <= 1 or (s % 8 == 0 and s >= cols and s < 1 << 38))
+                  for t, n, s in ((x, rows, xs), (weight, classes, ws)))
+    return _TYPES[x.dtype], rows, cols, xs, classes, ws, kind, w, 1 if aligned else 0
+
+
+def linear_cross_entropy_forward(x, weight, target, *, row_weight=None, loss=None, lse=None, stream=None):
+    """(loss, lse), float32, one per row: the cross entropy of the softmax of
+    ``x @ weight.t()`` with each row's target, without keeping the logits.
+
+        lse = logsumexp(x @ weight.t()),  loss = row_weight * (lse - logit of the target)
+
+    x: [..., cols], weight: [classes, cols], both float16 or bfloat16; target:
+    int32 or int64 of x's leading dimensions, negative for none (padding); a row
+    without a target or with weight 0 has loss 0.  lse is what the backward pass
+    wants; -(loss) with row_weight None is the target's log probability."""
+    c = _Call(x, (weight, row_weight), (target, loss, lse), stream)
+    kind, rows, cols, xs, classes, ws, ik, w, aligned = _hidden(c, x, weight, target, row_weight)
+    if x.dim() > 2:
+        _same_lead(x.shape[:-1], loss=(loss, 0), lse=(lse, 0))
+    if loss is None:
+        loss = c.empty(x.shape[:-1], torch.float32)
+    if lse is None:
+        lse = c.empty(x.shape[:-1], torch.float32)
+    need = _size_of("lopt_linear_ce_workspace", rows, classes, cols, aligned, 0, F32)
+    work, work_ptr = c.workspace(need)
+    _run(c, "lopt_linear_ce_forward", (loss, lse), x.data_ptr(), kind, rows, cols, xs, weight.data_ptr(), classes, ws,
+         target.data_ptr(), ik, w, _vector(loss, rows, "loss"), _vector(lse, rows, "lse"), work_ptr, need,
+         _ops._status_ptr(c.dev), c.handle)
+    return loss, lse
+
+
+def linear_cross_entropy_backward(x, weight, target, lse, *, row_weight=None, grad_x=None, grad_weight=None,
+                                  need_x: bool = True, need_weight: bool = True, accumulate: bool = False,
+                                  stream=None):
+    """(grad_x or None, grad_weight or None): the gradients of the sum of the
+    rows' losses, from the forward pass's lse; row_weight is then the gradient
+    that reaches each row's unweighted loss.
+
+    grad_weight: float32 [classes, cols] (default; ``accumulate`` adds to it),
+    or a buffer of the type of x, for which G is rounded to that type once: a
+    fifth fewer products.  Rows without a target or of weight 0 get zeros and add
+    nothing, whatever they hold."""
+    c = _Call(x, (weight, row_weight), (target, lse, grad_x, grad_weight), stream)
+    kind, rows, cols, xs, classes, ws, ik, w, aligned = _hidden(c, x, weight, target, row_weight)
+    if x.dim() > 2:
+        _same_lead(x.shape[:-1], lse=(lse, 0), grad_x=(grad_x, 1))
+    if lse is None:
+        raise TypeError("the operators take torch tensors")
+    if accumulate and (grad_weight is None or not need_weight):
+        raise ValueError("accumulate needs grad_weight")
+    gx = gxs = gw = gws = 0
+    gt = F32
+    written = []
+    if need_x:
+        grad_x, gx, gxs = _like(c, grad_x, x, (rows, cols), "grad_x")
+        written.append(grad_x)
+    elif grad_x is not None:
+        raise ValueError("grad_x is given, need_x is not")
+    if need_weight:
+        if grad_weight is None:
+            grad_weight = c.empty((classes, cols), torch.float32)
+        gr, gc, gws = _matrix(grad_weight, "grad_weight")
+        if (gr, gc) != (classes, cols):
+            raise ValueError("grad_weight must be %s" % ((classes, cols),))
+        if grad_weight.dtype is not torch.float32 and grad_weight.dtype is not x.dtype:
+            raise TypeError("grad_weight must be float32 or of the type of x")
+        gt = _TYPES[grad_weight.dtype]
+        if accumulate and gt != F32:
+            raise TypeError("accumulate needs a float32 grad_weight")
+        gw = grad_weight.data_ptr()
+        written.append(grad_weight)
+    elif grad_weight is not None:
+        raise ValueError("grad_weight is given, need_weight is not")
+    need = _size_of("lopt_linear_ce_workspace", rows, classes, cols, aligned, 1, gt)
+    work, work_ptr = c.workspace(need)
+    _run(c, "lopt_linear_ce_backward", written, x.data_ptr(), kind, rows, cols, xs, weight.data_ptr(), classes, ws,
+         target.data_ptr(), ik, w, _vector(lse, rows, "lse"), gx, gxs, gw, gt, gws, 1 if accumulate else 0, work_ptr,
+         need, _ops._status_ptr(c.dev), c.handle)
+    return (grad_x if need_x else None), (grad_weight if need_weight else None)
 
 
 # ---- AdamW ------------------------------------------------------------------------
