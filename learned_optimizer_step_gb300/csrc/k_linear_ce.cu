@@ -21,6 +21,18 @@
 // 128 rows of the accumulator in its tensor memory, twice, so that a tile's
 // epilogue runs beside the next tile's product.  Roles: warp 0 loads, warp 1 of the
 // pair's first CTA issues, warps 4 to 11 are the epilogue.
+//
+// The tensor cores cut the fp32 sums they carry rather than round them: over
+// thousands of steps that is more than fp32 results may be off.  What is cut goes
+// by the largest terms, and those are the targets'.  So a target's logit is a dot
+// product of its own in fp32, which replaces the tensor cores' in the sum of
+// exponentials and in G; and for a 32-bit grad_w of many tokens (kSplitRows) the
+// targets' entries stay out of G: their share is added in fp32, to grad_x by the last
+// kernel, to grad_w by the embedding's gradient.  Where they are in G an
+// accumulator takes a segment of some steps only, and the epilogue's warps add the
+// segments in registers, rounding to nearest.  In all products that costs more
+// power, which bounds the clock of such a kernel (8,192 x 2048 x 50,304, segments of
+// 4, 8, 16 steps: 5.79, 5.19, 4.88 ms, 4.42 without).
 #include <algorithm>
 #include <cmath>
 #include <cuda.h>
@@ -38,8 +50,12 @@ constexpr int kHalf = 128;                       // ... of one CTA's part of an 
 constexpr int kStep = 64;                        // K elements of a stage: 128 bytes
 constexpr int kStages = 6;
 constexpr int kOperand = kHalf * kStep * 2;      // bytes of one operand of a stage
-constexpr int kThreads = 384;
 constexpr int kEpilogueWarps = 8;
+constexpr int kThreads = 128 + 32 * kEpilogueWarps;
+// Registers of a thread at launch, and after the first warpgroup has handed some
+// to the epilogue's two: 128 * 40 + 256 * 224 is less than 384 * 168.
+constexpr int kRegs = 168, kRegsFew = 40, kRegsMany = 224;
+static_assert(128 * kRegsFew + 256 * kRegsMany <= kThreads * kRegs, "");
 constexpr size_t kSmem = (size_t)kStages * 2 * kOperand + 1024 + 256;
 constexpr int kRowGroup = 32;                    // tiles of rows that share the classes' operand in L2
 constexpr uint64_t kLimitNs = 1000000000ull;
@@ -55,6 +71,7 @@ struct Job {
   int buffer;                  // which G
   int v0, v1;                  // classes of the chunk
   int add;                     // grad_x: add to the sums
+  int segment;                 // K steps that one accumulator sums
 };
 constexpr int kJobs = 3;
 
@@ -70,11 +87,12 @@ struct Args {
   int index_type;
   const float* row_weight;     // NULL: 1
   const float* lse;
+  const float* hit;            // [rows]: exp(target logit - lse) - 1
+  int split;                   // the targets' entries stay out of G
   float2* part;                // [2 * class tiles][rows]: maximum, sum
-  float* chosen;               // [rows] target logits
   void* g[2][2];               // [buffer][part]
   int64_t g_stride;
-  const int* exponent;         // G is scaled by 2^(15 - *exponent)
+  const float* largest;        // the largest |row_weight|: G is scaled by 2^15 / *largest
   float* dx;
   int64_t dx_stride, dx_slice;
   void* dw;
@@ -131,7 +149,9 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 // Bounded: gives up after a second, or when another warp of the CTA has.
-static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort) {
+// Inline: a call would spill the sums that the epilogue holds meanwhile.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (try_wait(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   for (uint32_t it = 0; it < (1u << 30); ++it) {
     if (try_wait(bar, parity)) return true;
@@ -142,9 +162,6 @@ static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, vol
   }
   *abort = 1;
   return false;
-}
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort) {
-  return try_wait(bar, parity) || wait_slow(bar, parity, abort);
 }
 __device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
@@ -194,34 +211,31 @@ __device__ __forceinline__ const Job& job_of(const Args& a, int t) {
   return a.job[k];
 }
 
-// ---- epilogues: 32 columns of a row at a time ------------------------------------
-__device__ __forceinline__ void as_floats(const uint32_t (&r)[32], float (&v)[32]) {
+// ---- epilogues: a thread has 128 columns of a row, and takes 32 at a time ----------
+__device__ __forceinline__ void piece(const float (&acc)[kHalf], int c, float (&v)[32]) {
 #pragma unroll
-  for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
+  for (int k = 0; k < 32; ++k) v[k] = acc[32 * c + k];
 }
 
-// `get(c)` gives the 32 columns from 32 * c on, c < 4.
-template <typename Get>
-__device__ __forceinline__ void loss_tile(const Args& a, const Job& j, const Tile& t, int row, int col, int half, Get get) {
+__device__ __forceinline__ void loss_tile(const Args& a, const Tile& t, int row, int col, int half, const float (&acc)[kHalf]) {
   int64_t target = -1;
   if (row < a.rows) target = load_index(a.target, row, a.index_type);
   float most = -INFINITY, sum = 0.f;
+#pragma unroll
   for (int c = 0; c < 4; ++c) {
     float v[32];
-    get(c, v);
+    piece(acc, c, v);
     const int c0 = col + 32 * c;
     if (c0 + 32 > a.classes) {
 #pragma unroll
       for (int k = 0; k < 32; ++k)
         if (c0 + k >= a.classes) v[k] = -INFINITY;
     }
-    const int64_t at = target - c0;
-    if (at >= 0 && at < 32 && target < a.classes) {
-      float x = 0.f;
+    const int64_t at = target - c0;      // added by the rows' kernel
+    if (at >= 0 && at < 32) {
 #pragma unroll
       for (int k = 0; k < 32; ++k)
-        if (at == k) x = v[k];
-      a.chosen[row] = x;
+        if (at == k) v[k] = -INFINITY;
     }
     float m = most;
 #pragma unroll
@@ -240,29 +254,32 @@ __device__ __forceinline__ void loss_tile(const Args& a, const Job& j, const Til
   if (row < a.rows) a.part[(int64_t)(2 * t.n + half) * a.rows + row] = make_float2(most, sum);
 }
 
-template <typename T, typename Get>
-__device__ __forceinline__ void grad_tile(const Args& a, const Job& j, const Tile& t, int row, int col, Get get) {
+template <typename T>
+__device__ __forceinline__ void grad_tile(const Args& a, const Job& j, int row, int col, const float (&acc)[kHalf]) {
   int64_t target = -1;
-  float lse = 0.f, scale = 0.f;
+  float lse = 0.f, scale = 0.f, weight = 0.f;
   const bool live = row < a.rows;
   if (live) {
     target = load_index(a.target, row, a.index_type);
-    if (target >= 0 && target < a.classes) scale = a.row_weight ? a.row_weight[row] : 1.f;
+    if (target >= 0 && target < a.classes) weight = a.row_weight ? a.row_weight[row] : 1.f;
     lse = a.lse[row];
-    scale = scalbnf(scale, 15 - *a.exponent);
+    if (weight != 0.f) scale = weight / *a.largest * 32768.f;
+    else target = -1;
   }
   const int64_t out = (int64_t)row * a.g_stride + (col - j.v0);
+#pragma unroll
   for (int c = 0; c < 4; ++c) {
     float v[32];
-    get(c, v);
+    piece(acc, c, v);
     const int c0 = col + 32 * c;
 #pragma unroll
     for (int k = 0; k < 32; ++k) v[k] = exp2_fast((v[k] - lse) * kLog2e);
     const int64_t at = target - c0;
     if (at >= 0 && at < 32) {
 #pragma unroll
-      for (int k = 0; k < 32; ++k)
-        if (at == k) v[k] -= 1.f;
+      for (int k = 0; k < 32; ++k) {
+        if (at == k) v[k] = a.split ? 0.f : a.hit[row];
+      }
     }
 #pragma unroll
     for (int k = 0; k < 32; ++k) v[k] *= scale;
@@ -293,12 +310,12 @@ __device__ __forceinline__ void grad_tile(const Args& a, const Job& j, const Til
   }
 }
 
-template <typename Get>
-__device__ __forceinline__ void grad_x_tile(const Args& a, const Job& j, const Tile& t, int row, int col, Get get) {
+__device__ __forceinline__ void grad_x_tile(const Args& a, const Job& j, const Tile& t, int row, int col, const float (&acc)[kHalf]) {
   float* out = a.dx + t.split * a.dx_slice + (int64_t)row * a.dx_stride + col;
+#pragma unroll
   for (int c = 0; c < 4; ++c) {
     float v[32];
-    get(c, v);
+    piece(acc, c, v);
     if (row >= a.rows) continue;
 #pragma unroll
     for (int k = 0; k < 32; k += 4) {
@@ -333,16 +350,16 @@ __device__ __forceinline__ void put(O* p, int left, bool add, float f1, float f2
   }
 }
 // As many elements at a time as the rows' alignment allows: 16 bytes or one.
-template <typename O, typename Get>
-__device__ __forceinline__ void grad_w_tile(const Args& a, const Job& j, int v, int col, Get get) {
-  const int down = *a.exponent - 15, d1 = down / 2;
-  const float f1 = scalbnf(1.f, d1), f2 = scalbnf(1.f, down - d1);
+template <typename O>
+__device__ __forceinline__ void grad_w_tile(const Args& a, const Job& j, int v, int col, const float (&acc)[kHalf]) {
+  const float f1 = 1.f / 32768.f, f2 = *a.largest;
   constexpr int VEC = 16 / sizeof(O);
   O* out = static_cast<O*>(a.dw) + (int64_t)v * a.dw_stride + col;
   const bool vec = (a.cols % VEC == 0) && (a.dw_stride % VEC == 0) && (reinterpret_cast<uintptr_t>(a.dw) % 16 == 0);
+#pragma unroll
   for (int c = 0; c < 4; ++c) {
     float x[32];
-    get(c, x);
+    piece(acc, c, x);
     if (v >= j.v1) continue;
     const int left = a.cols - (col + 32 * c);
     if (vec) put<O, VEC>(out + 32 * c, left, a.accumulate, f1, f2, x);
@@ -374,7 +391,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 2) {
+  if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(smem_u32(&s_tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
@@ -387,8 +404,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   wait_for_previous();
   let_next_start();
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRegsFew));
+    if (warp == 0 && lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
       for (int t = pair; t < a.tiles; t += pairs) {
@@ -427,8 +445,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (++stage == kStages) stage = 0, phase ^= 1;
       }
     }
-  } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (warp == 1 && lane == 0 && rank == 0) {
       int stage = 0, buf = 0;
       uint32_t phase = 0, acc_phase = 0;
       for (int t = pair; t < a.tiles; t += pairs) {
@@ -439,67 +456,85 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                (bk ? 0u : 1u << 16) | ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
         // 16 of K further: 32 bytes along the rows, two groups of eight rows across.
         const uint32_t step_a = (ak ? 32 : 2048) >> 4, step_b = (bk ? 32 : 2048) >> 4;
-        if (!wait_for(smem_u32(&s_acc_empty[buf]), acc_phase ^ 1, abort)) break;
-        tc_fence_after();
-        const uint32_t d = tmem + buf * kTile;
-        for (int k = x.k0; k < x.k1; ++k) {
-          if (!wait_for(smem_u32(&s_full[stage]), phase, abort)) break;
+        for (int k = x.k0; k < x.k1;) {
+          if (!wait_for(smem_u32(&s_acc_empty[buf]), acc_phase ^ 1, abort)) break;
           tc_fence_after();
-          const uint32_t sa = stages + stage * 2 * kOperand;
-          const uint64_t da = operand_desc(sa, ak), db = operand_desc(sa + kOperand, bk);
+          const uint32_t d = tmem + buf * kTile;
+          const int first = k, end = min(k + j.segment, x.k1);
+          for (; k < end; ++k) {
+            if (!wait_for(smem_u32(&s_full[stage]), phase, abort)) break;
+            tc_fence_after();
+            const uint32_t sa = stages + stage * 2 * kOperand;
+            const uint64_t da = operand_desc(sa, ak), db = operand_desc(sa + kOperand, bk);
 #pragma unroll
-          for (int q = 0; q < kStep / 16; ++q) pair_mma(d, da + q * step_a, db + q * step_b, idesc, k > x.k0 || q > 0);
-          pair_commit(smem_u32(&s_empty[stage]));
-          if (++stage == kStages) stage = 0, phase ^= 1;
+            for (int q = 0; q < kStep / 16; ++q) pair_mma(d, da + q * step_a, db + q * step_b, idesc, k > first || q > 0);
+            pair_commit(smem_u32(&s_empty[stage]));
+            if (++stage == kStages) stage = 0, phase ^= 1;
+          }
+          if (*abort) break;
+          pair_commit(smem_u32(&s_acc_full[buf]));
+          if (++buf == 2) buf = 0, acc_phase ^= 1;
         }
         if (*abort) break;
-        pair_commit(smem_u32(&s_acc_full[buf]));
-        if (++buf == 2) buf = 0, acc_phase ^= 1;
       }
     }
-  } else if (warp >= 4) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kRegsMany));
     const int quarter = warp % 4, half = (warp - 4) / 4;
     int buf = 0;
     uint32_t phase = 0;
     for (int t = pair; t < a.tiles; t += pairs) {
       const Job& j = job_of(a, t);
       const Tile x = tile_of(j, t - j.first);
-      const bool ok = wait_for(smem_u32(&s_acc_full[buf]), phase, abort);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after();
-      const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTile + half * kHalf;
-      auto get = [&](int c, float (&v)[32]) {
-        if (x.k0 == x.k1) {      // a slice without classes: nothing was issued
+      float acc[kHalf];
+      if (x.k0 == x.k1) {      // a slice without classes
 #pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = 0.f;
-          return;
+        for (int k = 0; k < kHalf; ++k) acc[k] = 0.f;
+      }
+      bool ok = true;
+      for (int k = x.k0; k < x.k1; k += j.segment) {
+        ok = wait_for(smem_u32(&s_acc_full[buf]), phase, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTile + half * kHalf;
+        const bool start = k == x.k0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t r[32];
+          tmem_ld32(src + 32 * c, r);
+          tmem_wait_ld();
+          if (start) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) acc[32 * c + e] = __uint_as_float(r[e]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) acc[32 * c + e] += __uint_as_float(r[e]);
+          }
         }
-        uint32_t r[32];
+        tc_fence_before();
         __syncwarp();
-        tmem_ld32(src + 32 * c, r);
-        tmem_wait_ld();
-        as_floats(r, v);
-      };
+        if (lane == 0) arrive_at(in_cta(smem_u32(&s_acc_empty[buf]), 0));
+        if (++buf == 2) buf = 0, phase ^= 1;
+      }
+      if (!ok) break;
       const int row = x.m * kTile + rank * kHalf + quarter * 32 + lane;
       const int col = x.n * kTile + half * kHalf;
       if (j.mode == kLoss) {
-        loss_tile(a, j, x, row, j.v0 + col, half, get);
+        loss_tile(a, x, row, j.v0 + col, half, acc);
       } else if (j.mode == kGrad) {
-        if (a.is_bf16) grad_tile<__nv_bfloat16>(a, j, x, row, j.v0 + col, get);
-        else grad_tile<__half>(a, j, x, row, j.v0 + col, get);
+        if (a.is_bf16) grad_tile<__nv_bfloat16>(a, j, row, j.v0 + col, acc);
+        else grad_tile<__half>(a, j, row, j.v0 + col, acc);
       } else if (j.mode == kGradX) {
-        grad_x_tile(a, j, x, row, col, get);
+        grad_x_tile(a, j, x, row, col, acc);
       } else if (a.dw_type == LOPT_F32) {
-        grad_w_tile<float>(a, j, j.v0 + row, col, get);
+        grad_w_tile<float>(a, j, j.v0 + row, col, acc);
       } else if (a.dw_type == LOPT_F16) {
-        grad_w_tile<__half>(a, j, j.v0 + row, col, get);
+        grad_w_tile<__half>(a, j, j.v0 + row, col, acc);
       } else {
-        grad_w_tile<__nv_bfloat16>(a, j, j.v0 + row, col, get);
+        grad_w_tile<__nv_bfloat16>(a, j, j.v0 + row, col, acc);
       }
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_at(in_cta(smem_u32(&s_acc_empty[buf]), 0));
-      if (++buf == 2) buf = 0, phase ^= 1;
     }
   }
   __syncthreads();
@@ -518,23 +553,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncwarp();
   cluster_sync();
   tc_fence_after();
-  if (warp == 2)
+  if (warp == 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
 }
 
 // ---- the rows' losses from the tiles' statistics -----------------------------------
-__global__ void __launch_bounds__(512) k_linear_ce_rows(const float2* part, int parts, const float* chosen, const int* gave_up,
-                                                        int ctas, int64_t rows, int classes, const void* target,
-                                                        int index_type, const float* row_weight, float* loss,
-                                                        float* lse, int32_t* status) {
+// Dot product of two rows by a warp, fp32; every lane has it.
+template <typename T>
+__device__ __forceinline__ float row_dot(const T* x, const T* w, int cols, bool vec, int lane) {
+  float s = 0.f;
+  if (vec) {
+    for (int j = lane * 8; j < cols; j += 256) {
+      float a[8], b[8];
+      to_floats(*reinterpret_cast<const Pack<T, 8>*>(x + j), a);
+      to_floats(*reinterpret_cast<const Pack<T, 8>*>(w + j), b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s = fmaf(a[e], b[e], s);
+    }
+  } else {
+    for (int j = lane; j < cols; j += 32) s = fmaf(to_f(x[j]), to_f(w[j]), s);
+  }
+  return warp_sum(s);
+}
+__device__ __forceinline__ float row_dot(const uint16_t* x, const uint16_t* w, int cols, bool vec, bool bf16, int lane) {
+  return bf16 ? row_dot(reinterpret_cast<const __nv_bfloat16*>(x), reinterpret_cast<const __nv_bfloat16*>(w), cols, vec, lane)
+              : row_dot(reinterpret_cast<const __half*>(x), reinterpret_cast<const __half*>(w), cols, vec, lane);
+}
+
+// Rows of x and of W, as the caller gave them.
+struct Rows {
+  const uint16_t *x, *w;
+  int64_t x_stride, w_stride;
+  int cols, classes, bf16, vec;
+};
+
+__global__ void __launch_bounds__(512) k_linear_ce_rows(const float2* part, int parts, const int* gave_up, int ctas, const Rows q,
+                                                        int64_t rows, const void* target, int index_type,
+                                                        const float* row_weight, float* loss, float* lse, int32_t* status) {
   __shared__ float2 red[16][32];
+  __shared__ float s_hit[32];
   __shared__ int s_bad;
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
   const int64_t row = (int64_t)blockIdx.x * 32 + lane;
   if (threadIdx.x == 0) s_bad = 0;
+  // The targets' logits need none of what the kernel before this one makes, but
+  // x and W may be the one's before.
   wait_for_previous();
   __syncthreads();
   if (threadIdx.x < ctas && gave_up[threadIdx.x]) s_bad = 1;
+  for (int r = w; r < 32; r += 16) {
+    const int64_t at = (int64_t)blockIdx.x * 32 + r;
+    if (at >= rows) break;
+    const int64_t t = load_index(target, at, index_type);
+    float z = -INFINITY;
+    if (t >= 0 && t < q.classes) z = row_dot(q.x + at * q.x_stride, q.w + t * q.w_stride, q.cols, q.vec, q.bf16, lane);
+    if (lane == 0) s_hit[r] = z;
+  }
   float m = -INFINITY, s = 0.f;
   auto join = [&](float2 p) {
     const float top = fmaxf(m, p.x), base = top == -INFINITY ? 0.f : top;
@@ -550,24 +624,27 @@ __global__ void __launch_bounds__(512) k_linear_ce_rows(const float2* part, int 
   if (w || row >= rows) return;
   m = -INFINITY, s = 0.f;
   for (int k = 0; k < 16; ++k) join(red[k][lane]);
-  const float all = m == -INFINITY && s == 0.f ? -INFINITY : m + logf(s);
+  const float hit = s_hit[lane];
   const int64_t t = load_index(target, row, index_type);
+  // A target of -inf adds nothing, one of NaN makes the sum NaN.
+  if (t >= 0 && t < q.classes) join(make_float2(hit, 1.f));
+  const float all = m == -INFINITY && s == 0.f ? -INFINITY : m + logf(s);
   const float weight = row_weight ? row_weight[row] : 1.f;
-  if (t >= classes && status) atomicOr(status, kStatusIndex);
+  if (t >= q.classes && status) atomicOr(status, kStatusIndex);
   float l = 0.f;
-  if (t >= 0 && t < classes && weight != 0.f) l = weight * (all - chosen[row]);
+  if (t >= 0 && t < q.classes && weight != 0.f) l = weight * (all - hit);
   loss[row] = s_bad ? NAN : l;
   lse[row] = s_bad ? NAN : all;
 }
 
 // ---- before and after the backward products ------------------------------------------
 // Rows of 16-bit elements to rows that TMA can read.  With targets, rows that
-// do not count become zeros, whatever they hold, and the largest weight's
-// exponent is found.
+// do not count become zeros, whatever they hold, the largest weight is found and
+// the targets' entries of G (without weight) are made.
 __global__ void __launch_bounds__(256) k_linear_ce_copy(const uint16_t* x, int64_t stride, int64_t rows, int cols, uint16_t* out,
                                                         int64_t out_stride, const void* target, int index_type,
-                                                        int classes, const float* row_weight, int* exponent,
-                                                        int32_t* status) {
+                                                        const Rows q, const float* row_weight, const float* lse,
+                                                        float* largest, float* hit, int32_t* status) {
   const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
   wait_for_previous();
@@ -576,33 +653,61 @@ __global__ void __launch_bounds__(256) k_linear_ce_copy(const uint16_t* x, int64
   if (target) {
     const int64_t t = load_index(target, row, index_type);
     const float w = row_weight ? row_weight[row] : 1.f;
-    live = t >= 0 && t < classes && w != 0.f;
+    live = t >= 0 && t < q.classes && w != 0.f;
+    float z = 0.f;
+    if (live) z = row_dot(x + row * stride, q.w + t * q.w_stride, cols, q.vec, q.bf16, lane);
     if (lane == 0) {
-      if (t >= classes && status) atomicOr(status, kStatusIndex);
-      // The least e with |w| < 2^e.
-      if (live && isfinite(w)) atomicMax(exponent, ilogbf(w) + 1);
+      if (live) hit[row] = expm1f(z - lse[row]);
+      if (t >= q.classes && status) atomicOr(status, kStatusIndex);
+      // Floats above 0 are in the order of their bits.
+      if (live && isfinite(w)) atomicMax(reinterpret_cast<int*>(largest), __float_as_int(fabsf(w)));
     }
   }
   const uint16_t* p = x + row * stride;
-  uint16_t* q = out + row * out_stride;
+  uint16_t* to = out + row * out_stride;
   if (cols % 8 == 0 && stride % 8 == 0 && (uintptr_t)x % 16 == 0) {
     for (int j = lane * 8; j < cols; j += 256)
-      *reinterpret_cast<uint4*>(q + j) = live ? *reinterpret_cast<const uint4*>(p + j) : make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(to + j) = live ? *reinterpret_cast<const uint4*>(p + j) : make_uint4(0, 0, 0, 0);
   } else {
-    for (int j = lane; j < cols; j += 32) q[j] = live ? p[j] : 0;
+    for (int j = lane; j < cols; j += 32) to[j] = live ? p[j] : 0;
   }
 }
 
-__global__ void k_linear_ce_start(int* exponent, int* gave_up) {
-  if (threadIdx.x == 0) *exponent = -200;
+__global__ void k_linear_ce_start(float* largest, int* gave_up) {
+  if (threadIdx.x == 0) *largest = 0.f;
   gave_up[threadIdx.x] = 0;
+}
+
+// The targets' rows of grad_w's sum, fp32: row_weight * hit * x (x with zeros in
+// the rows that do not count).
+template <typename T>
+__global__ void __launch_bounds__(256) k_linear_ce_share(const T* x, int64_t stride, int64_t rows, int cols, const float* hit,
+                                                         const void* target, int index_type, int classes,
+                                                         const float* row_weight, float* out) {
+  const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+  wait_for_previous();
+  if (row >= rows) return;
+  const int64_t t = load_index(target, row, index_type);
+  const float w = row_weight ? row_weight[row] : 1.f;
+  const float c = t >= 0 && t < classes && w != 0.f ? hit[row] * w : 0.f;
+  const T* p = x + row * stride;
+  float* q = out + row * stride;
+  for (int j = threadIdx.x % 32 * 8; j < cols; j += 256) {     // whole rows of 8: the stride is a multiple
+    float v[8];
+    to_floats(*reinterpret_cast<const Pack<T, 8>*>(p + j), v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= c;
+    *reinterpret_cast<float4*>(q + j) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(q + j + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  }
 }
 
 // grad_x from the sums of its slices, in order.
 template <typename T>
 __global__ void __launch_bounds__(256) k_linear_ce_grad_x(const float* dx, int64_t dx_stride, int64_t slice, int slices,
-                                                          int64_t rows, int cols, const int* exponent, const void* target,
+                                                          int64_t rows, int cols, const float* largest, const void* target,
                                                           int index_type, int classes, const float* row_weight,
+                                                          const float* hit, const T* weight, int64_t weight_stride,
                                                           const int* gave_up, int ctas, T* out, int64_t out_stride) {
   __shared__ int s_bad;
   if (threadIdx.x == 0) s_bad = 0;
@@ -614,11 +719,13 @@ __global__ void __launch_bounds__(256) k_linear_ce_grad_x(const float* dx, int64
   const int64_t t = load_index(target, row, index_type);
   const float w = row_weight ? row_weight[row] : 1.f;
   const bool live = t >= 0 && t < classes && w != 0.f;
-  const int down = *exponent - 15, d1 = down / 2;
-  const float f1 = scalbnf(1.f, d1), f2 = scalbnf(1.f, down - d1);
+  const float f1 = 1.f / 32768.f, f2 = *largest;
   const float* p = dx + row * dx_stride;
   T* q = out + row * out_stride;
-  const bool vec = cols % 4 == 0 && out_stride % 4 == 0 && (uintptr_t)out % (4 * sizeof(T)) == 0;
+  const T* wt = hit && live ? weight + t * weight_stride : nullptr;
+  const float share = wt ? hit[row] * w : 0.f;
+  const bool vec = cols % 4 == 0 && out_stride % 4 == 0 && (uintptr_t)out % (4 * sizeof(T)) == 0 &&
+                   (!hit || (weight_stride % 4 == 0 && (uintptr_t)weight % (4 * sizeof(T)) == 0));
   if (vec) {
     for (int j = (blockIdx.y * 256 + threadIdx.x) * 4; j < cols; j += 1024 * gridDim.y) {
       float v[4] = {0.f, 0.f, 0.f, 0.f};
@@ -630,6 +737,12 @@ __global__ void __launch_bounds__(256) k_linear_ce_grad_x(const float* dx, int64
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = s_bad ? NAN : v[e] * f1 * f2;
+      if (wt) {
+        float w4[4];
+        to_floats(*reinterpret_cast<const Pack<T, 4>*>(wt + j), w4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = fmaf(share, w4[e], v[e]);
+      }
       *reinterpret_cast<Pack<T, 4>*>(q + j) = from_floats<T, 4>(v);
     }
   } else {
@@ -637,7 +750,8 @@ __global__ void __launch_bounds__(256) k_linear_ce_grad_x(const float* dx, int64
       float v = 0.f;
       if (live)
         for (int s = 0; s < slices; ++s) v += p[s * slice + j];
-      q[j] = from_f<T>(s_bad ? NAN : v * f1 * f2);
+      v = s_bad ? NAN : v * f1 * f2;
+      q[j] = from_f<T>(wt ? fmaf(share, to_f(wt[j]), v) : v);
     }
   }
 }
@@ -649,6 +763,10 @@ constexpr int64_t kPartBytes = (int64_t)256 << 20;    // of its statistics
 constexpr int kPairs = 76;                         // of a GB300: what a split of the classes counts on
 constexpr int64_t kChunkBytes = (int64_t)256 << 20;   // of one G
 constexpr int kMaxSplits = 64;
+constexpr int64_t kSplitRows = 512;                // more tokens: the targets' entries stay out of G
+// Steps of a segment: logits whose losses are fp32, a 32-bit grad_w without and with
+// the targets' entries; all for products that end in 16 bits.
+constexpr int kLossSegment = 32, kGradSegment = 32, kGradWSegment = 4, kSplitSegment = 64, kAll = 1 << 30;
 constexpr int kMaxCtas = 256;
 
 int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
@@ -717,12 +835,19 @@ cudaError_t launch_tiles(const Maps& maps, Args& a, int pairs, cudaStream_t s) {
   a.tiles = a.job[a.jobs - 1].first + a.job[a.jobs - 1].tiles;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&k_linear_ce), kSmem);
   if (e != cudaSuccess) return e;
+  // The kernel's warps wait for registers that only a launch with kRegs has.
+  static const int regs = [] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, reinterpret_cast<const void*>(&k_linear_ce)) == cudaSuccess ? at.numRegs : 0;
+  }();
+  if (regs != kRegs) return cudaErrorInvalidKernelImage;
   return launch(k_linear_ce, dim3(2 * (unsigned)std::min(pairs, a.tiles)), dim3(kThreads), kSmem, s, true, 1, maps, a);
 }
 
 // Where things are in the workspace, in bytes from its start.
 struct Plan {
-  int64_t x = 0, w = 0, part = 0, chosen = 0, g = 0, g_plane = 0, dx = 0, flags = 0, exponent = 0, size = 0;
+  int64_t x = 0, w = 0, part = 0, g = 0, g_plane = 0, dx = 0, flags = 0, largest = 0, size = 0;
+  int64_t hit = 0, share = 0, sort = 0, sort_bytes = 0;
   int64_t x_stride, w_stride, chunk = 0, dx_stride = 0, slice = 0;
   int splits = 1, buffers = 1;
 };
@@ -741,7 +866,6 @@ Plan plan_loss(int64_t rows, int64_t classes, int64_t cols, bool copy) {
   p.chunk = std::min(rows, std::min(kLossRows, std::max<int64_t>(kPartBytes / (parts * 8) / kTile, 1) * kTile));
   p.flags = take(p, kMaxCtas * 4);
   p.part = take(p, parts * p.chunk * 8);
-  p.chosen = take(p, p.chunk * 4);
   if (copy) {
     p.x = take(p, rows * p.x_stride * 2);
     p.w = take(p, classes * p.w_stride * 2);
@@ -752,8 +876,14 @@ Plan plan_loss(int64_t rows, int64_t classes, int64_t cols, bool copy) {
 Plan plan_grad(int64_t rows, int64_t classes, int64_t cols, int planes, bool copy) {
   Plan p;
   p.x_stride = p.w_stride = up(cols, 8);
+  if (planes == 2 && rows > kSplitRows) {
+    p.share = take(p, rows * p.x_stride * 4);
+    lopt_embed_workspace(rows, classes, cols, &p.sort_bytes);
+    p.sort = take(p, p.sort_bytes);
+  }
   p.flags = take(p, kMaxCtas * 4);
-  p.exponent = take(p, 4);
+  p.largest = take(p, 4);
+  p.hit = take(p, rows * 4);
   p.x = take(p, rows * p.x_stride * 2);
   if (copy) p.w = take(p, classes * p.w_stride * 2);
   const int64_t all = up(classes, kTile);
@@ -790,6 +920,13 @@ int check_call(const Call& c) {
   if (!c.target) return LOPT_E_ARG;
   if ((uintptr_t)c.target % index_size(c.index_type) || (uintptr_t)c.row_weight % 4) return LOPT_E_ALIGN;
   return LOPT_OK;
+}
+
+// Rows from r0 on.
+Rows rows_of(const Call& c, int64_t r0) {
+  return Rows{static_cast<const uint16_t*>(c.x) + r0 * c.mx.stride, static_cast<const uint16_t*>(c.w), c.mx.stride, c.mw.stride,
+              (int)c.cols, (int)c.classes, c.type == LOPT_BF16,
+              c.cols % 8 == 0 && rows_aligned(c.mx, 16) && rows_aligned(c.mw, 16)};
 }
 
 int check_alias(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
@@ -843,14 +980,14 @@ int lopt_linear_ce_forward(const void* x, int type, int64_t rows, int64_t cols, 
   if (!tma_rows(c.mx)) {
     xp = ws + p.x, xs = p.x_stride;
     e = launch(k_linear_ce_copy, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, true, 1, (const uint16_t*)x, x_stride, rows,
-               (int)cols, (uint16_t*)xp, xs, (const void*)nullptr, 0, 0, (const float*)nullptr, (int*)nullptr, (int32_t*)nullptr);
+               (int)cols, (uint16_t*)xp, xs, (const void*)nullptr, 0, Rows{}, (const float*)nullptr, (const float*)nullptr, (float*)nullptr, (float*)nullptr, (int32_t*)nullptr);
     if (e != cudaSuccess) return done(e);
   }
   if (!tma_rows(c.mw)) {
     wp = ws + p.w, wst = p.w_stride;
     e = launch(k_linear_ce_copy, dim3((unsigned)((classes + 7) / 8)), dim3(256), 0, s, true, 1, (const uint16_t*)weight, weight_stride,
-               classes, (int)cols, (uint16_t*)wp, wst, (const void*)nullptr, 0, 0, (const float*)nullptr, (int*)nullptr,
-               (int32_t*)nullptr);
+               classes, (int)cols, (uint16_t*)wp, wst, (const void*)nullptr, 0, Rows{}, (const float*)nullptr, (const float*)nullptr, (float*)nullptr,
+               (float*)nullptr, (int32_t*)nullptr);
     if (e != cudaSuccess) return done(e);
   }
   const int pairs = pair_count();
@@ -864,16 +1001,16 @@ int lopt_linear_ce_forward(const void* x, int type, int64_t rows, int64_t cols, 
       return LOPT_E_UNSUPPORTED;
     a.rows = (int)n, a.classes = (int)classes, a.cols = (int)cols, a.is_bf16 = bf16, a.planes = 1;
     a.target = static_cast<const char*>(target) + r0 * index_size(index_type), a.index_type = index_type;
-    a.part = reinterpret_cast<float2*>(ws + p.part), a.chosen = reinterpret_cast<float*>(ws + p.chosen);
+    a.part = reinterpret_cast<float2*>(ws + p.part);
     a.gave_up = reinterpret_cast<int*>(ws + p.flags), a.status = status;
     const int m_tiles = (int)(up(n, kTile) / kTile);
     a.jobs = 1;
-    a.job[0] = Job{kLoss, 0, m_tiles * n_tiles, m_tiles, n_tiles, 1, (int)(up(cols, kStep) / kStep), 0, 0, (int)classes, 0};
+    a.job[0] = Job{kLoss, 0, m_tiles * n_tiles, m_tiles, n_tiles, 1, (int)(up(cols, kStep) / kStep), 0, 0, (int)classes, 0,
+                   kLossSegment};
     if ((e = launch_tiles(maps, a, pairs, s)) != cudaSuccess) return done(e);
     const float* rw = row_weight ? row_weight + r0 : nullptr;
     e = launch(k_linear_ce_rows, dim3((unsigned)((n + 31) / 32)), dim3(512), 0, s, true, 1, (const float2*)a.part, 2 * n_tiles,
-               (const float*)a.chosen, (const int*)a.gave_up, 2 * std::min(pairs, a.tiles), n, (int)classes, a.target,
-               index_type, rw, loss + r0, lse + r0, status);
+               (const int*)a.gave_up, 2 * std::min(pairs, a.tiles), rows_of(c, r0), n, a.target, index_type, rw, loss + r0, lse + r0, status);
     if (e != cudaSuccess) return done(e);
   }
   return LOPT_OK;
@@ -905,6 +1042,8 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
   const int planes = grad_weight && grad_weight_type == LOPT_F32 ? 2 : 1;
   const int pairs = pair_count();
   const Plan p = plan_grad(rows, classes, cols, planes, !tma_rows(c.mw));
+  // The embedding's gradient adds to a contiguous table.
+  const bool split = p.sort_bytes && grad_weight_stride == cols;
   if (!lse || !workspace || workspace_bytes < p.size) return LOPT_E_ARG;
   if ((uintptr_t)lse % 4 || (uintptr_t)status % 4 || (uintptr_t)workspace % 256) return LOPT_E_ALIGN;
   const Span sl{lse, 1, rows, rows, 4}, sw{workspace, 1, p.size, p.size, 1};
@@ -912,20 +1051,20 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
   if ((rc = check_alias({mo, mg, sw}, {c.mx, c.mw, st, sr, sl}))) return rc;
   char* ws = static_cast<char*>(workspace);
   const bool bf16 = type == LOPT_BF16;
-  int* exponent = reinterpret_cast<int*>(ws + p.exponent);
-  cudaError_t e = launch(k_linear_ce_start, dim3(1), dim3(kMaxCtas), 0, s, false, 1, exponent, reinterpret_cast<int*>(ws + p.flags));
+  float *largest = reinterpret_cast<float*>(ws + p.largest), *hit = reinterpret_cast<float*>(ws + p.hit);
+  cudaError_t e = launch(k_linear_ce_start, dim3(1), dim3(kMaxCtas), 0, s, false, 1, largest, reinterpret_cast<int*>(ws + p.flags));
   if (e != cudaSuccess) return done(e);
   uint16_t* xp = reinterpret_cast<uint16_t*>(ws + p.x);
   e = launch(k_linear_ce_copy, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, true, 1, (const uint16_t*)x, x_stride, rows,
-             (int)cols, xp, p.x_stride, target, index_type, (int)classes, row_weight, exponent, status);
+             (int)cols, xp, p.x_stride, target, index_type, rows_of(c, 0), row_weight, lse, largest, hit, status);
   if (e != cudaSuccess) return done(e);
   const void* wp = weight;
   int64_t wst = weight_stride;
   if (!tma_rows(c.mw)) {
     wp = ws + p.w, wst = p.w_stride;
     e = launch(k_linear_ce_copy, dim3((unsigned)((classes + 7) / 8)), dim3(256), 0, s, true, 1, (const uint16_t*)weight, weight_stride,
-               classes, (int)cols, (uint16_t*)wp, wst, (const void*)nullptr, 0, 0, (const float*)nullptr, (int*)nullptr,
-               (int32_t*)nullptr);
+               classes, (int)cols, (uint16_t*)wp, wst, (const void*)nullptr, 0, Rows{}, (const float*)nullptr, (const float*)nullptr, (float*)nullptr,
+               (float*)nullptr, (int32_t*)nullptr);
     if (e != cudaSuccess) return done(e);
   }
   Maps maps{};
@@ -941,7 +1080,8 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
   if (!ok) return LOPT_E_UNSUPPORTED;
   a.rows = (int)rows, a.classes = (int)classes, a.cols = (int)cols, a.planes = planes, a.is_bf16 = bf16;
   a.target = target, a.index_type = index_type, a.row_weight = row_weight, a.lse = lse;
-  a.g_stride = p.chunk, a.exponent = exponent;
+  a.g_stride = p.chunk, a.largest = largest;
+  a.hit = hit, a.split = split;
   a.dx = reinterpret_cast<float*>(ws + p.dx), a.dx_stride = p.dx_stride, a.dx_slice = p.slice;
   a.dw = grad_weight, a.dw_type = grad_weight_type, a.dw_stride = grad_weight_stride, a.accumulate = accumulate;
   a.gave_up = reinterpret_cast<int*>(ws + p.flags), a.status = status;
@@ -950,7 +1090,7 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
   auto grad_job = [&](int64_t k) {
     const int64_t v0 = k * p.chunk, v1 = std::min(classes, v0 + p.chunk);
     const int n_tiles = (int)(up(v1 - v0, kTile) / kTile);
-    return Job{kGrad, 0, m_tiles * n_tiles, m_tiles, n_tiles, 1, (int)(up(cols, kStep) / kStep), (int)(k % p.buffers), (int)v0, (int)v1, 0};
+    return Job{kGrad, 0, m_tiles * n_tiles, m_tiles, n_tiles, 1, (int)(up(cols, kStep) / kStep), (int)(k % p.buffers), (int)v0, (int)v1, 0, kGradSegment};
   };
   // Launch k makes chunk k's G beside the products of chunk k - 1: the long
   // tiles first, the short ones of G fill the last round.
@@ -965,25 +1105,40 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
     if (k > 0) {
       Job g = grad_job(k - 1);
       if (grad_weight)
-        add(Job{kGradW, 0, g.n_tiles * d_tiles, g.n_tiles, d_tiles, 1, (int)(up(rows, kStep) / kStep) * planes, g.buffer, g.v0, g.v1, 0});
+        add(Job{kGradW, 0, g.n_tiles * d_tiles, g.n_tiles, d_tiles, 1, (int)(up(rows, kStep) / kStep) * planes, g.buffer, g.v0, g.v1, 0,
+                planes == 1 ? kAll : split ? kSplitSegment : kGradWSegment});
       if (grad_x)
         add(Job{kGradX, 0, m_tiles * d_tiles * p.splits, m_tiles, d_tiles, p.splits, (int)(up(g.v1 - g.v0, kStep) / kStep), g.buffer,
-                g.v0, g.v1, k > 1});
+                g.v0, g.v1, k > 1, kAll});
     }
     if (k < chunks) add(grad_job(k));
     if ((e = launch_tiles(maps, a, pairs, s)) != cudaSuccess) return done(e);
+  }
+  if (split) {
+    const dim3 grid((unsigned)((rows + 7) / 8));
+    float* share = reinterpret_cast<float*>(ws + p.share);
+    if (bf16)
+      e = launch(k_linear_ce_share<__nv_bfloat16>, grid, dim3(256), 0, s, true, 1, (const __nv_bfloat16*)xp, p.x_stride, rows, (int)cols,
+                 (const float*)hit, target, index_type, (int)classes, row_weight, share);
+    else
+      e = launch(k_linear_ce_share<__half>, grid, dim3(256), 0, s, true, 1, (const __half*)xp, p.x_stride, rows, (int)cols,
+                 (const float*)hit, target, index_type, (int)classes, row_weight, share);
+    if (e != cudaSuccess) return done(e);
+    rc = lopt_embed_backward(share, LOPT_F32, p.x_stride, target, index_type, rows, classes, cols, 1.f, 1,
+                             static_cast<float*>(grad_weight), ws + p.sort, p.sort_bytes, status, stream);
+    if (rc) return rc;
   }
   if (!grad_x) return LOPT_OK;
   const dim3 grid((unsigned)rows, (unsigned)((cols + 1023) / 1024));
   const int ctas = 2 * std::min(pairs, a.tiles);
   if (bf16)
     e = launch(k_linear_ce_grad_x<__nv_bfloat16>, grid, dim3(256), 0, s, true, 1, (const float*)a.dx, p.dx_stride, p.slice, p.splits,
-               rows, (int)cols, (const int*)exponent, target, index_type, (int)classes, row_weight, (const int*)a.gave_up, ctas,
-               (__nv_bfloat16*)grad_x, grad_x_stride);
+               rows, (int)cols, (const float*)largest, target, index_type, (int)classes, row_weight, (const float*)(split ? hit : nullptr), (const __nv_bfloat16*)wp, wst,
+               (const int*)a.gave_up, ctas, (__nv_bfloat16*)grad_x, grad_x_stride);
   else
     e = launch(k_linear_ce_grad_x<__half>, grid, dim3(256), 0, s, true, 1, (const float*)a.dx, p.dx_stride, p.slice, p.splits, rows,
-               (int)cols, (const int*)exponent, target, index_type, (int)classes, row_weight, (const int*)a.gave_up, ctas,
-               (__half*)grad_x, grad_x_stride);
+               (int)cols, (const float*)largest, target, index_type, (int)classes, row_weight, (const float*)(split ? hit : nullptr), (const __half*)wp, wst,
+               (const int*)a.gave_up, ctas, (__half*)grad_x, grad_x_stride);
   return done(e);
 }
 
