@@ -48,6 +48,30 @@ struct Hyper {
   float b1, nb1, b2, nb2, c1, c2, eps, keep;   // nb = 1 - b; c1 = lr / (1 - b1^t); c2 = 1 / sqrt(1 - b2^t); keep = 1 - lr * decay
   const float* clip;                           // the clip factor, below 0: change nothing; NULL: none
   int count, units;                            // tensors; warp units of a chunk
+  float minus_zero;                            // see Mul
+};
+
+// Two fp32 operations as one instruction, each rounded on its own.  A product is a
+// fused multiply-add of -0, which has to come from the launch's parameters: the
+// compiler joins mul.f32x2 (or one with a -0 that it knows) and add.f32x2, though
+// both say .rn.
+__device__ __forceinline__ uint64_t packed(float2 v) { return (uint64_t)__float_as_uint(v.y) << 32 | __float_as_uint(v.x); }
+__device__ __forceinline__ float2 unpacked(uint64_t v) { return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32))); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(packed(a)), "l"(packed(b)));
+  return unpacked(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(packed(a)), "l"(packed(b)), "l"(packed(c)));
+  return unpacked(r);
+}
+
+struct Mul {
+  float2 zero;
+  __device__ __forceinline__ explicit Mul(float minus_zero) : zero(make_float2(minus_zero, minus_zero)) {}
+  __device__ __forceinline__ float2 operator()(float2 a, float2 b) const { return fma2(a, b, zero); }
 };
 
 __host__ __device__ inline uint32_t mix(uint32_t h) {
@@ -126,24 +150,81 @@ __device__ __forceinline__ float largest(const float (&x)[8]) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, most));
 }
 
-// The code of |x| = y / inv units, 0 to top: floor(sqrt(y)), or one more.
+// 8-bit moments, two elements at a time.  Conversions between small integers and
+// floats go through the bits of 2^23 + integer: the conversion instructions run at an
+// eighth of the rate.
+__device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
+constexpr float k2p23 = 8388608.f;
+constexpr float kCode = 12582912.f;   // 1.5 * 2^23: kCode + q has the low byte of q, below 0 too
+
+// Bytes 2 * PAIR and 2 * PAIR + 1 of w, minus `bias`.
+template <int PAIR> __device__ __forceinline__ float2 bytes(uint32_t w, float bias) {
+  const float2 f = make_float2(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7650 | (2 * PAIR))),
+                               __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7650 | (2 * PAIR + 1))));
+  return add2(f, two(-k2p23 - bias));
+}
+
+__device__ __forceinline__ uint32_t low_bytes(float2 a, float2 b) {
+  const uint32_t lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
+  const uint32_t hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
+  return __byte_perm(lo, hi, 0x5410);
+}
+
+// A lane's eight codes, four in a word.
+__device__ __forceinline__ void load_codes(const uint8_t* p, bool vec, int lane, int left, uint32_t (&w)[2]) {
+  if (vec) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) w[j] = *reinterpret_cast<const uint32_t*>(p + j * 128 + lane * 4);
+  } else {
+    w[0] = w[1] = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k * 32 + lane < left) w[k / 4] |= (uint32_t)p[k * 32 + lane] << (8 * (k % 4));
+  }
+}
+__device__ __forceinline__ void store_codes(uint8_t* p, bool vec, int lane, int left, const uint32_t (&w)[2]) {
+  if (vec) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) *reinterpret_cast<uint32_t*>(p + j * 128 + lane * 4) = w[j];
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k * 32 + lane < left) p[k * 32 + lane] = (uint8_t)(w[k / 4] >> (8 * (k % 4)));
+  }
+}
+
+// The codes of |x| = y / inv units, 0 to TOP: floor(sqrt(y)), or one more where the
+// random number u = bits / 2^16 is below y's place between the two squares.  Gives
+// kCode + code.
 template <int TOP>
-__device__ __forceinline__ int encode(float x, float inv, uint32_t bits) {
-  const float y = fminf(__fmul_rn(fabsf(x), inv), (float)(TOP * TOP));
-  // The root's last bits do not matter: the two lines behind it make it the floor.
-  float r;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(y));
-  float low = floorf(r);
-  if (__fmul_rn(low, low) > y) low -= 1.f;
-  if (__fmul_rn(low + 1.f, low + 1.f) <= y) low += 1.f;
-  const float share = __fsub_rn(y, __fmul_rn(low, low));
-  const float step = __fadd_rn(__fmul_rn(2.f, low), 1.f);
-  return (int)low + (share > __fmul_rn(__fmul_rn((float)bits, 1.f / 65536.f), step) ? 1 : 0);
+__device__ __forceinline__ float2 encode(const Mul& mul, float2 x, float2 inv, uint32_t h0, uint32_t h1) {
+  constexpr float kMost = (float)(TOP * TOP);
+  float2 y = mul(make_float2(fabsf(x.x), fabsf(x.y)), inv);
+  y = make_float2(fminf(y.x, kMost), fminf(y.y, kMost));
+  // A root that is never above the true one; its floor is then at most one too low.
+  float2 r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(y.x));
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(y.y));
+  r = mul(r, two(1.f - 0x1p-21f));
+  float2 low = add2(make_float2(__fadd_rd(r.x, k2p23), __fadd_rd(r.y, k2p23)), two(-k2p23));
+  const float2 next = add2(low, two(1.f)), square = mul(next, next);
+  low = make_float2(square.x <= y.x ? next.x : low.x, square.y <= y.y ? next.y : low.y);
+  const float2 share = fma2(make_float2(-low.x, -low.y), low, y);
+  // u * (2 low + 1), rounded once: the step is scaled by 2^-16.
+  const float2 step = fma2(low, two(0x1p-15f), two(0x1p-16f));
+  // bits: the lower (255) or upper half of the hash, as a float.
+  constexpr uint32_t kSel = TOP == 127 ? 0x7632 : 0x7610;
+  const float2 u = add2(make_float2(__uint_as_float(__byte_perm(h0, 0x4b000000u, kSel)),
+                                          __uint_as_float(__byte_perm(h1, 0x4b000000u, kSel))), two(-k2p23));
+  const float2 edge = mul(u, step);
+  const float2 code = add2(low, make_float2(share.x > edge.x ? kCode + 1.f : kCode, share.y > edge.y ? kCode + 1.f : kCode));
+  return code;
 }
 
 template <int N, bool EIGHT>
 __global__ void __launch_bounds__(kWarps * 32) k_adamw(const __grid_constant__ List<N> list, const Hyper h) {
   const int lane = threadIdx.x % 32;
+  const Mul mul(h.minus_zero);
   float clip = 1.f;
   wait_for_previous();
   if (h.clip) {
@@ -162,25 +243,37 @@ __global__ void __launch_bounds__(kWarps * 32) k_adamw(const __grid_constant__ L
     load8(d.param + at, vec, lane, left, [&](int k, float x) { p[k] = x; });
     if (EIGHT) {
       const float ms = d.m_scale[unit], vs = d.v_scale[unit];
-      load8(static_cast<const int8_t*>(d.m) + at, vec, lane, left, [&](int k, int8_t x) { m[k] = decode(x, ms); });
-      load8(static_cast<const uint8_t*>(d.v) + at, vec, lane, left, [&](int k, uint8_t x) {
-        const float r = decode(x, vs);
-        v[k] = __fmul_rn(r, r);
-      });
+      uint32_t qm[2], qv[2];
+      load_codes(static_cast<const uint8_t*>(d.m) + at, vec, lane, left, qm);
+      load_codes(static_cast<const uint8_t*>(d.v) + at, vec, lane, left, qv);
+#pragma unroll
+      for (int k = 0; k < 8; k += 2) {
+        // int8 + 128 is a byte's value with the sign bit turned over.
+        const uint32_t wm = qm[k / 4] ^ 0x80808080u, wv = qv[k / 4];
+        const float2 a = k % 4 == 0 ? bytes<0>(wm, 128.f) : bytes<1>(wm, 128.f);
+        const float2 b = k % 4 == 0 ? bytes<0>(wv, 0.f) : bytes<1>(wv, 0.f);
+        const float2 x = mul(mul(a, make_float2(fabsf(a.x), fabsf(a.y))), two(ms));
+        const float2 r = mul(mul(b, b), two(vs)), r2 = mul(r, r);
+        m[k] = x.x, m[k + 1] = x.y, v[k] = r2.x, v[k + 1] = r2.y;
+      }
     } else {
       load8(static_cast<const float*>(d.m) + at, vec, lane, left, [&](int k, float x) { m[k] = x; });
       load8(static_cast<const float*>(d.v) + at, vec, lane, left, [&](int k, float x) { v[k] = x; });
     }
+    const float keep = d.decay ? h.keep : 1.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float x = __fmul_rn(g[k], clip);
-      m[k] = __fadd_rn(__fmul_rn(h.b1, m[k]), __fmul_rn(h.nb1, x));
-      v[k] = __fadd_rn(__fmul_rn(h.b2, v[k]), __fmul_rn(__fmul_rn(h.nb2, x), x));
-      const float root = __fsqrt_rn(v[k]);
-      const float step = __fdiv_rn(m[k], __fadd_rn(__fmul_rn(root, h.c2), h.eps));
-      if (d.decay) p[k] = __fmul_rn(p[k], h.keep);
-      p[k] = __fsub_rn(p[k], __fmul_rn(h.c1, step));
-      if (EIGHT) v[k] = root;
+    for (int k = 0; k < 8; k += 2) {
+      const float2 x = mul(make_float2(g[k], g[k + 1]), two(clip));
+      const float2 mk = add2(mul(make_float2(m[k], m[k + 1]), two(h.b1)), mul(x, two(h.nb1)));
+      const float2 vk = add2(mul(make_float2(v[k], v[k + 1]), two(h.b2)), mul(mul(x, two(h.nb2)), x));
+      const float2 root = make_float2(__fsqrt_rn(vk.x), __fsqrt_rn(vk.y));
+      const float2 under = add2(mul(root, two(h.c2)), two(h.eps));
+      const float2 step = make_float2(__fdiv_rn(mk.x, under.x), __fdiv_rn(mk.y, under.y));
+      // p * keep - c1 * step; the difference of two rounded products
+      const float2 pk = add2(mul(make_float2(p[k], p[k + 1]), two(keep)), mul(step, two(-h.c1)));
+      p[k] = pk.x, p[k + 1] = pk.y;
+      m[k] = mk.x, m[k + 1] = mk.y;
+      v[k] = EIGHT ? root.x : vk.x, v[k + 1] = EIGHT ? root.y : vk.y;
     }
     store8(d.param + at, vec, lane, left, [&](int k) { return p[k]; });
     if (d.copy) {
@@ -195,16 +288,22 @@ __global__ void __launch_bounds__(kWarps * 32) k_adamw(const __grid_constant__ L
       // NaN passes both tests and makes the block's scale NaN.
       const float im = am <= 1e-30f ? 0.f : __fdiv_rn(kM, am), iv = av <= 1e-30f ? 0.f : __fdiv_rn(kV, av);
       const uint32_t key = d.key ^ ((uint32_t)(at >> 32) * 0x85ebca6bu);
-      int qm[8], qv[8];
+      uint32_t qm[2], qv[2];
+      float2 fm[4], fv[4];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t bits = mix((uint32_t)(at + place(vec, lane, k)) ^ key);
-        const int q = encode<127>(m[k], im, bits >> 16);
-        qm[k] = m[k] < 0.f ? -q : q;
-        qv[k] = encode<255>(v[k], iv, bits & 0xffffu);
+      for (int k = 0; k < 8; k += 2) {
+        const uint32_t h0 = mix((uint32_t)(at + place(vec, lane, k)) ^ key), h1 = mix((uint32_t)(at + place(vec, lane, k + 1)) ^ key);
+        const float2 q = encode<127>(mul, make_float2(m[k], m[k + 1]), two(im), h0, h1);
+        fm[k / 2] = make_float2(m[k] < 0.f ? 2.f * kCode - q.x : q.x, m[k + 1] < 0.f ? 2.f * kCode - q.y : q.y);
+        fv[k / 2] = encode<255>(mul, make_float2(v[k], v[k + 1]), two(iv), h0, h1);
       }
-      store8(static_cast<int8_t*>(d.m) + at, vec, lane, left, [&](int k) { return (int8_t)qm[k]; });
-      store8(static_cast<uint8_t*>(d.v) + at, vec, lane, left, [&](int k) { return (uint8_t)qv[k]; });
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        qm[j] = low_bytes(fm[2 * j], fm[2 * j + 1]);
+        qv[j] = low_bytes(fv[2 * j], fv[2 * j + 1]);
+      }
+      store_codes(static_cast<uint8_t*>(d.m) + at, vec, lane, left, qm);
+      store_codes(static_cast<uint8_t*>(d.v) + at, vec, lane, left, qv);
       if (lane == 0) {
         d.m_scale[unit] = __fmul_rn(am, (float)(1.0 / (127 * 127)));
         d.v_scale[unit] = __fmul_rn(av, (float)(1.0 / (255 * 255)));
@@ -221,24 +320,31 @@ constexpr int kNormBlocks = 608;       // most blocks of a launch
 constexpr int kMaxPartials = 16 * kNormBlocks;
 
 // The sum of squares in about 48 bits: s the running sum, c the roundings of
-// the squares and of the sums (two-sum and fused multiply-add residuals).
+// the squares and of the sums (two-sum and fused multiply-add residuals), two sums
+// side by side.
 struct Sum {
-  float s = 0.f, c = 0.f;
+  float2 s = {0.f, 0.f}, c = {0.f, 0.f};
   uint32_t any = 0;
-  __device__ __forceinline__ void add(float x) {
-    const float p = __fmul_rn(x, x), e = __fmaf_rn(x, x, -p);
-    const float t = __fadd_rn(s, p), b = __fsub_rn(t, s);
-    c += __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(p, b)) + e;
+  __device__ __forceinline__ void add(const Mul& mul, float x, float y) {
+    const float2 v = make_float2(x, y), minus = make_float2(-1.f, -1.f);
+    const float2 p = mul(v, v), e = fma2(v, v, mul(p, minus));
+    const float2 t = add2(s, p), b = fma2(s, minus, t);
+    const float2 lost = add2(fma2(fma2(b, minus, t), minus, s), fma2(b, minus, p));
+    c = add2(c, add2(lost, e));
     s = t;
-    any |= __float_as_uint(x);
+    any |= __float_as_uint(x) | __float_as_uint(y);
   }
+  __device__ __forceinline__ double total() const { return ((double)s.x + (double)s.y) + ((double)c.x + (double)c.y); }
   // Squares that overflow or vanish in fp32: the caller adds again in fp64.
-  __device__ __forceinline__ bool lost() const { return !(s < 1e38f) || (s < 1e-20f && (any << 1)); }
+  __device__ __forceinline__ bool lost() const {
+    return !(s.x + s.y < 1e38f) || (s.x + s.y < 1e-20f && (any << 1));
+  }
 };
 
 template <int N>
 __global__ void __launch_bounds__(kWarps * 32) k_adamw_norm(const __grid_constant__ List<N> list, int count, int units,
-                                                            int chunks, double* part) {
+                                                            int chunks, float minus_zero, double* part) {
+  const Mul mul(minus_zero);
   __shared__ double red[kWarps];
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
   wait_for_previous();
@@ -248,17 +354,22 @@ __global__ void __launch_bounds__(kWarps * 32) k_adamw_norm(const __grid_constan
     const Desc& d = list.d[find(list, count, chunk)];
     const int64_t first = (int64_t)(chunk - d.first) * units;
     Sum sum;
-    for (int u = w; u < units; u += kWarps) {
-      const int64_t at = (first + u) * kUnit;
-      if (at >= d.n) break;
-      const int left = (int)min((int64_t)kUnit, d.n - at);
-      float g[8];
-      load_grad(d, at, d.vec && left == kUnit, lane, left, g);
+    // Four units' loads side by side: 80 KB of an SM on their way.
+    for (int u = w; u < units; u += 4 * kWarps) {
+      float g[4][8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum.add(g[k]);
+      for (int q = 0; q < 4; ++q) {
+        const int64_t at = (first + u + q * kWarps) * kUnit;
+        const int left = u + q * kWarps < units && at < d.n ? (int)min((int64_t)kUnit, d.n - at) : 0;
+        load_grad(d, at, d.vec && left == kUnit, lane, left, g[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) sum.add(mul, g[q][k], g[q][k + 1]);
     }
     if (!sum.lost()) {
-      total += (double)sum.s + (double)sum.c;
+      total += sum.total();
       continue;
     }
     for (int u = w; u < units; u += kWarps) {
@@ -384,7 +495,7 @@ bool all_aligned(const lopt_adamw_tensor& t) {
 
 // Warp units of a chunk: lists that would not fill the GPU otherwise get
 // small chunks.
-int chunk_units(int64_t units, int sms) { return units > (int64_t)sms * 8 * 4 * kWarps ? 4 * kWarps : kWarps; }
+int chunk_units(int64_t units, int sms) { return units > (int64_t)sms * 8 * 16 * kWarps ? 16 * kWarps : kWarps; }
 
 template <int N, bool EIGHT>
 cudaError_t launch_step(const List<N>& list, const Hyper& h, int chunks, cudaStream_t s) {
@@ -486,7 +597,7 @@ int step(const lopt_adamw_tensor* tensors, int32_t n, int64_t t, double lr, doub
   h.b1 = (float)beta1, h.nb1 = (float)(1.0 - beta1), h.b2 = (float)beta2, h.nb2 = (float)(1.0 - beta2);
   h.c1 = (float)(lr / (1.0 - std::pow(beta1, (double)t)));
   h.c2 = (float)(1.0 / std::sqrt(1.0 - std::pow(beta2, (double)t)));
-  h.eps = (float)eps, h.keep = (float)(1.0 - lr * weight_decay), h.clip = nullptr, h.units = per;
+  h.eps = (float)eps, h.keep = (float)(1.0 - lr * weight_decay), h.clip = nullptr, h.units = per, h.minus_zero = -0.f;
   cudaError_t e = cudaSuccess;
   if (clipped) {
     int count = 0;
@@ -497,7 +608,7 @@ int step(const lopt_adamw_tensor* tensors, int32_t n, int64_t t, double lr, doub
       e = with_list(tensors, p, per, seed, [&](const auto& list) {
         constexpr int N = sizeof(list.d) / sizeof(list.d[0]);
         return launch(k_adamw_norm<N>, dim3((unsigned)blocks), dim3(kWarps * 32), 0, s, true, 1, list,
-                      (int)p.index.size(), per, p.chunks, part + count);
+                      (int)p.index.size(), per, p.chunks, -0.f, part + count);
       });
       if (e != cudaSuccess) return done(e);
       count += blocks;

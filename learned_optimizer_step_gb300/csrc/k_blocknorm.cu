@@ -208,14 +208,19 @@ __global__ void __launch_bounds__(512) k_block_norm_fwd_long(const Fwd a) {
 }
 
 // ---- backward ------------------------------------------------------------------
-__host__ __device__ constexpr int bwd_threads(int L) { return L % 96 == 0 ? 480 / L * L : 512; }
+// Threads of a block, of which an SM takes one: 24 warps of lanes with 8 elements of
+// 16 bits, else 16.
+__host__ __device__ constexpr int bwd_threads(int E, int L, int es) {
+  return E <= 8 && es == 2 && L <= 256 ? 768 : L % 96 == 0 ? 480 : 512;
+}
 
 // Persistent: a block's groups of L threads take rows blockIdx.x * R + group,
-// striding by gridDim.x * R.  With AHEAD, the next row is loaded before the
-// current one is reduced.
+// striding by gridDim.x * R.  With AHEAD, the next row's grad_y and summed are loaded
+// before the current row is reduced; the second sum's inputs are loaded before the
+// first sum.
 template <typename T, int VEC, int SLOTS, int L, bool GATE, bool AHEAD>
-__global__ void __launch_bounds__(bwd_threads(L), 1) k_block_norm_bwd(const Bwd a) {
-  constexpr int TH = bwd_threads(L), R = TH / L, W = L * VEC * SLOTS;
+__global__ void __launch_bounds__(bwd_threads(VEC * SLOTS, L, sizeof(T)), 1) k_block_norm_bwd(const Bwd a) {
+  constexpr int TH = bwd_threads(VEC * SLOTS, L, sizeof(T)), R = TH / L, W = L * VEC * SLOTS;
   using P = Pack<T, VEC>;
   __shared__ float red[2][TH / 32];
   extern __shared__ __align__(16) float comb[];   // the groups' sums, at the end: [2][R][W]
@@ -231,34 +236,40 @@ __global__ void __launch_bounds__(bwd_threads(L), 1) k_block_norm_bwd(const Bwd 
   for (int s = 0; s < SLOTS; ++s)
 #pragma unroll
     for (int k = 0; k < VEC; ++k) dw1[s][k] = dw2[s][k] = 0.f;
-  struct Row {
-    P dy[SLOTS], x[SLOTS], h[SLOTS], g[SLOTS], ds[SLOTS];
-    float r1, r2;
+  struct First {
+    P dy[SLOTS], x[SLOTS];
+    float r2;
   };
-  auto load = [&](int64_t r, Row& q) {
-    q.r1 = a.rstd_post[r];
+  auto load = [&](int64_t r, First& q) {
     q.r2 = a.rstd_pre[r];
     const T* dp = static_cast<const T*>(a.dy) + r * a.dys + lane * VEC;
     const T* xp = static_cast<const T*>(a.summed) + r * a.xs + lane * VEC;
-    const T* hp = static_cast<const T*>(a.h) + r * a.hs + lane * VEC;
-    const T* gp = static_cast<const T*>(a.gate) + r * a.gs + lane * VEC;
-    const T* sp = static_cast<const T*>(a.dsum) + r * a.dss + lane * VEC;
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
       if (!in(s)) continue;
       q.dy[s] = *reinterpret_cast<const P*>(dp + s * L * VEC);
       q.x[s] = *reinterpret_cast<const P*>(xp + s * L * VEC);
-      q.h[s] = *reinterpret_cast<const P*>(hp + s * L * VEC);
-      if (GATE) q.g[s] = *reinterpret_cast<const P*>(gp + s * L * VEC);
-      if (sums) q.ds[s] = *reinterpret_cast<const P*>(sp + s * L * VEC);
     }
   };
   int64_t row = (int64_t)blockIdx.x * R + group;
-  Row q, next;
+  First q, next;
   if (row < a.rows) load(row, q);
   for (; row < a.rows; row += stride) {
+    P ph[SLOTS], pg[SLOTS], ps[SLOTS];
+    {
+      const T* hp = static_cast<const T*>(a.h) + row * a.hs + lane * VEC;
+      const T* sp = static_cast<const T*>(a.dsum) + row * a.dss + lane * VEC;
+      const T* gp = static_cast<const T*>(a.gate) + row * a.gs + lane * VEC;
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s) {
+        if (!in(s)) continue;
+        if (sums) ps[s] = *reinterpret_cast<const P*>(sp + s * L * VEC);
+        ph[s] = *reinterpret_cast<const P*>(hp + s * L * VEC);
+        if (GATE) pg[s] = *reinterpret_cast<const P*>(gp + s * L * VEC);
+      }
+    }
+    const float r1 = a.rstd_post[row], r2 = q.r2;
     if (AHEAD && row + stride < a.rows) load(row + stride, next);
-    const float r1 = q.r1, r2 = q.r2;
     float sg = 0.f;
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
@@ -288,14 +299,14 @@ __global__ void __launch_bounds__(bwd_threads(L), 1) k_block_norm_bwd(const Bwd 
 #pragma unroll
       for (int k = 0; k < VEC; ++k) o[k] = fmaf(x[k], c1, d[k] * w[k] * r2);
       if (sums) {
-        to_floats(q.ds[s], x);
+        to_floats(ps[s], x);
 #pragma unroll
         for (int k = 0; k < VEC; ++k) o[k] += x[k];
       }
       *reinterpret_cast<P*>(rp + s * L * VEC) = from_floats<T, VEC>(o);
       load_weights<T, VEC>(a.w_post, a.wtype, (s * L + lane) * VEC, w);
-      to_floats(q.h[s], h);
-      if (GATE) to_floats(q.g[s], x);
+      to_floats(ph[s], h);
+      if (GATE) to_floats(pg[s], x);
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
         float open = 1.f, shut = 0.f;
@@ -315,7 +326,7 @@ __global__ void __launch_bounds__(bwd_threads(L), 1) k_block_norm_bwd(const Bwd 
     for (int s = 0; s < SLOTS; ++s) {
       if (!in(s)) continue;
       float h[VEC];
-      to_floats(q.h[s], h);
+      to_floats(ph[s], h);
 #pragma unroll
       for (int k = 0; k < VEC; ++k) h[k] = fmaf(h[k], c2, qh[s][k] * r1);
       *reinterpret_cast<P*>(hp + s * L * VEC) = from_floats<T, VEC>(h);
@@ -485,7 +496,7 @@ template <typename T> struct BwdRun {
   cudaStream_t s;
   int* blocks;
   template <int V, int S, int L, bool G> cudaError_t run_as() {
-    constexpr int TH = bwd_threads(L), R = TH / L;
+    constexpr int TH = bwd_threads(V * S, L, sizeof(T)), R = TH / L;
     const size_t smem = R > 1 ? (size_t)TH * V * S * 8 : 0;
     auto* k = &k_block_norm_bwd<T, V, S, L, G, (V * S <= 8)>;
     const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem);
