@@ -2,8 +2,10 @@
 //
 // Forward: a row of h, residual and gate is read once into registers; two sums
 // of squares over the row, one after the other, give rms(h) and rms(summed).
-// Backward: two sums over the row again, sum(g xhat) and then sum(q hhat), whose
-// terms need the first; each thread keeps the sums over rows of its own
+// Backward: sum(q hhat) needs grad_residual, which needs sum(g xhat).  But it is
+// linear in it: with c1 = -rstd_pre^2 sum(g xhat) / cols, grad_residual = A + c1 summed,
+// and sum(q hhat) = sum(u A) + c1 sum(u summed) with u = scale open w_post hhat.  So
+// three sums over the row, taken together, do: a row waits once, not twice.  Each thread keeps the sums over rows of its own
 // columns (the gradients of both weights) in registers, the blocks' sums go to
 // the workspace and a second kernel adds them in block order.  Both directions
 // are bound by HBM bytes: 4 arrays forward, 6 backward, one and two more with a
@@ -53,6 +55,32 @@ __device__ __forceinline__ float group_sum(float v, float* red, int group) {
 #pragma unroll
   for (int k = 1; k < W; ++k) t += red[k];
   return t;
+}
+
+// Three sums; red alternates between two areas from row to row.
+struct Sums {
+  float a, b, c;
+};
+template <int L>
+__device__ __forceinline__ Sums group_sum3(Sums v, Sums* red, int group) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    v.a += __shfl_xor_sync(0xffffffffu, v.a, o);
+    v.b += __shfl_xor_sync(0xffffffffu, v.b, o);
+    v.c += __shfl_xor_sync(0xffffffffu, v.c, o);
+  }
+  if (L == 32) return v;
+  constexpr int W = L / 32;
+  red += group * W;
+  if (threadIdx.x % 32 == 0) red[threadIdx.x % L / 32] = v;
+  asm volatile("bar.sync %0, %1;" :: "r"(1 + group), "n"(L) : "memory");
+  v = red[0];
+#pragma unroll
+  for (int k = 1; k < W; ++k) {
+    const Sums t = red[k];
+    v.a += t.a, v.b += t.b, v.c += t.c;
+  }
+  return v;
 }
 
 template <typename T, int VEC>
@@ -208,21 +236,22 @@ __global__ void __launch_bounds__(512) k_block_norm_fwd_long(const Fwd a) {
 }
 
 // ---- backward ------------------------------------------------------------------
-// Threads of a block, of which an SM takes one: 24 warps of lanes with 8 elements of
-// 16 bits, else 16.
-__host__ __device__ constexpr int bwd_threads(int E, int L, int es) {
-  return E <= 8 && es == 2 && L <= 256 ? 768 : L % 96 == 0 ? 480 : 512;
+// Threads of a block, of which an SM takes one: 24 warps of lanes with one vector of 8
+// elements of 16 bits, else 16 (us, bfloat16: 32,768 x 2048 203 with 24 warps, 229 with
+// 16; with a gate 315, 317; element by element 32,768 x 2001 351, 296).
+__host__ __device__ constexpr int bwd_threads(int vec, int slots, int L, int es) {
+  return vec == 8 && slots == 1 && es == 2 && L <= 256 ? 768 : L % 96 == 0 ? 480 : 512;
 }
 
 // Persistent: a block's groups of L threads take rows blockIdx.x * R + group,
-// striding by gridDim.x * R.  With AHEAD, the next row's grad_y and summed are loaded
-// before the current row is reduced; the second sum's inputs are loaded before the
-// first sum.
-template <typename T, int VEC, int SLOTS, int L, bool GATE, bool AHEAD>
-__global__ void __launch_bounds__(bwd_threads(VEC * SLOTS, L, sizeof(T)), 1) k_block_norm_bwd(const Bwd a) {
-  constexpr int TH = bwd_threads(VEC * SLOTS, L, sizeof(T)), R = TH / L, W = L * VEC * SLOTS;
+// striding by gridDim.x * R.  With 16 warps the next row is fetched to L2 meanwhile
+// (16,384 x 4096 bfloat16 205 us, 224 without; with 24 it costs more than it gives: 203
+// us became 220).
+template <typename T, int VEC, int SLOTS, int L, bool GATE>
+__global__ void __launch_bounds__(bwd_threads(VEC, SLOTS, L, sizeof(T)), 1) k_block_norm_bwd(const Bwd a) {
+  constexpr int TH = bwd_threads(VEC, SLOTS, L, sizeof(T)), R = TH / L, W = L * VEC * SLOTS;
   using P = Pack<T, VEC>;
-  __shared__ float red[2][TH / 32];
+  __shared__ Sums red[2][TH / 32];
   extern __shared__ __align__(16) float comb[];   // the groups' sums, at the end: [2][R][W]
   const int lane = threadIdx.x % L, group = threadIdx.x / L;
   const int cols = (int)a.cols;
@@ -236,103 +265,100 @@ __global__ void __launch_bounds__(bwd_threads(VEC * SLOTS, L, sizeof(T)), 1) k_b
   for (int s = 0; s < SLOTS; ++s)
 #pragma unroll
     for (int k = 0; k < VEC; ++k) dw1[s][k] = dw2[s][k] = 0.f;
-  struct First {
-    P dy[SLOTS], x[SLOTS];
-    float r2;
-  };
-  auto load = [&](int64_t r, First& q) {
-    q.r2 = a.rstd_pre[r];
-    const T* dp = static_cast<const T*>(a.dy) + r * a.dys + lane * VEC;
-    const T* xp = static_cast<const T*>(a.summed) + r * a.xs + lane * VEC;
+  int par = 0;
+  for (int64_t row = (int64_t)blockIdx.x * R + group; row < a.rows; row += stride, par ^= 1) {
+    P pd[SLOTS], px[SLOTS], ph[SLOTS], pg[SLOTS], ps[SLOTS];
+    const T* dp = static_cast<const T*>(a.dy) + row * a.dys + lane * VEC;
+    const T* xp = static_cast<const T*>(a.summed) + row * a.xs + lane * VEC;
+    const T* hp = static_cast<const T*>(a.h) + row * a.hs + lane * VEC;
+    const T* sp = static_cast<const T*>(a.dsum) + row * a.dss + lane * VEC;
+    const T* gp = static_cast<const T*>(a.gate) + row * a.gs + lane * VEC;
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
       if (!in(s)) continue;
-      q.dy[s] = *reinterpret_cast<const P*>(dp + s * L * VEC);
-      q.x[s] = *reinterpret_cast<const P*>(xp + s * L * VEC);
+      pd[s] = *reinterpret_cast<const P*>(dp + s * L * VEC);
+      px[s] = *reinterpret_cast<const P*>(xp + s * L * VEC);
+      ph[s] = *reinterpret_cast<const P*>(hp + s * L * VEC);
+      if (sums) ps[s] = *reinterpret_cast<const P*>(sp + s * L * VEC);
+      if (GATE) pg[s] = *reinterpret_cast<const P*>(gp + s * L * VEC);
     }
-  };
-  int64_t row = (int64_t)blockIdx.x * R + group;
-  First q, next;
-  if (row < a.rows) load(row, q);
-  for (; row < a.rows; row += stride) {
-    P ph[SLOTS], pg[SLOTS], ps[SLOTS];
-    {
-      const T* hp = static_cast<const T*>(a.h) + row * a.hs + lane * VEC;
-      const T* sp = static_cast<const T*>(a.dsum) + row * a.dss + lane * VEC;
-      const T* gp = static_cast<const T*>(a.gate) + row * a.gs + lane * VEC;
+    const float r1 = a.rstd_post[row], r2 = a.rstd_pre[row];
+    if (TH <= 512 && row + stride < a.rows) {
 #pragma unroll
       for (int s = 0; s < SLOTS; ++s) {
         if (!in(s)) continue;
-        if (sums) ps[s] = *reinterpret_cast<const P*>(sp + s * L * VEC);
-        ph[s] = *reinterpret_cast<const P*>(hp + s * L * VEC);
-        if (GATE) pg[s] = *reinterpret_cast<const P*>(gp + s * L * VEC);
+        fetch_line(dp + stride * a.dys + s * L * VEC);
+        fetch_line(xp + stride * a.xs + s * L * VEC);
+        fetch_line(hp + stride * a.hs + s * L * VEC);
+        if (sums) fetch_line(sp + stride * a.dss + s * L * VEC);
+        if (GATE) fetch_line(gp + stride * a.gs + s * L * VEC);
       }
     }
-    const float r1 = a.rstd_post[row], r2 = q.r2;
-    if (AHEAD && row + stride < a.rows) load(row + stride, next);
-    float sg = 0.f;
+    float A[SLOTS][VEC];
+    Sums t{0.f, 0.f, 0.f};
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
       if (!in(s)) continue;
-      float d[VEC], x[VEC], w[VEC];
-      to_floats(q.dy[s], d);
-      to_floats(q.x[s], x);
+      float d[VEC], x[VEC], w[VEC], h[VEC];
+      to_floats(pd[s], d);
+      to_floats(px[s], x);
       load_weights<T, VEC>(a.w_pre, a.wtype, (s * L + lane) * VEC, w);
+      if (sums) to_floats(ps[s], A[s]);
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
-        const float dx = d[k] * (x[k] * r2);
-        dw2[s][k] += dx;
-        sg = fmaf(dx, w[k], sg);
+        const float dx = d[k] * x[k];
+        dw2[s][k] = fmaf(dx, r2, dw2[s][k]);
+        t.a = fmaf(dx, w[k], t.a);
+        A[s][k] = fmaf(d[k] * w[k], r2, sums ? A[s][k] : 0.f);
+      }
+      load_weights<T, VEC>(a.w_post, a.wtype, (s * L + lane) * VEC, w);
+      to_floats(ph[s], h);
+      if (GATE) to_floats(pg[s], d);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        float u = h[k] * w[k];
+        if (GATE) {
+          float open, shut;
+          sigmoid(d[k], open, shut);
+          u *= open;
+        }
+        t.b = fmaf(u, A[s][k], t.b);
+        t.c = fmaf(u, x[k], t.c);
       }
     }
-    const float c1 = -r2 * r2 * (group_sum<L>(sg, red[0], group) * inv);
-    float qh[SLOTS][VEC], sq = 0.f;       // q; then hhat is made again
-    T* rp = static_cast<T*>(a.dres) + row * a.drs + lane * VEC;
-    T* gp = static_cast<T*>(a.dgate) + row * a.dgs + lane * VEC;
+    t = group_sum3<L>(t, red[par], group);
+    const float c1 = -r2 * r2 * r2 * (t.a * inv);
+    const float c2 = -r1 * r1 * r1 * a.scale * (fmaf(c1, t.c, t.b) * inv);
+    T* to_r = static_cast<T*>(a.dres) + row * a.drs + lane * VEC;
+    T* to_g = static_cast<T*>(a.dgate) + row * a.dgs + lane * VEC;
+    T* to_h = static_cast<T*>(a.dh) + row * a.dhs + lane * VEC;
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
       if (!in(s)) continue;
-      float d[VEC], x[VEC], w[VEC], h[VEC], o[VEC];
-      to_floats(q.dy[s], d);
-      to_floats(q.x[s], x);
-      load_weights<T, VEC>(a.w_pre, a.wtype, (s * L + lane) * VEC, w);
+      float x[VEC], w[VEC], h[VEC];
+      to_floats(px[s], x);
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) o[k] = fmaf(x[k], c1, d[k] * w[k] * r2);
-      if (sums) {
-        to_floats(ps[s], x);
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) o[k] += x[k];
-      }
-      *reinterpret_cast<P*>(rp + s * L * VEC) = from_floats<T, VEC>(o);
+      for (int k = 0; k < VEC; ++k) A[s][k] = fmaf(x[k], c1, A[s][k]);
+      *reinterpret_cast<P*>(to_r + s * L * VEC) = from_floats<T, VEC>(A[s]);
       load_weights<T, VEC>(a.w_post, a.wtype, (s * L + lane) * VEC, w);
       to_floats(ph[s], h);
       if (GATE) to_floats(pg[s], x);
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
-        float open = 1.f, shut = 0.f;
-        if (GATE) sigmoid(x[k], open, shut);
-        const float dz = o[k] * a.scale * open, hh = h[k] * r1;
-        dw1[s][k] = fmaf(dz, hh, dw1[s][k]);
-        qh[s][k] = dz * w[k];
-        const float t = qh[s][k] * hh;
-        sq += t;
-        if (GATE) x[k] = t * shut;
+        float dz = A[s][k] * (a.scale * r1), shut = 0.f;     // times rstd_post already
+        if (GATE) {
+          float open;
+          sigmoid(x[k], open, shut);
+          dz *= open;
+        }
+        dw1[s][k] = fmaf(dz, h[k], dw1[s][k]);
+        const float q = dz * w[k];
+        if (GATE) x[k] = q * h[k] * shut;
+        h[k] = fmaf(h[k], c2, q);
       }
-      if (GATE) *reinterpret_cast<P*>(gp + s * L * VEC) = from_floats<T, VEC>(x);
+      if (GATE) *reinterpret_cast<P*>(to_g + s * L * VEC) = from_floats<T, VEC>(x);
+      *reinterpret_cast<P*>(to_h + s * L * VEC) = from_floats<T, VEC>(h);
     }
-    const float c2 = -r1 * r1 * (group_sum<L>(sq, red[1], group) * inv);
-    T* hp = static_cast<T*>(a.dh) + row * a.dhs + lane * VEC;
-#pragma unroll
-    for (int s = 0; s < SLOTS; ++s) {
-      if (!in(s)) continue;
-      float h[VEC];
-      to_floats(ph[s], h);
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) h[k] = fmaf(h[k], c2, qh[s][k] * r1);
-      *reinterpret_cast<P*>(hp + s * L * VEC) = from_floats<T, VEC>(h);
-    }
-    if (AHEAD) q = next;
-    else if (row + stride < a.rows) load(row + stride, q);
   }
   // The block's sums: over its groups in order.
   float* p1 = a.part + (int64_t)blockIdx.x * cols;
@@ -496,9 +522,9 @@ template <typename T> struct BwdRun {
   cudaStream_t s;
   int* blocks;
   template <int V, int S, int L, bool G> cudaError_t run_as() {
-    constexpr int TH = bwd_threads(V * S, L, sizeof(T)), R = TH / L;
+    constexpr int TH = bwd_threads(V, S, L, sizeof(T)), R = TH / L;
     const size_t smem = R > 1 ? (size_t)TH * V * S * 8 : 0;
-    auto* k = &k_block_norm_bwd<T, V, S, L, G, (V * S <= 8)>;
+    auto* k = &k_block_norm_bwd<T, V, S, L, G>;
     const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem);
     if (e != cudaSuccess) return e;
     *blocks = (int)std::min<int64_t>({(a.rows + R - 1) / R, (int64_t)sms, kMaxBlocks});

@@ -63,9 +63,21 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 enum Mode { kLoss = 0, kGrad = 1, kGradX = 2, kGradW = 3 };
 
+constexpr int kMaxPairs = 128;
+constexpr int kGroups = 12;
+
+// Which pair takes which of a job's tiles.  In round r the pairs that take more than r
+// tiles take the next ones, so that tiles side by side, which share an operand, are
+// worked on at the same time.  The pairs that take equally many are a group.
+struct Spread {
+  int count[kMaxPairs];
+  uint8_t place[kMaxPairs];    // among the pairs, those that take most first
+  int groups, size[kGroups], takes[kGroups];
+};
+
 // One kind of tiles of a launch.
 struct Job {
-  int mode, first, tiles;      // its tiles are [first, first + tiles) of the launch
+  int mode, tiles;
   int m_tiles, n_tiles, splits;
   int k_steps;                 // of the whole product
   int buffer;                  // which G
@@ -101,7 +113,8 @@ struct Args {
   int* gave_up;                // one word per CTA
   int32_t* status;
   Job job[kJobs];
-  int jobs, tiles;
+  Spread spread[kJobs];
+  int jobs;
 };
 
 // ---- PTX -----------------------------------------------------------------------
@@ -205,11 +218,23 @@ __device__ __forceinline__ Tile tile_of(const Job& j, int t) {
   r.k1 = (int)((int64_t)j.k_steps * (r.split + 1) / j.splits);
   return r;
 }
-__device__ __forceinline__ const Job& job_of(const Args& a, int t) {
-  int k = 0;
-  while (k + 1 < a.jobs && t >= a.job[k + 1].first) ++k;
-  return a.job[k];
-}
+// A pair's tiles of a launch, job after job.
+struct Walk {
+  const Args& a;
+  int pair, job = 0, round = 0;
+  __device__ __forceinline__ Walk(const Args& args, int p) : a(args), pair(p) {}
+  __device__ __forceinline__ bool more() {
+    while (job < a.jobs && round >= a.spread[job].count[pair]) ++job, round = 0;
+    return job < a.jobs;
+  }
+  __device__ __forceinline__ Tile next() {
+    const Spread& s = a.spread[job];
+    int t = s.place[pair];
+    for (int g = 0; g < s.groups; ++g) t += s.size[g] * min(s.takes[g], round);
+    ++round;
+    return tile_of(a.job[job], t);
+  }
+};
 
 // ---- epilogues: a thread has 128 columns of a row, and takes 32 at a time ----------
 __device__ __forceinline__ void piece(const float (&acc)[kHalf], int c, float (&v)[32]) {
@@ -217,9 +242,30 @@ __device__ __forceinline__ void piece(const float (&acc)[kHalf], int c, float (&
   for (int k = 0; k < 32; ++k) v[k] = acc[32 * c + k];
 }
 
-__device__ __forceinline__ void loss_tile(const Args& a, const Tile& t, int row, int col, int half, const float (&acc)[kHalf]) {
-  int64_t target = -1;
-  if (row < a.rows) target = load_index(a.target, row, a.index_type);
+// What an epilogue wants of its row, loaded before the tile's product is done.
+struct RowIn {
+  int target;            // -1: none
+  float lse, scale, hit;
+};
+__device__ __forceinline__ RowIn row_in(const Args& a, int mode, int row) {
+  RowIn r{-1, 0.f, 0.f, 0.f};
+  if (mode > kGrad || row >= a.rows) return r;
+  const int64_t t = load_index(a.target, row, a.index_type);
+  if (mode == kGrad) {
+    float weight = a.row_weight ? a.row_weight[row] : 1.f;
+    r.lse = a.lse[row];
+    r.hit = a.hit[row];
+    const float largest = *a.largest;
+    if (t < 0 || t >= a.classes) weight = 0.f;
+    if (weight != 0.f) r.scale = weight / largest * 32768.f;
+    if (weight == 0.f) return r;
+  }
+  if (t >= 0 && t < a.classes) r.target = (int)t;
+  return r;
+}
+
+__device__ __forceinline__ void loss_tile(const Args& a, const Tile& t, const RowIn& in, int row, int col, int half,
+                                          const float (&acc)[kHalf]) {
   float most = -INFINITY, sum = 0.f;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -231,7 +277,7 @@ __device__ __forceinline__ void loss_tile(const Args& a, const Tile& t, int row,
       for (int k = 0; k < 32; ++k)
         if (c0 + k >= a.classes) v[k] = -INFINITY;
     }
-    const int64_t at = target - c0;      // added by the rows' kernel
+    const int at = in.target - c0;      // added by the rows' kernel
     if (at >= 0 && at < 32) {
 #pragma unroll
       for (int k = 0; k < 32; ++k)
@@ -255,17 +301,9 @@ __device__ __forceinline__ void loss_tile(const Args& a, const Tile& t, int row,
 }
 
 template <typename T>
-__device__ __forceinline__ void grad_tile(const Args& a, const Job& j, int row, int col, const float (&acc)[kHalf]) {
-  int64_t target = -1;
-  float lse = 0.f, scale = 0.f, weight = 0.f;
+__device__ __forceinline__ void grad_tile(const Args& a, const Job& j, const RowIn& in, int row, int col, const float (&acc)[kHalf]) {
+  const float lse = in.lse, scale = in.scale;
   const bool live = row < a.rows;
-  if (live) {
-    target = load_index(a.target, row, a.index_type);
-    if (target >= 0 && target < a.classes) weight = a.row_weight ? a.row_weight[row] : 1.f;
-    lse = a.lse[row];
-    if (weight != 0.f) scale = weight / *a.largest * 32768.f;
-    else target = -1;
-  }
   const int64_t out = (int64_t)row * a.g_stride + (col - j.v0);
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -274,11 +312,11 @@ __device__ __forceinline__ void grad_tile(const Args& a, const Job& j, int row, 
     const int c0 = col + 32 * c;
 #pragma unroll
     for (int k = 0; k < 32; ++k) v[k] = exp2_fast((v[k] - lse) * kLog2e);
-    const int64_t at = target - c0;
+    const int at = in.target - c0;
     if (at >= 0 && at < 32) {
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
-        if (at == k) v[k] = a.split ? 0.f : a.hit[row];
+        if (at == k) v[k] = a.split ? 0.f : in.hit;
       }
     }
 #pragma unroll
@@ -376,7 +414,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __shared__ int s_abort;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = cta_rank();
-  const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  const int pair = blockIdx.x / 2;
   const uint32_t stages = (smem_u32(raw) + 1023) & ~1023u;
   volatile int* abort = &s_abort;
   if (threadIdx.x == 0) {
@@ -409,9 +447,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 0 && lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
-      for (int t = pair; t < a.tiles; t += pairs) {
-        const Job& j = job_of(a, t);
-        const Tile x = tile_of(j, t - j.first);
+      for (Walk walk(a, pair); walk.more();) {
+        const Job& j = a.job[walk.job];
+        const Tile x = walk.next();
         const int m0 = x.m * kTile + rank * kHalf, n0 = x.n * kTile + rank * kHalf;
         for (int k = x.k0; k < x.k1; ++k) {
           if (!wait_for(smem_u32(&s_empty[stage]), phase ^ 1, abort)) break;
@@ -448,9 +486,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 1 && lane == 0 && rank == 0) {
       int stage = 0, buf = 0;
       uint32_t phase = 0, acc_phase = 0;
-      for (int t = pair; t < a.tiles; t += pairs) {
-        const Job& j = job_of(a, t);
-        const Tile x = tile_of(j, t - j.first);
+      for (Walk walk(a, pair); walk.more();) {
+        const Job& j = a.job[walk.job];
+        const Tile x = walk.next();
         const bool ak = j.mode != kGradW, bk = j.mode <= kGrad;   // K along the rows of A, B
         const uint32_t idesc = (1u << 4) | ((uint32_t)a.is_bf16 << 7) | ((uint32_t)a.is_bf16 << 10) | (ak ? 0u : 1u << 15) |
                                (bk ? 0u : 1u << 16) | ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
@@ -483,9 +521,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int quarter = warp % 4, half = (warp - 4) / 4;
     int buf = 0;
     uint32_t phase = 0;
-    for (int t = pair; t < a.tiles; t += pairs) {
-      const Job& j = job_of(a, t);
-      const Tile x = tile_of(j, t - j.first);
+    for (Walk walk(a, pair); walk.more();) {
+      const Job& j = a.job[walk.job];
+      const Tile x = walk.next();
+      const int row = x.m * kTile + rank * kHalf + quarter * 32 + lane;
+      const int col = x.n * kTile + half * kHalf;
+      const RowIn in = row_in(a, j.mode, row);
       float acc[kHalf];
       if (x.k0 == x.k1) {      // a slice without classes
 #pragma unroll
@@ -518,13 +559,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (++buf == 2) buf = 0, phase ^= 1;
       }
       if (!ok) break;
-      const int row = x.m * kTile + rank * kHalf + quarter * 32 + lane;
-      const int col = x.n * kTile + half * kHalf;
       if (j.mode == kLoss) {
-        loss_tile(a, x, row, j.v0 + col, half, acc);
+        loss_tile(a, x, in, row, j.v0 + col, half, acc);
       } else if (j.mode == kGrad) {
-        if (a.is_bf16) grad_tile<__nv_bfloat16>(a, j, row, j.v0 + col, acc);
-        else grad_tile<__half>(a, j, row, j.v0 + col, acc);
+        if (a.is_bf16) grad_tile<__nv_bfloat16>(a, j, in, row, j.v0 + col, acc);
+        else grad_tile<__half>(a, j, in, row, j.v0 + col, acc);
       } else if (j.mode == kGradX) {
         grad_x_tile(a, j, x, row, col, acc);
       } else if (a.dw_type == LOPT_F32) {
@@ -587,43 +626,58 @@ struct Rows {
   int cols, classes, bf16, vec;
 };
 
+// A block has eight rows: 64 threads for the tiles' statistics of each, and a warp for
+// its target's logit.
+constexpr int kRowsOfBlock = 8;
 __global__ void __launch_bounds__(512) k_linear_ce_rows(const float2* part, int parts, const int* gave_up, int ctas, const Rows q,
                                                         int64_t rows, const void* target, int index_type,
                                                         const float* row_weight, float* loss, float* lse, int32_t* status) {
-  __shared__ float2 red[16][32];
-  __shared__ float s_hit[32];
+  __shared__ float2 red[16][kRowsOfBlock];
+  __shared__ float s_hit[kRowsOfBlock];
   __shared__ int s_bad;
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
-  const int64_t row = (int64_t)blockIdx.x * 32 + lane;
+  const int64_t first = (int64_t)blockIdx.x * kRowsOfBlock;
   if (threadIdx.x == 0) s_bad = 0;
-  // The targets' logits need none of what the kernel before this one makes, but
-  // x and W may be the one's before.
   wait_for_previous();
   __syncthreads();
   if (threadIdx.x < ctas && gave_up[threadIdx.x]) s_bad = 1;
-  for (int r = w; r < 32; r += 16) {
-    const int64_t at = (int64_t)blockIdx.x * 32 + r;
-    if (at >= rows) break;
-    const int64_t t = load_index(target, at, index_type);
-    float z = -INFINITY;
-    if (t >= 0 && t < q.classes) z = row_dot(q.x + at * q.x_stride, q.w + t * q.w_stride, q.cols, q.vec, q.bf16, lane);
-    if (lane == 0) s_hit[r] = z;
-  }
   float m = -INFINITY, s = 0.f;
   auto join = [&](float2 p) {
     const float top = fmaxf(m, p.x), base = top == -INFINITY ? 0.f : top;
     s = s * exp2_fast((m - base) * kLog2e) + p.y * exp2_fast((p.x - base) * kLog2e);
     m = top;
   };
+  const int64_t row = first + lane % 8;
   if (row < rows) {
-#pragma unroll 4
-    for (int k = w; k < parts; k += 16) join(part[(int64_t)k * rows + row]);
+    constexpr int U = 8;      // 512 tiles' halves in one go
+    for (int k0 = threadIdx.x / 8; k0 < parts; k0 += 64 * U) {
+      float2 p[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        p[u] = k0 + 64 * u < parts ? part[(int64_t)(k0 + 64 * u) * rows + row] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int u = 0; u < U; ++u) join(p[u]);
+    }
   }
-  red[w][lane] = make_float2(m, s);
+  if (w < kRowsOfBlock && first + w < rows) {
+    const int64_t at = first + w, t = load_index(target, at, index_type);
+    float z = -INFINITY;
+    if (t >= 0 && t < q.classes) z = row_dot(q.x + at * q.x_stride, q.w + t * q.w_stride, q.cols, q.vec, q.bf16, lane);
+    if (lane == 0) s_hit[w] = z;
+  }
+#pragma unroll
+  for (int o = 8; o < 32; o *= 2)
+    join(make_float2(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o)));
+  if (lane < 8) red[w][lane] = make_float2(m, s);
   __syncthreads();
-  if (w || row >= rows) return;
+  if (w) return;
   m = -INFINITY, s = 0.f;
-  for (int k = 0; k < 16; ++k) join(red[k][lane]);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) join(red[lane / 8 * 4 + k][lane % 8]);
+#pragma unroll
+  for (int o = 8; o < 32; o *= 2)
+    join(make_float2(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o)));
+  if (lane >= 8 || row >= rows) return;
   const float hit = s_hit[lane];
   const int64_t t = load_index(target, row, index_type);
   // A target of -inf adds nothing, one of NaN makes the sum NaN.
@@ -826,13 +880,71 @@ int pair_count() {
     cudaGetLastError();
     n = sm_count() / 2;
   }
-  n = std::min(std::max(n, 1), kMaxCtas / 2);
+  n = std::min(std::max(n, 1), kMaxPairs);
   known[dev & 63].store(n, std::memory_order_relaxed);
   return n;
 }
 
+// Spreads a job's tiles, each of `cost`, over the pairs such that with the loads
+// that they have all end together as nearly as whole tiles allow.
+void spread_tiles(Spread& s, int tiles, double cost, int pairs, double* load) {
+  // The highest level up to which filling all pairs takes no more than the tiles.
+  double lo = *std::min_element(load, load + pairs), hi = *std::max_element(load, load + pairs) + cost * ((double)tiles / pairs + 2);
+  auto filled = [&](double level, int p) { return level > load[p] ? (int64_t)((level - load[p]) / cost) : 0; };
+  for (int it = 0; it < 48; ++it) {
+    const double mid = 0.5 * (lo + hi);
+    int64_t n = 0;
+    for (int p = 0; p < pairs; ++p) n += filled(mid, p);
+    (n <= tiles ? lo : hi) = mid;
+  }
+  int left = tiles;
+  for (int p = 0; p < pairs; ++p) {
+    s.count[p] = (int)filled(lo, p);
+    left -= s.count[p];
+    load[p] += s.count[p] * cost;
+  }
+  for (; left > 0; --left) {
+    const int p = (int)(std::min_element(load, load + pairs) - load);
+    ++s.count[p];
+    load[p] += cost;
+  }
+  int order[kMaxPairs];
+  for (int p = 0; p < pairs; ++p) order[p] = p;
+  auto kinds = [&] {
+    int n = 0;
+    for (int k = 0; k < pairs; ++k) n += k == 0 || s.count[order[k]] != s.count[order[k - 1]];
+    return n;
+  };
+  std::sort(order, order + pairs, [&](int x, int y) { return s.count[x] != s.count[y] ? s.count[x] > s.count[y] : x < y; });
+  if (kinds() > kGroups) {     // then evenly, whatever the loads are
+    for (int p = 0; p < pairs; ++p) order[p] = p, s.count[p] = tiles / pairs + (p < tiles % pairs);
+  }
+  s.groups = 0;
+  for (int k = 0; k < pairs; ++k) {
+    s.place[order[k]] = (uint8_t)k;
+    const int takes = s.count[order[k]];
+    if (s.groups && s.takes[s.groups - 1] == takes) {
+      ++s.size[s.groups - 1];
+    } else {
+      s.takes[s.groups] = takes;
+      s.size[s.groups++] = 1;
+    }
+  }
+}
+
+// Steps of K that a tile costs, with its epilogue: G's takes as long as some 20, and
+// only the next tile's product runs beside it.
+double tile_cost(const Job& j) {
+  const double steps = (double)j.k_steps / j.splits;
+  return j.mode == kGrad ? std::max(steps + 2.0, 20.0) : steps + 4.0;
+}
+
 cudaError_t launch_tiles(const Maps& maps, Args& a, int pairs, cudaStream_t s) {
-  a.tiles = a.job[a.jobs - 1].first + a.job[a.jobs - 1].tiles;
+  int tiles = 0;
+  for (int k = 0; k < a.jobs; ++k) tiles += a.job[k].tiles;
+  pairs = std::min(pairs, tiles);
+  double load[kMaxPairs] = {};
+  for (int k = 0; k < a.jobs; ++k) spread_tiles(a.spread[k], a.job[k].tiles, tile_cost(a.job[k]), pairs, load);
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&k_linear_ce), kSmem);
   if (e != cudaSuccess) return e;
   // The kernel's warps wait for registers that only a launch with kRegs has.
@@ -841,7 +953,7 @@ cudaError_t launch_tiles(const Maps& maps, Args& a, int pairs, cudaStream_t s) {
     return cudaFuncGetAttributes(&at, reinterpret_cast<const void*>(&k_linear_ce)) == cudaSuccess ? at.numRegs : 0;
   }();
   if (regs != kRegs) return cudaErrorInvalidKernelImage;
-  return launch(k_linear_ce, dim3(2 * (unsigned)std::min(pairs, a.tiles)), dim3(kThreads), kSmem, s, true, 1, maps, a);
+  return launch(k_linear_ce, dim3(2 * (unsigned)pairs), dim3(kThreads), kSmem, s, true, 1, maps, a);
 }
 
 // Where things are in the workspace, in bytes from its start.
@@ -1005,12 +1117,12 @@ int lopt_linear_ce_forward(const void* x, int type, int64_t rows, int64_t cols, 
     a.gave_up = reinterpret_cast<int*>(ws + p.flags), a.status = status;
     const int m_tiles = (int)(up(n, kTile) / kTile);
     a.jobs = 1;
-    a.job[0] = Job{kLoss, 0, m_tiles * n_tiles, m_tiles, n_tiles, 1, (int)(up(cols, kStep) / kStep), 0, 0, (int)classes, 0,
+    a.job[0] = Job{kLoss, m_tiles * n_tiles, m_tiles, n_tiles, 1, (int)(up(cols, kStep) / kStep), 0, 0, (int)classes, 0,
                    kLossSegment};
     if ((e = launch_tiles(maps, a, pairs, s)) != cudaSuccess) return done(e);
     const float* rw = row_weight ? row_weight + r0 : nullptr;
-    e = launch(k_linear_ce_rows, dim3((unsigned)((n + 31) / 32)), dim3(512), 0, s, true, 1, (const float2*)a.part, 2 * n_tiles,
-               (const int*)a.gave_up, 2 * std::min(pairs, a.tiles), rows_of(c, r0), n, a.target, index_type, rw, loss + r0, lse + r0, status);
+    e = launch(k_linear_ce_rows, dim3((unsigned)((n + kRowsOfBlock - 1) / kRowsOfBlock)), dim3(512), 0, s, true, 1, (const float2*)a.part, 2 * n_tiles,
+               (const int*)a.gave_up, 2 * std::min(pairs, a.job[0].tiles), rows_of(c, r0), n, a.target, index_type, rw, loss + r0, lse + r0, status);
     if (e != cudaSuccess) return done(e);
   }
   return LOPT_OK;
@@ -1090,27 +1202,24 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
   auto grad_job = [&](int64_t k) {
     const int64_t v0 = k * p.chunk, v1 = std::min(classes, v0 + p.chunk);
     const int n_tiles = (int)(up(v1 - v0, kTile) / kTile);
-    return Job{kGrad, 0, m_tiles * n_tiles, m_tiles, n_tiles, 1, (int)(up(cols, kStep) / kStep), (int)(k % p.buffers), (int)v0, (int)v1, 0, kGradSegment};
+    return Job{kGrad, m_tiles * n_tiles, m_tiles, n_tiles, 1, (int)(up(cols, kStep) / kStep), (int)(k % p.buffers), (int)v0, (int)v1, 0, kGradSegment};
   };
   // Launch k makes chunk k's G beside the products of chunk k - 1: the long
   // tiles first, the short ones of G fill the last round.
   for (int64_t k = 0; k <= chunks; ++k) {
     a.jobs = 0;
-    int first = 0;
-    auto add = [&](Job j) {
-      j.first = first;
-      first += j.tiles;
-      a.job[a.jobs++] = j;
-    };
+    auto add = [&](const Job& j) { a.job[a.jobs++] = j; };
     if (k > 0) {
       Job g = grad_job(k - 1);
       if (grad_weight)
-        add(Job{kGradW, 0, g.n_tiles * d_tiles, g.n_tiles, d_tiles, 1, (int)(up(rows, kStep) / kStep) * planes, g.buffer, g.v0, g.v1, 0,
+        add(Job{kGradW, g.n_tiles * d_tiles, g.n_tiles, d_tiles, 1, (int)(up(rows, kStep) / kStep) * planes, g.buffer, g.v0, g.v1, 0,
                 planes == 1 ? kAll : split ? kSplitSegment : kGradWSegment});
       if (grad_x)
-        add(Job{kGradX, 0, m_tiles * d_tiles * p.splits, m_tiles, d_tiles, p.splits, (int)(up(g.v1 - g.v0, kStep) / kStep), g.buffer,
+        add(Job{kGradX, m_tiles * d_tiles * p.splits, m_tiles, d_tiles, p.splits, (int)(up(g.v1 - g.v0, kStep) / kStep), g.buffer,
                 g.v0, g.v1, k > 1, kAll});
     }
+    // The costliest first: the others even out what they leave.
+    if (a.jobs == 2 && tile_cost(a.job[1]) > tile_cost(a.job[0])) std::swap(a.job[0], a.job[1]);
     if (k < chunks) add(grad_job(k));
     if ((e = launch_tiles(maps, a, pairs, s)) != cudaSuccess) return done(e);
   }
@@ -1130,7 +1239,7 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
   }
   if (!grad_x) return LOPT_OK;
   const dim3 grid((unsigned)rows, (unsigned)((cols + 1023) / 1024));
-  const int ctas = 2 * std::min(pairs, a.tiles);
+  const int ctas = kMaxCtas;
   if (bf16)
     e = launch(k_linear_ce_grad_x<__nv_bfloat16>, grid, dim3(256), 0, s, true, 1, (const float*)a.dx, p.dx_stride, p.slice, p.splits,
                rows, (int)cols, (const float*)largest, target, index_type, (int)classes, row_weight, (const float*)(split ? hit : nullptr), (const __nv_bfloat16*)wp, wst,
