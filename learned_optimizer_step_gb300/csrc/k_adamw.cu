@@ -142,13 +142,16 @@ __device__ __forceinline__ void load_grad(const Desc& d, int64_t at, bool vec, i
 
 __device__ __forceinline__ float decode(int q, float scale) { return __fmul_rn((float)(q * abs(q)), scale); }
 
-// Largest |x| of a warp, as bits: NaN is above infinity.
+// Largest |x| of a warp; NaN if any is.
 __device__ __forceinline__ float largest(const float (&x)[8]) {
-  uint32_t most = 0;
+  float most = fabsf(x[0]);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) most = max(most, __float_as_uint(x[k]) & 0x7fffffffu);
-  return __uint_as_float(__reduce_max_sync(0xffffffffu, most));
+  for (int k = 1; k < 8; ++k) asm("max.NaN.f32 %0, %0, %1;" : "+f"(most) : "f"(fabsf(x[k])));
+  // Above 0 the bits are in the values' order, and NaN's are above infinity's.
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most) & 0x7fffffffu));
 }
+
+__device__ __forceinline__ void fetch_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // 8-bit moments, two elements at a time.  Conversions between small integers and
 // floats go through the bits of 2^23 + integer: the conversion instructions run at an
@@ -199,17 +202,17 @@ __device__ __forceinline__ void store_codes(uint8_t* p, bool vec, int lane, int 
 template <int TOP>
 __device__ __forceinline__ float2 encode(const Mul& mul, float2 x, float2 inv, uint32_t h0, uint32_t h1) {
   constexpr float kMost = (float)(TOP * TOP);
-  float2 y = mul(make_float2(fabsf(x.x), fabsf(x.y)), inv);
-  y = make_float2(fminf(y.x, kMost), fminf(y.y, kMost));
+  float2 y = mul(x, inv);
+  y = make_float2(fminf(fabsf(y.x), kMost), fminf(fabsf(y.y), kMost));
   // A root that is never above the true one; its floor is then at most one too low.
   float2 r;
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(y.x));
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(y.y));
-  r = mul(r, two(1.f - 0x1p-21f));
-  float2 low = add2(make_float2(__fadd_rd(r.x, k2p23), __fadd_rd(r.y, k2p23)), two(-k2p23));
+  constexpr float kLess = 1.f - 0x1p-21f;
+  float2 low = add2(make_float2(__fmaf_rd(r.x, kLess, k2p23), __fmaf_rd(r.y, kLess, k2p23)), two(-k2p23));
   const float2 next = add2(low, two(1.f)), square = mul(next, next);
   low = make_float2(square.x <= y.x ? next.x : low.x, square.y <= y.y ? next.y : low.y);
-  const float2 share = fma2(make_float2(-low.x, -low.y), low, y);
+  const float2 share = make_float2(__fmaf_rn(-low.x, low.x, y.x), __fmaf_rn(-low.y, low.y, y.y));
   // u * (2 low + 1), rounded once: the step is scaled by 2^-16.
   const float2 step = fma2(low, two(0x1p-15f), two(0x1p-16f));
   // bits: the lower (255) or upper half of the hash, as a float.
@@ -239,6 +242,13 @@ __global__ void __launch_bounds__(kWarps * 32) k_adamw(const __grid_constant__ L
     const int left = (int)min((int64_t)kUnit, d.n - at);
     const bool vec = d.vec && left == kUnit;
     float p[8], g[8], m[8], v[8];
+    if (EIGHT && vec && at + (kWarps + 1) * kUnit <= d.n) {
+      const int64_t next = at + kWarps * kUnit;
+      fetch_line(d.param + next + lane * 8);
+      fetch_line(static_cast<const char*>(d.grad) + (next + lane * 8) * (d.grad_type == LOPT_F32 ? 4 : 2));
+      if (lane < 8) fetch_line(static_cast<const uint8_t*>(d.m) + next + lane * 32);
+      else if (lane < 16) fetch_line(static_cast<const uint8_t*>(d.v) + next + lane * 32 - 256);
+    }
     load_grad(d, at, vec, lane, left, g);
     load8(d.param + at, vec, lane, left, [&](int k, float x) { p[k] = x; });
     if (EIGHT) {
