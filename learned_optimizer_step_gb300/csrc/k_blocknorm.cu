@@ -236,23 +236,35 @@ __global__ void __launch_bounds__(512) k_block_norm_fwd_long(const Fwd a) {
 }
 
 // ---- backward ------------------------------------------------------------------
-// Threads of a block, of which an SM takes one: 24 warps of lanes with one vector of 8
-// elements of 16 bits, else 16 (us, bfloat16: 32,768 x 2048 203 with 24 warps, 229 with
-// 16; with a gate 315, 317; element by element 32,768 x 2001 351, 296).
-__host__ __device__ constexpr int bwd_threads(int vec, int slots, int L, int es) {
-  return vec == 8 && slots == 1 && es == 2 && L <= 256 ? 768 : L % 96 == 0 ? 480 : 512;
+// Threads of a block, of which an SM takes one: 16 warps with 128 registers, 12 with 168
+// where a lane has 24 elements.  24 warps spill and are slower (32,768 x 2048 bfloat16 341
+// us against 185 with 8 elements a lane).
+__host__ __device__ constexpr int bwd_threads(int E, int L) { return E == 24 ? 384 : L % 96 == 0 ? 480 : 512; }
+
+// Rows of whole vectors come ahead into shared memory: every thread copies its own 16
+// bytes of each array asynchronously and reads them back itself, so that no barrier is
+// needed; slots of rows of at most 5 arrays.
+__host__ __device__ constexpr bool bwd_ring(int vec, int slots, int L, int es) {
+  return vec * es == 16 && bwd_threads(vec * slots, L) * slots * 16 * 5 * 2 <= 200 * 1024;
+}
+__host__ __device__ constexpr int bwd_depth(int vec, int slots, int L) {
+  return bwd_threads(vec * slots, L) * slots * 16 * 5 * 3 <= 200 * 1024 ? 3 : 2;
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
 }
 
 // Persistent: a block's groups of L threads take rows blockIdx.x * R + group,
-// striding by gridDim.x * R.  With 16 warps the next row is fetched to L2 meanwhile
-// (16,384 x 4096 bfloat16 205 us, 224 without; with 24 it costs more than it gives: 203
-// us became 220).
+// striding by gridDim.x * R.
 template <typename T, int VEC, int SLOTS, int L, bool GATE>
-__global__ void __launch_bounds__(bwd_threads(VEC, SLOTS, L, sizeof(T)), 1) k_block_norm_bwd(const Bwd a) {
-  constexpr int TH = bwd_threads(VEC, SLOTS, L, sizeof(T)), R = TH / L, W = L * VEC * SLOTS;
+__global__ void __launch_bounds__(bwd_threads(VEC * SLOTS, L), 1) k_block_norm_bwd(const Bwd a) {
+  constexpr int TH = bwd_threads(VEC * SLOTS, L), R = TH / L, W = L * VEC * SLOTS;
   using P = Pack<T, VEC>;
   __shared__ Sums red[2][TH / 32];
-  extern __shared__ __align__(16) float comb[];   // the groups' sums, at the end: [2][R][W]
+  // The rows ahead, and at the end the groups' sums: [2][R][W]
+  extern __shared__ __align__(16) float comb[];
+  constexpr bool RING = bwd_ring(VEC, SLOTS, L, sizeof(T));
+  constexpr int DEPTH = bwd_depth(VEC, SLOTS, L);
   const int lane = threadIdx.x % L, group = threadIdx.x / L;
   const int cols = (int)a.cols;
   const float inv = 1.f / (float)cols;
@@ -265,61 +277,77 @@ __global__ void __launch_bounds__(bwd_threads(VEC, SLOTS, L, sizeof(T)), 1) k_bl
   for (int s = 0; s < SLOTS; ++s)
 #pragma unroll
     for (int k = 0; k < VEC; ++k) dw1[s][k] = dw2[s][k] = 0.f;
-  int par = 0;
-  for (int64_t row = (int64_t)blockIdx.x * R + group; row < a.rows; row += stride, par ^= 1) {
-    P pd[SLOTS], px[SLOTS], ph[SLOTS], pg[SLOTS], ps[SLOTS];
-    const T* dp = static_cast<const T*>(a.dy) + row * a.dys + lane * VEC;
-    const T* xp = static_cast<const T*>(a.summed) + row * a.xs + lane * VEC;
-    const T* hp = static_cast<const T*>(a.h) + row * a.hs + lane * VEC;
-    const T* sp = static_cast<const T*>(a.dsum) + row * a.dss + lane * VEC;
-    const T* gp = static_cast<const T*>(a.gate) + row * a.gs + lane * VEC;
+  enum { kDy, kX, kH, kSum, kGate, kArrays };
+  const void* const base[kArrays] = {a.dy, a.summed, a.h, a.dsum, a.gate};
+  const int64_t strides[kArrays] = {a.dys, a.xs, a.hs, a.dss, a.gs};
+  auto slot = [&](int d, int k, int s) { return (((d * kArrays + k) * SLOTS + s) * TH + threadIdx.x) * 16; };
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(comb);
+  auto fetch = [&](int64_t r, int d) {
+    if (r < a.rows) {
 #pragma unroll
-    for (int s = 0; s < SLOTS; ++s) {
-      if (!in(s)) continue;
-      pd[s] = *reinterpret_cast<const P*>(dp + s * L * VEC);
-      px[s] = *reinterpret_cast<const P*>(xp + s * L * VEC);
-      ph[s] = *reinterpret_cast<const P*>(hp + s * L * VEC);
-      if (sums) ps[s] = *reinterpret_cast<const P*>(sp + s * L * VEC);
-      if (GATE) pg[s] = *reinterpret_cast<const P*>(gp + s * L * VEC);
-    }
-    const float r1 = a.rstd_post[row], r2 = a.rstd_pre[row];
-    if (TH <= 512 && row + stride < a.rows) {
+      for (int k = 0; k < kArrays; ++k) {
+        if ((k == kSum && !sums) || (k == kGate && !GATE)) continue;
+        const T* p = static_cast<const T*>(base[k]) + r * strides[k] + lane * VEC;
 #pragma unroll
-      for (int s = 0; s < SLOTS; ++s) {
-        if (!in(s)) continue;
-        fetch_line(dp + stride * a.dys + s * L * VEC);
-        fetch_line(xp + stride * a.xs + s * L * VEC);
-        fetch_line(hp + stride * a.hs + s * L * VEC);
-        if (sums) fetch_line(sp + stride * a.dss + s * L * VEC);
-        if (GATE) fetch_line(gp + stride * a.gs + s * L * VEC);
+        for (int s = 0; s < SLOTS; ++s)
+          if (in(s)) copy16(ring + slot(d, k, s), p + s * L * VEC);
       }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int64_t row = (int64_t)blockIdx.x * R + group;
+  if (RING) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) fetch(row + d * stride, d);
+  }
+  float r1 = 0.f, r2 = 0.f;
+  if (row < a.rows) r1 = a.rstd_post[row], r2 = a.rstd_pre[row];
+  for (int par = 0, d = 0; row < a.rows; row += stride, par ^= 1) {
+    P own[kArrays][SLOTS];
+    float r1_next = 0.f, r2_next = 0.f;
+    if (row + stride < a.rows) r1_next = a.rstd_post[row + stride], r2_next = a.rstd_pre[row + stride];
+    if (RING) {
+      asm volatile("cp.async.wait_group %0;" :: "n"(DEPTH - 1) : "memory");
+    } else {
+#pragma unroll
+      for (int k = 0; k < kArrays; ++k) {
+        if ((k == kSum && !sums) || (k == kGate && !GATE)) continue;
+        const T* p = static_cast<const T*>(base[k]) + row * strides[k] + lane * VEC;
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s)
+          if (in(s)) own[k][s] = *reinterpret_cast<const P*>(p + s * L * VEC);
+      }
+    }
+    auto get = [&](int k, int s, float (&v)[VEC]) {
+      if constexpr (RING) to_floats(*reinterpret_cast<const P*>(reinterpret_cast<const char*>(comb) + slot(d, k, s)), v);
+      else to_floats(own[k][s], v);
+    };
     float A[SLOTS][VEC];
     Sums t{0.f, 0.f, 0.f};
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
       if (!in(s)) continue;
-      float d[VEC], x[VEC], w[VEC], h[VEC];
-      to_floats(pd[s], d);
-      to_floats(px[s], x);
+      float dy[VEC], x[VEC], w[VEC], h[VEC];
+      get(kDy, s, dy);
+      get(kX, s, x);
       load_weights<T, VEC>(a.w_pre, a.wtype, (s * L + lane) * VEC, w);
-      if (sums) to_floats(ps[s], A[s]);
+      if (sums) get(kSum, s, A[s]);
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
-        const float dx = d[k] * x[k];
+        const float dx = dy[k] * x[k];
         dw2[s][k] = fmaf(dx, r2, dw2[s][k]);
         t.a = fmaf(dx, w[k], t.a);
-        A[s][k] = fmaf(d[k] * w[k], r2, sums ? A[s][k] : 0.f);
+        A[s][k] = fmaf(dy[k] * w[k], r2, sums ? A[s][k] : 0.f);
       }
       load_weights<T, VEC>(a.w_post, a.wtype, (s * L + lane) * VEC, w);
-      to_floats(ph[s], h);
-      if (GATE) to_floats(pg[s], d);
+      get(kH, s, h);
+      if (GATE) get(kGate, s, dy);
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
         float u = h[k] * w[k];
         if (GATE) {
           float open, shut;
-          sigmoid(d[k], open, shut);
+          sigmoid(dy[k], open, shut);
           u *= open;
         }
         t.b = fmaf(u, A[s][k], t.b);
@@ -336,13 +364,13 @@ __global__ void __launch_bounds__(bwd_threads(VEC, SLOTS, L, sizeof(T)), 1) k_bl
     for (int s = 0; s < SLOTS; ++s) {
       if (!in(s)) continue;
       float x[VEC], w[VEC], h[VEC];
-      to_floats(px[s], x);
+      get(kX, s, x);
 #pragma unroll
       for (int k = 0; k < VEC; ++k) A[s][k] = fmaf(x[k], c1, A[s][k]);
       *reinterpret_cast<P*>(to_r + s * L * VEC) = from_floats<T, VEC>(A[s]);
       load_weights<T, VEC>(a.w_post, a.wtype, (s * L + lane) * VEC, w);
-      to_floats(ph[s], h);
-      if (GATE) to_floats(pg[s], x);
+      get(kH, s, h);
+      if (GATE) get(kGate, s, x);
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
         float dz = A[s][k] * (a.scale * r1), shut = 0.f;     // times rstd_post already
@@ -359,6 +387,15 @@ __global__ void __launch_bounds__(bwd_threads(VEC, SLOTS, L, sizeof(T)), 1) k_bl
       if (GATE) *reinterpret_cast<P*>(to_g + s * L * VEC) = from_floats<T, VEC>(x);
       *reinterpret_cast<P*>(to_h + s * L * VEC) = from_floats<T, VEC>(h);
     }
+    r1 = r1_next, r2 = r2_next;
+    if (RING) {
+      fetch(row + DEPTH * stride, d);
+      if (++d == DEPTH) d = 0;
+    }
+  }
+  if (RING) {      // the ring's place is wanted for the sums
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
   }
   // The block's sums: over its groups in order.
   float* p1 = a.part + (int64_t)blockIdx.x * cols;
@@ -522,8 +559,9 @@ template <typename T> struct BwdRun {
   cudaStream_t s;
   int* blocks;
   template <int V, int S, int L, bool G> cudaError_t run_as() {
-    constexpr int TH = bwd_threads(V, S, L, sizeof(T)), R = TH / L;
-    const size_t smem = R > 1 ? (size_t)TH * V * S * 8 : 0;
+    constexpr int TH = bwd_threads(V * S, L), R = TH / L;
+    const size_t ring = bwd_ring(V, S, L, sizeof(T)) ? (size_t)bwd_depth(V, S, L) * 5 * S * TH * 16 : 0;
+    const size_t smem = std::max(ring, R > 1 ? (size_t)TH * V * S * 8 : (size_t)0);
     auto* k = &k_block_norm_bwd<T, V, S, L, G>;
     const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem);
     if (e != cudaSuccess) return e;
@@ -566,17 +604,30 @@ template <int FULL, typename F> cudaError_t pick_fwd(int64_t cols, bool vec, F f
   }
   return f.long_rows();
 }
+// Backward in 16 bits: a lane takes 16 elements (a row's sum costs the same whatever
+// it has), a warp alone up to 24; in 32 bits 8 (us, 33.5M elements: 2048 wide float32 138
+// with 8, 163 with 16; 67M: bfloat16 185, 164, with 24 192, 32 168; with a gate 248, 200,
+// 222, 242; 768 wide with a gate 265 with 8 by 96 threads, 202 with 24 by a warp).
 template <int FULL, typename F> cudaError_t pick_bwd(int64_t cols, bool vec, F f) {
   if (vec) {
-    constexpr int B = 8 / FULL;
     const int64_t n = cols / FULL;
-    LOPT_ROWS(FULL, B, 32);
-    LOPT_ROWS(FULL, B, 64);
-    LOPT_ROWS(FULL, B, 96);
-    LOPT_ROWS(FULL, B, 128);
-    LOPT_ROWS(FULL, B, 256);
-    LOPT_ROWS(FULL, B, 512);
-    LOPT_ROWS(FULL, 2 * B, 512);
+    if constexpr (FULL == 8) {
+      LOPT_ROWS(8, 1, 32);
+      LOPT_ROWS(8, 2, 32);
+      LOPT_ROWS(8, 3, 32);
+      LOPT_ROWS(8, 2, 64);
+      LOPT_ROWS(8, 2, 128);
+      LOPT_ROWS(8, 2, 256);
+      LOPT_ROWS(8, 2, 512);
+    } else {
+      LOPT_ROWS(4, 2, 32);
+      LOPT_ROWS(4, 2, 64);
+      LOPT_ROWS(4, 2, 96);
+      LOPT_ROWS(4, 2, 128);
+      LOPT_ROWS(4, 2, 256);
+      LOPT_ROWS(4, 2, 512);
+      LOPT_ROWS(4, 4, 512);
+    }
   } else {
     const int64_t n = cols;
     LOPT_ROWS(1, 4, 32);
