@@ -53,8 +53,8 @@ constexpr int kOperand = kHalf * kStep * 2;      // bytes of one operand of a st
 constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 // Registers of a thread at launch, and after the first warpgroup has handed some
-// to the epilogue's two: 128 * 40 + 256 * 224 is less than 384 * 168.
-constexpr int kRegs = 168, kRegsFew = 40, kRegsMany = 224;
+// to the epilogue's two: 128 * 40 + 256 * 232 is 384 * 168.
+constexpr int kRegs = 168, kRegsFew = 40, kRegsMany = 232;
 static_assert(128 * kRegsFew + 256 * kRegsMany <= kThreads * kRegs, "");
 constexpr size_t kSmem = (size_t)kStages * 2 * kOperand + 1024 + 256;
 constexpr int kRowGroup = 32;                    // tiles of rows that share the classes' operand in L2
@@ -237,40 +237,63 @@ struct Walk {
 };
 
 // ---- epilogues: a thread has 128 columns of a row, and takes 32 at a time ----------
-__device__ __forceinline__ void piece(const float (&acc)[kHalf], int c, float (&v)[32]) {
+// From the accumulator itself, where that has summed all of K: a loop, so that few
+// registers are in use.
+struct FromTmem {
+  static constexpr int kUnroll = 1;
+  uint32_t src;
+  __device__ __forceinline__ void get(int c, float (&v)[32]) const {
+    uint32_t r[32];
+    __syncwarp();
+    tmem_ld32(src + 32 * c, r);
+    tmem_wait_ld();
 #pragma unroll
-  for (int k = 0; k < 32; ++k) v[k] = acc[32 * c + k];
-}
+    for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
+  }
+};
+// From the sums of several segments.
+struct FromSums {
+  static constexpr int kUnroll = 4;
+  const float (&acc)[kHalf];
+  __device__ __forceinline__ void get(int c, float (&v)[32]) const {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = acc[32 * c + k];
+  }
+};
 
-// What an epilogue wants of its row, loaded before the tile's product is done.
+// What an epilogue wants of its row: loaded while the tile before is worked on.
+struct RowLoads {
+  int64_t target = -1;
+  float weight = 1.f, lse = 0.f, hit = 0.f;
+};
+__device__ __forceinline__ RowLoads load_row(const Args& a, int mode, int row) {
+  RowLoads r;
+  if (mode > kGrad || row >= a.rows) return r;
+  r.target = load_index(a.target, row, a.index_type);
+  if (mode == kGrad) {
+    if (a.row_weight) r.weight = a.row_weight[row];
+    r.lse = a.lse[row];
+    r.hit = a.hit[row];
+  }
+  return r;
+}
 struct RowIn {
   int target;            // -1: none
   float lse, scale, hit;
 };
-__device__ __forceinline__ RowIn row_in(const Args& a, int mode, int row) {
-  RowIn r{-1, 0.f, 0.f, 0.f};
-  if (mode > kGrad || row >= a.rows) return r;
-  const int64_t t = load_index(a.target, row, a.index_type);
-  if (mode == kGrad) {
-    float weight = a.row_weight ? a.row_weight[row] : 1.f;
-    r.lse = a.lse[row];
-    r.hit = a.hit[row];
-    const float largest = *a.largest;
-    if (t < 0 || t >= a.classes) weight = 0.f;
-    if (weight != 0.f) r.scale = weight / largest * 32768.f;
-    if (weight == 0.f) return r;
-  }
-  if (t >= 0 && t < a.classes) r.target = (int)t;
-  return r;
+__device__ __forceinline__ RowIn row_in(const Args& a, const RowLoads& q, float largest) {
+  const bool live = q.target >= 0 && q.target < a.classes && q.weight != 0.f;
+  return RowIn{live ? (int)q.target : -1, q.lse, live ? q.weight / largest * 32768.f : 0.f, q.hit};
 }
+__device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
 
-__device__ __forceinline__ void loss_tile(const Args& a, const Tile& t, const RowIn& in, int row, int col, int half,
-                                          const float (&acc)[kHalf]) {
+template <typename Src>
+__device__ __forceinline__ void loss_tile(const Args& a, const Tile& t, const RowIn& in, int row, int col, int half, const Src& src) {
   float most = -INFINITY, sum = 0.f;
-#pragma unroll
+#pragma unroll Src::kUnroll
   for (int c = 0; c < 4; ++c) {
     float v[32];
-    piece(acc, c, v);
+    src.get(c, v);
     const int c0 = col + 32 * c;
     if (c0 + 32 > a.classes) {
 #pragma unroll
@@ -288,39 +311,41 @@ __device__ __forceinline__ void loss_tile(const Args& a, const Tile& t, const Ro
     for (int k = 0; k < 32; ++k) m = fmaxf(m, v[k]);
     // Nothing but -inf so far: 0 keeps exponents of it at 0.
     const float base = m == -INFINITY ? 0.f : m;
-    float s0 = 0.f, s1 = 0.f;
+    float2 s2 = two(0.f);
 #pragma unroll
     for (int k = 0; k < 32; k += 2) {
-      s0 += exp2_fast((v[k] - base) * kLog2e);
-      s1 += exp2_fast((v[k + 1] - base) * kLog2e);
+      const float2 z = __fmul2_rn(__fadd2_rn(make_float2(v[k], v[k + 1]), two(-base)), two(kLog2e));
+      s2 = __fadd2_rn(s2, make_float2(exp2_fast(z.x), exp2_fast(z.y)));
     }
-    sum = fmaf(sum, exp2_fast((most - base) * kLog2e), s0 + s1);
+    sum = fmaf(sum, exp2_fast((most - base) * kLog2e), s2.x + s2.y);
     most = m;
   }
   if (row < a.rows) a.part[(int64_t)(2 * t.n + half) * a.rows + row] = make_float2(most, sum);
 }
 
-template <typename T>
-__device__ __forceinline__ void grad_tile(const Args& a, const Job& j, const RowIn& in, int row, int col, const float (&acc)[kHalf]) {
+template <typename T, typename Src>
+__device__ __forceinline__ void grad_tile(const Args& a, const Job& j, const RowIn& in, int row, int col, const Src& src) {
   const float lse = in.lse, scale = in.scale;
   const bool live = row < a.rows;
   const int64_t out = (int64_t)row * a.g_stride + (col - j.v0);
-#pragma unroll
+#pragma unroll Src::kUnroll
   for (int c = 0; c < 4; ++c) {
     float v[32];
-    piece(acc, c, v);
+    src.get(c, v);
     const int c0 = col + 32 * c;
 #pragma unroll
-    for (int k = 0; k < 32; ++k) v[k] = exp2_fast((v[k] - lse) * kLog2e);
+    for (int k = 0; k < 32; k += 2) {
+      const float2 z = __fmul2_rn(__fadd2_rn(make_float2(v[k], v[k + 1]), two(-lse)), two(kLog2e));
+      const float2 p = __fmul2_rn(make_float2(exp2_fast(z.x), exp2_fast(z.y)), two(scale));
+      v[k] = p.x, v[k + 1] = p.y;
+    }
     const int at = in.target - c0;
     if (at >= 0 && at < 32) {
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
-        if (at == k) v[k] = a.split ? 0.f : in.hit;
+        if (at == k) v[k] = a.split ? 0.f : in.hit * scale;
       }
     }
-#pragma unroll
-    for (int k = 0; k < 32; ++k) v[k] *= scale;
     // Rows that do not count, whatever their logits hold, and classes past the last.
     if (scale == 0.f || c0 + 32 > a.classes) {
 #pragma unroll
@@ -333,12 +358,13 @@ __device__ __forceinline__ void grad_tile(const Args& a, const Job& j, const Row
       uint32_t hi[8], lo[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float x = v[16 * h + 2 * k], y = v[16 * h + 2 * k + 1];
-        Pack<T, 2> p, q;
-        p.v[0] = from_f<T>(x);
-        p.v[1] = from_f<T>(y);
-        q.v[0] = from_f<T>(x - to_f(p.v[0]));
-        q.v[1] = from_f<T>(y - to_f(p.v[1]));
+        const float x[2] = {v[16 * h + 2 * k], v[16 * h + 2 * k + 1]};
+        const Pack<T, 2> p = from_floats<T, 2>(x);
+        float y[2];
+        to_floats(p, y);
+        const float2 rest = __fadd2_rn(make_float2(x[0], x[1]), make_float2(-y[0], -y[1]));
+        const float z[2] = {rest.x, rest.y};
+        const Pack<T, 2> q = from_floats<T, 2>(z);
         hi[k] = *reinterpret_cast<const uint32_t*>(&p);
         lo[k] = *reinterpret_cast<const uint32_t*>(&q);
       }
@@ -348,12 +374,13 @@ __device__ __forceinline__ void grad_tile(const Args& a, const Job& j, const Row
   }
 }
 
-__device__ __forceinline__ void grad_x_tile(const Args& a, const Job& j, const Tile& t, int row, int col, const float (&acc)[kHalf]) {
+template <typename Src>
+__device__ __forceinline__ void grad_x_tile(const Args& a, const Job& j, const Tile& t, int row, int col, const Src& src) {
   float* out = a.dx + t.split * a.dx_slice + (int64_t)row * a.dx_stride + col;
-#pragma unroll
+#pragma unroll Src::kUnroll
   for (int c = 0; c < 4; ++c) {
     float v[32];
-    piece(acc, c, v);
+    src.get(c, v);
     if (row >= a.rows) continue;
 #pragma unroll
     for (int k = 0; k < 32; k += 4) {
@@ -388,20 +415,39 @@ __device__ __forceinline__ void put(O* p, int left, bool add, float f1, float f2
   }
 }
 // As many elements at a time as the rows' alignment allows: 16 bytes or one.
-template <typename O>
-__device__ __forceinline__ void grad_w_tile(const Args& a, const Job& j, int v, int col, const float (&acc)[kHalf]) {
+template <typename O, typename Src>
+__device__ __forceinline__ void grad_w_tile(const Args& a, const Job& j, int v, int col, const Src& src) {
   const float f1 = 1.f / 32768.f, f2 = *a.largest;
   constexpr int VEC = 16 / sizeof(O);
   O* out = static_cast<O*>(a.dw) + (int64_t)v * a.dw_stride + col;
   const bool vec = (a.cols % VEC == 0) && (a.dw_stride % VEC == 0) && (reinterpret_cast<uintptr_t>(a.dw) % 16 == 0);
-#pragma unroll
+#pragma unroll Src::kUnroll
   for (int c = 0; c < 4; ++c) {
     float x[32];
-    piece(acc, c, x);
+    src.get(c, x);
     if (v >= j.v1) continue;
     const int left = a.cols - (col + 32 * c);
     if (vec) put<O, VEC>(out + 32 * c, left, a.accumulate, f1, f2, x);
     else put<O, 1>(out + 32 * c, left, a.accumulate, f1, f2, x);
+  }
+}
+
+template <typename Src>
+__device__ __forceinline__ void finish_tile(const Args& a, const Job& j, const Tile& t, const RowIn& in, int row, int col, int half,
+                                            const Src& src) {
+  if (j.mode == kLoss) {
+    loss_tile(a, t, in, row, j.v0 + col, half, src);
+  } else if (j.mode == kGrad) {
+    if (a.is_bf16) grad_tile<__nv_bfloat16>(a, j, in, row, j.v0 + col, src);
+    else grad_tile<__half>(a, j, in, row, j.v0 + col, src);
+  } else if (j.mode == kGradX) {
+    grad_x_tile(a, j, t, row, col, src);
+  } else if (a.dw_type == LOPT_F32) {
+    grad_w_tile<float>(a, j, j.v0 + row, col, src);
+  } else if (a.dw_type == LOPT_F16) {
+    grad_w_tile<__half>(a, j, j.v0 + row, col, src);
+  } else {
+    grad_w_tile<__nv_bfloat16>(a, j, j.v0 + row, col, src);
   }
 }
 
@@ -521,58 +567,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int quarter = warp % 4, half = (warp - 4) / 4;
     int buf = 0;
     uint32_t phase = 0;
-    for (Walk walk(a, pair); walk.more();) {
-      const Job& j = a.job[walk.job];
-      const Tile x = walk.next();
-      const int row = x.m * kTile + rank * kHalf + quarter * 32 + lane;
+    const int own_row = rank * kHalf + quarter * 32 + lane;
+    const float largest = a.lse ? *a.largest : 1.f;
+    Walk walk(a, pair);
+    bool more = walk.more();
+    int job = walk.job;
+    Tile x{};
+    RowLoads ahead;
+    if (more) {
+      x = walk.next();
+      ahead = load_row(a, a.job[job].mode, x.m * kTile + own_row);
+    }
+    while (more) {
+      const Job& j = a.job[job];
+      const int row = x.m * kTile + own_row;
       const int col = x.n * kTile + half * kHalf;
-      const RowIn in = row_in(a, j.mode, row);
-      float acc[kHalf];
-      if (x.k0 == x.k1) {      // a slice without classes
-#pragma unroll
-        for (int k = 0; k < kHalf; ++k) acc[k] = 0.f;
-      }
-      bool ok = true;
-      for (int k = x.k0; k < x.k1; k += j.segment) {
-        ok = wait_for(smem_u32(&s_acc_full[buf]), phase, abort);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+      const RowIn in = row_in(a, ahead, largest);
+      const Tile now = x;
+      auto ready = [&] {
+        const bool ok = __all_sync(0xffffffffu, wait_for(smem_u32(&s_acc_full[buf]), phase, abort));
         tc_fence_after();
-        const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTile + half * kHalf;
-        const bool start = k == x.k0;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t r[32];
-          tmem_ld32(src + 32 * c, r);
-          tmem_wait_ld();
-          if (start) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) acc[32 * c + e] = __uint_as_float(r[e]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) acc[32 * c + e] += __uint_as_float(r[e]);
-          }
-        }
+        return ok;
+      };
+      auto source = [&] { return tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTile + half * kHalf; };
+      auto release = [&] {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_at(in_cta(smem_u32(&s_acc_empty[buf]), 0));
         if (++buf == 2) buf = 0, phase ^= 1;
+      };
+      auto look_ahead = [&] {
+        more = walk.more();
+        job = walk.job;
+        if (more) {
+          x = walk.next();
+          ahead = load_row(a, a.job[job].mode, x.m * kTile + own_row);
+        }
+      };
+      if (now.k1 - now.k0 <= j.segment && now.k1 > now.k0) {
+        if (!ready()) break;
+        look_ahead();
+        finish_tile(a, j, now, in, row, col, half, FromTmem{source()});
+        release();
+        continue;
+      }
+      float acc[kHalf];      // zeros for a slice without classes
+#pragma unroll
+      for (int k = 0; k < kHalf; ++k) acc[k] = 0.f;
+      bool ok = true;
+      for (int k = now.k0; k < now.k1; k += j.segment) {
+        ok = ready();
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float v[32];
+          FromTmem{source()}.get(c, v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) acc[32 * c + e] += v[e];
+        }
+        release();
       }
       if (!ok) break;
-      if (j.mode == kLoss) {
-        loss_tile(a, x, in, row, j.v0 + col, half, acc);
-      } else if (j.mode == kGrad) {
-        if (a.is_bf16) grad_tile<__nv_bfloat16>(a, j, in, row, j.v0 + col, acc);
-        else grad_tile<__half>(a, j, in, row, j.v0 + col, acc);
-      } else if (j.mode == kGradX) {
-        grad_x_tile(a, j, x, row, col, acc);
-      } else if (a.dw_type == LOPT_F32) {
-        grad_w_tile<float>(a, j, j.v0 + row, col, acc);
-      } else if (a.dw_type == LOPT_F16) {
-        grad_w_tile<__half>(a, j, j.v0 + row, col, acc);
-      } else {
-        grad_w_tile<__nv_bfloat16>(a, j, j.v0 + row, col, acc);
-      }
+      look_ahead();
+      finish_tile(a, j, now, in, row, col, half, FromSums{acc});
       __syncwarp();
     }
   }
