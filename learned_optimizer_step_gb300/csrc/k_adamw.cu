@@ -46,7 +46,10 @@ constexpr int kSmall = 24, kLarge = 400;
 
 struct Hyper {
   float b1, nb1, b2, nb2, c1, c2, eps, keep;   // nb = 1 - b; c1 = lr / (1 - b1^t); c2 = 1 / sqrt(1 - b2^t); keep = 1 - lr * decay
-  const float* clip;                           // the clip factor, below 0: change nothing; NULL: none
+  const double* part;                          // sums of squares of the gradients; NULL: no clipping
+  int parts;
+  double max_norm;
+  float* norm;
   int count, units;                            // tensors; warp units of a chunk
   float minus_zero;                            // see Mul
 };
@@ -224,16 +227,61 @@ __device__ __forceinline__ float2 encode(const Mul& mul, float2 x, float2 inv, u
   return code;
 }
 
+// A root and a quotient in some 46 bits: Newton's step on fp32's, whose residual alone
+// is taken in fp64.  (The fp64 functions take microseconds here.)
+__device__ __forceinline__ double root(double t) {
+  if (!(t > 1e-30 && t < 1e30)) return sqrt(t);
+  const float n = __fsqrt_rn((float)t);
+  return (double)n + (double)__fdiv_rn((float)fma(-(double)n, (double)n, t), 2.f * n);
+}
+// min(1, a / b) for a, b > 0
+__device__ __forceinline__ float clip_of(double a, double b) {
+  if (a >= b) return 1.f;
+  if (!(a > 1e-30 && b < 1e30)) return (float)(a / b);
+  const float d = (float)b, q = __fdiv_rn((float)a, d);
+  return (float)((double)q + (double)__fdiv_rn((float)fma(-(double)q, b, a), d));
+}
+
+// The clip factor from the blocks' sums, in a fixed order; false: the norm is not
+// finite.  Every block adds them again, by one warp: some 600 numbers from L2, beside a
+// launch that would do it once (4.7 us).  fp64 is slow here: all warps' sums cost a
+// small step 11 us.
+__device__ __forceinline__ bool clip_factor(const Hyper& h, float& clip) {
+  __shared__ float s_clip;
+  if (threadIdx.x < 32) {
+    double t = 0.0;
+    constexpr int U = 20;
+    for (int k = threadIdx.x; k < h.parts; k += U * 32) {
+      double v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = k + u * 32 < h.parts ? h.part[k + u * 32] : 0.0;
+#pragma unroll
+      for (int n = U; n > 1; n = (n + 1) / 2)      // as a tree: few additions one after the other
+#pragma unroll
+        for (int u = 0; u < n / 2; ++u) v[u] += v[u + (n + 1) / 2];
+      t += v[0];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if (threadIdx.x == 0) {
+      t = root(t);
+      const float n = (float)t;
+      if (h.norm && blockIdx.x == 0) *h.norm = n;
+      s_clip = n <= 3.4028235e38f ? clip_of(h.max_norm, t + 1e-6) : -1.f;
+    }
+  }
+  __syncthreads();
+  clip = s_clip;
+  return clip >= 0.f;
+}
+
 template <int N, bool EIGHT>
 __global__ void __launch_bounds__(kWarps * 32) k_adamw(const __grid_constant__ List<N> list, const Hyper h) {
   const int lane = threadIdx.x % 32;
   const Mul mul(h.minus_zero);
   float clip = 1.f;
   wait_for_previous();
-  if (h.clip) {
-    clip = *h.clip;
-    if (clip < 0.f) return;
-  }
+  if (h.part && !clip_factor(h, clip)) return;
   const Desc& d = list.d[find(list, h.count, blockIdx.x)];
   const int64_t first = (int64_t)(blockIdx.x - d.first) * h.units;
   for (int u = threadIdx.x / 32; u < h.units; u += kWarps) {
@@ -371,7 +419,12 @@ __global__ void __launch_bounds__(kWarps * 32) k_adamw_norm(const __grid_constan
       for (int q = 0; q < 4; ++q) {
         const int64_t at = (first + u + q * kWarps) * kUnit;
         const int left = u + q * kWarps < units && at < d.n ? (int)min((int64_t)kUnit, d.n - at) : 0;
-        load_grad(d, at, d.vec && left == kUnit, lane, left, g[q]);
+        if (left > 0) {
+          load_grad(d, at, d.vec && left == kUnit, lane, left, g[q]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) g[q][k] = 0.f;
+        }
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q)
@@ -402,24 +455,8 @@ __global__ void __launch_bounds__(kWarps * 32) k_adamw_norm(const __grid_constan
   }
 }
 
-// part[0 .. count) in a fixed order; out: the norm, and the clip factor or -1.
-__global__ void __launch_bounds__(256) k_adamw_clip(const double* part, int count, double max_norm, float* norm, float* clip) {
-  __shared__ double red[8];
-  wait_for_previous();
-  let_next_start();
-  double t = 0.0;
-  for (int k = threadIdx.x; k < count; k += 256) t += part[k];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = t;
-  __syncthreads();
-  if (threadIdx.x) return;
-  for (int k = 1; k < 8; ++k) t += red[k];
-  t = sqrt(t);
-  const float n = (float)t;
-  *norm = n;
-  *clip = !(n <= 3.4028235e38f) ? -1.f : (float)fmin(1.0, max_norm / (t + 1e-6));
-}
+// For a list without elements.
+__global__ void k_adamw_no_norm(float* norm) { *norm = 0.f; }
 
 // ---- the moments as values ----------------------------------------------------------
 struct Out {
@@ -607,7 +644,7 @@ int step(const lopt_adamw_tensor* tensors, int32_t n, int64_t t, double lr, doub
   h.b1 = (float)beta1, h.nb1 = (float)(1.0 - beta1), h.b2 = (float)beta2, h.nb2 = (float)(1.0 - beta2);
   h.c1 = (float)(lr / (1.0 - std::pow(beta1, (double)t)));
   h.c2 = (float)(1.0 / std::sqrt(1.0 - std::pow(beta2, (double)t)));
-  h.eps = (float)eps, h.keep = (float)(1.0 - lr * weight_decay), h.clip = nullptr, h.units = per, h.minus_zero = -0.f;
+  h.eps = (float)eps, h.keep = (float)(1.0 - lr * weight_decay), h.part = nullptr, h.parts = 0, h.max_norm = max_norm, h.norm = nullptr, h.units = per, h.minus_zero = -0.f;
   cudaError_t e = cudaSuccess;
   if (clipped) {
     int count = 0;
@@ -623,10 +660,8 @@ int step(const lopt_adamw_tensor* tensors, int32_t n, int64_t t, double lr, doub
       if (e != cudaSuccess) return done(e);
       count += blocks;
     }
-    float* clip = reinterpret_cast<float*>(part + kMaxPartials);
-    h.clip = clip;
-    e = launch(k_adamw_clip, dim3(1), dim3(256), 0, s, true, 1, (const double*)part, count, max_norm, norm, clip);
-    if (e != cudaSuccess) return done(e);
+    if (count == 0) return done(launch(k_adamw_no_norm, dim3(1), dim3(1), 0, s, true, 1, norm));
+    h.part = part, h.parts = count, h.norm = norm;
   }
   for (int bits : {32, 8}) {
     for (const Part& p : parts(tensors, n, bits, per)) {
@@ -636,6 +671,7 @@ int step(const lopt_adamw_tensor* tensors, int32_t n, int64_t t, double lr, doub
                          : launch_step<sizeof(list.d) / sizeof(list.d[0]), false>(list, h, p.chunks, s);
       });
       if (e != cudaSuccess) return done(e);
+      h.norm = nullptr;      // one launch writes it
     }
   }
   return LOPT_OK;
@@ -669,7 +705,7 @@ int lopt_adamw_check(const lopt_adamw_tensor* tensors, int32_t n) try {
 
 int lopt_adamw_workspace(int64_t* bytes) {
   if (!bytes) return LOPT_E_ARG;
-  *bytes = kMaxPartials * 8 + 256;   // partial sums, then the clip factor
+  *bytes = kMaxPartials * 8;   // partial sums
   return LOPT_OK;
 }
 

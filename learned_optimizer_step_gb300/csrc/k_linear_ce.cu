@@ -841,9 +841,14 @@ __global__ void __launch_bounds__(256) k_linear_ce_grad_x(const float* dx, int64
     for (int j = (blockIdx.y * 256 + threadIdx.x) * 4; j < cols; j += 1024 * gridDim.y) {
       float v[4] = {0.f, 0.f, 0.f, 0.f};
       if (live) {
-        for (int s = 0; s < slices; ++s) {
-          const float4 x = *reinterpret_cast<const float4*>(p + s * slice + j);
-          v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+        constexpr int U = 8;      // slices whose loads are on their way together
+        for (int s = 0; s < slices; s += U) {
+          float4 x[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            x[u] = s + u < slices ? *reinterpret_cast<const float4*>(p + (s + u) * slice + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int u = 0; u < U; ++u) v[0] += x[u].x, v[1] += x[u].y, v[2] += x[u].z, v[3] += x[u].w;
         }
       }
 #pragma unroll
@@ -945,28 +950,30 @@ int pair_count() {
 // Spreads a job's tiles, each of `cost`, over the pairs such that with the loads
 // that they have all end together as nearly as whole tiles allow.
 void spread_tiles(Spread& s, int tiles, double cost, int pairs, double* load) {
-  // The highest level up to which filling all pairs takes no more than the tiles.
-  double lo = *std::min_element(load, load + pairs), hi = *std::max_element(load, load + pairs) + cost * ((double)tiles / pairs + 2);
-  auto filled = [&](double level, int p) { return level > load[p] ? (int64_t)((level - load[p]) / cost) : 0; };
-  for (int it = 0; it < 48; ++it) {
-    const double mid = 0.5 * (lo + hi);
-    int64_t n = 0;
-    for (int p = 0; p < pairs; ++p) n += filled(mid, p);
-    (n <= tiles ? lo : hi) = mid;
+  // The level up to which the tiles fill those pairs that are below it.
+  double level = 0.0;
+  for (int n = pairs, before = 0; n != before;) {
+    double sum = tiles * cost;
+    before = n;
+    for (int p = 0; p < pairs; ++p) sum += before == pairs || load[p] < level ? load[p] : 0.0;
+    level = sum / n;
+    n = 0;
+    for (int p = 0; p < pairs; ++p) n += load[p] < level;
   }
   int left = tiles;
   for (int p = 0; p < pairs; ++p) {
-    s.count[p] = (int)filled(lo, p);
+    s.count[p] = load[p] < level ? std::min(left, (int)((level - load[p]) / cost)) : 0;
     left -= s.count[p];
     load[p] += s.count[p] * cost;
   }
-  for (; left > 0; --left) {
-    const int p = (int)(std::min_element(load, load + pairs) - load);
-    ++s.count[p];
-    load[p] += cost;
-  }
   int order[kMaxPairs];
   for (int p = 0; p < pairs; ++p) order[p] = p;
+  // What whole tiles leave over, one each to those with the least.
+  std::sort(order, order + pairs, [&](int x, int y) { return load[x] != load[y] ? load[x] < load[y] : x < y; });
+  for (int k = 0; left > 0; --left, k = (k + 1) % pairs) {
+    ++s.count[order[k]];
+    load[order[k]] += cost;
+  }
   auto kinds = [&] {
     int n = 0;
     for (int k = 0; k < pairs; ++k) n += k == 0 || s.count[order[k]] != s.count[order[k - 1]];
