@@ -56,7 +56,9 @@ constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 // to the epilogue's two: 128 * 40 + 256 * 232 is 384 * 168.
 constexpr int kRegs = 168, kRegsFew = 40, kRegsMany = 232;
 static_assert(128 * kRegsFew + 256 * kRegsMany <= kThreads * kRegs, "");
-constexpr size_t kSmem = (size_t)kStages * 2 * kOperand + 1024 + 256;
+constexpr int kPitch = 20;
+constexpr int kTurn = 32 * kPitch;               // floats of a warp's place to turn 16 columns of 32 rows
+constexpr size_t kSmem = (size_t)kStages * 2 * kOperand + 1024 + kEpilogueWarps * kTurn * 4;
 constexpr int kRowGroup = 32;                    // tiles of rows that share the classes' operand in L2
 constexpr uint64_t kLimitNs = 1000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -374,80 +376,102 @@ __device__ __forceinline__ void grad_tile(const Args& a, const Job& j, const Row
   }
 }
 
-template <typename Src>
-__device__ __forceinline__ void grad_x_tile(const Args& a, const Job& j, const Tile& t, int row, int col, const Src& src) {
-  float* out = a.dx + t.split * a.dx_slice + (int64_t)row * a.dx_stride + col;
-#pragma unroll Src::kUnroll
-  for (int c = 0; c < 4; ++c) {
-    float v[32];
-    src.get(c, v);
-    if (row >= a.rows) continue;
+// A warp's 32 rows of 32 columns to memory, times f1 f2.  They are turned in shared
+// memory, 16 columns at a time, so that the lanes of a store fill whole sectors: each
+// thread writing its own row leaves a sector to two stores of 32 rows each, or, element
+// by element, to 16 (us, grad_w of 100 x 100,000 classes fp16: 2000 wide 448 in all, 1999
+// wide 3,012).  Rows on 16-byte boundaries by vectors.
+struct Block {
+  int rows, cols;      // that there are, from the first on
+  int64_t stride;
+  bool vec, add;
+  float f1, f2;
+};
+template <typename O>
+__device__ __forceinline__ void store_block(O* out, const Block& b, float* turn, const float (&x)[32]) {
+  constexpr int VEC = 16 / sizeof(O), N = 16 / VEC;      // lanes of a row's 16 columns
+  const int lane = threadIdx.x % 32;
 #pragma unroll
-    for (int k = 0; k < 32; k += 4) {
-      if (col + 32 * c + k >= a.dx_stride) continue;
-      float4* p = reinterpret_cast<float4*>(out + 32 * c + k);
-      float4 x = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-      if (j.add) {
-        const float4 o = *p;
-        x = make_float4(x.x + o.x, x.y + o.y, x.z + o.z, x.w + o.w);
+  for (int h = 0; h < 2; ++h) {
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 16; k += 4)
+      *reinterpret_cast<float4*>(turn + lane * kPitch + k) =
+          make_float4(x[16 * h + k] * b.f1 * b.f2, x[16 * h + k + 1] * b.f1 * b.f2, x[16 * h + k + 2] * b.f1 * b.f2, x[16 * h + k + 3] * b.f1 * b.f2);
+    __syncwarp();
+    if (b.vec) {
+      const int k = lane % N * VEC;
+#pragma unroll
+      for (int r = lane / N; r < 32; r += 32 / N) {
+        if (r >= b.rows || 16 * h + k >= b.cols) continue;
+        float y[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) y[e] = turn[r * kPitch + k + e];
+        Pack<O, VEC>* q = reinterpret_cast<Pack<O, VEC>*>(out + r * b.stride + 16 * h + k);
+        if (b.add) {
+          float o[VEC];
+          to_floats(*q, o);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) y[e] += o[e];
+        }
+        *q = from_floats<O, VEC>(y);
       }
-      *p = x;
+    } else {
+      const int k = lane % 16;
+#pragma unroll 4
+      for (int r = lane / 16; r < 32; r += 2) {
+        if (r >= b.rows || 16 * h + k >= b.cols) continue;
+        O* q = out + r * b.stride + 16 * h + k;
+        const float y = turn[r * kPitch + k];
+        *q = from_f<O>(b.add ? y + to_f(*q) : y);
+      }
     }
   }
 }
 
-template <typename O, int VEC>
-__device__ __forceinline__ void put(O* p, int left, bool add, float f1, float f2, const float (&v)[32]) {
-#pragma unroll
-  for (int k = 0; k < 32; k += VEC) {
-    if (k >= left) continue;
-    float o[VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) o[e] = v[k + e] * f1 * f2;
-    Pack<O, VEC>* q = reinterpret_cast<Pack<O, VEC>*>(p + k);
-    if (add) {
-      float b[VEC];
-      to_floats(*q, b);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) o[e] += b[e];
-    }
-    *q = from_floats<O, VEC>(o);
+template <typename Src>
+__device__ __forceinline__ void grad_x_tile(const Args& a, const Job& j, const Tile& t, int row, int col, float* turn, const Src& src) {
+  const int first = row - threadIdx.x % 32;
+  float* out = a.dx + t.split * a.dx_slice + (int64_t)first * a.dx_stride + col;
+#pragma unroll Src::kUnroll
+  for (int c = 0; c < 4; ++c) {
+    float v[32];
+    src.get(c, v);
+    store_block<float>(out + 32 * c, Block{a.rows - first, (int)a.dx_stride - col - 32 * c, a.dx_stride, true, j.add != 0, 1.f, 1.f}, turn, v);
   }
 }
-// As many elements at a time as the rows' alignment allows: 16 bytes or one.
+
 template <typename O, typename Src>
-__device__ __forceinline__ void grad_w_tile(const Args& a, const Job& j, int v, int col, const Src& src) {
-  const float f1 = 1.f / 32768.f, f2 = *a.largest;
+__device__ __forceinline__ void grad_w_tile(const Args& a, const Job& j, int v, int col, float* turn, const Src& src) {
   constexpr int VEC = 16 / sizeof(O);
-  O* out = static_cast<O*>(a.dw) + (int64_t)v * a.dw_stride + col;
   const bool vec = (a.cols % VEC == 0) && (a.dw_stride % VEC == 0) && (reinterpret_cast<uintptr_t>(a.dw) % 16 == 0);
+  const int first = v - threadIdx.x % 32;
+  O* out = static_cast<O*>(a.dw) + (int64_t)first * a.dw_stride + col;
+  const float largest = *a.largest;
 #pragma unroll Src::kUnroll
   for (int c = 0; c < 4; ++c) {
     float x[32];
     src.get(c, x);
-    if (v >= j.v1) continue;
-    const int left = a.cols - (col + 32 * c);
-    if (vec) put<O, VEC>(out + 32 * c, left, a.accumulate, f1, f2, x);
-    else put<O, 1>(out + 32 * c, left, a.accumulate, f1, f2, x);
+    store_block<O>(out + 32 * c, Block{j.v1 - first, a.cols - col - 32 * c, a.dw_stride, vec, a.accumulate != 0, 1.f / 32768.f, largest}, turn, x);
   }
 }
 
 template <typename Src>
 __device__ __forceinline__ void finish_tile(const Args& a, const Job& j, const Tile& t, const RowIn& in, int row, int col, int half,
-                                            const Src& src) {
+                                            float* turn, const Src& src) {
   if (j.mode == kLoss) {
     loss_tile(a, t, in, row, j.v0 + col, half, src);
   } else if (j.mode == kGrad) {
     if (a.is_bf16) grad_tile<__nv_bfloat16>(a, j, in, row, j.v0 + col, src);
     else grad_tile<__half>(a, j, in, row, j.v0 + col, src);
   } else if (j.mode == kGradX) {
-    grad_x_tile(a, j, t, row, col, src);
+    grad_x_tile(a, j, t, row, col, turn, src);
   } else if (a.dw_type == LOPT_F32) {
-    grad_w_tile<float>(a, j, j.v0 + row, col, src);
+    grad_w_tile<float>(a, j, j.v0 + row, col, turn, src);
   } else if (a.dw_type == LOPT_F16) {
-    grad_w_tile<__half>(a, j, j.v0 + row, col, src);
+    grad_w_tile<__half>(a, j, j.v0 + row, col, turn, src);
   } else {
-    grad_w_tile<__nv_bfloat16>(a, j, j.v0 + row, col, src);
+    grad_w_tile<__nv_bfloat16>(a, j, j.v0 + row, col, turn, src);
   }
 }
 
@@ -567,6 +591,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int quarter = warp % 4, half = (warp - 4) / 4;
     int buf = 0;
     uint32_t phase = 0;
+    float* turn = reinterpret_cast<float*>(raw + (stages - smem_u32(raw)) + (size_t)kStages * 2 * kOperand) + (warp - 4) * kTurn;
     const int own_row = rank * kHalf + quarter * 32 + lane;
     const float largest = a.lse ? *a.largest : 1.f;
     Walk walk(a, pair);
@@ -607,7 +632,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (now.k1 - now.k0 <= j.segment && now.k1 > now.k0) {
         if (!ready()) break;
         look_ahead();
-        finish_tile(a, j, now, in, row, col, half, FromTmem{source()});
+        finish_tile(a, j, now, in, row, col, half, turn, FromTmem{source()});
         release();
         continue;
       }
@@ -629,7 +654,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       look_ahead();
-      finish_tile(a, j, now, in, row, col, half, FromSums{acc});
+      finish_tile(a, j, now, in, row, col, half, turn, FromSums{acc});
       __syncwarp();
     }
   }
@@ -667,6 +692,7 @@ __device__ __forceinline__ float row_dot(const T* x, const T* w, int cols, bool 
       for (int e = 0; e < 8; ++e) s = fmaf(a[e], b[e], s);
     }
   } else {
+#pragma unroll 8
     for (int j = lane; j < cols; j += 32) s = fmaf(to_f(x[j]), to_f(w[j]), s);
   }
   return warp_sum(s);
@@ -780,7 +806,28 @@ __global__ void __launch_bounds__(256) k_linear_ce_copy(const uint16_t* x, int64
     for (int j = lane * 8; j < cols; j += 256)
       *reinterpret_cast<uint4*>(to + j) = live ? *reinterpret_cast<const uint4*>(p + j) : make_uint4(0, 0, 0, 0);
   } else {
-    for (int j = lane; j < cols; j += 32) to[j] = live ? p[j] : 0;
+    // Eight elements at a time from 4-byte words, shifted where the row starts between
+    // two; words that reach past either end of the row are read in halves.
+    const bool odd = reinterpret_cast<uintptr_t>(p) & 2;
+#pragma unroll 2
+    for (int j = lane * 8; j < cols; j += 256) {
+      uint32_t w[4] = {0, 0, 0, 0};
+      if (live && (j + 8 > cols || (odd && (j == 0 || j + 9 > cols)))) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (j + e < cols) w[e / 2] |= (uint32_t)p[j + e] << (16 * (e % 2));
+      } else if (live) {
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(p + j - odd);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = q[e];
+        if (odd) {
+          const uint32_t last = q[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = __funnelshift_r(w[e], e < 3 ? w[e + 1] : last, 16);
+        }
+      }
+      *reinterpret_cast<uint4*>(to + j) = make_uint4(w[0], w[1], w[2], w[3]);      // the rows' ends are padded to 8
+    }
   }
 }
 
