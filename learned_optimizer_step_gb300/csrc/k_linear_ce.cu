@@ -74,7 +74,22 @@ constexpr int kGroups = 12;
 struct Spread {
   int count[kMaxPairs];
   uint8_t place[kMaxPairs];    // among the pairs, those that take most first
-  int groups, size[kGroups], takes[kGroups];
+  int pairs, groups, size[kGroups], takes[kGroups];
+};
+
+// Division of 0 <= t < 2^31 by d: with 2^(l - 1) < d <= 2^l and mul = ceil(2^(31 + l) / d),
+// t * mul / 2^(31 + l) is above t / d by less than 1 / d.  (A division in the instruction
+// stream of the thread that feeds the tensor cores takes as long as two steps of K.)
+struct FastDiv {
+  uint32_t mul = 1u << 31, shift = 31;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t d) {
+    uint32_t l = 0;
+    while ((1ull << l) < d) ++l;
+    shift = 31 + l;
+    mul = (uint32_t)(((1ull << shift) + d - 1) / d);
+  }
+  __device__ __forceinline__ int operator()(int t) const { return (int)((uint64_t)(uint32_t)t * mul >> shift); }
 };
 
 // One kind of tiles of a launch.
@@ -86,6 +101,7 @@ struct Job {
   int v0, v1;                  // classes of the chunk
   int add;                     // grad_x: add to the sums
   int segment;                 // K steps that one accumulator sums
+  FastDiv by_group, by_rows, by_last, by_n, by_splits;   // divisions by numbers of tiles
 };
 constexpr int kJobs = 3;
 
@@ -205,36 +221,64 @@ __device__ __forceinline__ Tile tile_of(const Job& j, int t) {
   Tile r;
   if (j.mode <= kGrad) {
     // Rows fastest, in groups that stay in L2 while the classes pass by.
-    const int group = t / (kRowGroup * j.n_tiles), left = t - group * kRowGroup * j.n_tiles;
+    const int group = j.by_group(t), left = t - group * kRowGroup * j.n_tiles;
     const int in_group = min(kRowGroup, j.m_tiles - group * kRowGroup);
-    r.n = left / in_group;
+    r.n = in_group == kRowGroup ? j.by_rows(left) : j.by_last(left);
     r.m = group * kRowGroup + left - r.n * in_group;
     r.split = 0;
   } else {
-    r.n = t % j.n_tiles;
-    t /= j.n_tiles;
-    r.split = t % j.splits;
-    r.m = t / j.splits;
+    const int q = j.by_n(t);
+    r.n = t - q * j.n_tiles;
+    r.m = j.by_splits(q);
+    r.split = q - r.m * j.splits;
   }
-  r.k0 = (int)((int64_t)j.k_steps * r.split / j.splits);
-  r.k1 = (int)((int64_t)j.k_steps * (r.split + 1) / j.splits);
+  r.k0 = j.by_splits(j.k_steps * r.split);
+  r.k1 = j.by_splits(j.k_steps * (r.split + 1));
   return r;
 }
 // A pair's tiles of a launch, job after job.
 struct Walk {
   const Args& a;
   int pair, job = 0, round = 0;
-  __device__ __forceinline__ Walk(const Args& args, int p) : a(args), pair(p) {}
+  int base = 0, active = 0, group = 0;      // the round's first tile; the pairs that take one
+  __device__ __forceinline__ Walk(const Args& args, int p) : a(args), pair(p) { start(); }
+  __device__ __forceinline__ void start() {
+    round = base = 0;
+    if (job >= a.jobs) return;
+    active = a.spread[job].pairs;
+    group = a.spread[job].groups;
+    leave();
+  }
+  // The groups that have had all of theirs.
+  __device__ __forceinline__ void leave() {
+    const Spread& s = a.spread[job];
+    while (group > 0 && s.takes[group - 1] <= round) active -= s.size[--group];
+  }
   __device__ __forceinline__ bool more() {
-    while (job < a.jobs && round >= a.spread[job].count[pair]) ++job, round = 0;
+    while (job < a.jobs && round >= a.spread[job].count[pair]) {
+      ++job;
+      start();
+    }
     return job < a.jobs;
   }
   __device__ __forceinline__ Tile next() {
-    const Spread& s = a.spread[job];
-    int t = s.place[pair];
-    for (int g = 0; g < s.groups; ++g) t += s.size[g] * min(s.takes[g], round);
+    const int t = base + a.spread[job].place[pair];
+    base += active;
     ++round;
+    leave();
     return tile_of(a.job[job], t);
+  }
+  // Its K steps alone.
+  __device__ __forceinline__ void next_steps(int& k0, int& k1) {
+    if (a.job[job].splits == 1) {
+      k0 = 0;
+      k1 = a.job[job].k_steps;
+      ++round;
+    } else {
+      const Tile t = next();
+      k0 = t.k0;
+      k1 = t.k1;
+    }
   }
 };
 
@@ -558,17 +602,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t phase = 0, acc_phase = 0;
       for (Walk walk(a, pair); walk.more();) {
         const Job& j = a.job[walk.job];
-        const Tile x = walk.next();
+        int k0, k1;
+        walk.next_steps(k0, k1);
         const bool ak = j.mode != kGradW, bk = j.mode <= kGrad;   // K along the rows of A, B
         const uint32_t idesc = (1u << 4) | ((uint32_t)a.is_bf16 << 7) | ((uint32_t)a.is_bf16 << 10) | (ak ? 0u : 1u << 15) |
                                (bk ? 0u : 1u << 16) | ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
         // 16 of K further: 32 bytes along the rows, two groups of eight rows across.
         const uint32_t step_a = (ak ? 32 : 2048) >> 4, step_b = (bk ? 32 : 2048) >> 4;
-        for (int k = x.k0; k < x.k1;) {
+        for (int k = k0; k < k1;) {
           if (!wait_for(smem_u32(&s_acc_empty[buf]), acc_phase ^ 1, abort)) break;
           tc_fence_after();
           const uint32_t d = tmem + buf * kTile;
-          const int first = k, end = min(k + j.segment, x.k1);
+          const int first = k, end = min(k + j.segment, k1);
           for (; k < end; ++k) {
             if (!wait_for(smem_u32(&s_full[stage]), phase, abort)) break;
             tc_fence_after();
@@ -1031,6 +1076,7 @@ void spread_tiles(Spread& s, int tiles, double cost, int pairs, double* load) {
     for (int p = 0; p < pairs; ++p) order[p] = p, s.count[p] = tiles / pairs + (p < tiles % pairs);
   }
   s.groups = 0;
+  s.pairs = pairs;
   for (int k = 0; k < pairs; ++k) {
     s.place[order[k]] = (uint8_t)k;
     const int takes = s.count[order[k]];
@@ -1055,7 +1101,12 @@ cudaError_t launch_tiles(const Maps& maps, Args& a, int pairs, cudaStream_t s) {
   for (int k = 0; k < a.jobs; ++k) tiles += a.job[k].tiles;
   pairs = std::min(pairs, tiles);
   double load[kMaxPairs] = {};
-  for (int k = 0; k < a.jobs; ++k) spread_tiles(a.spread[k], a.job[k].tiles, tile_cost(a.job[k]), pairs, load);
+  for (int k = 0; k < a.jobs; ++k) {
+    Job& j = a.job[k];
+    spread_tiles(a.spread[k], j.tiles, tile_cost(j), pairs, load);
+    j.by_group = FastDiv(kRowGroup * j.n_tiles), j.by_rows = FastDiv(kRowGroup), j.by_n = FastDiv(j.n_tiles);
+    j.by_last = FastDiv(j.m_tiles % kRowGroup ? j.m_tiles % kRowGroup : kRowGroup), j.by_splits = FastDiv(j.splits);
+  }
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&k_linear_ce), kSmem);
   if (e != cudaSuccess) return e;
   // The kernel's warps wait for registers that only a launch with kRegs has.
