@@ -45,9 +45,10 @@ struct Bwd {
 // of a row's two sums; the other sum's barrier stands between two uses of it.
 template <int L>
 __device__ __forceinline__ float group_sum(float v, float* red, int group) {
-  v = warp_sum(v);
-  if (L == 32) return v;
-  constexpr int W = L / 32;
+#pragma unroll
+  for (int o = (L < 32 ? L : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (L <= 32) return v;
+  constexpr int W = L <= 32 ? 1 : L / 32;
   red += group * W;
   if (threadIdx.x % 32 == 0) red[threadIdx.x % L / 32] = v;
   asm volatile("bar.sync %0, %1;" :: "r"(1 + group), "n"(L) : "memory");
@@ -115,12 +116,14 @@ template <typename T, int VEC, int SLOTS, int L, bool GATE>
 __global__ void __launch_bounds__(fwd_threads(L)) k_block_norm_fwd(const Fwd a) {
   constexpr int TH = fwd_threads(L), R = TH / L;
   using P = Pack<T, VEC>;
-  __shared__ float red[2][L / 32];
+  __shared__ float red[2][L <= 32 ? 1 : L / 32];
   const int lane = threadIdx.x % L;
   const int cols = (int)a.cols;
   const float inv = 1.f / (float)cols;
-  const int64_t row = (int64_t)blockIdx.x * R + threadIdx.x / L;
-  if (row >= a.rows) return;            // whole warps when L == 32, else never
+  int64_t row = (int64_t)blockIdx.x * R + threadIdx.x / L;
+  const bool live = row < a.rows;
+  if (L >= 32 && !live) return;         // whole warps when L == 32, else never
+  if (!live) row = a.rows - 1;          // half a warp: reads, and writes nothing
   const T* hp = static_cast<const T*>(a.h) + row * a.hs + lane * VEC;
   const T* rp = static_cast<const T*>(a.residual) + row * a.rs + lane * VEC;
   const T* gp = GATE ? static_cast<const T*>(a.gate) + row * a.gs + lane * VEC : nullptr;
@@ -176,9 +179,10 @@ __global__ void __launch_bounds__(fwd_threads(L)) k_block_norm_fwd(const Fwd a) 
       v[s][k] = fmaf(v[s][k] * r1 * w[k], a.scale, r[k]);
       sum = fmaf(v[s][k], v[s][k], sum);
     }
-    *reinterpret_cast<P*>(sp + s * L * VEC) = from_floats<T, VEC>(v[s]);
+    if (live) *reinterpret_cast<P*>(sp + s * L * VEC) = from_floats<T, VEC>(v[s]);
   }
   const float r2 = rsqrtf(group_sum<L>(sum, red[1], 0) * inv + a.eps);
+  if (!live) return;
   if (lane == 0) {
     a.rstd_post[row] = r1;
     a.rstd_pre[row] = r2;
@@ -580,17 +584,22 @@ template <typename T> struct BwdRun {
   }
 };
 
-// Slots and threads by the row's accesses of V elements.
+// Slots and threads by the row's accesses of V elements.  Forward: half a warp for the
+// shortest; a warp, with up to 24 elements a lane, while that holds a row; then 16 (us,
+// bfloat16 with a gate: 65,536 x 768 77.8 by warps, 86.8 by 96 threads; 32,768 x 1024
+// 53.2 by 64 threads, 60.1 by 128; 16,384 x 2048 54.1 by 128, 62.4 by 256; 8,192 x 4096
+// 58.3 by 256, 68.3 by 512).
 #define LOPT_ROWS(V, S, L_) if (n <= (int64_t)(S) * (L_)) return f.template run<V, S, L_>()
 template <int FULL, typename F> cudaError_t pick_fwd(int64_t cols, bool vec, F f) {
   if (vec) {
     constexpr int B = 8 / FULL;   // slots of 8 elements
     const int64_t n = cols / FULL;
+    LOPT_ROWS(FULL, 1, 16);
     LOPT_ROWS(FULL, 1, 32);
     LOPT_ROWS(FULL, 2 * B, 32);
     LOPT_ROWS(FULL, 3 * B, 32);
     LOPT_ROWS(FULL, 2 * B, 64);
-    LOPT_ROWS(FULL, B, 256);
+    LOPT_ROWS(FULL, 2 * B, 128);
     LOPT_ROWS(FULL, 2 * B, 256);
     LOPT_ROWS(FULL, 2 * B, 512);
     LOPT_ROWS(FULL, 4 * B, 512);

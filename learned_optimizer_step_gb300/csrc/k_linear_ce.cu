@@ -29,10 +29,17 @@
 // exponentials and in G; and for a 32-bit grad_w of many tokens (kSplitRows) the
 // targets' entries stay out of G: their share is added in fp32, to grad_x by the last
 // kernel, to grad_w by the embedding's gradient.  Where they are in G an
-// accumulator takes a segment of some steps only, and the epilogue's warps add the
-// segments in registers, rounding to nearest.  In all products that costs more
-// power, which bounds the clock of such a kernel (8,192 x 2048 x 50,304, segments of
-// 4, 8, 16 steps: 5.79, 5.19, 4.88 ms, 4.42 without).
+// accumulator takes a segment of a few steps only, and the epilogue's warps add the
+// segments in registers, rounding to nearest.  (Segments of 4, 8 and 16 steps in all
+// products instead, 8,192 x 2048 x 50,304, with an earlier epilogue: 5.79, 5.19, 4.88
+// ms, 4.42 without; grad_w 3e-6 to 2e-5 off, now 3e-7.)
+//
+// Bound by the tensor cores and the power they draw: of 8,192 x 2048 x 50,304 the
+// forward pass takes 0.97 to 1.09 ms (1,740 to 1,550 TFLOP/s; library products 1,914 at
+// first, 1,705 once the GPU draws 1.4 kW), the backward pass 4.45 to 4.54 ms (1,520 to
+// 1,490 over 6.75 TFLOP: logits again, grad_x, grad_w with both parts of G).  4,099 x 768 x
+// 50,257: 0.99 to 1.06 ms; a tile of 12 steps of K is over before the epilogue that makes G.
+// Few tokens read W at 2.5 TB/s: a tile is 256 rows of x whatever there are.
 #include <algorithm>
 #include <cmath>
 #include <cuda.h>
@@ -969,9 +976,13 @@ constexpr int64_t kMaxTokens = (int64_t)1 << 22, kMaxClasses = (int64_t)1 << 22,
 constexpr int64_t kLossRows = 32768;               // most rows of a forward launch
 constexpr int64_t kPartBytes = (int64_t)256 << 20;    // of its statistics
 constexpr int kPairs = 76;                         // of a GB300: what a split of the classes counts on
-constexpr int64_t kChunkBytes = (int64_t)256 << 20;   // of one G
+// Of one G (8,192 x 2048 x 50,304 backward: 4.81 ms with 128 MB, 4.65 with 256, 4.56 with 512).
+constexpr int64_t kChunkBytes = (int64_t)256 << 20;
 constexpr int kMaxSplits = 64;
-constexpr int64_t kSplitRows = 512;                // more tokens: the targets' entries stay out of G
+// More tokens: the targets' entries stay out of G.  That costs some 25 us of small
+// kernels and saves grad_w's short segments (768 x 20,000 bfloat16, us in G / apart: 200
+// tokens 80 / 98, 800 140 / 147, 1,600 210 / 201, 3,200 355 / 329; grad_w is 1.5e-6 / 4e-7 off).
+constexpr int64_t kSplitRows = 1024;
 // Steps of a segment: logits whose losses are fp32, a 32-bit grad_w without and with
 // the targets' entries; all for products that end in 16 bits.
 constexpr int kLossSegment = 32, kGradSegment = 32, kGradWSegment = 4, kSplitSegment = 64, kAll = 1 << 30;
