@@ -428,8 +428,8 @@ class AdamW:
                 norm = c.empty((), torch.float32)
             norm_ptr = _vector(norm, 1, "norm")
         _run(c, "lopt_adamw_step", self._written + [norm] if clipped else self._written, self._array,
-             len(self.tensors), t, lr, self.beta1, self.beta2, self.eps, self.weight_decay,
-             max_norm if clipped else 0.0, (t if seed is None else seed) & 0xFFFFFFFF, norm_ptr, ws_ptr, need,
+             len(self.tensors), int(t), float(lr), self.beta1, self.beta2, self.eps, self.weight_decay,
+             float(max_norm) if clipped else 0.0, int(t if seed is None else seed) & 0xFFFFFFFF, norm_ptr, ws_ptr, need,
              c.handle)
         return norm if clipped else None
 
