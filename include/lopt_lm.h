@@ -101,6 +101,16 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
                             void* workspace, int64_t workspace_bytes, int32_t* status, void* stream);
 
 /*
+ * Self-test of the bounded waits: lopt_linear_ce_forward() whose waits run out
+ * after limit_ns (0 to 10^9) instead of 1 s.  Nothing hangs or faults: if one did, all
+ * losses and lse of the launch (32,768 rows or fewer) are NaN, and bit 1 of *status is set.
+ */
+int lopt_selftest_linear_ce(int64_t limit_ns, const void* x, int type, int64_t rows, int64_t cols, int64_t x_stride,
+                            const void* weight, int64_t classes, int64_t weight_stride, const void* target,
+                            int index_type, const float* row_weight, float* loss, float* lse, void* workspace,
+                            int64_t workspace_bytes, int32_t* status, void* stream);
+
+/*
  * AdamW.  For every element of every tensor, in fp32, each operation rounded
  * once (no fused multiply-add), with g the gradient times the clip factor:
  *   m = beta1 * m + (1 - beta1) * g

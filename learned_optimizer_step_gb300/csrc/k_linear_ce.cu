@@ -137,6 +137,7 @@ struct Args {
   int64_t dw_stride;
   int* gave_up;                // one word per CTA
   int32_t* status;
+  uint64_t limit_ns;           // of a wait
   Job job[kJobs];
   Spread spread[kJobs];
   int jobs;
@@ -186,16 +187,31 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
       : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok != 0;
 }
-// Bounded: gives up after a second, or when another warp of the CTA has.
+// The same without the instruction's own short wait.
+__device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+// Bounded: gives up after limit_ns, or when another warp of the CTA has.
 // Inline: a call would spill the sums that the epilogue holds meanwhile.
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+  if (limit_ns == 0) {      // the self-test's
+    if (!*abort && test_wait(bar, parity)) return true;
+    *abort = 1;
+    return false;
+  }
   if (try_wait(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   for (uint32_t it = 0; it < (1u << 30); ++it) {
     if (try_wait(bar, parity)) return true;
     if ((it & 15) == 15) {
       if (*abort) return false;
-      if (global_ns() - t0 > kLimitNs) break;
+      if (global_ns() - t0 > limit_ns) break;
     }
   }
   *abort = 1;
@@ -573,7 +589,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const Tile x = walk.next();
         const int m0 = x.m * kTile + rank * kHalf, n0 = x.n * kTile + rank * kHalf;
         for (int k = x.k0; k < x.k1; ++k) {
-          if (!wait_for(smem_u32(&s_empty[stage]), phase ^ 1, abort)) break;
+          if (!wait_for(smem_u32(&s_empty[stage]), phase ^ 1, abort, a.limit_ns)) break;
           const uint32_t sa = stages + stage * 2 * kOperand, sb = sa + kOperand;
           const uint32_t bar = in_cta(smem_u32(&s_full[stage]), 0);
           if (rank == 0) mbar_arrive_expect_tx(&s_full[stage], 4 * kOperand);
@@ -600,7 +616,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       // No stage is left with the pair's barriers still to be told of it.
       for (int k = 0; k < kStages && !*abort; ++k) {
-        wait_for(smem_u32(&s_empty[stage]), phase ^ 1, abort);
+        wait_for(smem_u32(&s_empty[stage]), phase ^ 1, abort, a.limit_ns);
         if (++stage == kStages) stage = 0, phase ^= 1;
       }
     }
@@ -617,12 +633,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // 16 of K further: 32 bytes along the rows, two groups of eight rows across.
         const uint32_t step_a = (ak ? 32 : 2048) >> 4, step_b = (bk ? 32 : 2048) >> 4;
         for (int k = k0; k < k1;) {
-          if (!wait_for(smem_u32(&s_acc_empty[buf]), acc_phase ^ 1, abort)) break;
+          if (!wait_for(smem_u32(&s_acc_empty[buf]), acc_phase ^ 1, abort, a.limit_ns)) break;
           tc_fence_after();
           const uint32_t d = tmem + buf * kTile;
           const int first = k, end = min(k + j.segment, k1);
           for (; k < end; ++k) {
-            if (!wait_for(smem_u32(&s_full[stage]), phase, abort)) break;
+            if (!wait_for(smem_u32(&s_full[stage]), phase, abort, a.limit_ns)) break;
             tc_fence_after();
             const uint32_t sa = stages + stage * 2 * kOperand;
             const uint64_t da = operand_desc(sa, ak), db = operand_desc(sa + kOperand, bk);
@@ -662,7 +678,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const RowIn in = row_in(a, ahead, largest);
       const Tile now = x;
       auto ready = [&] {
-        const bool ok = __all_sync(0xffffffffu, wait_for(smem_u32(&s_acc_full[buf]), phase, abort));
+        const bool ok = __all_sync(0xffffffffu, wait_for(smem_u32(&s_acc_full[buf]), phase, abort, a.limit_ns));
         tc_fence_after();
         return ok;
       };
@@ -1246,10 +1262,9 @@ int lopt_linear_ce_workspace(int64_t rows, int64_t classes, int64_t cols, int al
   return LOPT_OK;
 }
 
-int lopt_linear_ce_forward(const void* x, int type, int64_t rows, int64_t cols, int64_t x_stride, const void* weight,
-                           int64_t classes, int64_t weight_stride, const void* target, int index_type,
-                           const float* row_weight, float* loss, float* lse, void* workspace, int64_t workspace_bytes,
-                           int32_t* status, void* stream) {
+static int forward(uint64_t limit_ns, const void* x, int type, int64_t rows, int64_t cols, int64_t x_stride, const void* weight,
+                   int64_t classes, int64_t weight_stride, const void* target, int index_type, const float* row_weight,
+                   float* loss, float* lse, void* workspace, int64_t workspace_bytes, int32_t* status, void* stream) {
   const Call c{x, weight, target, row_weight, type, index_type, rows, classes, cols,
                Span{x, rows, cols, x_stride, 2}, Span{weight, classes, cols, weight_stride, 2}};
   int rc = check_call(c);
@@ -1288,7 +1303,7 @@ int lopt_linear_ce_forward(const void* x, int type, int64_t rows, int64_t cols, 
     if (!make_map(&maps.x_k, static_cast<const uint16_t*>(xp) + r0 * xs, n, cols, xs, kHalf, bf16) ||
         !make_map(&maps.w_k, wp, classes, cols, wst, kHalf, bf16))
       return LOPT_E_UNSUPPORTED;
-    a.rows = (int)n, a.classes = (int)classes, a.cols = (int)cols, a.is_bf16 = bf16, a.planes = 1;
+    a.rows = (int)n, a.classes = (int)classes, a.cols = (int)cols, a.is_bf16 = bf16, a.planes = 1, a.limit_ns = limit_ns;
     a.target = static_cast<const char*>(target) + r0 * index_size(index_type), a.index_type = index_type;
     a.part = reinterpret_cast<float2*>(ws + p.part);
     a.gave_up = reinterpret_cast<int*>(ws + p.flags), a.status = status;
@@ -1303,6 +1318,23 @@ int lopt_linear_ce_forward(const void* x, int type, int64_t rows, int64_t cols, 
     if (e != cudaSuccess) return done(e);
   }
   return LOPT_OK;
+}
+
+int lopt_linear_ce_forward(const void* x, int type, int64_t rows, int64_t cols, int64_t x_stride, const void* weight,
+                           int64_t classes, int64_t weight_stride, const void* target, int index_type,
+                           const float* row_weight, float* loss, float* lse, void* workspace, int64_t workspace_bytes,
+                           int32_t* status, void* stream) {
+  return forward(kLimitNs, x, type, rows, cols, x_stride, weight, classes, weight_stride, target, index_type, row_weight, loss, lse,
+                 workspace, workspace_bytes, status, stream);
+}
+
+int lopt_selftest_linear_ce(int64_t limit_ns, const void* x, int type, int64_t rows, int64_t cols, int64_t x_stride,
+                            const void* weight, int64_t classes, int64_t weight_stride, const void* target, int index_type,
+                            const float* row_weight, float* loss, float* lse, void* workspace, int64_t workspace_bytes,
+                            int32_t* status, void* stream) {
+  if (limit_ns < 0 || limit_ns > (int64_t)kLimitNs) return LOPT_E_ARG;
+  return forward((uint64_t)limit_ns, x, type, rows, cols, x_stride, weight, classes, weight_stride, target, index_type, row_weight,
+                 loss, lse, workspace, workspace_bytes, status, stream);
 }
 
 int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols, int64_t x_stride, const void* weight,
@@ -1367,7 +1399,7 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
     if (planes == 2) ok = ok && make_map(&maps.g_low[b], a.g[b][1], rows, p.chunk, p.chunk, kStep, bf16);
   }
   if (!ok) return LOPT_E_UNSUPPORTED;
-  a.rows = (int)rows, a.classes = (int)classes, a.cols = (int)cols, a.planes = planes, a.is_bf16 = bf16;
+  a.rows = (int)rows, a.classes = (int)classes, a.cols = (int)cols, a.planes = planes, a.is_bf16 = bf16, a.limit_ns = kLimitNs;
   a.target = target, a.index_type = index_type, a.row_weight = row_weight, a.lse = lse;
   a.g_stride = p.chunk, a.largest = largest;
   a.hit = hit, a.split = split;

@@ -25,6 +25,7 @@ from .train_ops import BF16, F16, F32, _Call, _index, _like, _matrix, _same_lead
 
 LM_EXPORTED = ("lopt_block_norm_forward", "lopt_block_norm_workspace", "lopt_block_norm_backward",
                "lopt_linear_ce_workspace", "lopt_linear_ce_forward", "lopt_linear_ce_backward",
+               "lopt_selftest_linear_ce",
                "lopt_adamw_check", "lopt_adamw_workspace", "lopt_adamw_step", "lopt_adamw_moments")
 
 ADAMW_BLOCK = 256
@@ -63,6 +64,7 @@ def _load():
             "lopt_adamw_step": [pt, i32, i64, d, d, d, d, d, d, ctypes.c_uint32, vp, vp, i64, vp],
             "lopt_adamw_moments": [pt, i32, pvp, pvp, vp],
         }
+        sig["lopt_selftest_linear_ce"] = [i64] + sig["lopt_linear_ce_forward"]
         for name, args in sig.items():
             fn = getattr(lib, name)
             fn.argtypes, fn.restype = args, i32

@@ -104,6 +104,13 @@ def test_refusals(fns, name, base, changes):
         assert fns[name](*{**base, **change}.values()) == code, (name, change)
 
 
+def test_the_self_test_refuses_what_the_call_does(fns):
+    for limit in (-1, 10 ** 9 + 1):
+        assert fns["lopt_selftest_linear_ce"](limit, *CF.values()) == ARG
+    for change, code in REFUSED[2][2]:
+        assert fns["lopt_selftest_linear_ce"](0, *{**CF, **change}.values()) == code, change
+
+
 def test_nothing_to_do_is_no_launch(fns):
     assert fns["lopt_block_norm_forward"](*{**NF, "rows": 0}.values()) == 0
     assert fns["lopt_block_norm_backward"](*{**NB, "rows": 0, "accumulate": 1}.values()) == 0
