@@ -843,16 +843,37 @@ __global__ void __launch_bounds__(512) k_linear_ce_rows(const float2* part, int 
 }
 
 // ---- before and after the backward products ------------------------------------------
+// What k_linear_ce_start and the atomics do, by one block, for few rows: a launch less.
+__device__ __forceinline__ void start_few(int64_t rows, const void* target, int index_type, int classes, const float* row_weight,
+                                          float* largest, int* gave_up) {
+  __shared__ float red[8];
+  gave_up[threadIdx.x] = 0;      // as many words as threads
+  float most = 0.f;
+  for (int64_t r = threadIdx.x; r < rows; r += 256) {
+    const int64_t t = load_index(target, r, index_type);
+    const float w = row_weight ? row_weight[r] : 1.f;
+    if (t >= 0 && t < classes && isfinite(w)) most = fmaxf(most, fabsf(w));
+  }
+  most = warp_max(most);
+  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = most;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int k = 1; k < 8; ++k) most = fmaxf(most, red[k]);
+    *largest = most;
+  }
+}
+
 // Rows of 16-bit elements to rows that TMA can read.  With targets, rows that
 // do not count become zeros, whatever they hold, the largest weight is found and
 // the targets' entries of G (without weight) are made.
 __global__ void __launch_bounds__(256) k_linear_ce_copy(const uint16_t* x, int64_t stride, int64_t rows, int cols, uint16_t* out,
                                                         int64_t out_stride, const void* target, int index_type,
                                                         const Rows q, const float* row_weight, const float* lse,
-                                                        float* largest, float* hit, int32_t* status) {
+                                                        float* largest, float* hit, int* gave_up, int32_t* status) {
   const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
   wait_for_previous();
+  if (gave_up && blockIdx.x == 0) start_few(rows, target, index_type, q.classes, row_weight, largest, gave_up);
   if (row >= rows) return;
   bool live = true;
   if (target) {
@@ -865,7 +886,7 @@ __global__ void __launch_bounds__(256) k_linear_ce_copy(const uint16_t* x, int64
       if (live) hit[row] = expm1f(z - lse[row]);
       if (t >= q.classes && status) atomicOr(status, kStatusIndex);
       // Floats above 0 are in the order of their bits.
-      if (live && isfinite(w)) atomicMax(reinterpret_cast<int*>(largest), __float_as_int(fabsf(w)));
+      if (!gave_up && live && isfinite(w)) atomicMax(reinterpret_cast<int*>(largest), __float_as_int(fabsf(w)));
     }
   }
   const uint16_t* p = x + row * stride;
@@ -995,6 +1016,7 @@ constexpr int kPairs = 76;                         // of a GB300: what a split o
 // Of one G (8,192 x 2048 x 50,304 backward: 4.81 ms with 128 MB, 4.65 with 256, 4.56 with 512).
 constexpr int64_t kChunkBytes = (int64_t)256 << 20;
 constexpr int kMaxSplits = 64;
+constexpr int64_t kFewRows = 4096;                 // rows whose weights one block looks through: some 2 us, as a launch
 // More tokens: the targets' entries stay out of G.  That costs some 25 us of small
 // kernels and saves grad_w's short segments (768 x 20,000 bfloat16, us in G / apart: 200
 // tokens 80 / 98, 800 140 / 147, 1,600 210 / 201, 3,200 355 / 329; grad_w is 1.5e-6 / 4e-7 off).
@@ -1284,14 +1306,14 @@ static int forward(uint64_t limit_ns, const void* x, int type, int64_t rows, int
   if (!tma_rows(c.mx)) {
     xp = ws + p.x, xs = p.x_stride;
     e = launch(k_linear_ce_copy, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, true, 1, (const uint16_t*)x, x_stride, rows,
-               (int)cols, (uint16_t*)xp, xs, (const void*)nullptr, 0, Rows{}, (const float*)nullptr, (const float*)nullptr, (float*)nullptr, (float*)nullptr, (int32_t*)nullptr);
+               (int)cols, (uint16_t*)xp, xs, (const void*)nullptr, 0, Rows{}, (const float*)nullptr, (const float*)nullptr, (float*)nullptr, (float*)nullptr, (int*)nullptr, (int32_t*)nullptr);
     if (e != cudaSuccess) return done(e);
   }
   if (!tma_rows(c.mw)) {
     wp = ws + p.w, wst = p.w_stride;
     e = launch(k_linear_ce_copy, dim3((unsigned)((classes + 7) / 8)), dim3(256), 0, s, true, 1, (const uint16_t*)weight, weight_stride,
                classes, (int)cols, (uint16_t*)wp, wst, (const void*)nullptr, 0, Rows{}, (const float*)nullptr, (const float*)nullptr, (float*)nullptr,
-               (float*)nullptr, (int32_t*)nullptr);
+               (float*)nullptr, (int*)nullptr, (int32_t*)nullptr);
     if (e != cudaSuccess) return done(e);
   }
   const int pairs = pair_count();
@@ -1373,11 +1395,17 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
   char* ws = static_cast<char*>(workspace);
   const bool bf16 = type == LOPT_BF16;
   float *largest = reinterpret_cast<float*>(ws + p.largest), *hit = reinterpret_cast<float*>(ws + p.hit);
-  cudaError_t e = launch(k_linear_ce_start, dim3(1), dim3(kMaxCtas), 0, s, false, 1, largest, reinterpret_cast<int*>(ws + p.flags));
-  if (e != cudaSuccess) return done(e);
+  cudaError_t e;
+  int* flags = reinterpret_cast<int*>(ws + p.flags);
+  static_assert(kMaxCtas == 256, "start_few clears a word a thread");
+  const bool start = rows > kFewRows;
+  if (start) {
+    e = launch(k_linear_ce_start, dim3(1), dim3(kMaxCtas), 0, s, false, 1, largest, flags);
+    if (e != cudaSuccess) return done(e);
+  }
   uint16_t* xp = reinterpret_cast<uint16_t*>(ws + p.x);
   e = launch(k_linear_ce_copy, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, true, 1, (const uint16_t*)x, x_stride, rows,
-             (int)cols, xp, p.x_stride, target, index_type, rows_of(c, 0), row_weight, lse, largest, hit, status);
+             (int)cols, xp, p.x_stride, target, index_type, rows_of(c, 0), row_weight, lse, largest, hit, start ? (int*)nullptr : flags, status);
   if (e != cudaSuccess) return done(e);
   const void* wp = weight;
   int64_t wst = weight_stride;
@@ -1385,7 +1413,7 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
     wp = ws + p.w, wst = p.w_stride;
     e = launch(k_linear_ce_copy, dim3((unsigned)((classes + 7) / 8)), dim3(256), 0, s, true, 1, (const uint16_t*)weight, weight_stride,
                classes, (int)cols, (uint16_t*)wp, wst, (const void*)nullptr, 0, Rows{}, (const float*)nullptr, (const float*)nullptr, (float*)nullptr,
-               (float*)nullptr, (int32_t*)nullptr);
+               (float*)nullptr, (int*)nullptr, (int32_t*)nullptr);
     if (e != cudaSuccess) return done(e);
   }
   Maps maps{};

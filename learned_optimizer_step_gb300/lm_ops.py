@@ -219,8 +219,8 @@ def _hidden(c, x, weight, target, row_weight):
     if x.dim() > 2:
         _same_lead(x.shape[:-1], target=(target, 0), row_weight=(row_weight, 0))
     w = 0 if row_weight is None else _vector(row_weight, rows, "row_weight")
-    aligned = all(t.data_ptr() % 16 == 0 and (n <= 1 or (s % 8 == 0 and s >= cols and s < 1 << 38))
-                  for t, n, s in ((x, rows, xs), (weight, classes, ws)))
+    aligned = (x.data_ptr() % 16 == 0 and (rows <= 1 or (xs % 8 == 0 and cols <= xs < 1 << 38))
+               and weight.data_ptr() % 16 == 0 and (classes <= 1 or (ws % 8 == 0 and cols <= ws < 1 << 38)))
     return _TYPES[x.dtype], rows, cols, xs, classes, ws, kind, w, 1 if aligned else 0
 
 
