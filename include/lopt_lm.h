@@ -79,7 +79,7 @@ int lopt_block_norm_backward(const void* grad_y, int type, int64_t rows, int64_t
  * (of `type`) or grad_weight may be NULL.  grad_weight is of LOPT_F32, which
  * accumulate = 1 adds to, or of `type`; G is rounded to 16 bits for the products
  * (relative to 2^-15 of the largest row_weight at least), for an fp32 grad_weight
- * to twice as many.
+ * to two or three such parts.
  *
  * Bit 1 of *status: a bounded wait (1 s) ran out; losses, lse and grad_x are then
  * NaN and grad_weight is not valid.

@@ -12,9 +12,10 @@
 //
 // The backward pass goes over the vocabulary in chunks whose G fits a bounded
 // workspace; the chunk's grad_x is added to fp32 sums, its rows of grad_w are
-// written.  For a 32-bit grad_w, G is held as the sum of two 16-bit numbers
-// (16 bits of bfloat16, 22 of float16): rounded once to bfloat16 it would be off by
-// 2^-9, which is what a 16-bit grad_w is rounded by anyway.
+// written.  For a 32-bit grad_w, G is held as the sum of 16-bit numbers: two (16 bits
+// of bfloat16, 22 of float16), or three of bfloat16 while the targets' entries are in
+// it.  Rounded once to bfloat16 it would be off by 2^-9, which is what a 16-bit grad_w
+// is rounded by anyway.
 //
 // A pair of CTAs (cta_group::2) computes a 256 x 256 tile: each holds 128 rows of
 // A and 128 of B per 64-wide step of K in shared memory (TMA, 128-byte swizzle) and
@@ -113,12 +114,12 @@ struct Job {
 constexpr int kJobs = 3;
 
 struct Maps {
-  CUtensorMap x_k, x_m, w_k, w_m, g_k[2], g_m[2], g_low[2];
+  CUtensorMap x_k, x_m, w_k, w_m, g_k[2], g_m[2][3];     // by buffer, by part
 };
 
 struct Args {
   int rows, classes, cols;
-  int planes;                  // 2: G in two parts
+  int planes;                  // parts of G
   int is_bf16;
   const void* target;
   int index_type;
@@ -127,7 +128,7 @@ struct Args {
   const float* hit;            // [rows]: exp(target logit - lse) - 1
   int split;                   // the targets' entries stay out of G
   float2* part;                // [2 * class tiles][rows]: maximum, sum
-  void* g[2][2];               // [buffer][part]
+  void* g[2][3];               // [buffer][part]
   int64_t g_stride;
   const float* largest;        // the largest |row_weight|: G is scaled by 2^15 / *largest
   float* dx;
@@ -438,7 +439,20 @@ __device__ __forceinline__ void grad_tile(const Args& a, const Job& j, const Row
         lo[k] = *reinterpret_cast<const uint32_t*>(&q);
       }
       store32(static_cast<T*>(a.g[j.buffer][0]) + out + 32 * c + 16 * h, hi);
-      if (a.planes == 2) store32(static_cast<T*>(a.g[j.buffer][1]) + out + 32 * c + 16 * h, lo);
+      if (a.planes == 1) continue;
+      store32(static_cast<T*>(a.g[j.buffer][1]) + out + 32 * c + 16 * h, lo);
+      if (a.planes == 2) continue;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float y[2], z[2], x[2] = {v[16 * h + 2 * k], v[16 * h + 2 * k + 1]};
+        to_floats(*reinterpret_cast<const Pack<T, 2>*>(&hi[k]), y);
+        to_floats(*reinterpret_cast<const Pack<T, 2>*>(&lo[k]), z);
+        x[0] = (x[0] - y[0]) - z[0];
+        x[1] = (x[1] - y[1]) - z[1];
+        const Pack<T, 2> q = from_floats<T, 2>(x);
+        lo[k] = *reinterpret_cast<const uint32_t*>(&q);
+      }
+      store32(static_cast<T*>(a.g[j.buffer][2]) + out + 32 * c + 16 * h, lo);
     }
   }
 }
@@ -602,9 +616,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             load_box(sb, &maps.w_m, n0, j.v0 + kk, bar);
             load_box(sb + kOperand / 2, &maps.w_m, n0 + 64, j.v0 + kk, bar);
           } else {
-            // Both parts of G against the same tokens, one after the other.
-            const int y = (a.planes == 2 ? k >> 1 : k) * kStep;
-            const CUtensorMap* g = a.planes == 2 && (k & 1) ? &maps.g_low[j.buffer] : &maps.g_m[j.buffer];
+            // The parts of G against the same tokens, one after the other.
+            const int tokens = a.planes == 1 ? k : a.planes == 2 ? k >> 1 : k / 3, y = tokens * kStep;
+            const CUtensorMap* g = &maps.g_m[j.buffer][k - tokens * a.planes];
             load_box(sa, g, m0, y, bar);
             load_box(sa + kOperand / 2, g, m0 + 64, y, bar);
             load_box(sb, &maps.x_m, n0, y, bar);
@@ -1018,9 +1032,10 @@ constexpr int64_t kChunkBytes = (int64_t)256 << 20;
 constexpr int kMaxSplits = 64;
 constexpr int64_t kFewRows = 4096;                 // rows whose weights one block looks through: some 2 us, as a launch
 // More tokens: the targets' entries stay out of G.  That costs some 25 us of small
-// kernels and saves grad_w's short segments (768 x 20,000 bfloat16, us in G / apart: 200
-// tokens 80 / 98, 800 140 / 147, 1,600 210 / 201, 3,200 355 / 329; grad_w is 1.5e-6 / 4e-7 off).
-constexpr int64_t kSplitRows = 1024;
+// kernels, and saves grad_w's short segments and in bfloat16 G's third part (768 x 20,000,
+// us in G / apart: bfloat16 64 tokens 67 / 87, 200 97 / 98, 400 126 / 109, 800 181 / 147;
+// float16 200 85 / 98, 400 106 / 109, 800 147 / 148; grad_w is 5e-7 / 4e-7 off).
+constexpr int64_t kSplitRows = 256;
 // Steps of a segment: logits whose losses are fp32, a 32-bit grad_w without and with
 // the targets' entries; all for products that end in 16 bits.
 constexpr int kLossSegment = 32, kGradSegment = 32, kGradWSegment = 4, kSplitSegment = 64, kAll = 1 << 30;
@@ -1200,10 +1215,12 @@ Plan plan_loss(int64_t rows, int64_t classes, int64_t cols, bool copy) {
   return p;
 }
 
-Plan plan_grad(int64_t rows, int64_t classes, int64_t cols, int planes, bool copy) {
+Plan plan_grad(int64_t rows, int64_t classes, int64_t cols, bool fp32_weight, bool copy) {
   Plan p;
   p.x_stride = p.w_stride = up(cols, 8);
-  if (planes == 2 && rows > kSplitRows) {
+  // G in one part, in two, or, with the targets' entries in it, in three (for float16 two do).
+  const int planes = !fp32_weight ? 1 : rows > kSplitRows ? 2 : 3;
+  if (planes == 2) {
     p.share = take(p, rows * p.x_stride * 4);
     lopt_embed_workspace(rows, classes, cols, &p.sort_bytes);
     p.sort = take(p, p.sort_bytes);
@@ -1279,7 +1296,7 @@ int lopt_linear_ce_workspace(int64_t rows, int64_t classes, int64_t cols, int al
   if (!bytes || (aligned != 0 && aligned != 1) || (backward != 0 && backward != 1) || (backward && !type_size(grad_weight_type))) return LOPT_E_ARG;
   if (rows < 0 || rows > kMaxTokens || classes < 1 || classes > kMaxClasses || cols < 1 || cols > kMaxWidth) return LOPT_E_SHAPE;
   const int64_t n = std::max<int64_t>(rows, 1);
-  *bytes = backward ? plan_grad(n, classes, cols, grad_weight_type == LOPT_F32 ? 2 : 1, !aligned).size
+  *bytes = backward ? plan_grad(n, classes, cols, grad_weight_type == LOPT_F32, !aligned).size
                     : plan_loss(n, classes, cols, !aligned).size;
   return LOPT_OK;
 }
@@ -1382,9 +1399,10 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
   const Span mo{grad_x, rows, cols, grad_x_stride, 2};
   if (grad_x && (rc = check_matrix(mo, true))) return rc;
   if (!grad_x && !grad_weight) return LOPT_OK;
-  const int planes = grad_weight && grad_weight_type == LOPT_F32 ? 2 : 1;
+  const bool fp32_weight = grad_weight && grad_weight_type == LOPT_F32;
+  const int planes = !fp32_weight ? 1 : type == LOPT_F16 || rows > kSplitRows ? 2 : 3;
   const int pairs = pair_count();
-  const Plan p = plan_grad(rows, classes, cols, planes, !tma_rows(c.mw));
+  const Plan p = plan_grad(rows, classes, cols, fp32_weight, !tma_rows(c.mw));
   // The embedding's gradient adds to a contiguous table.
   const bool split = p.sort_bytes && grad_weight_stride == cols;
   if (!lse || !workspace || workspace_bytes < p.size) return LOPT_E_ARG;
@@ -1423,8 +1441,8 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
   for (int b = 0; b < p.buffers; ++b) {
     for (int k = 0; k < planes; ++k) a.g[b][k] = ws + p.g + (b * planes + k) * p.g_plane;
     ok = ok && make_map(&maps.g_k[b], a.g[b][0], rows, p.chunk, p.chunk, kHalf, bf16) &&
-         make_map(&maps.g_m[b], a.g[b][0], rows, p.chunk, p.chunk, kStep, bf16);
-    if (planes == 2) ok = ok && make_map(&maps.g_low[b], a.g[b][1], rows, p.chunk, p.chunk, kStep, bf16);
+         make_map(&maps.g_m[b][0], a.g[b][0], rows, p.chunk, p.chunk, kStep, bf16);
+    for (int k = 1; k < planes; ++k) ok = ok && make_map(&maps.g_m[b][k], a.g[b][k], rows, p.chunk, p.chunk, kStep, bf16);
   }
   if (!ok) return LOPT_E_UNSUPPORTED;
   a.rows = (int)rows, a.classes = (int)classes, a.cols = (int)cols, a.planes = planes, a.is_bf16 = bf16, a.limit_ns = kLimitNs;
