@@ -114,12 +114,12 @@ struct Job {
 constexpr int kJobs = 3;
 
 struct Maps {
-  CUtensorMap x_k, x_m, w_k, w_m, g_k[2], g_m[2][3];     // by buffer, by part
+  CUtensorMap x_k, x_m, w_k, w_m, g_k[2][2], g_m[2][3];     // by buffer, by part
 };
 
 struct Args {
   int rows, classes, cols;
-  int planes;                  // parts of G
+  int planes, planes_x;        // parts of G, those that grad_x uses
   int is_bf16;
   const void* target;
   int index_type;
@@ -612,9 +612,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             load_box(sa, &maps.x_k, kk, m0, bar);
             load_box(sb, &maps.w_k, kk, j.v0 + n0, bar);
           } else if (j.mode == kGradX) {
-            load_box(sa, &maps.g_k[j.buffer], kk, m0, bar);
-            load_box(sb, &maps.w_m, n0, j.v0 + kk, bar);
-            load_box(sb + kOperand / 2, &maps.w_m, n0 + 64, j.v0 + kk, bar);
+            const int part = a.planes_x == 2 ? k & 1 : 0, v = (a.planes_x == 2 ? k >> 1 : k) * kStep;
+            load_box(sa, &maps.g_k[j.buffer][part], v, m0, bar);
+            load_box(sb, &maps.w_m, n0, j.v0 + v, bar);
+            load_box(sb + kOperand / 2, &maps.w_m, n0 + 64, j.v0 + v, bar);
           } else {
             // The parts of G against the same tokens, one after the other.
             const int tokens = a.planes == 1 ? k : a.planes == 2 ? k >> 1 : k / 3, y = tokens * kStep;
@@ -1036,6 +1037,10 @@ constexpr int64_t kFewRows = 4096;                 // rows whose weights one blo
 // us in G / apart: bfloat16 64 tokens 67 / 87, 200 97 / 98, 400 126 / 109, 800 181 / 147;
 // float16 200 85 / 98, 400 106 / 109, 800 147 / 148; grad_w is 5e-7 / 4e-7 off).
 constexpr int64_t kSplitRows = 256;
+// Up to so many tokens 16-bit gradients too are made from two parts of G, which costs
+// nothing there: a row's few large entries are rounded alike, so that rounding them
+// once more shows (gradients 2.7e-3 off in bfloat16, 1.7e-3 with two).
+constexpr int64_t kExactRows = 16;
 // Steps of a segment: logits whose losses are fp32, a 32-bit grad_w without and with
 // the targets' entries; all for products that end in 16 bits.
 constexpr int kLossSegment = 32, kGradSegment = 32, kGradWSegment = 4, kSplitSegment = 64, kAll = 1 << 30;
@@ -1218,9 +1223,10 @@ Plan plan_loss(int64_t rows, int64_t classes, int64_t cols, bool copy) {
 Plan plan_grad(int64_t rows, int64_t classes, int64_t cols, bool fp32_weight, bool copy) {
   Plan p;
   p.x_stride = p.w_stride = up(cols, 8);
-  // G in one part, in two, or, with the targets' entries in it, in three (for float16 two do).
-  const int planes = !fp32_weight ? 1 : rows > kSplitRows ? 2 : 3;
-  if (planes == 2) {
+  // G in one part (two for very few rows), for an fp32 grad_w in two or, with the targets'
+  // entries in it, in three (for float16 two do).
+  const int planes = !fp32_weight ? (rows > kExactRows ? 1 : 2) : rows > kSplitRows ? 2 : 3;
+  if (fp32_weight && planes == 2) {
     p.share = take(p, rows * p.x_stride * 4);
     lopt_embed_workspace(rows, classes, cols, &p.sort_bytes);
     p.sort = take(p, p.sort_bytes);
@@ -1400,7 +1406,8 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
   if (grad_x && (rc = check_matrix(mo, true))) return rc;
   if (!grad_x && !grad_weight) return LOPT_OK;
   const bool fp32_weight = grad_weight && grad_weight_type == LOPT_F32;
-  const int planes = !fp32_weight ? 1 : type == LOPT_F16 || rows > kSplitRows ? 2 : 3;
+  const int planes_x = rows > kExactRows ? 1 : 2;
+  const int planes = !fp32_weight ? planes_x : type == LOPT_F16 || rows > kSplitRows ? 2 : 3;
   const int pairs = pair_count();
   const Plan p = plan_grad(rows, classes, cols, fp32_weight, !tma_rows(c.mw));
   // The embedding's gradient adds to a contiguous table.
@@ -1440,12 +1447,12 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
             make_map(&maps.w_k, wp, classes, cols, wst, kHalf, bf16) && make_map(&maps.w_m, wp, classes, cols, wst, kStep, bf16);
   for (int b = 0; b < p.buffers; ++b) {
     for (int k = 0; k < planes; ++k) a.g[b][k] = ws + p.g + (b * planes + k) * p.g_plane;
-    ok = ok && make_map(&maps.g_k[b], a.g[b][0], rows, p.chunk, p.chunk, kHalf, bf16) &&
-         make_map(&maps.g_m[b][0], a.g[b][0], rows, p.chunk, p.chunk, kStep, bf16);
+    for (int k = 0; k < planes_x; ++k) ok = ok && make_map(&maps.g_k[b][k], a.g[b][k], rows, p.chunk, p.chunk, kHalf, bf16);
+    ok = ok && make_map(&maps.g_m[b][0], a.g[b][0], rows, p.chunk, p.chunk, kStep, bf16);
     for (int k = 1; k < planes; ++k) ok = ok && make_map(&maps.g_m[b][k], a.g[b][k], rows, p.chunk, p.chunk, kStep, bf16);
   }
   if (!ok) return LOPT_E_UNSUPPORTED;
-  a.rows = (int)rows, a.classes = (int)classes, a.cols = (int)cols, a.planes = planes, a.is_bf16 = bf16, a.limit_ns = kLimitNs;
+  a.rows = (int)rows, a.classes = (int)classes, a.cols = (int)cols, a.planes = planes, a.planes_x = planes_x, a.is_bf16 = bf16, a.limit_ns = kLimitNs;
   a.target = target, a.index_type = index_type, a.row_weight = row_weight, a.lse = lse;
   a.g_stride = p.chunk, a.largest = largest;
   a.hit = hit, a.split = split;
@@ -1468,9 +1475,9 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
       Job g = grad_job(k - 1);
       if (grad_weight)
         add(Job{kGradW, g.n_tiles * d_tiles, g.n_tiles, d_tiles, 1, (int)(up(rows, kStep) / kStep) * planes, g.buffer, g.v0, g.v1, 0,
-                planes == 1 ? kAll : split ? kSplitSegment : kGradWSegment});
+                !fp32_weight ? kAll : split ? kSplitSegment : kGradWSegment});
       if (grad_x)
-        add(Job{kGradX, m_tiles * d_tiles * p.splits, m_tiles, d_tiles, p.splits, (int)(up(g.v1 - g.v0, kStep) / kStep), g.buffer,
+        add(Job{kGradX, m_tiles * d_tiles * p.splits, m_tiles, d_tiles, p.splits, (int)(up(g.v1 - g.v0, kStep) / kStep) * planes_x, g.buffer,
                 g.v0, g.v1, k > 1, kAll});
     }
     // The costliest first: the others even out what they leave.
