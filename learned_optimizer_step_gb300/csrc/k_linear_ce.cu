@@ -4,8 +4,8 @@
 // Three matrix products by one persistent kernel on the tensor cores, with what
 // surrounds them in its epilogues, so that logits never leave the SM:
 //
-//   loss     tile of x W^T  ->  each row's maximum, sum of exponentials and
-//                               target logit over the tile's classes
+//   loss     tile of x W^T  ->  each row's maximum and sum of exponentials over the
+//                               tile's classes but its target
 //   grad     tile of x W^T  ->  G = (exp(logit - lse) - [target]) * weight, 16-bit
 //   grad_x   tile of G W        (sum over classes, in pieces of the vocabulary)
 //   grad_w   tile of G^T x      (sum over tokens)

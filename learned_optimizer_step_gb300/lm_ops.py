@@ -259,7 +259,7 @@ def linear_cross_entropy_backward(x, weight, target, lse, *, row_weight=None, gr
 
     grad_weight: float32 [classes, cols] (default; ``accumulate`` adds to it),
     or a buffer of the type of x, for which G is rounded to that type once: a
-    fifth fewer products.  Rows without a target or of weight 0 get zeros and add
+    quarter fewer products.  Rows without a target or of weight 0 get zeros and add
     nothing, whatever they hold."""
     c = _Call(x, (weight, row_weight), (target, lse, grad_x, grad_weight), stream)
     kind, rows, cols, xs, classes, ws, ik, w, aligned = _hidden(c, x, weight, target, row_weight)

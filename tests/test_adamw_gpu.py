@@ -206,6 +206,13 @@ def test_moments():
     assert torch.equal(t.copy, t.param.bfloat16())
 
 
+def test_tensors_without_elements():
+    e = lambda: torch.zeros(0, device="cuda")   # noqa: E731
+    a = L.AdamW([L.AdamWTensor(e(), e(), e(), e())])
+    assert float(a.step(1, 0.1, max_norm=1.0)) == 0.0 and a.step(2, 0.1) is None
+    assert a.moments()[0][0].shape == (0,)
+
+
 def test_tiny_blocks_become_zeros():
     n = 512
     t = L.AdamWTensor.zeros(torch.zeros(n, device="cuda"), torch.full((n,), 1e-31, device="cuda"), "8bit")
