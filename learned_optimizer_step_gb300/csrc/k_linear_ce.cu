@@ -1400,7 +1400,7 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
   cudaStream_t s = (cudaStream_t)stream;
   if (rows == 0) {
     if (!grad_weight || accumulate) return LOPT_OK;
-    return done(cudaMemset2DAsync(grad_weight, grad_weight_stride * gs, 0, cols * gs, classes, s));
+    return done(cudaMemset2DAsync(grad_weight, (classes == 1 ? cols : grad_weight_stride) * gs, 0, cols * gs, classes, s));
   }
   const Span mo{grad_x, rows, cols, grad_x_stride, 2};
   if (grad_x && (rc = check_matrix(mo, true))) return rc;
