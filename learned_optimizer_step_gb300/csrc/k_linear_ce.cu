@@ -26,7 +26,7 @@
 // The tensor cores cut the fp32 sums they carry rather than round them: over
 // thousands of steps that is more than fp32 results may be off.  What is cut goes
 // by the largest terms, and those are the targets'.  So a target's logit is a dot
-// product of its own in fp32, which replaces the tensor cores' in the sum of
+// product of its own, summed in two floats, which replaces the tensor cores' in the sum of
 // exponentials and in G; and for a 32-bit grad_w of many tokens (kSplitRows) the
 // targets' entries stay out of G: their share is added in fp32, to grad_x by the last
 // kernel, to grad_w by the embedding's gradient.  Where they are in G an
@@ -762,25 +762,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ---- the rows' losses from the tiles' statistics -----------------------------------
-// Dot product of two rows by a warp, fp32; every lane has it.
+// Dot product of two rows by a warp, as the sum x + y of two floats, in some 45 bits (the
+// products are exact, the sums' roundings are kept): where a target is nearly certain
+// its entry of G is the difference of two nearly equal numbers.  Every lane has it.
+struct Sum2 {
+  float x = 0.f, y = 0.f;
+  __device__ __forceinline__ void add(float p) {
+    const float t = __fadd_rn(x, p), b = __fsub_rn(t, x);
+    y = __fadd_rn(y, __fadd_rn(__fsub_rn(x, __fsub_rn(t, b)), __fsub_rn(p, b)));
+    x = t;
+  }
+};
 template <typename T>
-__device__ __forceinline__ float row_dot(const T* x, const T* w, int cols, bool vec, int lane) {
-  float s = 0.f;
+__device__ __forceinline__ Sum2 row_dot(const T* x, const T* w, int cols, bool vec, int lane) {
+  Sum2 s;
   if (vec) {
     for (int j = lane * 8; j < cols; j += 256) {
       float a[8], b[8];
       to_floats(*reinterpret_cast<const Pack<T, 8>*>(x + j), a);
       to_floats(*reinterpret_cast<const Pack<T, 8>*>(w + j), b);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s = fmaf(a[e], b[e], s);
+      for (int e = 0; e < 8; ++e) s.add(__fmul_rn(a[e], b[e]));
     }
   } else {
 #pragma unroll 8
-    for (int j = lane; j < cols; j += 32) s = fmaf(to_f(x[j]), to_f(w[j]), s);
+    for (int j = lane; j < cols; j += 32) s.add(__fmul_rn(to_f(x[j]), to_f(w[j])));
   }
-  return warp_sum(s);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float y = __shfl_xor_sync(0xffffffffu, s.y, o);
+    s.add(__shfl_xor_sync(0xffffffffu, s.x, o));
+    s.y = __fadd_rn(s.y, y);
+  }
+  // Infinities and NaN leave NaN as their rounding errors.
+  if (!(fabsf(s.x) <= 3.4028235e38f)) s.y = 0.f;
+  return Sum2{s.x, s.y};
 }
-__device__ __forceinline__ float row_dot(const uint16_t* x, const uint16_t* w, int cols, bool vec, bool bf16, int lane) {
+__device__ __forceinline__ Sum2 row_dot(const uint16_t* x, const uint16_t* w, int cols, bool vec, bool bf16, int lane) {
   return bf16 ? row_dot(reinterpret_cast<const __nv_bfloat16*>(x), reinterpret_cast<const __nv_bfloat16*>(w), cols, vec, lane)
               : row_dot(reinterpret_cast<const __half*>(x), reinterpret_cast<const __half*>(w), cols, vec, lane);
 }
@@ -799,7 +817,7 @@ __global__ void __launch_bounds__(512) k_linear_ce_rows(const float2* part, int 
                                                         int64_t rows, const void* target, int index_type,
                                                         const float* row_weight, float* loss, float* lse, int32_t* status) {
   __shared__ float2 red[16][kRowsOfBlock];
-  __shared__ float s_hit[kRowsOfBlock];
+  __shared__ float2 s_hit[kRowsOfBlock];
   __shared__ int s_bad;
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
   const int64_t first = (int64_t)blockIdx.x * kRowsOfBlock;
@@ -827,9 +845,9 @@ __global__ void __launch_bounds__(512) k_linear_ce_rows(const float2* part, int 
   }
   if (w < kRowsOfBlock && first + w < rows) {
     const int64_t at = first + w, t = load_index(target, at, index_type);
-    float z = -INFINITY;
+    Sum2 z{-INFINITY, 0.f};
     if (t >= 0 && t < q.classes) z = row_dot(q.x + at * q.x_stride, q.w + t * q.w_stride, q.cols, q.vec, q.bf16, lane);
-    if (lane == 0) s_hit[w] = z;
+    if (lane == 0) s_hit[w] = make_float2(z.x, z.y);
   }
 #pragma unroll
   for (int o = 8; o < 32; o *= 2)
@@ -844,15 +862,20 @@ __global__ void __launch_bounds__(512) k_linear_ce_rows(const float2* part, int 
   for (int o = 8; o < 32; o *= 2)
     join(make_float2(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o)));
   if (lane >= 8 || row >= rows) return;
-  const float hit = s_hit[lane];
+  const float2 hit = s_hit[lane];
   const int64_t t = load_index(target, row, index_type);
-  // A target of -inf adds nothing, one of NaN makes the sum NaN.
-  if (t >= 0 && t < q.classes) join(make_float2(hit, 1.f));
-  const float all = m == -INFINITY && s == 0.f ? -INFINITY : m + logf(s);
-  const float weight = row_weight ? row_weight[row] : 1.f;
-  if (t >= q.classes && status) atomicOr(status, kStatusIndex);
+  // The loss is log(1 + sum over the others of e^(z - target)): exact also where the
+  // target is nearly certain.
   float l = 0.f;
-  if (t >= 0 && t < q.classes && weight != 0.f) l = weight * (all - hit);
+  const float weight = row_weight ? row_weight[row] : 1.f;
+  if (t >= 0 && t < q.classes && weight != 0.f) {
+    const float d = (m - hit.x) - hit.y;
+    l = weight * (hit.x == INFINITY ? NAN : d <= 0.f ? log1pf(s * expf(d)) : d + logf(s + expf(-d)));
+  }
+  // A target of -inf adds nothing, one of NaN makes the sum NaN.
+  if (t >= 0 && t < q.classes) join(make_float2(hit.x, 1.f));
+  const float all = m == -INFINITY && s == 0.f ? -INFINITY : m + logf(s);
+  if (t >= q.classes && status) atomicOr(status, kStatusIndex);
   loss[row] = s_bad ? NAN : l;
   lse[row] = s_bad ? NAN : all;
 }
@@ -895,10 +918,10 @@ __global__ void __launch_bounds__(256) k_linear_ce_copy(const uint16_t* x, int64
     const int64_t t = load_index(target, row, index_type);
     const float w = row_weight ? row_weight[row] : 1.f;
     live = t >= 0 && t < q.classes && w != 0.f;
-    float z = 0.f;
+    Sum2 z;
     if (live) z = row_dot(x + row * stride, q.w + t * q.w_stride, cols, q.vec, q.bf16, lane);
     if (lane == 0) {
-      if (live) hit[row] = expm1f(z - lse[row]);
+      if (live) hit[row] = expm1f((z.x - lse[row]) + z.y);
       if (t >= q.classes && status) atomicOr(status, kStatusIndex);
       // Floats above 0 are in the order of their bits.
       if (!gave_up && live && isfinite(w)) atomicMax(reinterpret_cast<int*>(largest), __float_as_int(fabsf(w)));

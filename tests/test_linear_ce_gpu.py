@@ -245,6 +245,33 @@ def test_large_and_small_weights_of_rows():
         assert float((dx.double() - rx).norm()) <= 2 ** -7 * float(rx.norm())
 
 
+@pytest.mark.parametrize("dtype", HALF, ids=ids)
+def test_targets_that_are_nearly_certain(dtype):
+    """Losses from 10 to 1e-10 and what is left of G where they are small, to a relative
+    2^-13: a loss is a sum of exponentials of the others' logits, each off by their errors
+    (up to 100 half steps and the logits' size, here below 40, times 30 units)."""
+    g = gen(12)
+    v, d = 300, 64
+    w = normal(g, v, d, dtype=dtype, std=0.125)
+    t = torch.arange(40, device="cuda")
+    x = (normal(g, 40, d, std=0.5) + torch.linspace(0, 30, 40, device="cuda")[:, None] * w[t].float()).to(dtype)
+    loss, lse = L.linear_cross_entropy_forward(x, w, t)
+    z = x.double() @ w.double().t()
+    rest = z.clone()
+    rest[torch.arange(40, device="cuda"), t] = -math.inf
+    want = torch.nn.functional.softplus(torch.logsumexp(rest, 1) - z[torch.arange(40, device="cuda"), t], threshold=1e9)
+    assert float(want.min()) < 1e-5 < 1 < float(want.max())
+    assert float(((loss.double() - want) / want).abs().max()) <= 2 ** -13
+    exact = torch.logsumexp(z, 1)
+    dx, dw = L.linear_cross_entropy_backward(x[:16], w, t[:16], lse[:16])
+    _, rd, _ = R.ce_backward(x[:16], w, t[:16], lse[:16], None)
+    assert float((dw.double() - rd).norm()) <= 4e-6 * float(rd.norm())
+    for k in range(40):          # one token: its own small gradient
+        _, dw = L.linear_cross_entropy_backward(x[k:k + 1], w, t[k:k + 1], exact[k:k + 1].float())
+        _, rd, _ = R.ce_backward(x[k:k + 1], w, t[k:k + 1], exact[k:k + 1].float(), None)
+        assert float((dw.double() - rd).norm()) <= 2 ** -13 * float(rd.norm()), k
+
+
 def test_infinite_logits():
     x = torch.zeros(4, 16, dtype=torch.bfloat16, device="cuda")
     w = torch.zeros(600, 16, dtype=torch.bfloat16, device="cuda")
