@@ -29,7 +29,8 @@
 // product of its own, summed in two floats, which replaces the tensor cores' in the sum of
 // exponentials and in G; and for a 32-bit grad_w of many tokens (kSplitRows) the
 // targets' entries stay out of G: their share is added in fp32, to grad_x by the last
-// kernel, to grad_w by the embedding's gradient.  Where they are in G an
+// kernel, to grad_w by the epilogue of its tiles, from a table whose rows are the classes
+// that are targets (summed by the embedding's gradient).  Where they are in G an
 // accumulator takes a segment of a few steps only, and the epilogue's warps add the
 // segments in registers, rounding to nearest.  (Segments of 4, 8 and 16 steps in all
 // products instead, 8,192 x 2048 x 50,304, with an earlier epilogue: 5.79, 5.19, 4.88
@@ -74,6 +75,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 enum Mode { kLoss = 0, kGrad = 1, kGradX = 2, kGradW = 3 };
 
 constexpr int kMaxPairs = 128;
+constexpr int kMaxCtas = 256;
 constexpr int kGroups = 12;
 
 // Which pair takes which of a job's tiles.  In round r the pairs that take more than r
@@ -127,6 +129,9 @@ struct Args {
   const float* lse;
   const float* hit;            // [rows]: exp(target logit - lse) - 1
   int split;                   // the targets' entries stay out of G
+  const int* slot;             // [classes]: a class's row of `table`, -1: none; NULL: none has
+  const float* table;          // the targets' share of grad_w
+  int64_t table_stride;
   float2* part;                // [2 * class tiles][rows]: maximum, sum
   void* g[2][3];               // [buffer][part]
   int64_t g_stride;
@@ -336,11 +341,15 @@ struct RowLoads {
   int64_t target = -1;
   float weight = 1.f, lse = 0.f, hit = 0.f;
 };
-__device__ __forceinline__ RowLoads load_row(const Args& a, int mode, int row) {
+__device__ __forceinline__ RowLoads load_row(const Args& a, const Job& j, int row) {
   RowLoads r;
-  if (mode > kGrad || row >= a.rows) return r;
+  if (j.mode == kGradW) {      // its row is a class
+    if (a.slot && j.v0 + row < j.v1) r.target = a.slot[j.v0 + row];
+    return r;
+  }
+  if (j.mode > kGrad || row >= a.rows) return r;
   r.target = load_index(a.target, row, a.index_type);
-  if (mode == kGrad) {
+  if (j.mode == kGrad) {
     if (a.row_weight) r.weight = a.row_weight[row];
     r.lse = a.lse[row];
     r.hit = a.hit[row];
@@ -348,10 +357,11 @@ __device__ __forceinline__ RowLoads load_row(const Args& a, int mode, int row) {
   return r;
 }
 struct RowIn {
-  int target;            // -1: none
+  int target;            // -1: none; grad_w: the class's row of `table`
   float lse, scale, hit;
 };
-__device__ __forceinline__ RowIn row_in(const Args& a, const RowLoads& q, float largest) {
+__device__ __forceinline__ RowIn row_in(const Args& a, int mode, const RowLoads& q, float largest) {
+  if (mode == kGradW) return RowIn{(int)q.target, 0.f, 0.f, 0.f};
   const bool live = q.target >= 0 && q.target < a.classes && q.weight != 0.f;
   return RowIn{live ? (int)q.target : -1, q.lse, live ? q.weight / largest * 32768.f : 0.f, q.hit};
 }
@@ -467,6 +477,9 @@ struct Block {
   int64_t stride;
   bool vec, add;
   float f1, f2;
+  const float* table;  // a row of it is added to a lane's row; NULL: none
+  int64_t table_stride;
+  int slot;            // which, -1: none
 };
 template <typename O>
 __device__ __forceinline__ void store_block(O* out, const Block& b, float* turn, const float (&x)[32]) {
@@ -484,10 +497,19 @@ __device__ __forceinline__ void store_block(O* out, const Block& b, float* turn,
       const int k = lane % N * VEC;
 #pragma unroll
       for (int r = lane / N; r < 32; r += 32 / N) {
+        const int slot = b.table ? __shfl_sync(0xffffffffu, b.slot, r) : -1;
         if (r >= b.rows || 16 * h + k >= b.cols) continue;
         float y[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) y[e] = turn[r * kPitch + k + e];
+        if (slot >= 0) {
+          const float* q = b.table + slot * b.table_stride + 16 * h + k;
+#pragma unroll
+          for (int e = 0; e < VEC; e += 4) {
+            const float4 t = *reinterpret_cast<const float4*>(q + e);
+            y[e] += t.x, y[e + 1] += t.y, y[e + 2] += t.z, y[e + 3] += t.w;
+          }
+        }
         Pack<O, VEC>* q = reinterpret_cast<Pack<O, VEC>*>(out + r * b.stride + 16 * h + k);
         if (b.add) {
           float o[VEC];
@@ -501,9 +523,11 @@ __device__ __forceinline__ void store_block(O* out, const Block& b, float* turn,
       const int k = lane % 16;
 #pragma unroll 4
       for (int r = lane / 16; r < 32; r += 2) {
+        const int slot = b.table ? __shfl_sync(0xffffffffu, b.slot, r) : -1;
         if (r >= b.rows || 16 * h + k >= b.cols) continue;
         O* q = out + r * b.stride + 16 * h + k;
-        const float y = turn[r * kPitch + k];
+        float y = turn[r * kPitch + k];
+        if (slot >= 0) y += b.table[slot * b.table_stride + 16 * h + k];
         *q = from_f<O>(b.add ? y + to_f(*q) : y);
       }
     }
@@ -518,12 +542,12 @@ __device__ __forceinline__ void grad_x_tile(const Args& a, const Job& j, const T
   for (int c = 0; c < 4; ++c) {
     float v[32];
     src.get(c, v);
-    store_block<float>(out + 32 * c, Block{a.rows - first, (int)a.dx_stride - col - 32 * c, a.dx_stride, true, j.add != 0, 1.f, 1.f}, turn, v);
+    store_block<float>(out + 32 * c, Block{a.rows - first, (int)a.dx_stride - col - 32 * c, a.dx_stride, true, j.add != 0, 1.f, 1.f, nullptr, 0, -1}, turn, v);
   }
 }
 
 template <typename O, typename Src>
-__device__ __forceinline__ void grad_w_tile(const Args& a, const Job& j, int v, int col, float* turn, const Src& src) {
+__device__ __forceinline__ void grad_w_tile(const Args& a, const Job& j, int v, int slot, int col, float* turn, const Src& src) {
   constexpr int VEC = 16 / sizeof(O);
   const bool vec = (a.cols % VEC == 0) && (a.dw_stride % VEC == 0) && (reinterpret_cast<uintptr_t>(a.dw) % 16 == 0);
   const int first = v - threadIdx.x % 32;
@@ -533,7 +557,8 @@ __device__ __forceinline__ void grad_w_tile(const Args& a, const Job& j, int v, 
   for (int c = 0; c < 4; ++c) {
     float x[32];
     src.get(c, x);
-    store_block<O>(out + 32 * c, Block{j.v1 - first, a.cols - col - 32 * c, a.dw_stride, vec, a.accumulate != 0, 1.f / 32768.f, largest}, turn, x);
+    store_block<O>(out + 32 * c, Block{j.v1 - first, a.cols - col - 32 * c, a.dw_stride, vec, a.accumulate != 0, 1.f / 32768.f, largest,
+                                       a.table ? a.table + col + 32 * c : nullptr, a.table_stride, slot}, turn, x);
   }
 }
 
@@ -548,11 +573,11 @@ __device__ __forceinline__ void finish_tile(const Args& a, const Job& j, const T
   } else if (j.mode == kGradX) {
     grad_x_tile(a, j, t, row, col, turn, src);
   } else if (a.dw_type == LOPT_F32) {
-    grad_w_tile<float>(a, j, j.v0 + row, col, turn, src);
+    grad_w_tile<float>(a, j, j.v0 + row, in.target, col, turn, src);
   } else if (a.dw_type == LOPT_F16) {
-    grad_w_tile<__half>(a, j, j.v0 + row, col, turn, src);
+    grad_w_tile<__half>(a, j, j.v0 + row, in.target, col, turn, src);
   } else {
-    grad_w_tile<__nv_bfloat16>(a, j, j.v0 + row, col, turn, src);
+    grad_w_tile<__nv_bfloat16>(a, j, j.v0 + row, in.target, col, turn, src);
   }
 }
 
@@ -684,13 +709,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     RowLoads ahead;
     if (more) {
       x = walk.next();
-      ahead = load_row(a, a.job[job].mode, x.m * kTile + own_row);
+      ahead = load_row(a, a.job[job], x.m * kTile + own_row);
     }
     while (more) {
       const Job& j = a.job[job];
       const int row = x.m * kTile + own_row;
       const int col = x.n * kTile + half * kHalf;
-      const RowIn in = row_in(a, ahead, largest);
+      const RowIn in = row_in(a, j.mode, ahead, largest);
       const Tile now = x;
       auto ready = [&] {
         const bool ok = __all_sync(0xffffffffu, wait_for(smem_u32(&s_acc_full[buf]), phase, abort, a.limit_ns));
@@ -709,7 +734,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         job = walk.job;
         if (more) {
           x = walk.next();
-          ahead = load_row(a, a.job[job].mode, x.m * kTile + own_row);
+          ahead = load_row(a, a.job[job], x.m * kTile + own_row);
         }
       };
       if (now.k1 - now.k0 <= j.segment && now.k1 > now.k0) {
@@ -907,7 +932,7 @@ __device__ __forceinline__ void start_few(int64_t rows, const void* target, int 
 __global__ void __launch_bounds__(256) k_linear_ce_copy(const uint16_t* x, int64_t stride, int64_t rows, int cols, uint16_t* out,
                                                         int64_t out_stride, const void* target, int index_type,
                                                         const Rows q, const float* row_weight, const float* lse,
-                                                        float* largest, float* hit, int* gave_up, int32_t* status) {
+                                                        float* largest, float* hit, unsigned* slot, int* gave_up, int32_t* status) {
   const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
   wait_for_previous();
@@ -925,6 +950,8 @@ __global__ void __launch_bounds__(256) k_linear_ce_copy(const uint16_t* x, int64
       if (t >= q.classes && status) atomicOr(status, kStatusIndex);
       // Floats above 0 are in the order of their bits.
       if (!gave_up && live && isfinite(w)) atomicMax(reinterpret_cast<int*>(largest), __float_as_int(fabsf(w)));
+      // A class's slot is its first row: a look at it spares a common class's many atomics.
+      if (slot && live && (unsigned)row < *reinterpret_cast<volatile unsigned*>(slot + t)) atomicMin(slot + t, (unsigned)row);
     }
   }
   const uint16_t* p = x + row * stride;
@@ -958,23 +985,29 @@ __global__ void __launch_bounds__(256) k_linear_ce_copy(const uint16_t* x, int64
   }
 }
 
-__global__ void k_linear_ce_start(float* largest, int* gave_up) {
-  if (threadIdx.x == 0) *largest = 0.f;
-  gave_up[threadIdx.x] = 0;
+__global__ void __launch_bounds__(kMaxCtas) k_linear_ce_start(float* largest, int* gave_up, unsigned* slot, int classes) {
+  if (blockIdx.x == 0) {
+    if (threadIdx.x == 0) *largest = 0.f;
+    gave_up[threadIdx.x] = 0;
+  }
+  if (!slot) return;
+  for (int v = blockIdx.x * kMaxCtas + threadIdx.x; v < classes; v += gridDim.x * kMaxCtas) slot[v] = 0xffffffffu;
 }
 
-// The targets' rows of grad_w's sum, fp32: row_weight * hit * x (x with zeros in
-// the rows that do not count).
+// The targets' terms of grad_w's sum, fp32: row_weight * hit * x (x with zeros in
+// the rows that do not count), and the slot that each belongs to.
 template <typename T>
 __global__ void __launch_bounds__(256) k_linear_ce_share(const T* x, int64_t stride, int64_t rows, int cols, const float* hit,
                                                          const void* target, int index_type, int classes,
-                                                         const float* row_weight, float* out) {
+                                                         const float* row_weight, float* out, const int* slot, int* to) {
   const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
   wait_for_previous();
   if (row >= rows) return;
   const int64_t t = load_index(target, row, index_type);
   const float w = row_weight ? row_weight[row] : 1.f;
-  const float c = t >= 0 && t < classes && w != 0.f ? hit[row] * w : 0.f;
+  const bool live = t >= 0 && t < classes && w != 0.f;
+  const float c = live ? hit[row] * w : 0.f;
+  if (threadIdx.x % 32 == 0) to[row] = live ? slot[t] : -1;
   const T* p = x + row * stride;
   float* q = out + row * stride;
   for (int j = threadIdx.x % 32 * 8; j < cols; j += 256) {     // whole rows of 8: the stride is a multiple
@@ -1067,7 +1100,6 @@ constexpr int64_t kExactRows = 16;
 // Steps of a segment: logits whose losses are fp32, a 32-bit grad_w without and with
 // the targets' entries; all for products that end in 16 bits.
 constexpr int kLossSegment = 32, kGradSegment = 32, kGradWSegment = 4, kSplitSegment = 64, kAll = 1 << 30;
-constexpr int kMaxCtas = 256;
 
 int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
@@ -1217,7 +1249,7 @@ cudaError_t launch_tiles(const Maps& maps, Args& a, int pairs, cudaStream_t s) {
 // Where things are in the workspace, in bytes from its start.
 struct Plan {
   int64_t x = 0, w = 0, part = 0, g = 0, g_plane = 0, dx = 0, flags = 0, largest = 0, size = 0;
-  int64_t hit = 0, share = 0, sort = 0, sort_bytes = 0;
+  int64_t hit = 0, share = 0, table = 0, slot = 0, to = 0, sort = 0, sort_bytes = 0;
   int64_t x_stride, w_stride, chunk = 0, dx_stride = 0, slice = 0;
   int splits = 1, buffers = 1;
 };
@@ -1243,15 +1275,28 @@ Plan plan_loss(int64_t rows, int64_t classes, int64_t cols, bool copy) {
   return p;
 }
 
-Plan plan_grad(int64_t rows, int64_t classes, int64_t cols, bool fp32_weight, bool copy) {
+// How a backward call holds G.
+struct Parts {
+  int planes, planes_x;      // its parts for grad_w, for grad_x
+  bool split;                // the targets' entries stay out of it
+};
+Parts parts_of(int64_t rows, bool fp32_weight, bool bf16) {
+  Parts q;
+  q.split = fp32_weight && rows > kSplitRows;
+  q.planes_x = rows > kExactRows ? 1 : 2;
+  q.planes = !fp32_weight ? q.planes_x : q.split || !bf16 ? 2 : 3;
+  return q;
+}
+
+Plan plan_grad(int64_t rows, int64_t classes, int64_t cols, const Parts& q, bool copy) {
   Plan p;
   p.x_stride = p.w_stride = up(cols, 8);
-  // G in one part (two for very few rows), for an fp32 grad_w in two or, with the targets'
-  // entries in it, in three (for float16 two do).
-  const int planes = !fp32_weight ? (rows > kExactRows ? 1 : 2) : rows > kSplitRows ? 2 : 3;
-  if (fp32_weight && planes == 2) {
+  if (q.split) {
     p.share = take(p, rows * p.x_stride * 4);
-    lopt_embed_workspace(rows, classes, cols, &p.sort_bytes);
+    p.table = take(p, rows * p.x_stride * 4);
+    p.slot = take(p, classes * 4);
+    p.to = take(p, rows * 4);
+    lopt_embed_workspace(rows, rows, p.x_stride, &p.sort_bytes);
     p.sort = take(p, p.sort_bytes);
   }
   p.flags = take(p, kMaxCtas * 4);
@@ -1260,10 +1305,10 @@ Plan plan_grad(int64_t rows, int64_t classes, int64_t cols, bool fp32_weight, bo
   p.x = take(p, rows * p.x_stride * 2);
   if (copy) p.w = take(p, classes * p.w_stride * 2);
   const int64_t all = up(classes, kTile);
-  p.chunk = std::min(all, std::max<int64_t>(kChunkBytes / (rows * 2 * planes) / kTile, 1) * kTile);
+  p.chunk = std::min(all, std::max<int64_t>(kChunkBytes / (rows * 2 * q.planes) / kTile, 1) * kTile);
   p.buffers = p.chunk < all ? 2 : 1;
   p.g_plane = up(rows * p.chunk * 2, 1024);
-  p.g = take(p, p.g_plane * planes * p.buffers);
+  p.g = take(p, p.g_plane * q.planes * p.buffers);
   p.dx_stride = up(cols, 8);
   p.slice = up(rows * p.dx_stride, 256);
   // Few tiles of grad_x: the classes are split over slices, added in order at the end.
@@ -1325,8 +1370,13 @@ int lopt_linear_ce_workspace(int64_t rows, int64_t classes, int64_t cols, int al
   if (!bytes || (aligned != 0 && aligned != 1) || (backward != 0 && backward != 1) || (backward && !type_size(grad_weight_type))) return LOPT_E_ARG;
   if (rows < 0 || rows > kMaxTokens || classes < 1 || classes > kMaxClasses || cols < 1 || cols > kMaxWidth) return LOPT_E_SHAPE;
   const int64_t n = std::max<int64_t>(rows, 1);
-  *bytes = backward ? plan_grad(n, classes, cols, grad_weight_type == LOPT_F32, !aligned).size
-                    : plan_loss(n, classes, cols, !aligned).size;
+  if (!backward) {
+    *bytes = plan_loss(n, classes, cols, !aligned).size;
+    return LOPT_OK;
+  }
+  *bytes = 0;      // x of either type
+  for (bool bf16 : {false, true})
+    *bytes = std::max(*bytes, plan_grad(n, classes, cols, parts_of(n, grad_weight_type == LOPT_F32, bf16), !aligned).size);
   return LOPT_OK;
 }
 
@@ -1352,14 +1402,14 @@ static int forward(uint64_t limit_ns, const void* x, int type, int64_t rows, int
   if (!tma_rows(c.mx)) {
     xp = ws + p.x, xs = p.x_stride;
     e = launch(k_linear_ce_copy, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, true, 1, (const uint16_t*)x, x_stride, rows,
-               (int)cols, (uint16_t*)xp, xs, (const void*)nullptr, 0, Rows{}, (const float*)nullptr, (const float*)nullptr, (float*)nullptr, (float*)nullptr, (int*)nullptr, (int32_t*)nullptr);
+               (int)cols, (uint16_t*)xp, xs, (const void*)nullptr, 0, Rows{}, (const float*)nullptr, (const float*)nullptr, (float*)nullptr, (float*)nullptr, (unsigned*)nullptr, (int*)nullptr, (int32_t*)nullptr);
     if (e != cudaSuccess) return done(e);
   }
   if (!tma_rows(c.mw)) {
     wp = ws + p.w, wst = p.w_stride;
     e = launch(k_linear_ce_copy, dim3((unsigned)((classes + 7) / 8)), dim3(256), 0, s, true, 1, (const uint16_t*)weight, weight_stride,
                classes, (int)cols, (uint16_t*)wp, wst, (const void*)nullptr, 0, Rows{}, (const float*)nullptr, (const float*)nullptr, (float*)nullptr,
-               (float*)nullptr, (int*)nullptr, (int32_t*)nullptr);
+               (float*)nullptr, (unsigned*)nullptr, (int*)nullptr, (int32_t*)nullptr);
     if (e != cudaSuccess) return done(e);
   }
   const int pairs = pair_count();
@@ -1429,31 +1479,33 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
   if (grad_x && (rc = check_matrix(mo, true))) return rc;
   if (!grad_x && !grad_weight) return LOPT_OK;
   const bool fp32_weight = grad_weight && grad_weight_type == LOPT_F32;
-  const int planes_x = rows > kExactRows ? 1 : 2;
-  const int planes = !fp32_weight ? planes_x : type == LOPT_F16 || rows > kSplitRows ? 2 : 3;
+  const bool bf16 = type == LOPT_BF16;
+  const Parts parts = parts_of(rows, fp32_weight, bf16);
+  const int planes = parts.planes, planes_x = parts.planes_x;
+  const bool split = parts.split;
   const int pairs = pair_count();
-  const Plan p = plan_grad(rows, classes, cols, fp32_weight, !tma_rows(c.mw));
-  // The embedding's gradient adds to a contiguous table.
-  const bool split = p.sort_bytes && grad_weight_stride == cols;
+  const Plan p = plan_grad(rows, classes, cols, parts, !tma_rows(c.mw));
   if (!lse || !workspace || workspace_bytes < p.size) return LOPT_E_ARG;
   if ((uintptr_t)lse % 4 || (uintptr_t)status % 4 || (uintptr_t)workspace % 256) return LOPT_E_ALIGN;
   const Span sl{lse, 1, rows, rows, 4}, sw{workspace, 1, p.size, p.size, 1};
   const Span st{target, 1, rows, rows, index_size(index_type)}, sr{row_weight, 1, rows, rows, 4};
   if ((rc = check_alias({mo, mg, sw}, {c.mx, c.mw, st, sr, sl}))) return rc;
   char* ws = static_cast<char*>(workspace);
-  const bool bf16 = type == LOPT_BF16;
   float *largest = reinterpret_cast<float*>(ws + p.largest), *hit = reinterpret_cast<float*>(ws + p.hit);
   cudaError_t e;
   int* flags = reinterpret_cast<int*>(ws + p.flags);
   static_assert(kMaxCtas == 256, "start_few clears a word a thread");
-  const bool start = rows > kFewRows;
+  int* slot = split ? reinterpret_cast<int*>(ws + p.slot) : nullptr;
+  const bool start = rows > kFewRows || slot;
   if (start) {
-    e = launch(k_linear_ce_start, dim3(1), dim3(kMaxCtas), 0, s, false, 1, largest, flags);
+    e = launch(k_linear_ce_start, dim3(slot ? (unsigned)std::min<int64_t>((classes + kMaxCtas - 1) / kMaxCtas, 304) : 1u), dim3(kMaxCtas), 0, s,
+               false, 1, largest, flags, reinterpret_cast<unsigned*>(slot), (int)classes);
     if (e != cudaSuccess) return done(e);
   }
   uint16_t* xp = reinterpret_cast<uint16_t*>(ws + p.x);
   e = launch(k_linear_ce_copy, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, true, 1, (const uint16_t*)x, x_stride, rows,
-             (int)cols, xp, p.x_stride, target, index_type, rows_of(c, 0), row_weight, lse, largest, hit, start ? (int*)nullptr : flags, status);
+             (int)cols, xp, p.x_stride, target, index_type, rows_of(c, 0), row_weight, lse, largest, hit, reinterpret_cast<unsigned*>(slot),
+             start ? (int*)nullptr : flags, status);
   if (e != cudaSuccess) return done(e);
   const void* wp = weight;
   int64_t wst = weight_stride;
@@ -1461,8 +1513,24 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
     wp = ws + p.w, wst = p.w_stride;
     e = launch(k_linear_ce_copy, dim3((unsigned)((classes + 7) / 8)), dim3(256), 0, s, true, 1, (const uint16_t*)weight, weight_stride,
                classes, (int)cols, (uint16_t*)wp, wst, (const void*)nullptr, 0, Rows{}, (const float*)nullptr, (const float*)nullptr, (float*)nullptr,
-               (float*)nullptr, (int*)nullptr, (int32_t*)nullptr);
+               (float*)nullptr, (unsigned*)nullptr, (int*)nullptr, (int32_t*)nullptr);
     if (e != cudaSuccess) return done(e);
+  }
+  // The targets' share of grad_w: its rows are the classes that are targets.
+  if (slot) {
+    const dim3 grid((unsigned)((rows + 7) / 8));
+    float* share = reinterpret_cast<float*>(ws + p.share);
+    int* to = reinterpret_cast<int*>(ws + p.to);
+    if (bf16)
+      e = launch(k_linear_ce_share<__nv_bfloat16>, grid, dim3(256), 0, s, true, 1, (const __nv_bfloat16*)xp, p.x_stride, rows, (int)cols,
+                 (const float*)hit, target, index_type, (int)classes, row_weight, share, (const int*)slot, to);
+    else
+      e = launch(k_linear_ce_share<__half>, grid, dim3(256), 0, s, true, 1, (const __half*)xp, p.x_stride, rows, (int)cols,
+                 (const float*)hit, target, index_type, (int)classes, row_weight, share, (const int*)slot, to);
+    if (e != cudaSuccess) return done(e);
+    rc = lopt_embed_backward(share, LOPT_F32, p.x_stride, to, LOPT_I32, rows, rows, p.x_stride, 1.f, 0,
+                             reinterpret_cast<float*>(ws + p.table), ws + p.sort, p.sort_bytes, nullptr, stream);
+    if (rc) return rc;
   }
   Maps maps{};
   Args a{};
@@ -1479,6 +1547,7 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
   a.target = target, a.index_type = index_type, a.row_weight = row_weight, a.lse = lse;
   a.g_stride = p.chunk, a.largest = largest;
   a.hit = hit, a.split = split;
+  if (slot) a.slot = slot, a.table = reinterpret_cast<const float*>(ws + p.table), a.table_stride = p.x_stride;
   a.dx = reinterpret_cast<float*>(ws + p.dx), a.dx_stride = p.dx_stride, a.dx_slice = p.slice;
   a.dw = grad_weight, a.dw_type = grad_weight_type, a.dw_stride = grad_weight_stride, a.accumulate = accumulate;
   a.gave_up = reinterpret_cast<int*>(ws + p.flags), a.status = status;
@@ -1507,20 +1576,6 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
     if (a.jobs == 2 && tile_cost(a.job[1]) > tile_cost(a.job[0])) std::swap(a.job[0], a.job[1]);
     if (k < chunks) add(grad_job(k));
     if ((e = launch_tiles(maps, a, pairs, s)) != cudaSuccess) return done(e);
-  }
-  if (split) {
-    const dim3 grid((unsigned)((rows + 7) / 8));
-    float* share = reinterpret_cast<float*>(ws + p.share);
-    if (bf16)
-      e = launch(k_linear_ce_share<__nv_bfloat16>, grid, dim3(256), 0, s, true, 1, (const __nv_bfloat16*)xp, p.x_stride, rows, (int)cols,
-                 (const float*)hit, target, index_type, (int)classes, row_weight, share);
-    else
-      e = launch(k_linear_ce_share<__half>, grid, dim3(256), 0, s, true, 1, (const __half*)xp, p.x_stride, rows, (int)cols,
-                 (const float*)hit, target, index_type, (int)classes, row_weight, share);
-    if (e != cudaSuccess) return done(e);
-    rc = lopt_embed_backward(share, LOPT_F32, p.x_stride, target, index_type, rows, classes, cols, 1.f, 1,
-                             static_cast<float*>(grad_weight), ws + p.sort, p.sort_bytes, status, stream);
-    if (rc) return rc;
   }
   if (!grad_x) return LOPT_OK;
   const dim3 grid((unsigned)rows, (unsigned)((cols + 1023) / 1024));
