@@ -85,7 +85,8 @@ int lopt_block_norm_backward(const void* grad_y, int type, int64_t rows, int64_t
  * NaN and grad_weight is not valid.
  * workspace: lopt_linear_ce_workspace() bytes for the direction, 256-byte aligned,
  * any contents; aligned = 1 where the rows of x and weight start on 16-byte
- * boundaries (others are copied first), grad_weight_type LOPT_F32 or other.
+ * boundaries (others are copied first), grad_weight_type LOPT_F32 or other; without
+ * grad_weight either type's size is enough, another's than LOPT_F32 the smaller.
  * rows and classes up to 2^22, cols up to 2^16.
  */
 int lopt_linear_ce_workspace(int64_t rows, int64_t classes, int64_t cols, int aligned, int backward,

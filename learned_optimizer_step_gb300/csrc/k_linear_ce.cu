@@ -1374,9 +1374,12 @@ int lopt_linear_ce_workspace(int64_t rows, int64_t classes, int64_t cols, int al
     *bytes = plan_loss(n, classes, cols, !aligned).size;
     return LOPT_OK;
   }
-  *bytes = 0;      // x of either type
+  // x of either type, grad_weight of this one or NULL: fewer parts of G may take more,
+  // since chunks are whole tiles of classes.
+  *bytes = 0;
   for (bool bf16 : {false, true})
-    *bytes = std::max(*bytes, plan_grad(n, classes, cols, parts_of(n, grad_weight_type == LOPT_F32, bf16), !aligned).size);
+    for (bool fp32 : {false, grad_weight_type == LOPT_F32})
+      *bytes = std::max(*bytes, plan_grad(n, classes, cols, parts_of(n, fp32, bf16), !aligned).size);
   return LOPT_OK;
 }
 

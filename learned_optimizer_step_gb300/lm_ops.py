@@ -270,7 +270,7 @@ def linear_cross_entropy_backward(x, weight, target, lse, *, row_weight=None, gr
     if accumulate and (grad_weight is None or not need_weight):
         raise ValueError("accumulate needs grad_weight")
     gx = gxs = gw = gws = 0
-    gt = F32
+    gt = kind
     written = []
     if need_x:
         grad_x, gx, gxs = _like(c, grad_x, x, (rows, cols), "grad_x")

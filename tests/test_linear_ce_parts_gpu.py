@@ -36,3 +36,15 @@ def test_a_block_of_columns_has_the_bits_of_a_buffer_of_its_own(n, extra, dtype)
         assert torch.equal(got, want)
     part.fill_(5.0)
     assert bool((wide == 5).all())
+
+
+def test_without_grad_weight_over_several_chunks():
+    """A frozen table: its gradient is not asked for.  G of 4,099 tokens, 50,257 classes is
+    two chunks.  grad_x is the same to what one part of G leaves, half a step of an entry."""
+    x, w, t, rw = inputs(gen(3), 4099, 50257, 128, torch.bfloat16)
+    _, lse = L.linear_cross_entropy_forward(x, w, t, row_weight=rw)
+    dx, none = L.linear_cross_entropy_backward(x, w, t, lse, row_weight=rw, need_weight=False)
+    want, _, g = R.ce_backward(x, w, t, lse, rw)
+    assert none is None
+    size = g.abs() @ w.double().abs()
+    R.within(dx, want, 1, size * (2.0 ** -8 / R.U), "grad_x")

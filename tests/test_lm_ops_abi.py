@@ -5,6 +5,7 @@ must be refused are made, with addresses that are never read."""
 import ctypes
 import math
 import os
+import random
 import re
 
 import pytest
@@ -141,6 +142,32 @@ def test_workspace_sizes(fns):
         assert fns["lopt_block_norm_workspace"](rows, cols, need) == 0 and need.value >= 8 * cols + 4 * rows
     assert fns["lopt_block_norm_workspace"](1, 0, need) == SHAPE and fns["lopt_block_norm_workspace"](1, 1, None) == ARG
     assert fns["lopt_adamw_workspace"](need) == 0 and need.value > 0 and fns["lopt_adamw_workspace"](None) == ARG
+
+
+def test_the_size_asked_for_is_enough(fns):
+    """Over the range of sizes, with either gradient left out.  The calls stop at a
+    workspace that is not aligned, which is looked at after its size."""
+    rng, need = random.Random(7), ctypes.c_int64()
+    spread = lambda low, high: int(math.exp(rng.uniform(math.log(low), math.log(high + 1))))   # noqa: E731
+    sizes = [(4099, 50257, 128), (4099, 50257, 64), (12000, 16384, 128), (19000, 8000, 64), (6000, 50257, 128), (256, 1 << 20, 8)]
+    sizes += [(spread(1, 60000), spread(1, 200000), spread(1, 3000)) for _ in range(4000)]
+    far = [(k + 1) << 50 for k in range(8)]
+    for rows, classes, cols in sizes:
+        cols8 = (cols + 7) // 8 * 8
+        for dtype in (F16, BF16):
+            for asked, given in ((F32, F32), (dtype, dtype), (F32, None), (dtype, None)):
+                assert fns["lopt_linear_ce_workspace"](rows, classes, cols, 1, 1, asked, need) == 0
+                call = {**CB, "type": dtype, "rows": rows, "cols": cols, "x_stride": cols8, "classes": classes, "weight_stride": cols8,
+                        "grad_x_stride": cols, "grad_weight": 0 if given is None else far[0], "grad_weight_stride": cols,
+                        "grad_weight_type": asked, "x": far[1], "weight": far[2], "target": far[3], "row_weight": far[4],
+                        "lse": far[5], "grad_x": far[6], "workspace": far[7] + 128, "workspace_bytes": need.value}
+                code = fns["lopt_linear_ce_backward"](*call.values())
+                assert code == ALIGN, (rows, classes, cols, dtype, asked, given, code)
+        assert fns["lopt_linear_ce_workspace"](rows, classes, cols, 1, 0, F32, need) == 0
+        call = {**CF, "rows": rows, "cols": cols, "x_stride": cols8, "classes": classes, "weight_stride": cols8, "x": far[1],
+                "weight": far[2], "target": far[3], "row_weight": far[4], "loss": far[5], "lse": far[6], "workspace": far[7] + 128,
+                "workspace_bytes": need.value}
+        assert fns["lopt_linear_ce_forward"](*call.values()) == ALIGN
 
 
 def tensor(**change):
