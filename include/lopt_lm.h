@@ -77,16 +77,17 @@ int lopt_block_norm_backward(const void* grad_y, int type, int64_t rows, int64_t
  *   grad_x = G weight,   grad_weight = G^T x
  * Rows that do not count give zeros and add nothing, whatever they hold.  grad_x
  * (of `type`) or grad_weight may be NULL.  grad_weight is of LOPT_F32, which
- * accumulate = 1 adds to, or of `type`; G is rounded to 16 bits for the products
- * (relative to 2^-15 of the largest row_weight at least), for an fp32 grad_weight
- * to two or three such parts.
+ * accumulate = 1 adds to, or of `type`.  For the products G is the sum of 16-bit
+ * parts, the first rounded relative to 2^-15 of the largest row_weight at least: two or
+ * three for an fp32 grad_weight; for one of `type` and for grad_x two, or one, beside
+ * which the targets' entries are fp32.
  *
  * Bit 1 of *status: a bounded wait (1 s) ran out; losses, lse and grad_x are then
  * NaN and grad_weight is not valid.
  * workspace: lopt_linear_ce_workspace() bytes for the direction, 256-byte aligned,
  * any contents; aligned = 1 where the rows of x and weight start on 16-byte
- * boundaries (others are copied first), grad_weight_type LOPT_F32 or other; without
- * grad_weight either type's size is enough, another's than LOPT_F32 the smaller.
+ * boundaries (others are copied first), grad_weight_type LOPT_F32 or other.  LOPT_F32's
+ * size does for the other types too, and either does without grad_weight.
  * rows and classes up to 2^22, cols up to 2^16.
  */
 int lopt_linear_ce_workspace(int64_t rows, int64_t classes, int64_t cols, int aligned, int backward,

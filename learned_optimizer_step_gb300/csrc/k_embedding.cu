@@ -353,7 +353,7 @@ struct EmbedSum {
   int32_t* counters;       // [chunks][gridDim.y]: arrivals of the run that starts in the chunk
   float* part;             // [chunks][2][cols]: sums of a run entering / leaving the chunk
   float* grad;
-  int64_t gs, cols;
+  int64_t gs, cols, os;    // os: between rows of grad
   int rows, log_blocks, ids_per_block, last_offset, chunk, accumulate;
   int zero_blocks, zero_vec, n;
   float scale;
@@ -406,7 +406,7 @@ __device__ __forceinline__ void zero_rows(const EmbedSum& a, int b) {
     if (v >= a.rows) break;
     const int at = place_of(a, v);
     if (a.offsets[at] != a.offsets[at + 1]) continue;
-    float* g = a.grad + (int64_t)v * a.cols;
+    float* g = a.grad + (int64_t)v * a.os;
     if (a.zero_vec) {
       for (int64_t j = lane * 4; j < a.cols; j += 128) __stcs(reinterpret_cast<float4*>(g + j), make_float4(0.f, 0.f, 0.f, 0.f));
     } else {
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(256, 3) k_embed_sum(const EmbedSum a) {
         if (from_before || goes_on) {
           store_sums<VEC>(a.part + ((int64_t)chunk * 2 + (from_before ? 0 : 1)) * a.cols + j, acc);
         } else {
-          float* g = a.grad + (int64_t)key[i + 1] * a.cols + j;
+          float* g = a.grad + (int64_t)key[i + 1] * a.os + j;
 #pragma unroll
           for (int e = 0; e < VEC; ++e) acc[e] *= a.scale;
           if (a.accumulate) add_sums<VEC>(g, acc);
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(256, 3) k_embed_sum(const EmbedSum a) {
     add_sums<VEC>(a.part + ((int64_t)first * 2 + 1) * a.cols + j, acc);
 #pragma unroll 8
     for (int c = first + 1; c <= last; ++c) add_sums<VEC>(a.part + (int64_t)c * 2 * a.cols + j, acc);
-    float* g = a.grad + (int64_t)v * a.cols + j;
+    float* g = a.grad + (int64_t)v * a.os + j;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) acc[e] *= a.scale;
     if (a.accumulate) add_sums<VEC>(g, acc);
@@ -639,15 +639,24 @@ int lopt_embed_workspace(int64_t n, int64_t rows, int64_t cols, int64_t* bytes) 
 int lopt_embed_backward(const void* grad_out, int type, int64_t grad_out_stride, const void* index, int index_type,
                         int64_t n, int64_t rows, int64_t cols, float scale, int accumulate, float* grad,
                         void* workspace, int64_t workspace_bytes, int32_t* status, void* stream) {
+  return embed_backward_to(grad_out, type, grad_out_stride, index, index_type, n, rows, cols, scale, accumulate, grad, cols,
+                           workspace, workspace_bytes, status, stream);
+}
+
+}  // extern "C"
+
+int lopt::train::embed_backward_to(const void* grad_out, int type, int64_t grad_out_stride, const void* index, int index_type,
+                                   int64_t n, int64_t rows, int64_t cols, float scale, int accumulate, float* grad,
+                                   int64_t grad_stride, void* workspace, int64_t workspace_bytes, int32_t* status, void* stream) {
   const int es = type_size(type), is = index_size(index_type);
   if (!es || !is || (accumulate != 0 && accumulate != 1)) return LOPT_E_ARG;
   int64_t need = 0;
   int rc = lopt_embed_workspace(n, rows, cols, &need);
   if (rc) return rc;
-  const Span mg{grad, rows, cols, cols, 4};
+  const Span mg{grad, rows, cols, grad_stride, 4};
   if ((rc = check_matrix(mg, true))) return rc;
   cudaStream_t s = (cudaStream_t)stream;
-  if (n == 0) return accumulate ? LOPT_OK : done(cudaMemsetAsync(grad, 0, (size_t)rows * cols * 4, s));
+  if (n == 0) return accumulate ? LOPT_OK : done(cudaMemset2DAsync(grad, (rows == 1 ? cols : grad_stride) * 4, 0, cols * 4, rows, s));
   const Span md{grad_out, n, cols, grad_out_stride, es}, mi{index, 1, n, n, is}, ws{workspace, 1, need, need, 1};
   if ((rc = check_matrix(md, false)) || (rc = check_matrix(mi, false))) return rc;
   if (!workspace || workspace_bytes < need) return LOPT_E_ARG;
@@ -655,7 +664,7 @@ int lopt_embed_backward(const void* grad_out, int type, int64_t grad_out_stride,
   if (overlap(mg, md) || overlap(mg, mi) || overlap(mg, ws) || overlap(ws, md) || overlap(ws, mi)) return LOPT_E_ALIAS;
   const Plan p = plan(n, rows, cols);
   char* w = static_cast<char*>(workspace);
-  const bool v4 = cols % 4 == 0 && (uintptr_t)grad % 16 == 0;
+  const bool v4 = cols % 4 == 0 && rows_aligned(mg, 16);
   EmbedSort a{};
   a.index = index;
   a.n = (int)n;
@@ -684,6 +693,7 @@ int lopt_embed_backward(const void* grad_out, int type, int64_t grad_out_stride,
   b.grad = grad;
   b.gs = grad_out_stride;
   b.cols = cols;
+  b.os = grad_stride;
   b.rows = (int)rows;
   b.n = (int)n;
   b.zero_blocks = accumulate ? 0 : (int)((rows + kZeroRows - 1) / kZeroRows);
@@ -703,5 +713,3 @@ int lopt_embed_backward(const void* grad_out, int type, int64_t grad_out_stride,
       return done(rows16 ? sum_as<__nv_bfloat16, 8>(b, p.chunks, s) : sum_as<__nv_bfloat16, 1>(b, p.chunks, s));
   }
 }
-
-}  // extern "C"

@@ -12,10 +12,9 @@
 //
 // The backward pass goes over the vocabulary in chunks whose G fits a bounded
 // workspace; the chunk's grad_x is added to fp32 sums, its rows of grad_w are
-// written.  For a 32-bit grad_w, G is held as the sum of 16-bit numbers: two (16 bits
+// written.  G is held as the sum of 16-bit numbers: for a 32-bit grad_w two (16 bits
 // of bfloat16, 22 of float16), or three of bfloat16 while the targets' entries are in
-// it.  Rounded once to bfloat16 it would be off by 2^-9, which is what a 16-bit grad_w
-// is rounded by anyway.
+// it; for a 16-bit grad_w two, or one without the targets' entries.
 //
 // A pair of CTAs (cta_group::2) computes a 256 x 256 tile: each holds 128 rows of
 // A and 128 of B per 64-wide step of K in shared memory (TMA, 128-byte swizzle) and
@@ -29,9 +28,9 @@
 // product of its own, summed in two floats, which replaces the tensor cores' in the sum of
 // exponentials and in G; and for a 32-bit grad_w of many tokens (kSplitRows) the
 // targets' entries stay out of G: their share is added in fp32, to grad_x by the last
-// kernel, to grad_w by the epilogue of its tiles, from a table whose rows are the classes
-// that are targets (summed by the embedding's gradient).  Where they are in G an
-// accumulator takes a segment of a few steps only, and the epilogue's warps add the
+// kernel, to grad_w by the embedding's gradient.  (To a 16-bit grad_w, of more tokens, from
+// a table whose rows are the classes that are targets, by its tiles' epilogue.)  Where they are in G an
+// accumulator of a 32-bit grad_w takes a segment of a few steps only, and the epilogue's warps add the
 // segments in registers, rounding to nearest.  (Segments of 4, 8 and 16 steps in all
 // products instead, 8,192 x 2048 x 50,304, with an earlier epilogue: 5.79, 5.19, 4.88
 // ms, 4.42 without; grad_w 3e-6 to 2e-5 off, now 3e-7.)
@@ -130,7 +129,7 @@ struct Args {
   const float* hit;            // [rows]: exp(target logit - lse) - 1
   int split;                   // the targets' entries stay out of G
   const int* slot;             // [classes]: a class's row of `table`, -1: none; NULL: none has
-  const float* table;          // the targets' share of grad_w
+  const float* table;          // the targets' share of a 16-bit grad_w
   int64_t table_stride;
   float2* part;                // [2 * class tiles][rows]: maximum, sum
   void* g[2][3];               // [buffer][part]
@@ -467,7 +466,7 @@ __device__ __forceinline__ void grad_tile(const Args& a, const Job& j, const Row
   }
 }
 
-// A warp's 32 rows of 32 columns to memory, times f1 f2.  They are turned in shared
+// A warp's 32 rows of 32 columns to memory.  They are turned in shared
 // memory, 16 columns at a time, so that the lanes of a store fill whole sectors: each
 // thread writing its own row leaves a sector to two stores of 32 rows each, or, element
 // by element, to 16 (us, grad_w of 100 x 100,000 classes fp16: 2000 wide 448 in all, 1999
@@ -476,10 +475,6 @@ struct Block {
   int rows, cols;      // that there are, from the first on
   int64_t stride;
   bool vec, add;
-  float f1, f2;
-  const float* table;  // a row of it is added to a lane's row; NULL: none
-  int64_t table_stride;
-  int slot;            // which, -1: none
 };
 template <typename O>
 __device__ __forceinline__ void store_block(O* out, const Block& b, float* turn, const float (&x)[32]) {
@@ -491,25 +486,16 @@ __device__ __forceinline__ void store_block(O* out, const Block& b, float* turn,
 #pragma unroll
     for (int k = 0; k < 16; k += 4)
       *reinterpret_cast<float4*>(turn + lane * kPitch + k) =
-          make_float4(x[16 * h + k] * b.f1 * b.f2, x[16 * h + k + 1] * b.f1 * b.f2, x[16 * h + k + 2] * b.f1 * b.f2, x[16 * h + k + 3] * b.f1 * b.f2);
+          make_float4(x[16 * h + k], x[16 * h + k + 1], x[16 * h + k + 2], x[16 * h + k + 3]);
     __syncwarp();
     if (b.vec) {
       const int k = lane % N * VEC;
 #pragma unroll
       for (int r = lane / N; r < 32; r += 32 / N) {
-        const int slot = b.table ? __shfl_sync(0xffffffffu, b.slot, r) : -1;
         if (r >= b.rows || 16 * h + k >= b.cols) continue;
         float y[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) y[e] = turn[r * kPitch + k + e];
-        if (slot >= 0) {
-          const float* q = b.table + slot * b.table_stride + 16 * h + k;
-#pragma unroll
-          for (int e = 0; e < VEC; e += 4) {
-            const float4 t = *reinterpret_cast<const float4*>(q + e);
-            y[e] += t.x, y[e + 1] += t.y, y[e + 2] += t.z, y[e + 3] += t.w;
-          }
-        }
         Pack<O, VEC>* q = reinterpret_cast<Pack<O, VEC>*>(out + r * b.stride + 16 * h + k);
         if (b.add) {
           float o[VEC];
@@ -523,11 +509,9 @@ __device__ __forceinline__ void store_block(O* out, const Block& b, float* turn,
       const int k = lane % 16;
 #pragma unroll 4
       for (int r = lane / 16; r < 32; r += 2) {
-        const int slot = b.table ? __shfl_sync(0xffffffffu, b.slot, r) : -1;
         if (r >= b.rows || 16 * h + k >= b.cols) continue;
         O* q = out + r * b.stride + 16 * h + k;
-        float y = turn[r * kPitch + k];
-        if (slot >= 0) y += b.table[slot * b.table_stride + 16 * h + k];
+        const float y = turn[r * kPitch + k];
         *q = from_f<O>(b.add ? y + to_f(*q) : y);
       }
     }
@@ -542,7 +526,7 @@ __device__ __forceinline__ void grad_x_tile(const Args& a, const Job& j, const T
   for (int c = 0; c < 4; ++c) {
     float v[32];
     src.get(c, v);
-    store_block<float>(out + 32 * c, Block{a.rows - first, (int)a.dx_stride - col - 32 * c, a.dx_stride, true, j.add != 0, 1.f, 1.f, nullptr, 0, -1}, turn, v);
+    store_block<float>(out + 32 * c, Block{a.rows - first, (int)a.dx_stride - col - 32 * c, a.dx_stride, true, j.add != 0}, turn, v);
   }
 }
 
@@ -557,8 +541,17 @@ __device__ __forceinline__ void grad_w_tile(const Args& a, const Job& j, int v, 
   for (int c = 0; c < 4; ++c) {
     float x[32];
     src.get(c, x);
-    store_block<O>(out + 32 * c, Block{j.v1 - first, a.cols - col - 32 * c, a.dw_stride, vec, a.accumulate != 0, 1.f / 32768.f, largest,
-                                       a.table ? a.table + col + 32 * c : nullptr, a.table_stride, slot}, turn, x);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) x[k] = x[k] * (1.f / 32768.f) * largest;
+    if (slot >= 0) {      // the thread's class is a target: a line of its share
+      const float* q = a.table + slot * a.table_stride + col + 32 * c;
+#pragma unroll
+      for (int k = 0; k < 32; k += 4) {
+        const float4 t = *reinterpret_cast<const float4*>(q + k);
+        x[k] += t.x, x[k + 1] += t.y, x[k + 2] += t.z, x[k + 3] += t.w;
+      }
+    }
+    store_block<O>(out + 32 * c, Block{j.v1 - first, a.cols - col - 32 * c, a.dw_stride, vec, a.accumulate != 0}, turn, x);
   }
 }
 
@@ -1007,7 +1000,7 @@ __global__ void __launch_bounds__(256) k_linear_ce_share(const T* x, int64_t str
   const float w = row_weight ? row_weight[row] : 1.f;
   const bool live = t >= 0 && t < classes && w != 0.f;
   const float c = live ? hit[row] * w : 0.f;
-  if (threadIdx.x % 32 == 0) to[row] = live ? slot[t] : -1;
+  if (slot && threadIdx.x % 32 == 0) to[row] = live ? slot[t] : -1;
   const T* p = x + row * stride;
   float* q = out + row * stride;
   for (int j = threadIdx.x % 32 * 8; j < cols; j += 256) {     // whole rows of 8: the stride is a multiple
@@ -1020,19 +1013,19 @@ __global__ void __launch_bounds__(256) k_linear_ce_share(const T* x, int64_t str
   }
 }
 
+__device__ __forceinline__ void fetch_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // grad_x from the sums of its slices, in order.
 template <typename T>
 __global__ void __launch_bounds__(256) k_linear_ce_grad_x(const float* dx, int64_t dx_stride, int64_t slice, int slices,
                                                           int64_t rows, int cols, const float* largest, const void* target,
                                                           int index_type, int classes, const float* row_weight,
-                                                          const float* hit, const T* weight, int64_t weight_stride,
+                                                          const float* hit, int split, const T* weight, int64_t weight_stride,
                                                           const int* gave_up, int ctas, T* out, int64_t out_stride) {
   __shared__ int s_bad;
   if (threadIdx.x == 0) s_bad = 0;
-  wait_for_previous();
-  __syncthreads();
-  if (threadIdx.x < ctas && gave_up[threadIdx.x]) s_bad = 1;
-  __syncthreads();
+  // What the kernel before does not write (and those before that one, for which it has
+  // waited, have) is read ahead of its end.
   const int64_t row = (int64_t)blockIdx.x;
   const int64_t t = load_index(target, row, index_type);
   const float w = row_weight ? row_weight[row] : 1.f;
@@ -1041,9 +1034,21 @@ __global__ void __launch_bounds__(256) k_linear_ce_grad_x(const float* dx, int64
   const float* p = dx + row * dx_stride;
   T* q = out + row * out_stride;
   const T* wt = hit && live ? weight + t * weight_stride : nullptr;
-  const float share = wt ? hit[row] * w : 0.f;
+  // The target's entry of G, or what its rounding left out.
+  float share = 0.f;
+  if (wt && split) {
+    share = hit[row] * w;
+  } else if (wt) {
+    const float entry = hit[row] * (w / f2 * 32768.f);
+    share = (entry - to_f(from_f<T>(entry))) * f1 * f2;
+  }
   const bool vec = cols % 4 == 0 && out_stride % 4 == 0 && (uintptr_t)out % (4 * sizeof(T)) == 0 &&
                    (!hit || (weight_stride % 4 == 0 && (uintptr_t)weight % (4 * sizeof(T)) == 0));
+  if (wt && vec && (blockIdx.y * 256 + threadIdx.x) * 4 < cols) fetch_line(wt + (blockIdx.y * 256 + threadIdx.x) * 4);
+  wait_for_previous();
+  __syncthreads();
+  if (threadIdx.x < ctas && gave_up[threadIdx.x]) s_bad = 1;
+  __syncthreads();
   if (vec) {
     for (int j = (blockIdx.y * 256 + threadIdx.x) * 4; j < cols; j += 1024 * gridDim.y) {
       float v[4] = {0.f, 0.f, 0.f, 0.f};
@@ -1088,14 +1093,23 @@ constexpr int kPairs = 76;                         // of a GB300: what a split o
 constexpr int64_t kChunkBytes = (int64_t)256 << 20;
 constexpr int kMaxSplits = 64;
 constexpr int64_t kFewRows = 4096;                 // rows whose weights one block looks through: some 2 us, as a launch
-// More tokens: the targets' entries stay out of G.  That costs some 25 us of small
-// kernels, and saves grad_w's short segments and in bfloat16 G's third part (768 x 20,000,
+// More tokens: the targets' entries stay out of the G of a 32-bit grad_w.  That costs some 25
+// us of small kernels, and saves grad_w's short segments and in bfloat16 G's third part (768 x 20,000,
 // us in G / apart: bfloat16 64 tokens 67 / 87, 200 97 / 98, 400 126 / 109, 800 181 / 147;
 // float16 200 85 / 98, 400 106 / 109, 800 147 / 148; grad_w is 5e-7 / 4e-7 off).
 constexpr int64_t kSplitRows = 256;
-// Up to so many tokens 16-bit gradients too are made from two parts of G, which costs
-// nothing there: a row's few large entries are rounded alike, so that rounding them
-// once more shows (gradients 2.7e-3 off in bfloat16, 1.7e-3 with two).
+// A 16-bit grad_w is made from two parts of G, or from one without the targets' entries:
+// from one with them a bfloat16 gradient would be 2.0e-3 off, 1.66e-3 of which is its own
+// rounding.  Two parts cost products, the other form some 30 us of small kernels (us, two
+// parts / apart, bfloat16 in all: 5,003 x 256 of 1,000 tokens 51 / 60, 2,000 70 / 68, 4,096
+// 111 / 99; 20,000 x 768 of 300 78 / 93, 600 100 / 104, 1,000 134 / 120; 50,304 x 2048 of 300
+// 283 / 328, 600 392 / 382, 1,000 555 / 455; with one part and the targets in it 5,003 x 256
+// of 1,000 43, 20,000 x 768 of 1,000 95).
+constexpr int64_t kSplitRows16 = 512, kSplitRowsAlways = 2048, kSplitProducts = (int64_t)1 << 33;
+// Up to so many tokens grad_x is made from two parts of G; with more from one, and what its
+// rounding leaves out of the targets' entries, the large ones, is added at the end: as exact
+// where the others are small beside them (grad_x alone of 64 tokens, 20,000 x 768: 41 us,
+// 43 with two parts, 39 with neither).
 constexpr int64_t kExactRows = 16;
 // Steps of a segment: logits whose losses are fp32, a 32-bit grad_w without and with
 // the targets' entries; all for products that end in 16 bits.
@@ -1275,16 +1289,17 @@ Plan plan_loss(int64_t rows, int64_t classes, int64_t cols, bool copy) {
   return p;
 }
 
-// How a backward call holds G.
+// How a backward call holds G, for a grad_w of so many bits (0: none is asked for).
 struct Parts {
   int planes, planes_x;      // its parts for grad_w, for grad_x
   bool split;                // the targets' entries stay out of it
 };
-Parts parts_of(int64_t rows, bool fp32_weight, bool bf16) {
+Parts parts_of(int64_t rows, int64_t classes, int64_t cols, int bits, bool bf16) {
   Parts q;
-  q.split = fp32_weight && rows > kSplitRows;
+  q.split = bits == 32 ? rows > kSplitRows
+                       : bits == 16 && rows > kSplitRows16 && (rows > kSplitRowsAlways || rows * classes * cols > kSplitProducts);
   q.planes_x = rows > kExactRows ? 1 : 2;
-  q.planes = !fp32_weight ? q.planes_x : q.split || !bf16 ? 2 : 3;
+  q.planes = bits == 0 ? q.planes_x : q.split ? bits / 16 : bits == 32 && bf16 ? 3 : 2;
   return q;
 }
 
@@ -1293,10 +1308,14 @@ Plan plan_grad(int64_t rows, int64_t classes, int64_t cols, const Parts& q, bool
   p.x_stride = p.w_stride = up(cols, 8);
   if (q.split) {
     p.share = take(p, rows * p.x_stride * 4);
-    p.table = take(p, rows * p.x_stride * 4);
-    p.slot = take(p, classes * 4);
-    p.to = take(p, rows * 4);
-    lopt_embed_workspace(rows, rows, p.x_stride, &p.sort_bytes);
+    if (q.planes == 1) {      // a 16-bit grad_w
+      p.table = take(p, (rows * p.x_stride + kTile) * 4);      // the epilogue reads whole tiles of its rows
+      p.slot = take(p, classes * 4);
+      p.to = take(p, rows * 4);
+      lopt_embed_workspace(rows, rows, p.x_stride, &p.sort_bytes);
+    } else {
+      lopt_embed_workspace(rows, classes, cols, &p.sort_bytes);
+    }
     p.sort = take(p, p.sort_bytes);
   }
   p.flags = take(p, kMaxCtas * 4);
@@ -1374,12 +1393,12 @@ int lopt_linear_ce_workspace(int64_t rows, int64_t classes, int64_t cols, int al
     *bytes = plan_loss(n, classes, cols, !aligned).size;
     return LOPT_OK;
   }
-  // x of either type, grad_weight of this one or NULL: fewer parts of G may take more,
-  // since chunks are whole tiles of classes.
+  // x of either type, grad_weight of 16 bits, of 32 where those are asked for, or NULL:
+  // fewer parts of G may take more, since chunks are whole tiles of classes.
   *bytes = 0;
   for (bool bf16 : {false, true})
-    for (bool fp32 : {false, grad_weight_type == LOPT_F32})
-      *bytes = std::max(*bytes, plan_grad(n, classes, cols, parts_of(n, fp32, bf16), !aligned).size);
+    for (int bits : {0, 16, grad_weight_type == LOPT_F32 ? 32 : 16})
+      *bytes = std::max(*bytes, plan_grad(n, classes, cols, parts_of(n, classes, cols, bits, bf16), !aligned).size);
   return LOPT_OK;
 }
 
@@ -1483,7 +1502,7 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
   if (!grad_x && !grad_weight) return LOPT_OK;
   const bool fp32_weight = grad_weight && grad_weight_type == LOPT_F32;
   const bool bf16 = type == LOPT_BF16;
-  const Parts parts = parts_of(rows, fp32_weight, bf16);
+  const Parts parts = parts_of(rows, classes, cols, !grad_weight ? 0 : fp32_weight ? 32 : 16, bf16);
   const int planes = parts.planes, planes_x = parts.planes_x;
   const bool split = parts.split;
   const int pairs = pair_count();
@@ -1498,7 +1517,9 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
   cudaError_t e;
   int* flags = reinterpret_cast<int*>(ws + p.flags);
   static_assert(kMaxCtas == 256, "start_few clears a word a thread");
-  int* slot = split ? reinterpret_cast<int*>(ws + p.slot) : nullptr;
+  // The targets' share goes into an fp32 grad_w when that is done, into a 16-bit one, which
+  // is rounded once, from a table (300 tokens, 50,304 x 2048, fp32: 338 us, 380 from a table).
+  int* slot = split && !fp32_weight ? reinterpret_cast<int*>(ws + p.slot) : nullptr;
   const bool start = rows > kFewRows || slot;
   if (start) {
     e = launch(k_linear_ce_start, dim3(slot ? (unsigned)std::min<int64_t>((classes + kMaxCtas - 1) / kMaxCtas, 304) : 1u), dim3(kMaxCtas), 0, s,
@@ -1519,22 +1540,22 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
                (float*)nullptr, (unsigned*)nullptr, (int*)nullptr, (int32_t*)nullptr);
     if (e != cudaSuccess) return done(e);
   }
-  // The targets' share of grad_w: its rows are the classes that are targets.
-  if (slot) {
+  // The targets' share, summed into the rows of `to` (a class, or its slot).
+  auto add_share = [&](int64_t to_rows, int64_t to_cols, const void* to, int to_type, float* out, int64_t out_stride, int add) {
     const dim3 grid((unsigned)((rows + 7) / 8));
     float* share = reinterpret_cast<float*>(ws + p.share);
-    int* to = reinterpret_cast<int*>(ws + p.to);
+    int* slots = slot ? reinterpret_cast<int*>(ws + p.to) : nullptr;
     if (bf16)
       e = launch(k_linear_ce_share<__nv_bfloat16>, grid, dim3(256), 0, s, true, 1, (const __nv_bfloat16*)xp, p.x_stride, rows, (int)cols,
-                 (const float*)hit, target, index_type, (int)classes, row_weight, share, (const int*)slot, to);
+                 (const float*)hit, target, index_type, (int)classes, row_weight, share, (const int*)slot, slots);
     else
       e = launch(k_linear_ce_share<__half>, grid, dim3(256), 0, s, true, 1, (const __half*)xp, p.x_stride, rows, (int)cols,
-                 (const float*)hit, target, index_type, (int)classes, row_weight, share, (const int*)slot, to);
+                 (const float*)hit, target, index_type, (int)classes, row_weight, share, (const int*)slot, slots);
     if (e != cudaSuccess) return done(e);
-    rc = lopt_embed_backward(share, LOPT_F32, p.x_stride, to, LOPT_I32, rows, rows, p.x_stride, 1.f, 0,
-                             reinterpret_cast<float*>(ws + p.table), ws + p.sort, p.sort_bytes, nullptr, stream);
-    if (rc) return rc;
-  }
+    return embed_backward_to(share, LOPT_F32, p.x_stride, to, to_type, rows, to_rows, to_cols, 1.f, add, out, out_stride,
+                             ws + p.sort, p.sort_bytes, status, stream);
+  };
+  if (slot && (rc = add_share(rows, p.x_stride, ws + p.to, LOPT_I32, reinterpret_cast<float*>(ws + p.table), p.x_stride, 0))) return rc;
   Maps maps{};
   Args a{};
   bool ok = make_map(&maps.x_k, xp, rows, cols, p.x_stride, kHalf, bf16) && make_map(&maps.x_m, xp, rows, cols, p.x_stride, kStep, bf16) &&
@@ -1580,16 +1601,19 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
     if (k < chunks) add(grad_job(k));
     if ((e = launch_tiles(maps, a, pairs, s)) != cudaSuccess) return done(e);
   }
+  if (split && fp32_weight &&
+      (rc = add_share(classes, cols, target, index_type, static_cast<float*>(grad_weight), classes == 1 ? cols : grad_weight_stride, 1)))
+    return rc;
   if (!grad_x) return LOPT_OK;
   const dim3 grid((unsigned)rows, (unsigned)((cols + 1023) / 1024));
   const int ctas = kMaxCtas;
   if (bf16)
     e = launch(k_linear_ce_grad_x<__nv_bfloat16>, grid, dim3(256), 0, s, true, 1, (const float*)a.dx, p.dx_stride, p.slice, p.splits,
-               rows, (int)cols, (const float*)largest, target, index_type, (int)classes, row_weight, (const float*)(split ? hit : nullptr), (const __nv_bfloat16*)wp, wst,
+               rows, (int)cols, (const float*)largest, target, index_type, (int)classes, row_weight, (const float*)(planes_x == 1 ? hit : nullptr), (int)split, (const __nv_bfloat16*)wp, wst,
                (const int*)a.gave_up, ctas, (__nv_bfloat16*)grad_x, grad_x_stride);
   else
     e = launch(k_linear_ce_grad_x<__half>, grid, dim3(256), 0, s, true, 1, (const float*)a.dx, p.dx_stride, p.slice, p.splits, rows,
-               (int)cols, (const float*)largest, target, index_type, (int)classes, row_weight, (const float*)(split ? hit : nullptr), (const __half*)wp, wst,
+               (int)cols, (const float*)largest, target, index_type, (int)classes, row_weight, (const float*)(planes_x == 1 ? hit : nullptr), (int)split, (const __half*)wp, wst,
                (const int*)a.gave_up, ctas, (__half*)grad_x, grad_x_stride);
   return done(e);
 }

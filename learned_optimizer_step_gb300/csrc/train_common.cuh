@@ -220,6 +220,11 @@ inline bool overlap(const Span& a, const Span& b) {
   return true;
 }
 
+// lopt_embed_backward() into rows `grad_stride` apart (k_embedding.cu).
+int embed_backward_to(const void* grad_out, int type, int64_t grad_out_stride, const void* index, int index_type, int64_t n,
+                      int64_t rows, int64_t cols, float scale, int accumulate, float* grad, int64_t grad_stride, void* workspace,
+                      int64_t workspace_bytes, int32_t* status, void* stream);
+
 // Rows that start on `bytes` boundaries.
 inline bool rows_aligned(const Span& s, int bytes) {
   return !s.p || (s.lo() % bytes == 0 && (s.rows <= 1 || (s.stride * s.es) % bytes == 0));

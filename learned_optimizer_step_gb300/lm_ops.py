@@ -258,8 +258,8 @@ def linear_cross_entropy_backward(x, weight, target, lse, *, row_weight=None, gr
     that reaches each row's unweighted loss.
 
     grad_weight: float32 [classes, cols] (default; ``accumulate`` adds to it),
-    or a buffer of the type of x, for which G is rounded to that type once: a
-    quarter fewer products.  Rows without a target or of weight 0 get zeros and add
+    or a buffer of the type of x, which with many tokens takes a quarter fewer
+    products: what of G is not a target's is rounded to that type once.  Rows without a target or of weight 0 get zeros and add
     nothing, whatever they hold."""
     c = _Call(x, (weight, row_weight), (target, lse, grad_x, grad_weight), stream)
     kind, rows, cols, xs, classes, ws, ik, w, aligned = _hidden(c, x, weight, target, row_weight)

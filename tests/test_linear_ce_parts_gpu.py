@@ -48,3 +48,32 @@ def test_without_grad_weight_over_several_chunks():
     assert none is None
     size = g.abs() @ w.double().abs()
     R.within(dx, want, 1, size * (2.0 ** -8 / R.U), "grad_x")
+
+
+def off(got, want):
+    return float((got.double() - want).norm() / want.norm())
+
+
+@pytest.mark.parametrize("dtype", HALF, ids=ids)
+@pytest.mark.parametrize("n,v,d", [(5, 5003, 256), (17, 5003, 256), (64, 5003, 256), (203, 5003, 256), (700, 5003, 256),
+                                   (2100, 5003, 101), (700, 20000, 640)])
+def test_16_bit_gradients_are_as_exact_as_their_type(n, v, d, dtype):
+    """What rounding the exact gradients would leave, 5 % for its being other elements that
+    are rounded, 2^-16 for the logits' errors and the second part of G, and, where G has one
+    part, half a step of each of its entries but the targets', which are independent: the
+    root of the sum of their squares."""
+    x, w, t, rw = inputs(gen(n), n, v, d, dtype, padding=0.1)
+    _, lse = L.linear_cross_entropy_forward(x, w, t, row_weight=rw)
+    want_x, want_w, g = R.ce_backward(x, w, t, lse, rw)
+    others = g.clone()
+    others[torch.arange(n, device="cuda"), t.clamp(min=0)] = 0
+    half = R.half_step(dtype)
+    one_x = half * float(((others ** 2) @ (w.double() ** 2)).sum().sqrt() / want_x.norm()) if n > 16 else 0.0
+    one_w = half * float(((others ** 2).t() @ (x.double() ** 2)).sum().sqrt() / want_w.norm()) if n > 512 else 0.0
+    assert one_x < 0.1 * half and one_w < 0.1 * half       # else the bound would say nothing
+    for kind in (dtype, torch.float32, None):
+        gw = None if kind is None else torch.empty(v, d, dtype=kind, device="cuda")
+        dx, dw = L.linear_cross_entropy_backward(x, w, t, lse, row_weight=rw, grad_weight=gw, need_weight=gw is not None)
+        assert off(dx, want_x) <= 1.05 * off(want_x.to(dtype), want_x) + 2.0 ** -16 + one_x
+        if kind is dtype:
+            assert off(dw, want_w) <= 1.05 * off(want_w.to(dtype), want_w) + 2.0 ** -16 + one_w
