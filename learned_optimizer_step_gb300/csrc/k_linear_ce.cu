@@ -1113,7 +1113,11 @@ constexpr int64_t kSplitRows16 = 512, kSplitRowsAlways = 2048, kSplitProducts = 
 constexpr int64_t kExactRows = 16;
 // Steps of a segment: logits whose losses are fp32, a 32-bit grad_w without and with
 // the targets' entries; products that end in 16 bits.  Terms of one sign lose some 4e-7 of
-// the sum a step (1.05M tokens in one segment 6e-3, more than either type's half step).
+// the sum a step (1.05M tokens in one segment 6e-3, more than either type's half step), in
+// float16 three times what they do in bfloat16, whose logits and 32-bit sums therefore
+// take segments half as long (2048 wide, logits of 20 from terms of one sign: losses
+// 3.3e-5 off with 32 steps, 1.6e-5 with 16, 7e-6 with 8; bfloat16 9e-6 with 32; 8,192 x 2048 x
+// 50,304 float16 forward 1.10, 1.14, 1.19 ms).
 constexpr int kLossSegment = 32, kGradSegment = 32, kGradWSegment = 4, kSplitSegment = 64, kLongSegment = 128;
 
 int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
@@ -1451,7 +1455,7 @@ static int forward(uint64_t limit_ns, const void* x, int type, int64_t rows, int
     const int m_tiles = (int)(up(n, kTile) / kTile);
     a.jobs = 1;
     a.job[0] = Job{kLoss, m_tiles * n_tiles, m_tiles, n_tiles, 1, (int)(up(cols, kStep) / kStep), 0, 0, (int)classes, 0,
-                   kLossSegment};
+                   bf16 ? kLossSegment : kLossSegment / 2};
     if ((e = launch_tiles(maps, a, pairs, s)) != cudaSuccess) return done(e);
     const float* rw = row_weight ? row_weight + r0 : nullptr;
     e = launch(k_linear_ce_rows, dim3((unsigned)((n + kRowsOfBlock - 1) / kRowsOfBlock)), dim3(512), 0, s, true, 1, (const float2*)a.part, 2 * n_tiles,
@@ -1581,7 +1585,8 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
   auto grad_job = [&](int64_t k) {
     const int64_t v0 = k * p.chunk, v1 = std::min(classes, v0 + p.chunk);
     const int n_tiles = (int)(up(v1 - v0, kTile) / kTile);
-    return Job{kGrad, m_tiles * n_tiles, m_tiles, n_tiles, 1, (int)(up(cols, kStep) / kStep), (int)(k % p.buffers), (int)v0, (int)v1, 0, kGradSegment};
+    return Job{kGrad, m_tiles * n_tiles, m_tiles, n_tiles, 1, (int)(up(cols, kStep) / kStep), (int)(k % p.buffers), (int)v0, (int)v1, 0,
+               bf16 ? kGradSegment : kGradSegment / 2};
   };
   // Launch k makes chunk k's G beside the products of chunk k - 1: the long
   // tiles first, the short ones of G fill the last round.
@@ -1592,7 +1597,7 @@ int lopt_linear_ce_backward(const void* x, int type, int64_t rows, int64_t cols,
       Job g = grad_job(k - 1);
       if (grad_weight)
         add(Job{kGradW, g.n_tiles * d_tiles, g.n_tiles, d_tiles, 1, (int)(up(rows, kStep) / kStep) * planes, g.buffer, g.v0, g.v1, 0,
-                !fp32_weight ? kLongSegment : split ? kSplitSegment : kGradWSegment});
+                !fp32_weight ? kLongSegment : !split ? kGradWSegment : bf16 ? kSplitSegment : kSplitSegment / 2});
       if (grad_x)
         add(Job{kGradX, m_tiles * d_tiles * p.splits, m_tiles, d_tiles, p.splits, (int)(up(g.v1 - g.v0, kStep) / kStep) * planes_x, g.buffer,
                 g.v0, g.v1, k > 1, kLongSegment});

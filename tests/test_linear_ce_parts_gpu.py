@@ -99,3 +99,22 @@ def test_long_sums_of_one_sign(dtype):
     mean = float(((dw[1:].double() - want[1:]) / want[1:]).mean())
     assert abs(mean) <= (128 * 4 * 4 + n / 64 / 128) * R.U + 4 * 2 ** 0.5 * R.half_step(dtype) / (3 * 63) ** 0.5
     assert off(dw[0], want[0]) <= 2 * R.half_step(dtype)
+
+
+@pytest.mark.parametrize("dtype", HALF, ids=ids)
+@pytest.mark.parametrize("d", [256, 2048, 5000])
+def test_logits_of_terms_of_one_sign(d, dtype):
+    """Logits near 20 all of whose terms are positive.  A product of 16 cuts a sum by less than
+    a step of its last place, two half steps; float16 sums end after 16 steps of four
+    products, bfloat16 ones after 32; what the segments' sums, the exponentials, their sum and
+    the logarithm add is what test_linear_ce_gpu allows."""
+    g = gen(d)
+    n, v = 300, 2000
+    x = (1 + 0.3 * normal(g, n, d)).abs().to(dtype)
+    w = ((1 + 0.3 * normal(g, v, d)).abs() * 20 / d).to(dtype)
+    t = torch.randint(0, v, (n,), generator=g, device="cuda")
+    loss, lse = L.linear_cross_entropy_forward(x, w, t)
+    want, exact, size = R.ce_forward(x, w, t, None)
+    units = 2 * min(4 * (32 if dtype is torch.bfloat16 else 16), d / 16) + d / 1024 + 4
+    R.within(lse, exact, 1, units * size + 300 + 4 * exact, "lse")
+    R.within(loss, want, 1, units * size + 300 + 8 * exact + 4 * want, "loss")
