@@ -3,15 +3,17 @@
 // Forward: a row of h, residual and gate is read once into registers; two sums
 // of squares over the row, one after the other, give rms(h) and rms(summed).
 // Backward: sum(q hhat) needs grad_residual, which needs sum(g xhat).  But it is
-// linear in it: with c1 = -rstd_pre^2 sum(g xhat) / cols, grad_residual = A + c1 summed,
-// and sum(q hhat) = sum(u A) + c1 sum(u summed) with u = scale open w_post hhat.  So
-// three sums over the row, taken together, do: a row waits once, not twice.  Each thread keeps the sums over rows of its own
-// columns (the gradients of both weights) in registers, the blocks' sums go to
+// linear in it: with c1 = -rstd_pre sum(g xhat) / cols, grad_residual = A + c1 xhat,
+// and sum(q hhat) = scale (sum(u A) + c1 sum(u xhat)) with u = open w_post hhat.  So
+// three sums over the row, taken together, do: a row waits once, not twice.  They are taken
+// of summed and h themselves, as the products of two rows of the same size as the sums of
+// squares are, and the roots come in afterwards.  Each thread keeps the sums over rows of its
+// own columns (the gradients of both weights) in registers, the blocks' sums go to
 // the workspace and a second kernel adds them in block order.  Both directions
 // are bound by HBM bytes: 4 arrays forward, 6 backward, one and two more with a
 // gate.  65,536 x 768 bfloat16 with a gate forward 78 us (6.5 TB/s), 16,421 rows 25 us
-// (launch and first loads are a quarter of it); backward 32,768 x 2048 162 us (5.0 TB/s;
-// a row's chain of sum, barrier and stores at 16 warps), with a gate 200 us (5.4 TB/s).
+// (launch and first loads are a quarter of it); backward 32,768 x 2048 144 us (5.6 TB/s;
+// a row's chain of sum, barrier and stores at 16 warps), with a gate 194 us (5.5 TB/s).
 #include <algorithm>
 #include <cmath>
 #include <initializer_list>
@@ -361,37 +363,51 @@ __global__ void __launch_bounds__(bwd_threads(VEC * SLOTS, L), 1) k_block_norm_b
       }
     }
     t = group_sum3<L>(t, red[par], group);
-    const float c1 = -r2 * r2 * r2 * (t.a * inv);
-    const float c2 = -r1 * r1 * r1 * a.scale * (fmaf(c1, t.c, t.b) * inv);
     T* to_r = static_cast<T*>(a.dres) + row * a.drs + lane * VEC;
     T* to_g = static_cast<T*>(a.dgate) + row * a.dgs + lane * VEC;
     T* to_h = static_cast<T*>(a.dh) + row * a.dhs + lane * VEC;
+    // From xhat = f2(summed) and hhat = f1(h), or from the rows themselves with the roots in
+    // the coefficients, which spares three products an element (32,768 x 2048 bfloat16 144
+    // us, 166 with them).  Their cubes are then in these, so that only rows of ordinary size may.
+    auto gradients = [&](float c1, float c2, auto f2, auto f1, float scale, auto last) {
 #pragma unroll
-    for (int s = 0; s < SLOTS; ++s) {
-      if (!in(s)) continue;
-      float x[VEC], w[VEC], h[VEC];
-      get(kX, s, x);
+      for (int s = 0; s < SLOTS; ++s) {
+        if (!in(s)) continue;
+        float x[VEC], w[VEC], h[VEC];
+        get(kX, s, x);
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) A[s][k] = fmaf(x[k], c1, A[s][k]);
-      *reinterpret_cast<P*>(to_r + s * L * VEC) = from_floats<T, VEC>(A[s]);
-      load_weights<T, VEC>(a.w_post, a.wtype, (s * L + lane) * VEC, w);
-      get(kH, s, h);
-      if (GATE) get(kGate, s, x);
+        for (int k = 0; k < VEC; ++k) A[s][k] = fmaf(f2(x[k]), c1, A[s][k]);
+        *reinterpret_cast<P*>(to_r + s * L * VEC) = from_floats<T, VEC>(A[s]);
+        load_weights<T, VEC>(a.w_post, a.wtype, (s * L + lane) * VEC, w);
+        get(kH, s, h);
+        if (GATE) get(kGate, s, x);
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        float dz = A[s][k] * (a.scale * r1), shut = 0.f;     // times rstd_post already
-        if (GATE) {
-          float open;
-          sigmoid(x[k], open, shut);
-          dz *= open;
+        for (int k = 0; k < VEC; ++k) {
+          float dz = A[s][k] * scale, shut = 0.f;
+          if (GATE) {
+            float open;
+            sigmoid(x[k], open, shut);
+            dz *= open;
+          }
+          h[k] = f1(h[k]);
+          dw1[s][k] = fmaf(dz, h[k], dw1[s][k]);
+          const float q = dz * w[k];
+          if (GATE) x[k] = q * h[k] * shut;
+          h[k] = last(fmaf(h[k], c2, q));
         }
-        dw1[s][k] = fmaf(dz, h[k], dw1[s][k]);
-        const float q = dz * w[k];
-        if (GATE) x[k] = q * h[k] * shut;
-        h[k] = fmaf(h[k], c2, q);
+        if (GATE) *reinterpret_cast<P*>(to_g + s * L * VEC) = from_floats<T, VEC>(x);
+        *reinterpret_cast<P*>(to_h + s * L * VEC) = from_floats<T, VEC>(h);
       }
-      if (GATE) *reinterpret_cast<P*>(to_g + s * L * VEC) = from_floats<T, VEC>(x);
-      *reinterpret_cast<P*>(to_h + s * L * VEC) = from_floats<T, VEC>(h);
+    };
+    auto same = [](float v) { return v; };
+    if (fminf(r1, r2) > 0x1p-24f && fmaxf(r1, r2) < 0x1p24f) {
+      const float c1 = -r2 * r2 * r2 * (t.a * inv);
+      gradients(c1, -r1 * r1 * r1 * a.scale * (fmaf(c1, t.c, t.b) * inv), same, same, a.scale * r1, same);
+    } else {
+      auto times1 = [&](float v) { return v * r1; };
+      auto times2 = [&](float v) { return v * r2; };
+      const float c1 = -r2 * (r2 * (t.a * inv));
+      gradients(c1, -a.scale * (fmaf(c1, r1 * (r2 * t.c), r1 * t.b) * inv), times2, times1, a.scale, times1);
     }
     r1 = r1_next, r2 = r2_next;
     if (RING) {
