@@ -378,7 +378,8 @@ __global__ void __launch_bounds__(kWarps * 32) k_adamw(const __grid_constant__ L
 
 // ---- the gradients' norm ----------------------------------------------------------
 constexpr int kNormBlocks = 608;       // most blocks of a launch
-constexpr int kMaxPartials = 16 * kNormBlocks;
+constexpr int kNormLaunches = 16;      // that have partial sums of their own; more add to theirs in turn
+constexpr int kMaxPartials = kNormLaunches * kNormBlocks;
 
 // The sum of squares in about 48 bits: s the running sum, c the roundings of
 // the squares and of the sums (two-sum and fused multiply-add residuals), two sums
@@ -404,7 +405,7 @@ struct Sum {
 
 template <int N>
 __global__ void __launch_bounds__(kWarps * 32) k_adamw_norm(const __grid_constant__ List<N> list, int count, int units,
-                                                            int chunks, float minus_zero, double* part) {
+                                                            int chunks, float minus_zero, double* part, bool add) {
   const Mul mul(minus_zero);
   __shared__ double red[kWarps];
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
@@ -454,7 +455,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_adamw_norm(const __grid_constan
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int k = 1; k < kWarps; ++k) total += red[k];
-    part[blockIdx.x] = total;
+    part[blockIdx.x] = add ? part[blockIdx.x] + total : total;
   }
 }
 
@@ -652,16 +653,19 @@ int step(const lopt_adamw_tensor* tensors, int32_t n, int64_t t, double lr, doub
   if (clipped) {
     int count = 0;
     const std::vector<Part> ps = parts(tensors, n, 0, per);
-    if (ps.size() > kMaxPartials / kNormBlocks) return LOPT_E_TOO_LARGE;
-    for (const Part& p : ps) {
-      const int blocks = std::min(p.chunks, kNormBlocks);
+    int first[kNormLaunches], size[kNormLaunches];
+    for (size_t i = 0; i < ps.size(); ++i) {
+      const Part& p = ps[i];
+      const int slot = (int)(i % kNormLaunches);
+      const bool add = i >= kNormLaunches;
+      const int blocks = std::min(p.chunks, add ? size[slot] : kNormBlocks);
+      if (!add) first[slot] = count, size[slot] = blocks, count += blocks;
       e = with_list(tensors, p, per, seed, [&](const auto& list) {
         constexpr int N = sizeof(list.d) / sizeof(list.d[0]);
         return launch(k_adamw_norm<N>, dim3((unsigned)blocks), dim3(kWarps * 32), 0, s, true, 1, list,
-                      (int)p.index.size(), per, p.chunks, -0.f, part + count);
+                      (int)p.index.size(), per, p.chunks, -0.f, part + first[slot], add);
       });
       if (e != cudaSuccess) return done(e);
-      count += blocks;
     }
     if (count == 0) return done(launch(k_adamw_no_norm, dim3(1), dim3(1), 0, s, true, 1, norm));
     h.part = part, h.parts = count, h.norm = norm;
