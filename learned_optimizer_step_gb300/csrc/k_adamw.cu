@@ -460,7 +460,10 @@ __global__ void __launch_bounds__(kWarps * 32) k_adamw_norm(const __grid_constan
 }
 
 // For a list without elements.
-__global__ void k_adamw_no_norm(float* norm) { *norm = 0.f; }
+__global__ void k_adamw_no_norm(float* norm) {
+  wait_for_previous();
+  *norm = 0.f;
+}
 
 // ---- the moments as values ----------------------------------------------------------
 struct Out {
