@@ -118,3 +118,39 @@ def test_logits_of_terms_of_one_sign(d, dtype):
     units = 2 * min(4 * (32 if dtype is torch.bfloat16 else 16), d / 16) + d / 1024 + 4
     R.within(lse, exact, 1, units * size + 300 + 4 * exact, "lse")
     R.within(loss, want, 1, units * size + 300 + 8 * exact + 4 * want, "loss")
+
+
+@pytest.mark.parametrize("dtype", HALF, ids=ids)
+@pytest.mark.parametrize("n", [13, 300, 2100])
+def test_the_same_bits_again_captured_and_after_anything_in_the_workspace(n, dtype):
+    """16-bit gradients, and grad_x alone, with weights of 0, padding and a class most rows have."""
+    v, d = 1003, 101
+    x, w, t, rw = inputs(gen(n), n, v, d, dtype)
+    t[::3] = 7
+    rw[::5] = 0
+    _, lse = L.linear_cross_entropy_forward(x, w, t, row_weight=rw)
+
+    def both(x, rw):
+        dx, dw = L.linear_cross_entropy_backward(x, w, t, lse, row_weight=rw,
+                                                 grad_weight=torch.empty(v, d, dtype=dtype, device="cuda"))
+        only, _ = L.linear_cross_entropy_backward(x, w, t, lse, row_weight=rw, need_weight=False)
+        return dx, dw, only
+
+    want = both(x, rw)
+    from learned_optimizer_step_gb300 import train_ops
+    for buf, _, _ in train_ops._workspaces.values():
+        buf.fill_(255)
+    assert all(map(torch.equal, both(x, rw), want))
+    other = rw.flip(0).contiguous()
+    want_other = both(x, other)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph, buf = torch.cuda.CUDAGraph(), rw.clone()
+    with torch.cuda.stream(s):
+        with torch.cuda.graph(graph, stream=s):
+            got = both(x, buf)
+    for weights, right in ((rw, want), (other, want_other), (rw, want)):
+        buf.copy_(weights)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(map(torch.equal, got, right))
