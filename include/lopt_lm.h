@@ -30,6 +30,7 @@ extern "C" {
  * gate may be NULL (no sigmoid factor).  w_post and w_pre are [cols] of
  * weight_type: LOPT_F32 or `type`.  rstd_post and rstd_pre receive rms(h) and
  * rms(summed), fp32 [rows].  y and the statistics come from the unrounded sum.
+ * Sums of squares are fp32: a row whose sum is above its range counts as infinite.
  * In place: y or summed on h, residual or gate.
  */
 int lopt_block_norm_forward(const void* h, int type, int64_t rows, int64_t cols, int64_t h_stride,
@@ -126,9 +127,11 @@ int lopt_selftest_linear_ce(int64_t limit_ns, const void* x, int type, int64_t r
  * code q of m (int8) stands for sign(q) * q^2 * m_scale, a code of v (uint8)
  * for (q^2 * v_scale)^2: it holds the root of v.  After the step scale is the
  * block's largest |m| (or root of v) over 127^2 (255^2), and a value between
- * two codes takes the upper one with the chance that makes the mean of the
- * decoded values right: repeated steps do not lose changes smaller than the
- * distance of two codes.  A block whose largest value is at most 1e-30 is
+ * two codes takes the upper one with the chance that makes the mean of what the
+ * codes stand for right, of m and of the root of v: repeated steps do not lose
+ * changes smaller than the distance of two codes.  (v itself, the root's square, is
+ * then above its value on average, by the variance of that rounding: some 3 % for a
+ * root of 5e-4 of its block's largest, some 50 % for one of 1e-5.)  A block whose largest value is at most 1e-30 is
  * stored as zeros.  The chance is decided by bits of
  *   h = mix((i ^ key) & 0xffffffff), with i >> 32 times 0x85ebca6b, modulo 2^32, XORed into key,
  *   key = mix(seed ^ (index + 1) * 0x9e3779b9 modulo 2^32),

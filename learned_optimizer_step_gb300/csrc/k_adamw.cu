@@ -1,7 +1,9 @@
 // AdamW over a list of tensors (see lopt_lm.h for the formulas).
 //
 // One pass over param, grad and the moments; bound by HBM bytes (28 a float32
-// element, 30 with a 16-bit copy, 16 with 8-bit moments and 16-bit gradients).
+// element, 30 with a 16-bit copy, 16 with 8-bit moments and 16-bit gradients).  Tensors that
+// are not on 16-byte boundaries go element by element: 100M with bfloat16 gradients and copy
+// 516 us (432 on them), with 8-bit moments 501 (367).
 // The list travels in the kernel's parameters, so a step copies nothing to the
 // device and may be captured.  1.31G float32 elements with a bfloat16 copy take 5.64 ms
 // (7.0 TB/s), the norm of their gradients before it 0.79 ms (6.6 TB/s); 304M elements with

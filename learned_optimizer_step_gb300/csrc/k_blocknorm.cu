@@ -245,8 +245,9 @@ __global__ void __launch_bounds__(512) k_block_norm_fwd_long(const Fwd a) {
 
 // ---- backward ------------------------------------------------------------------
 // Threads of a block, of which an SM takes one: 16 warps with 128 registers, 12 with 168
-// where a lane has 24 elements.  24 warps spill and are slower (32,768 x 2048 bfloat16 341
-// us against 185 with 8 elements a lane).
+// where a lane has 24 elements.  24 warps spilled and were slower (32,768 x 2048 bfloat16 with
+// 8 elements a lane 341 us against 185).  The forms of 16-byte accesses do not spill, but for
+// float32 rows above 8,192; of those of single elements the widest do, by up to 230 bytes.
 __host__ __device__ constexpr int bwd_threads(int E, int L) { return E == 24 ? 384 : L % 96 == 0 ? 480 : 512; }
 
 // Rows of whole vectors come ahead into shared memory: every thread copies its own 16
@@ -606,7 +607,9 @@ template <typename T> struct BwdRun {
 // shortest; a warp, with up to 24 elements a lane, while that holds a row; then 16 (us,
 // bfloat16 with a gate: 65,536 x 768 77.8 by warps, 86.8 by 96 threads; 32,768 x 1024
 // 53.2 by 64 threads, 60.1 by 128; 16,384 x 2048 54.1 by 128, 62.4 by 256; 8,192 x 4096
-// 58.3 by 256, 68.3 by 512).
+// 58.3 by 256, 68.3 by 512).  Without a gate: 16,384 x 2048 float32 82; single elements
+// 32,768 x 2001 bfloat16 113 (82 at 2000), 16,384 x 2001 float32 109; 4,096 x 16,384 bfloat16
+// 127, floor 79; read three times, 2,048 x 20,000 150, floor 48.
 #define LOPT_ROWS(V, S, L_) if (n <= (int64_t)(S) * (L_)) return f.template run<V, S, L_>()
 template <int FULL, typename F> cudaError_t pick_fwd(int64_t cols, bool vec, F f) {
   if (vec) {
@@ -632,9 +635,11 @@ template <int FULL, typename F> cudaError_t pick_fwd(int64_t cols, bool vec, F f
   return f.long_rows();
 }
 // Backward in 16 bits: a lane takes 16 elements (a row's sum costs the same whatever
-// it has), a warp alone up to 24; in 32 bits 8 (us, 33.5M elements: 2048 wide float32 138
-// with 8, 163 with 16; 67M: bfloat16 185, 164, with 24 192, 32 168; with a gate 248, 200,
-// 222, 242; 768 wide with a gate 265 with 8 by 96 threads, 202 with 24 by a warp).
+// it has), a warp alone up to 24; in 32 bits 8 (us, 2048 wide, 33.5M elements float32 138
+// with 8, 203 with 16; 67M bfloat16 183 with 8, 144 with 16, 166 with 24, 342 with 32; with a
+// gate 256, 195, 220, 493; 50M 768 wide with a gate 204 with 8 by 96 threads, 154 with 24 by
+// a warp).  Single elements: 32,768 x 2001 bfloat16 273 us (152 at 2000), 16,384 x 2001
+// float32 177 (145 at 2048).  Longer rows: 4,096 x 12,288 bfloat16 472 us, floor 89.
 template <int FULL, typename F> cudaError_t pick_bwd(int64_t cols, bool vec, F f) {
   if (vec) {
     const int64_t n = cols / FULL;

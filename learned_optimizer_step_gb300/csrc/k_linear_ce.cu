@@ -26,20 +26,20 @@
 // thousands of steps that is more than fp32 results may be off.  What is cut goes
 // by the largest terms, and those are the targets'.  So a target's logit is a dot
 // product of its own, summed in two floats, which replaces the tensor cores' in the sum of
-// exponentials and in G; and for a 32-bit grad_w of many tokens (kSplitRows) the
-// targets' entries stay out of G: their share is added in fp32, to grad_x by the last
-// kernel, to grad_w by the embedding's gradient.  (To a 16-bit grad_w, of more tokens, from
-// a table whose rows are the classes that are targets, by its tiles' epilogue.)  Where they are in G an
-// accumulator of a 32-bit grad_w takes a segment of a few steps only, and the epilogue's warps add the
-// segments in registers, rounding to nearest.  (Segments of 4, 8 and 16 steps in all
-// products instead, 8,192 x 2048 x 50,304, with an earlier epilogue: 5.79, 5.19, 4.88
-// ms, 4.42 without; grad_w 3e-6 to 2e-5 off, now 3e-7.)
+// exponentials and in G; and with many tokens the targets' entries stay out of G: their
+// share is added in fp32, to grad_x by the last kernel, to a 32-bit grad_w by the
+// embedding's gradient, to a 16-bit one by its tiles' epilogue, from a table whose rows are
+// the classes that are targets.  Where they are in the G of a 32-bit grad_w, an accumulator
+// takes a segment of a few steps only, and the epilogue's warps add the segments in
+// registers, rounding to nearest (short segments in all products cost a fifth: 4 steps
+// for logits and 8 for grad_w 5.09 ms, 8,192 x 2048 x 50,304).
 //
-// Bound by the tensor cores and the power they draw: of 8,192 x 2048 x 50,304 the
-// forward pass takes 0.97 to 1.09 ms (1,740 to 1,550 TFLOP/s; library products 1,914 at
-// first, 1,705 once the GPU draws 1.4 kW), the backward pass 4.45 to 4.54 ms (1,520 to
-// 1,490 over 6.75 TFLOP: logits again, grad_x, grad_w with both parts of G).  4,099 x 768 x
-// 50,257: 0.99 to 1.06 ms; a tile of 12 steps of K is over before the epilogue that makes G.
+// Bound by the tensor cores and the power they draw: of 8,192 x 2048 x 50,304 bfloat16 the
+// forward pass takes 1.00 ms (1,690 TFLOP/s; library products 1,914 at first, 1,705 once the
+// GPU draws 1.4 kW; float16 1.09 to 1.13), the backward pass 4.5 to 4.6 ms (1,500 to 1,470
+// over 6.75 TFLOP: logits again, grad_x, grad_w with both parts of G), with a 16-bit grad_w
+// 3.2 to 3.3.  4,099 x 768 x 50,257 float16: 1.03 to 1.07 ms; a tile of 12 steps of K is over
+// before the epilogue that makes G.  That of several segments spills 56 bytes.
 // Few tokens read W at 2.5 TB/s: a tile is 256 rows of x whatever there are.
 #include <algorithm>
 #include <cmath>
@@ -56,7 +56,7 @@ namespace {
 constexpr int kTile = 256;                       // rows and columns of a pair's tile
 constexpr int kHalf = 128;                       // ... of one CTA's part of an operand
 constexpr int kStep = 64;                        // K elements of a stage: 128 bytes
-constexpr int kStages = 5;                       // 6 are no faster (8,192 x 2048 x 50,304 backward 4.50 ms, 4.45 with 5)
+constexpr int kStages = 5;                       // 6 were no faster (8,192 x 2048 x 50,304 backward 4.50 ms, 4.45 with 5)
 constexpr int kOperand = kHalf * kStep * 2;      // bytes of one operand of a stage
 constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;
